@@ -73,7 +73,8 @@ typedef enum {
 
 typedef enum {
     W4A16_F16 = 0,
-    W4A16_BF16 = 1
+    W4A16_BF16 = 1,
+    W4A16_F32 = 2 /* only where an entry point says so; the layers take F16 and BF16 */
 } w4a16_dtype;
 
 /* Same type as cudaStream_t; declared here so the header needs no CUDA include. */
@@ -337,6 +338,67 @@ w4a16_status w4a16_mxfp4_gemv(const void* x, const int32_t* qweight, const uint8
 w4a16_status w4a16_mxfp4_gemm(const void* x, const int32_t* qweight, const uint8_t* escale, void* y, int64_t M,
                               int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
                               w4a16_stream stream);
+
+/*
+ * MXFP4 in the row layout, and quantisation to MXFP4. (No counterpart on the
+ * pages this library follows: they take quantised weights as given.)
+ *
+ * The layout above keeps the eight codes of a word along K of a [K, N] weight
+ * (dim 0 of w4a16_pack). The row layout keeps them along the rows of a matrix
+ * [R, K] whose rows are contracted (dim 1): activations, or a weight stored
+ * one output feature per row.
+ *   codes   int32 [R, K/8]: nibble j of word [r, w] is the code of element
+ *           [r, 8w + j]
+ *   escale  uint8 [ceil(R/128), ceil(K/128), 32, 4, 4]: tiles of 128 rows x 4
+ *           blocks (a block is 32 consecutive elements of a row), 512 bytes a
+ *           tile. The byte of row r, block b has index [r/128, b/4, r%32,
+ *           (r/32)%4, b%4], the order in which the tensor cores take the
+ *           scales of 128 operand rows. Bytes of blocks past the row's end are
+ *           zero; bytes of rows past R are never used for a result.
+ */
+
+/*
+ * w4a16_mxfp4_quantize -- codes and exponent bytes of x [rows, cols], dtype
+ * `dt` (F16, BF16 or F32), row-major. Blocks run along `dim`:
+ *   dim 0  blocks of 32 rows of a column -> codes int32 [rows/8, cols], escale
+ *          uint8 [rows/32, cols]: the weight layout of w4a16_mxfp4_gemv,
+ *          w4a16_mxfp4_gemm and w4a16_mxfp4_moe. rows % 32 == 0, cols % 16 == 0.
+ *   dim 1  blocks of 32 columns of a row -> the row layout. cols % 32 == 0.
+ *
+ * With amax the largest magnitude of a block,
+ *
+ *     e = max(floor(log2(amax)) - 2 + 127, 0)
+ *     c = E2M1(v * 2^(127 - e)), to nearest, ties to the code with bit 0 clear;
+ *         magnitudes above 6 become 6
+ *
+ * so the largest magnitude is scaled into [4, 8). A block of zeros has e = 0.
+ * A block that holds an infinity or a NaN has e = 255 and codes 0: each of its
+ * values reads as NaN. Values that MXFP4 represents exactly are kept exactly,
+ * so quantising a dense copy gives its values back. Bit-exact; deterministic.
+ * Streams each operand once; launched with programmatic stream serialization
+ * (every read and write follows the completion of the kernel before it).
+ * Errors: NULL, DTYPE, SHAPE (non-positive, not a multiple as above, dim),
+ * ALIGN (a pointer not 16-byte aligned), DEVICE, CUDA.
+ */
+w4a16_status w4a16_mxfp4_quantize(const void* x, int32_t* codes, uint8_t* escale, int64_t rows, int64_t cols, int dim,
+                                  w4a16_dtype dt, w4a16_stream stream);
+
+/*
+ * w4a16_mxfp4_dequant_rows -- dense bf16 copy [rows, cols] (row-major) of the
+ * row layout. Bit-exact. Errors: NULL, SHAPE (non-positive, cols % 32), ALIGN,
+ * DEVICE, CUDA.
+ */
+w4a16_status w4a16_mxfp4_dequant_rows(const int32_t* codes, const uint8_t* escale, void* w, int64_t rows, int64_t cols,
+                                      w4a16_stream stream);
+
+/*
+ * w4a16_mxfp4_tile_scales -- exponent bytes stored one row after the other,
+ * src uint8 [rows, cols/32], to the tiles of the row layout (for operands
+ * quantised elsewhere). dst must not overlap src. Errors: NULL, SHAPE
+ * (non-positive, cols % 32), ALIGN (dst not 16-byte aligned), DEVICE, CUDA.
+ */
+w4a16_status w4a16_mxfp4_tile_scales(const uint8_t* src, uint8_t* dst, int64_t rows, int64_t cols,
+                                     w4a16_stream stream);
 
 /*
  * w4a16_device_status -- synchronise `stream`, then read and clear the

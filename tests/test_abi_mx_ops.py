@@ -1,0 +1,57 @@
+"""CPU checks of the MXFP4 operators' entry points: every bad argument is
+refused on the host, before the device gate."""
+import os
+
+import pytest
+
+import weight_only_int4_gb300 as w4
+from weight_only_int4_gb300 import build as w4build
+
+# Pointers that are never dereferenced: every call below ends at a host check.
+P = 0x10000
+MIS = 0x10008
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(w4.LIB_PATH):
+        w4build.build()
+    return w4.load_library()
+
+
+def quantize(lib, **kw):
+    a = dict(x=P, c=P, e=P, rows=64, cols=64, dim=1, dt=w4.BF16)
+    a.update(kw)
+    return lib.w4a16_mxfp4_quantize(a["x"], a["c"], a["e"], a["rows"], a["cols"], a["dim"], a["dt"], None)
+
+
+@pytest.mark.parametrize("dim", [0, 1])
+def test_quantize_rejections(lib, dim):
+    for name in ("x", "c", "e"):
+        assert quantize(lib, dim=dim, **{name: None}) == w4.ERR_NULL
+        assert quantize(lib, dim=dim, **{name: MIS}) == w4.ERR_ALIGN
+    assert quantize(lib, dim=dim, dt=3) == w4.ERR_DTYPE
+    assert quantize(lib, dim=dim, rows=0) == w4.ERR_SHAPE
+    assert quantize(lib, dim=dim, cols=-32) == w4.ERR_SHAPE
+    assert quantize(lib, dim=dim, rows=1 << 31) == w4.ERR_SHAPE
+    assert quantize(lib, dim=2) == w4.ERR_SHAPE
+    if dim == 0:
+        assert quantize(lib, dim=0, rows=48) == w4.ERR_SHAPE      # whole blocks of 32 rows
+        assert quantize(lib, dim=0, cols=24) == w4.ERR_SHAPE      # exponent rows start 16-byte aligned
+    else:
+        assert quantize(lib, dim=1, cols=48) == w4.ERR_SHAPE      # whole blocks of 32 columns
+
+
+def test_row_layout_rejections(lib):
+    d = lambda **k: lib.w4a16_mxfp4_dequant_rows(k.get("c", P), k.get("e", P), k.get("w", P), k.get("rows", 5),
+                                                 k.get("cols", 64), None)
+    t = lambda **k: lib.w4a16_mxfp4_tile_scales(k.get("src", P), k.get("dst", P), k.get("rows", 5),
+                                                k.get("cols", 64), None)
+    for name in ("c", "e", "w"):
+        assert d(**{name: None}) == w4.ERR_NULL
+        assert d(**{name: MIS}) == w4.ERR_ALIGN
+    assert t(src=None) == w4.ERR_NULL and t(dst=None) == w4.ERR_NULL
+    assert t(dst=MIS) == w4.ERR_ALIGN
+    for f in (d, t):
+        assert f(rows=0) == w4.ERR_SHAPE
+        assert f(cols=40) == w4.ERR_SHAPE

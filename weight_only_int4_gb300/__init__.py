@@ -37,7 +37,7 @@ STATUS_NAMES = [
 ]
 OK, ERR_NULL, ERR_SHAPE, ERR_DTYPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_DEVICE, ERR_WORKSPACE, \
     ERR_CUDA, ERR_TIMEOUT = range(10)
-F16, BF16 = 0, 1
+F16, BF16, F32 = 0, 1, 2
 OP_GEMV, OP_GEMM = 0, 1
 
 # Every symbol include/w4a16.h declares, with (restype, argtypes).
@@ -56,6 +56,9 @@ SIGNATURES = {
     "w4a16_mxfp4_dequant": (_INT, [_VP, _VP, _VP, _I64, _I64, _VP]),
     "w4a16_mxfp4_gemv": (_INT, [_VP, _VP, _VP, _VP, _I64, _I64, _I64, _VP, _SZ, _VP]),
     "w4a16_mxfp4_gemm": (_INT, [_VP, _VP, _VP, _VP, _I64, _I64, _I64, _VP, _SZ, _VP]),
+    "w4a16_mxfp4_quantize": (_INT, [_VP, _VP, _VP, _I64, _I64, _INT, _INT, _VP]),
+    "w4a16_mxfp4_dequant_rows": (_INT, [_VP, _VP, _VP, _I64, _I64, _VP]),
+    "w4a16_mxfp4_tile_scales": (_INT, [_VP, _VP, _I64, _I64, _VP]),
     "w4a16_status_string": (ctypes.c_char_p, [_INT]),
     "w4a16_abi_version": (_INT, []),
 }
@@ -119,6 +122,15 @@ def _act_code(dtype) -> int:
     if dtype == torch.bfloat16:
         return BF16
     raise TypeError(f"activations must be float16 or bfloat16, got {dtype}")
+
+
+def _dtype_code(dtype) -> int:
+    torch = _torch()
+    if dtype == torch.float32:
+        return F32
+    if dtype in (torch.float16, torch.bfloat16):
+        return _act_code(dtype)
+    raise TypeError(f"dtype must be float16, bfloat16 or float32, got {dtype}")
 
 
 def _cuda_contig(name: str, t) -> None:
@@ -368,6 +380,98 @@ def mxfp4_dequant(qweight, escale, out=None, stream=None):
         raise ValueError(f"out must be bf16 [K, N] = [{K}, {N}]")
     _check("w4a16_mxfp4_dequant", load_library().w4a16_mxfp4_dequant(qweight.data_ptr(), escale.data_ptr(),
                                                                        out.data_ptr(), N, K, _stream_ptr(stream)))
+    return out
+
+
+def mxfp4_scale_shape(rows: int, cols: int):
+    """Shape of the exponent bytes of a row-layout operand [rows, cols]: tiles of
+    128 rows x 4 blocks, [row tile, block tile, row % 32, row // 32 % 4, block % 4]."""
+    return (-(-rows // 128), -(-cols // 128), 32, 4, 4)
+
+
+def _out(name: str, t, shape, dtype, device, stream=None):
+    """`t`, checked, or a new tensor that belongs to the call's stream."""
+    torch = _torch()
+    if t is None:
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+    _cuda_contig(name, t)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def mxfp4_quantize(x, dim: int, out=None, stream=None):
+    """Quantise x (float16, bfloat16 or float32) to MXFP4 in blocks of 32 along
+    `dim`. Returns (codes, escale); `out` may give both to write into.
+
+    dim 0: x [K, N], or [E, K, N] for a stack of matrices -> int32 [(E,) K/8, N]
+           and uint8 [(E,) K/32, N], the weight layout of mxfp4_gemv, mxfp4_gemm
+           and mxfp4_moe.
+    dim 1: x [R, K] -> int32 [R, K/8] and uint8 mxfp4_scale_shape(R, K), the row
+           layout of mxfp4_matmul."""
+    torch = _torch()
+    _cuda_contig("x", x)
+    dt = _dtype_code(x.dtype)
+    if dim not in (0, 1):
+        raise ValueError(f"dim must be 0 or 1, got {dim}")
+    if not (x.dim() == 2 or (x.dim() == 3 and dim == 0)):
+        raise ValueError("x must be 2-D (or 3-D with dim 0)")
+    K = x.shape[-2] if dim == 0 else x.shape[-1]
+    if K % 32 or not x.numel():
+        raise ValueError(f"x must hold whole blocks of 32 along dim {dim}, got shape {tuple(x.shape)}")
+    if dim == 0:
+        lead, cols = tuple(x.shape[:-2]), x.shape[-1]
+        rows = x.numel() // cols
+        shapes = (*lead, K // 8, cols), (*lead, K // 32, cols)
+    else:
+        rows, cols = x.shape
+        shapes = (rows, K // 8), mxfp4_scale_shape(rows, cols)
+    codes, escale = (None, None) if out is None else out
+    sp = _stream_ptr(stream)
+    codes = _out("codes", codes, shapes[0], torch.int32, x.device, stream)
+    escale = _out("escale", escale, shapes[1], torch.uint8, x.device, stream)
+    _check("w4a16_mxfp4_quantize", load_library().w4a16_mxfp4_quantize(x.data_ptr(), codes.data_ptr(),
+                                                                        escale.data_ptr(), rows, cols, dim, dt, sp))
+    return codes, escale
+
+
+def _mx_rows(name: str, codes, escale):
+    """Checks a row-layout operand, returns its rows and K."""
+    torch = _torch()
+    for n, t in ((name, codes), (f"{name} scales", escale)):
+        _cuda_contig(n, t)
+    if codes.dim() != 2 or codes.dtype != torch.int32:
+        raise TypeError(f"{name} must be a 2-D torch.int32 tensor of codes")
+    R, K = codes.shape[0], codes.shape[1] * 8
+    if escale.dtype != torch.uint8 or tuple(escale.shape) != mxfp4_scale_shape(R, K):
+        raise ValueError(f"{name} scales must be torch.uint8 {mxfp4_scale_shape(R, K)}, got {escale.dtype} "
+                         f"{tuple(escale.shape)}")
+    return R, K
+
+
+def mxfp4_dequant_rows(codes, escale, out=None, stream=None):
+    """Dense bf16 copy [R, K] of the row layout."""
+    torch = _torch()
+    R, K = _mx_rows("codes", codes, escale)
+    out = _out("out", out, (R, K), torch.bfloat16, codes.device, stream)
+    _check("w4a16_mxfp4_dequant_rows", load_library().w4a16_mxfp4_dequant_rows(
+        codes.data_ptr(), escale.data_ptr(), out.data_ptr(), R, K, _stream_ptr(stream)))
+    return out
+
+
+def mxfp4_tile_scales(escale, out=None, stream=None):
+    """Exponent bytes [R, K/32], one row after the other, to the tiles of the row layout."""
+    torch = _torch()
+    _cuda_contig("escale", escale)
+    if escale.dim() != 2 or escale.dtype != torch.uint8:
+        raise TypeError("escale must be a 2-D torch.uint8 tensor")
+    R, K = escale.shape[0], escale.shape[1] * 32
+    out = _out("out", out, mxfp4_scale_shape(R, K), torch.uint8, escale.device, stream)
+    _check("w4a16_mxfp4_tile_scales", load_library().w4a16_mxfp4_tile_scales(escale.data_ptr(), out.data_ptr(), R, K,
+                                                                              _stream_ptr(stream)))
     return out
 
 

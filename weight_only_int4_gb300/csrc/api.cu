@@ -113,6 +113,12 @@ w4a16_status check_mx_args(const void* x, const int32_t* qweight, const uint8_t*
     return W4A16_OK;
 }
 
+// MXFP4 rows [rows, cols], blocks along the columns.
+w4a16_status check_mx_rows(int64_t rows, int64_t cols) {
+    if (rows < 1 || cols < 1 || rows > kMaxDim || cols > kMaxDim || cols % 32 != 0) return W4A16_ERR_SHAPE;
+    return W4A16_OK;
+}
+
 w4a16_status from_cuda(cudaError_t e) { return e == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA; }
 
 }  // namespace
@@ -310,6 +316,44 @@ w4a16_status w4a16_mxfp4_gemm(const void* x, const int32_t* qweight, const uint8
             reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + w4a16::skinny_partial_bytes(dp)), dp, s));
     }
     return from_cuda(w4a16::launch_mx_gemm(x, qw, escale, y, (int)M, (int)N, (int)K, dp, s));
+}
+
+w4a16_status w4a16_mxfp4_quantize(const void* x, int32_t* codes, uint8_t* escale, int64_t rows, int64_t cols, int dim,
+                                  w4a16_dtype dt, w4a16_stream stream) {
+    if (!x || !codes || !escale) return W4A16_ERR_NULL;
+    if (dt != W4A16_F16 && dt != W4A16_BF16 && dt != W4A16_F32) return W4A16_ERR_DTYPE;
+    if (dim != 0 && dim != 1) return W4A16_ERR_SHAPE;
+    w4a16_status st = dim == 1 ? check_mx_rows(rows, cols)
+                               : check_mx_weights(codes, escale, cols, rows);
+    if (st != W4A16_OK) return st;
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(escale)) return W4A16_ERR_ALIGN;
+    DeviceProps dp;
+    if ((st = device_gate(&dp)) != W4A16_OK) return st;
+    return from_cuda(w4a16::launch_mx_quantize(x, reinterpret_cast<uint32_t*>(codes), escale, rows, cols, dim,
+                                               static_cast<int>(dt), dp, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status w4a16_mxfp4_dequant_rows(const int32_t* codes, const uint8_t* escale, void* w, int64_t rows, int64_t cols,
+                                      w4a16_stream stream) {
+    if (!codes || !escale || !w) return W4A16_ERR_NULL;
+    w4a16_status st = check_mx_rows(rows, cols);
+    if (st != W4A16_OK) return st;
+    if (!aligned16(codes) || !aligned16(escale) || !aligned16(w)) return W4A16_ERR_ALIGN;
+    DeviceProps dp;
+    if ((st = device_gate(&dp)) != W4A16_OK) return st;
+    return from_cuda(w4a16::launch_mx_dequant_rows(reinterpret_cast<const uint32_t*>(codes), escale, w, rows, cols, dp,
+                                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status w4a16_mxfp4_tile_scales(const uint8_t* src, uint8_t* dst, int64_t rows, int64_t cols,
+                                     w4a16_stream stream) {
+    if (!src || !dst) return W4A16_ERR_NULL;
+    w4a16_status st = check_mx_rows(rows, cols);
+    if (st != W4A16_OK) return st;
+    if (!aligned16(dst)) return W4A16_ERR_ALIGN;
+    DeviceProps dp;
+    if ((st = device_gate(&dp)) != W4A16_OK) return st;
+    return from_cuda(w4a16::launch_mx_tile_scales(src, dst, rows, cols, dp, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 w4a16_status w4a16_selftest_wait_timeout(w4a16_stream stream) {

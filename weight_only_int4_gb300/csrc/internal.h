@@ -127,6 +127,15 @@ cudaError_t launch_mx_gemm_skinny(const void* x, const uint32_t* qw, const uint8
 cudaError_t launch_mx_gemv(const void* x, const uint32_t* qw, const uint8_t* es, void* y, int M, int N, int K,
                            const GemvPlan& plan, float* partials, uint32_t* tickets, cudaStream_t s);
 
+// Quantisation to MXFP4 (dim 0: along rows, the weight layout; dim 1: along
+// columns, the row layout with tiled exponent bytes); type as w4a16_dtype.
+cudaError_t launch_mx_quantize(const void* x, uint32_t* codes, uint8_t* es, int64_t rows, int64_t cols, int dim,
+                               int type, const DeviceProps& dp, cudaStream_t s);
+cudaError_t launch_mx_dequant_rows(const uint32_t* codes, const uint8_t* es, void* w, int64_t rows, int64_t cols,
+                                   const DeviceProps& dp, cudaStream_t s);
+cudaError_t launch_mx_tile_scales(const uint8_t* src, uint8_t* dst, int64_t rows, int64_t cols, const DeviceProps& dp,
+                                  cudaStream_t s);
+
 // Workspace of the GEMV entry points (w4a16_mxfp4_gemv runs either the GEMV
 // kernel or, for 5..16 rows of a large layer, the few-row tensor-core kernel):
 // both kernels' partial-sum regions (sizes fixed per device), then one ticket

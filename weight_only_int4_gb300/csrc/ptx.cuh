@@ -327,6 +327,75 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
 }
 
 // ---------------------------------------------------------------------------
+// tcgen05 on block-scaled 4-bit operands (kind::mxf4: E2M1 codes, one E8M0
+// byte per 32 elements of K, FP32 accumulator)
+// ---------------------------------------------------------------------------
+// Instruction descriptor: E2M1 A and B, E8M0 scales, both operands K-major.
+// One MMA is 64 deep and takes two scale bytes per row: bytes 0 and 1 of the
+// row's 32-bit word in tensor memory (`half` 0) or bytes 2 and 3 (`half` 1).
+__host__ __device__ constexpr uint32_t umma_idesc_mxf4(int M, int N, int half) {
+    return (static_cast<uint32_t>(2 * half) << 4)     // scale bytes of B
+           | (1u << 7)                                // A format: E2M1
+           | (1u << 10)                               // B format: E2M1
+           | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
+           | (1u << 23)                               // scale format: E8M0
+           | (static_cast<uint32_t>(M >> 4) << 24)    // M / 16
+           | (static_cast<uint32_t>(2 * half) << 29);   // scale bytes of A
+}
+
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+// One thread of the pair's even CTA, as umma_f16_pair. Each CTA's tensor
+// memory holds the scales of its own half of A's rows and of all of B's.
+__device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// Copy 32 rows x 16 bytes (512 contiguous bytes of shared memory) to four
+// columns of tensor memory, the same in each of its four lane quarters. Ordered
+// before the MMAs that this thread issues after it.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// The same in both CTAs of the pair, each from its own shared memory.
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Shared-memory descriptor of that source: no swizzle, 8-row groups of 16-byte
+// rows 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_copy_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);   // start address
+    d |= static_cast<uint64_t>(128 >> 4) << 32;             // stride byte offset: 8-row groups
+    d |= static_cast<uint64_t>(1) << 46;                    // descriptor version
+    return d;
+}
+
+// As tma_load_2d, but completing on the barrier at local offset `bar` of the
+// pair's even CTA; dst is this CTA's.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int32_t c0, int32_t c1,
+                                                 uint32_t even_bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(even_bar)
+        : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // bit tricks and mixed-precision FMA
 // ---------------------------------------------------------------------------
 // d = (a & b) | c  (one LOP3)
