@@ -83,7 +83,8 @@ typedef struct CUstream_st* w4a16_stream;
 /* Which kernel a workspace query is for. */
 typedef enum {
     W4A16_OP_GEMV = 0,
-    W4A16_OP_GEMM = 1
+    W4A16_OP_GEMM = 1,
+    W4A16_OP_MXFP4_MATMUL = 2
 } w4a16_op;
 
 /*
@@ -124,7 +125,10 @@ w4a16_status w4a16_unpack(const int32_t* src, uint8_t* dst, int64_t rows, int64_
  * with M <= 128: FP32 partial slots of 128 KB per SM, followed by four 32-bit
  * tickets per 128 columns (rounded up to 256 bytes); 0 for the GEMM with
  * M > 128. The same sizes serve w4a16_mxfp4_gemv and w4a16_mxfp4_gemm with
- * g = 32. Returns 0 for shapes the op rejects and when no GB300 is current.
+ * g = 32. For the MXFP4 product (g = 32): FP32 partial tiles of 128 KB per SM,
+ * then four 32-bit tickets per 128 x 128 tile of y (rounded up to 256 bytes);
+ * 0 for shapes large enough for its CTA-pair kernel.
+ * Returns 0 for shapes the op rejects and when no GB300 is current.
  */
 size_t w4a16_workspace_bytes(w4a16_op op, int64_t M, int64_t N, int64_t K, int64_t g);
 
@@ -399,6 +403,37 @@ w4a16_status w4a16_mxfp4_dequant_rows(const int32_t* codes, const uint8_t* escal
  */
 w4a16_status w4a16_mxfp4_tile_scales(const uint8_t* src, uint8_t* dst, int64_t rows, int64_t cols,
                                      w4a16_stream stream);
+
+/*
+ * w4a16_mxfp4_matmul -- product of two MXFP4 operands in the row layout,
+ *
+ *     y[m, n] = sum_k A[m, k] * B[n, k]
+ *
+ * A [M, K] (codes `a`, exponent tiles `ea`), B [N, K] (`b`, `eb`): activations
+ * quantised by w4a16_mxfp4_quantize(dim 1) against a weight quantised once, one
+ * output feature per row. The tensor cores multiply the 4-bit codes
+ * themselves, apply both exponents per 32 elements of K and accumulate in
+ * FP32; the sum is rounded once to `dt` (F16, BF16 or F32). An exponent byte of
+ * 255 makes every y of its row (of A) or column (of B) NaN. Exponents whose
+ * product leaves the FP32 range overflow to infinity or flush to zero.
+ *
+ * Many tiles of 256 x 256 run on CTA pairs; otherwise (always for M <= 128) a
+ * kernel with 128 rows of B per tile splits its K steps evenly over the SMs and
+ * needs a workspace of w4a16_workspace_bytes(W4A16_OP_MXFP4_MATMUL, M, N, K, 32)
+ * bytes, with the ownership and zero-fill rules of w4a16_gemv's; a workspace of
+ * this op serves this op only. Tiles shared by several CTAs are summed in a
+ * fixed order: the result is deterministic. After a W4A16_ERR_TIMEOUT reported
+ * by w4a16_device_status, zero the workspace again.
+ *
+ * M >= 1, N % 8 == 0, K % 32 == 0. Launched with programmatic stream
+ * serialization: its prologue (barriers, tensor memory) may overlap the end of
+ * the kernel before it; every read and write of caller memory follows that
+ * kernel's completion.
+ * Errors: NULL, DTYPE, SHAPE, ALIGN, WORKSPACE, DEVICE, CUDA.
+ */
+w4a16_status w4a16_mxfp4_matmul(const int32_t* a, const uint8_t* ea, const int32_t* b, const uint8_t* eb, void* y,
+                                int64_t M, int64_t N, int64_t K, w4a16_dtype dt, void* workspace,
+                                size_t workspace_bytes, w4a16_stream stream);
 
 /*
  * w4a16_device_status -- synchronise `stream`, then read and clear the

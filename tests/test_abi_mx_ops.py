@@ -55,3 +55,26 @@ def test_row_layout_rejections(lib):
     for f in (d, t):
         assert f(rows=0) == w4.ERR_SHAPE
         assert f(cols=40) == w4.ERR_SHAPE
+
+
+def matmul(lib, **kw):
+    a = dict(a=P, ea=P, b=P, eb=P, y=P, M=5, N=64, K=128, dt=w4.BF16, ws=P, n=1 << 40)
+    a.update(kw)
+    return lib.w4a16_mxfp4_matmul(a["a"], a["ea"], a["b"], a["eb"], a["y"], a["M"], a["N"], a["K"], a["dt"], a["ws"],
+                                  a["n"], None)
+
+
+def test_matmul_rejections(lib):
+    for name in ("a", "ea", "b", "eb", "y"):
+        assert matmul(lib, **{name: None}) == w4.ERR_NULL
+        assert matmul(lib, **{name: MIS}) == w4.ERR_ALIGN
+    assert matmul(lib, dt=3) == w4.ERR_DTYPE
+    assert matmul(lib, M=0) == w4.ERR_SHAPE
+    assert matmul(lib, N=12) == w4.ERR_SHAPE
+    assert matmul(lib, K=48) == w4.ERR_SHAPE
+    assert matmul(lib, K=-32) == w4.ERR_SHAPE
+    assert matmul(lib, N=1 << 31) == w4.ERR_SHAPE
+    # exponent tiles past 32-bit coordinates
+    assert matmul(lib, N=(1 << 31) - 8, K=(1 << 31) - 32) == w4.ERR_SHAPE
+    assert matmul(lib, ws=None) == w4.ERR_WORKSPACE      # M <= 128 always needs one
+    assert matmul(lib, ws=MIS) == w4.ERR_WORKSPACE

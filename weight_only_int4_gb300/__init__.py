@@ -38,7 +38,7 @@ STATUS_NAMES = [
 OK, ERR_NULL, ERR_SHAPE, ERR_DTYPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_DEVICE, ERR_WORKSPACE, \
     ERR_CUDA, ERR_TIMEOUT = range(10)
 F16, BF16, F32 = 0, 1, 2
-OP_GEMV, OP_GEMM = 0, 1
+OP_GEMV, OP_GEMM, OP_MXFP4_MATMUL = 0, 1, 2
 
 # Every symbol include/w4a16.h declares, with (restype, argtypes).
 _VP, _I64, _SZ, _INT = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
@@ -59,6 +59,7 @@ SIGNATURES = {
     "w4a16_mxfp4_quantize": (_INT, [_VP, _VP, _VP, _I64, _I64, _INT, _INT, _VP]),
     "w4a16_mxfp4_dequant_rows": (_INT, [_VP, _VP, _VP, _I64, _I64, _VP]),
     "w4a16_mxfp4_tile_scales": (_INT, [_VP, _VP, _I64, _I64, _VP]),
+    "w4a16_mxfp4_matmul": (_INT, [_VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _INT, _VP, _SZ, _VP]),
     "w4a16_status_string": (ctypes.c_char_p, [_INT]),
     "w4a16_abi_version": (_INT, []),
 }
@@ -472,6 +473,32 @@ def mxfp4_tile_scales(escale, out=None, stream=None):
     out = _out("out", out, mxfp4_scale_shape(R, K), torch.uint8, escale.device, stream)
     _check("w4a16_mxfp4_tile_scales", load_library().w4a16_mxfp4_tile_scales(escale.data_ptr(), out.data_ptr(), R, K,
                                                                               _stream_ptr(stream)))
+    return out
+
+
+def mxfp4_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, workspace=None, stream=None):
+    """y = A @ B.T of two row-layout operands: A [M, K] (activations through
+    mxfp4_quantize(x, 1)) and B [N, K] (a weight, one output feature per row).
+    4-bit tensor-core product, FP32 sums; returns y [M, N] in `out_dtype`
+    (bfloat16 unless given; float16 and float32 too)."""
+    torch = _torch()
+    M, K = _mx_rows("a", a, a_scale)
+    N, Kb = _mx_rows("b", b, b_scale)
+    if K != Kb:
+        raise ValueError(f"a has K = {K}, b has K = {Kb}")
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    dt = _dtype_code(out_dtype)
+    lib = load_library()
+    out = _out("out", out, (M, N), out_dtype, a.device, stream)
+    if workspace is None:
+        need = lib.w4a16_workspace_bytes(OP_MXFP4_MATMUL, M, N, K, 32)
+        workspace = _cached_workspace(need, a.device, stream, OP_MXFP4_MATMUL) if need else None
+    ws_ptr, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(),
+                                                          workspace.numel() * workspace.element_size())
+    _check("w4a16_mxfp4_matmul", lib.w4a16_mxfp4_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(),
+                                                        b_scale.data_ptr(), out.data_ptr(), M, N, K, dt, ws_ptr,
+                                                        ws_bytes, _stream_ptr(stream)))
     return out
 
 

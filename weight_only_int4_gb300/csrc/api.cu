@@ -119,6 +119,16 @@ w4a16_status check_mx_rows(int64_t rows, int64_t cols) {
     return W4A16_OK;
 }
 
+// Product of row-layout operands. The exponent tiles of an operand are
+// addressed by 32-bit coordinates, one per 512 bytes.
+w4a16_status check_mx_product(int64_t M, int64_t N, int64_t K) {
+    w4a16_status st = check_mx_rows(M, K);
+    if (st == W4A16_OK) st = check_mx_rows(N, K);
+    if (st != W4A16_OK) return st;
+    if (N % 8 != 0 || ((M > N ? M : N) / 128 + 2) * (K / 128 + 2) > kMaxDim) return W4A16_ERR_SHAPE;
+    return W4A16_OK;
+}
+
 w4a16_status from_cuda(cudaError_t e) { return e == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA; }
 
 }  // namespace
@@ -164,13 +174,15 @@ w4a16_status w4a16_unpack(const int32_t* src, uint8_t* dst, int64_t rows, int64_
 }
 
 size_t w4a16_workspace_bytes(w4a16_op op, int64_t M, int64_t N, int64_t K, int64_t g) {
-    if (op != W4A16_OP_GEMV && op != W4A16_OP_GEMM) return 0;
+    if (op != W4A16_OP_GEMV && op != W4A16_OP_GEMM && op != W4A16_OP_MXFP4_MATMUL) return 0;
     if (M < 1 || N < 8 || N % 8 || K < 1 || K > kMaxDim || N > kMaxDim || M > kMaxDim || !supported_group(g) || K % g)
         return 0;
     if (op == W4A16_OP_GEMV && M > 16) return 0;
     if (op == W4A16_OP_GEMM && M > w4a16::kSkinnyMaxM) return 0;
     DeviceProps dp;
     if (device_gate(&dp) != W4A16_OK) return 0;
+    if (op == W4A16_OP_MXFP4_MATMUL)
+        return check_mx_product(M, N, K) == W4A16_OK ? w4a16::mx_matmul_workspace_bytes(M, N, dp) : 0;
     if (op == W4A16_OP_GEMM) return w4a16::skinny_workspace_bytes((int)N, dp);
     return w4a16::gemv_workspace(w4a16::plan_gemv((int)M, (int)N, (int)K, (int)g, dp), (int)N, dp).total();
 }
@@ -244,11 +256,12 @@ w4a16_status w4a16_device_status(w4a16_stream stream) {
     DeviceProps dp;
     w4a16_status st = device_gate(&dp);
     if (st != W4A16_OK) return st;
-    uint32_t v = 0, u = 0, k = 0;
+    uint32_t v = 0, u = 0, k = 0, p = 0;
     if (w4a16::read_and_clear_device_error(&v, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess ||
-        w4a16::read_and_clear_gemv_error(&u) != cudaSuccess || w4a16::read_and_clear_skinny_error(&k) != cudaSuccess)
+        w4a16::read_and_clear_gemv_error(&u) != cudaSuccess || w4a16::read_and_clear_skinny_error(&k) != cudaSuccess ||
+        w4a16::read_and_clear_mx_matmul_error(&p) != cudaSuccess)
         return W4A16_ERR_CUDA;
-    return (v | u | k) ? W4A16_ERR_TIMEOUT : W4A16_OK;
+    return (v | u | k | p) ? W4A16_ERR_TIMEOUT : W4A16_OK;
 }
 
 w4a16_status w4a16_dequant(const int32_t* qweight, const void* scales, const int32_t* qzeros, void* w, int64_t N,
@@ -354,6 +367,25 @@ w4a16_status w4a16_mxfp4_tile_scales(const uint8_t* src, uint8_t* dst, int64_t r
     DeviceProps dp;
     if ((st = device_gate(&dp)) != W4A16_OK) return st;
     return from_cuda(w4a16::launch_mx_tile_scales(src, dst, rows, cols, dp, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status w4a16_mxfp4_matmul(const int32_t* a, const uint8_t* ea, const int32_t* b, const uint8_t* eb, void* y,
+                                int64_t M, int64_t N, int64_t K, w4a16_dtype dt, void* workspace,
+                                size_t workspace_bytes, w4a16_stream stream) {
+    if (!a || !ea || !b || !eb || !y) return W4A16_ERR_NULL;
+    if (dt != W4A16_F16 && dt != W4A16_BF16 && dt != W4A16_F32) return W4A16_ERR_DTYPE;
+    w4a16_status st = check_mx_product(M, N, K);
+    if (st != W4A16_OK) return st;
+    if (!aligned16(a) || !aligned16(ea) || !aligned16(b) || !aligned16(eb) || !aligned16(y)) return W4A16_ERR_ALIGN;
+    if (M <= 128 && (!workspace || !aligned16(workspace))) return W4A16_ERR_WORKSPACE;
+    DeviceProps dp;
+    if ((st = device_gate(&dp)) != W4A16_OK) return st;
+    const size_t need = w4a16::mx_matmul_workspace_bytes(M, N, dp);
+    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+    const w4a16::MxMatmulArgs args{reinterpret_cast<const uint32_t*>(a), ea, reinterpret_cast<const uint32_t*>(b), eb, y,
+                                   (int)M, (int)N, (int)K};
+    return from_cuda(w4a16::launch_mx_matmul(args, static_cast<int>(dt), workspace, dp,
+                                             reinterpret_cast<cudaStream_t>(stream)));
 }
 
 w4a16_status w4a16_selftest_wait_timeout(w4a16_stream stream) {

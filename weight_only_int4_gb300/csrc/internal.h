@@ -136,6 +136,23 @@ cudaError_t launch_mx_dequant_rows(const uint32_t* codes, const uint8_t* es, voi
 cudaError_t launch_mx_tile_scales(const uint8_t* src, uint8_t* dst, int64_t rows, int64_t cols, const DeviceProps& dp,
                                   cudaStream_t s);
 
+// Product of two MXFP4 row-layout operands, y [M, N] = A [M, K] B [N, K]^T.
+struct MxMatmulArgs {
+    const uint32_t* a;
+    const uint8_t* ea;
+    const uint32_t* b;
+    const uint8_t* eb;
+    void* y;
+    int M, N, K;
+};
+// 0 where the kernel for this shape needs none; else FP32 partial tiles (128 KB
+// per SM, a size fixed per device), then four ticket words per 128 x 128 tile
+// (zero before the first call; every call leaves them zero).
+size_t mx_matmul_workspace_bytes(int64_t M, int64_t N, const DeviceProps& dp);
+cudaError_t launch_mx_matmul(const MxMatmulArgs& a, int out_type, void* workspace, const DeviceProps& dp,
+                             cudaStream_t s);
+cudaError_t read_and_clear_mx_matmul_error(uint32_t* out);
+
 // Workspace of the GEMV entry points (w4a16_mxfp4_gemv runs either the GEMV
 // kernel or, for 5..16 rows of a large layer, the few-row tensor-core kernel):
 // both kernels' partial-sum regions (sizes fixed per device), then one ticket

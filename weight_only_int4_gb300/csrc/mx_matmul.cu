@@ -1,0 +1,733 @@
+// Product of two MXFP4 operands on the 5th-generation tensor cores,
+//
+//     y[m, n] = sum_k A[m, k] B[n, k],   A = a * 2^(ea - 127) per 32 elements of K, B alike,
+//
+// both in the row layout (codes along K, exponent bytes in tiles of 128 rows x
+// 4 blocks). tcgen05.mma kind::mxf4 multiplies the codes as they are, applies
+// both rows' exponents to every 32-deep partial product and accumulates in
+// FP32, so nothing is decoded: codes and exponent tiles go from global memory
+// to shared memory by TMA, the exponents on to tensor memory by tcgen05.cp.
+// FP32 sums are rounded once to the output type.
+//
+// A K step is 256 deep: 128 bytes of codes per row, the width of one
+// 128-byte-swizzled row, four MMAs of 64, two exponent tiles per 128 rows.
+// Codes past K are zero-filled by TMA and their exponent bytes are zero
+// (2^-127), so the tail of a block group adds nothing.
+//
+// Two kernels:
+//   pair_kernel  CTA pairs own 256 x 256 tiles of y (cta_group::2).
+//   rows_kernel  128 rows of B against 16..128 rows of A, its work split
+//                stream-K over (tile, K step) units: what has few tiles.
+//
+// Every mbarrier wait is bounded (about two seconds). On expiry the kernel
+// records the timeout in a device word, raises the abort flag, every role
+// stops, copies and MMAs in flight are waited for (bounded), tensor memory is
+// freed and the kernel returns.
+#include "internal.h"
+#include "ptx.cuh"
+#include "tmap.h"
+
+#include <algorithm>
+#include <mutex>
+
+namespace w4a16 {
+
+__device__ unsigned int g_mx_matmul_error = 0;
+
+namespace {
+
+constexpr int kStepK = 256;                 // elements of K per step
+constexpr uint32_t kRowBytes = kStepK / 2;  // codes of one row of a step
+constexpr uint32_t kScaleTile = 512;        // exponent bytes of 128 rows x 128 elements
+constexpr int kThreads = 256;
+constexpr int kEpiWarp0 = 4;                // warps 4..7: one tensor-memory lane quarter each
+constexpr uint32_t kSuspendNs = 20000;
+constexpr unsigned long long kWaitLimitCycles = 4000000000ull;   // ~2 s at 2 GHz
+constexpr unsigned int kErrTimeout = 9u;
+
+enum : int { kF16 = 0, kBf16 = 1, kF32 = 2 };
+
+// Abort flag of this CTA; in a pair a timeout raises the peer's flag too.
+struct Abort {
+    volatile int* flag;
+    uint32_t addr;
+    uint32_t peer;   // cluster rank of the peer, or ~0
+};
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Abort& ab) {
+    const unsigned long long t0 = clock64();
+    for (;;) {
+        if (mbar_try_wait_suspend(bar, parity, kSuspendNs)) return true;
+        if (*ab.flag) return false;
+        if (clock64() - t0 > kWaitLimitCycles) {
+            *ab.flag = 1;
+            if (ab.peer != ~0u) st_cluster_u32(ab.addr, ab.peer, 1u);
+            atomicOr(&g_mx_matmul_error, 1u << kErrTimeout);
+            return false;
+        }
+    }
+}
+
+// Lane 0 waits; the shuffle orders the other lanes' accesses after its acquire.
+__device__ __forceinline__ bool warp_wait_bar(uint32_t bar, uint32_t parity, const Abort& ab, int lane) {
+    int ok = 1;
+    if (lane == 0) ok = wait_bar(bar, parity, ab) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    __syncwarp();
+    return ok != 0;
+}
+
+// Bounded wait for the last phase of each ring barrier that `steps` steps have
+// used, before the ring's shared memory is given back: no copy, and no arrival
+// of a tensor-core commit, may be in flight to a CTA that has left (the next
+// kernel's CTA, started early, keeps its own barriers there).
+__device__ __forceinline__ void drain_ring(const uint64_t* bars, int stages, long long steps) {
+    const unsigned long long t0 = clock64();
+    for (long long i = steps > stages ? steps - stages : 0; i < steps; ++i)
+        while (!mbar_try_wait(smem_u32(bars + i % stages), static_cast<uint32_t>(i / stages) & 1u) &&
+               clock64() - t0 < kWaitLimitCycles) {
+        }
+}
+
+template <int kOut>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (kOut == kBf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+template <int kOut>
+__device__ __forceinline__ void store1(void* y, size_t at, float v) {
+    if constexpr (kOut == kF32) static_cast<float*>(y)[at] = v;
+    if constexpr (kOut == kBf16) static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
+    if constexpr (kOut == kF16) static_cast<__half*>(y)[at] = __float2half_rn(v);
+}
+
+// 32 consecutive columns of one row, in groups of 8 (N % 8 == 0).
+template <int kOut>
+__device__ __forceinline__ void store_row32(void* y, size_t row_at, int n, int N, const uint32_t (&r)[32]) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        if (n + 8 * v >= N) break;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r[8 * v + i]);
+        if constexpr (kOut == kF32) {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(y) + row_at + n + 8 * v);
+            dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+            dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + row_at + n + 8 * v) =
+                make_uint4(pack2<kOut>(f[0], f[1]), pack2<kOut>(f[2], f[3]), pack2<kOut>(f[4], f[5]),
+                           pack2<kOut>(f[6], f[7]));
+        }
+    }
+}
+
+// MMAs (64 deep) and exponent tiles (128 deep) of a K step.
+__device__ __forceinline__ int step_mmas(int K, int kt) { return min(4, (K - kt * kStepK + 63) >> 6); }
+__device__ __forceinline__ int step_groups(int groups, int kt) { return min(2, groups - 2 * kt); }
+
+// ---------------------------------------------------------------------------
+// CTA pairs, 256 x 256 tiles
+// ---------------------------------------------------------------------------
+// CTA r of the pair holds rows [128r, 128r + 128) of the tile's A block and of
+// its B block, the exponents of those A rows and of all 256 B rows. Per K step
+// an SM receives 35 KB for 16.8 MFLOP. All loads of both CTAs complete on the
+// even CTA's barrier; its MMA thread copies the exponents to tensor memory in
+// both CTAs and issues the pair's MMAs.
+//
+// Tensor memory (512 columns): two 256-column accumulators that overlap by 64
+// columns, [0, 256) and [192, 448), and two exponent buffers of 32 columns. The
+// epilogue reads the shared 64 columns first and then lets the next tile's
+// MMAs start into the other accumulator, so only that read, not the whole
+// epilogue, separates two tiles' MMAs.
+namespace pair {
+
+constexpr int BM = 256, BN = 256, CM = 128, CN = 128;
+constexpr int kStages = 6;
+constexpr uint32_t kABytes = CM * kRowBytes, kBBytes = CN * kRowBytes;
+constexpr uint32_t kSfaBytes = 2 * kScaleTile, kSfbBytes = 4 * kScaleTile;
+constexpr uint32_t kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
+static_assert(kStageBytes % 1024 == 0, "operand tiles stay 1024-byte aligned");
+constexpr uint32_t kAcc1 = 192, kScaleCol = 448, kScaleCols = 32;
+constexpr uint32_t kTmemCols = 512;
+
+struct __align__(8) Barriers {
+    uint64_t full[kStages];     // even CTA: both CTAs' copies landed
+    uint64_t empty[kStages];    // both: the step's MMAs retired
+    uint64_t tfull[2];          // both: accumulator complete
+    uint64_t tempty;            // even CTA: the shared columns were read (one arrival per epilogue warp of the pair)
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + sizeof(Barriers);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+
+template <int kOut>
+__global__ void __launch_bounds__(kThreads, 1)
+pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+            const __grid_constant__ CUtensorMap tsa, const __grid_constant__ CUtensorMap tsb, void* __restrict__ y,
+            int M, int N, int K) {
+    extern __shared__ uint8_t smem_raw[];
+    // the same layout in both CTAs: the MMA and the exponent copies address the peer's at this CTA's offsets
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Barriers* bars = reinterpret_cast<Barriers*>(smem + kStages * kStageBytes);
+    const uint32_t base = smem_u32(smem);
+    auto st_a = [&](int s) { return base + s * kStageBytes; };
+    auto st_b = [&](int s) { return base + s * kStageBytes + kABytes; };
+    auto st_sfa = [&](int s) { return base + s * kStageBytes + kABytes + kBBytes; };
+    auto st_sfb = [&](int s) { return base + s * kStageBytes + kABytes + kBBytes + kSfaBytes; };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair_id = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int num_m = (M + BM - 1) / BM, num_n = (N + BN - 1) / BN;
+    const long long tiles = static_cast<long long>(num_m) * num_n;
+    const int kt_total = (K + kStepK - 1) / kStepK, groups = (K + 127) >> 7;
+    const Abort ab{&bars->abort, smem_u32(&bars->abort), rank ^ 1u};
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&bars->full[s]), 1);
+            mbar_init(smem_u32(&bars->empty[s]), 1);
+        }
+        mbar_init(smem_u32(&bars->tfull[0]), 1);
+        mbar_init(smem_u32(&bars->tfull[1]), 1);
+        mbar_init(smem_u32(&bars->tempty), 2 * 4);
+        mbar_init(smem_u32(&bars->drain), 1);
+        bars->abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&ta);
+        tma_prefetch_desc(&tb);
+        tma_prefetch_desc(&tsa);
+        tma_prefetch_desc(&tsb);
+    }
+    if (warp == 2) tmem_alloc_pair(smem_u32(&bars->tmem_base), kTmemCols);
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            long long j = 0;
+            bool ok = true;
+            for (long long t = pair_id; t < tiles && ok; t += npairs) {
+                const int m_blk = static_cast<int>(t % num_m), n_blk = static_cast<int>(t / num_m);
+                for (int kt = 0; kt < kt_total; ++kt, ++j) {
+                    const int s = static_cast<int>(j % kStages);
+                    const uint32_t ph = static_cast<uint32_t>(j / kStages) & 1u;
+                    if (!wait_bar(smem_u32(&bars->empty[s]), ph ^ 1u, ab)) { ok = false; break; }
+                    const uint32_t fb = smem_u32(&bars->full[s]);
+                    if (rank == 0) mbar_arrive_expect_tx(fb, 2 * kStageBytes);
+                    const uint32_t even = map_to_cta(fb, 0);
+                    const int r = static_cast<int>(rank);
+                    tma_load_2d_pair(st_a(s), &ta, kt * static_cast<int>(kRowBytes), m_blk * BM + r * CM, even);
+                    tma_load_2d_pair(st_b(s), &tb, kt * static_cast<int>(kRowBytes), n_blk * BN + r * CN, even);
+                    tma_load_2d_pair(st_sfa(s), &tsa, 0, (m_blk * 2 + r) * groups + 2 * kt, even);
+                    tma_load_2d_pair(st_sfb(s), &tsb, 0, n_blk * 2 * groups + 2 * kt, even);
+                    tma_load_2d_pair(st_sfb(s) + 2 * kScaleTile, &tsb, 0, (n_blk * 2 + 1) * groups + 2 * kt, even);
+                }
+            }
+            // every step's copies (counted in the even CTA) and commits have arrived
+            if (rank == 0) drain_ring(bars->full, kStages, j);
+            drain_ring(bars->empty, kStages, j);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ exponent copies and MMAs (even CTA)
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t kIdesc0 = umma_idesc_mxf4(BM, BN, 0), kIdesc1 = umma_idesc_mxf4(BM, BN, 1);
+            constexpr uint16_t kPair = 0x3;
+            long long j = 0;
+            int it = 0;
+            bool ok = true;
+            for (long long t = pair_id; t < tiles && ok; t += npairs, ++it) {
+                if (it > 0 && !wait_bar(smem_u32(&bars->tempty), (it - 1) & 1, ab)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d = tmem + ((it & 1) ? kAcc1 : 0u);
+                for (int kt = 0; kt < kt_total; ++kt, ++j) {
+                    const int s = static_cast<int>(j % kStages);
+                    if (!wait_bar(smem_u32(&bars->full[s]), static_cast<uint32_t>(j / kStages) & 1u, ab)) {
+                        ok = false;
+                        break;
+                    }
+                    // the MMAs that read this exponent buffer two steps ago have retired
+                    if (j >= 2 && !wait_bar(smem_u32(&bars->empty[(j - 2) % kStages]),
+                                            static_cast<uint32_t>((j - 2) / kStages) & 1u, ab)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sfa = tmem + kScaleCol + static_cast<uint32_t>(j & 1) * kScaleCols, sfb = sfa + 8;
+                    const int ng = step_groups(groups, kt), nk = step_mmas(K, kt);
+                    for (int gq = 0; gq < ng; ++gq) {
+                        tmem_cp_scales_pair(sfa + 4 * gq, scale_copy_desc(st_sfa(s) + gq * kScaleTile));
+                        tmem_cp_scales_pair(sfb + 8 * gq, scale_copy_desc(st_sfb(s) + gq * kScaleTile));
+                        tmem_cp_scales_pair(sfb + 8 * gq + 4, scale_copy_desc(st_sfb(s) + (2 + gq) * kScaleTile));
+                    }
+                    const uint64_t adesc = sw128_kmajor_desc(st_a(s)), bdesc = sw128_kmajor_desc(st_b(s));
+                    // 64 elements (32 bytes) further along K inside the swizzle atom
+                    for (int kk = 0; kk < nk; ++kk)
+                        umma_mxf4_pair(d, adesc + 2u * kk, bdesc + 2u * kk, (kk & 1) ? kIdesc1 : kIdesc0,
+                                       sfa + 4 * (kk >> 1), sfb + 8 * (kk >> 1), (kt | kk) != 0);
+                    umma_commit_pair_mc(smem_u32(&bars->empty[s]), kPair);
+                }
+                if (!ok) break;
+                umma_commit_pair_mc(smem_u32(&bars->tfull[it & 1]), kPair);
+            }
+            umma_commit_pair(smem_u32(&bars->drain));
+            drain_ring(&bars->drain, 1, 1);
+        }
+    } else if (warp >= kEpiWarp0) {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+        int it = 0;
+        for (long long t = pair_id; t < tiles; t += npairs, ++it) {
+            const int m_blk = static_cast<int>(t % num_m), n_blk = static_cast<int>(t / num_m);
+            if (!warp_wait_bar(smem_u32(&bars->tfull[it & 1]), (it >> 1) & 1, ab, lane)) break;
+            tc_fence_after();
+            const uint32_t d = tmem + lanes + ((it & 1) ? kAcc1 : 0u);
+            const int m = m_blk * BM + static_cast<int>(rank) * CM + q * 32 + lane;
+            const size_t row_at = static_cast<size_t>(m) * N;
+            const int n0 = n_blk * BN;
+            // columns shared with the other accumulator first: the last 64 of the even one, the first 64 of the odd
+            const int c0 = (it & 1) ? 0 : 6;
+            {
+                uint32_t r0[32], r1[32];
+                tmem_ld_32x32b_x32(d + c0 * 32, r0);
+                tmem_ld_32x32b_x32(d + c0 * 32 + 32, r1);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(smem_u32(&bars->tempty), 0);
+                if (m < M) {
+                    store_row32<kOut>(y, row_at, n0 + c0 * 32, N, r0);
+                    store_row32<kOut>(y, row_at, n0 + c0 * 32 + 32, N, r1);
+                }
+            }
+#pragma unroll 1
+            for (int i = 0; i < 6; ++i) {
+                const int ch = (it & 1) ? i + 2 : i;
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(d + ch * 32, r);
+                tmem_wait_ld();
+                if (m < M) store_row32<kOut>(y, row_at, n0 + ch * 32, N, r);
+            }
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();   // neither CTA leaves while the pair's copies, MMAs or arrivals may touch it
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+}  // namespace pair
+
+// ---------------------------------------------------------------------------
+// few rows of A: 128 rows of B per tile, stream-K
+// ---------------------------------------------------------------------------
+// The tile's 128 rows of B are the MMA's M, MP rows of A its N: with few rows
+// of A the kernel streams B and is bound by HBM bandwidth, so every SM gets the
+// same number of K steps whatever the number of tiles. A tile shared by several
+// CTAs is finished by the last of them (a ticket per tile and epilogue warp),
+// which adds their FP32 partial tiles in ascending CTA order: deterministic.
+namespace rows {
+
+constexpr int BN = 128;
+constexpr size_t kSlotFloats = 128 * 128;   // partial tile, [row of A][row of B]
+
+template <int MP>
+struct Cfg {
+    static constexpr int kStages = MP == 128 ? 6 : MP == 64 ? 8 : 10;
+    static constexpr uint32_t kABytes = BN * kRowBytes;   // the MMA's A: rows of B
+    static constexpr uint32_t kXBytes = MP * kRowBytes;
+    static constexpr uint32_t kStageBytes = kABytes + kXBytes + 4 * kScaleTile;
+    static_assert(kStageBytes % 1024 == 0, "operand tiles stay 1024-byte aligned");
+    static constexpr uint32_t kAccCols = MP < 32 ? 32 : MP;   // the epilogue reads 32 columns at a time
+    static constexpr uint32_t kScaleCol = 2 * kAccCols;       // 16 columns of exponents per stage
+    static constexpr uint32_t kTmemCols = kScaleCol + 16 * kStages <= 256 ? 256 : 512;
+    static_assert(kScaleCol + 16 * kStages <= 512, "tensor memory budget");
+};
+
+template <int MP>
+struct __align__(8) Barriers {
+    uint64_t full[Cfg<MP>::kStages];
+    uint64_t empty[Cfg<MP>::kStages];
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+template <int MP>
+constexpr size_t smem_bytes() {
+    return 1024 + Cfg<MP>::kStages * Cfg<MP>::kStageBytes + sizeof(Barriers<MP>);
+}
+
+// CTA b of G owns units [b U / G, (b + 1) U / G); the owner of unit u.
+__device__ __forceinline__ long long first_unit(long long b, long long U, int G) { return b * U / G; }
+__device__ __forceinline__ int unit_owner(long long u, long long U, int G) {
+    return static_cast<int>(((u + 1) * G - 1) / U);
+}
+
+template <int kOut, int MP>
+__global__ void __launch_bounds__(kThreads, 1)
+rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
+            const __grid_constant__ CUtensorMap tsw, const __grid_constant__ CUtensorMap tsx, void* __restrict__ y,
+            int M, int N, int K, float* __restrict__ partials, uint32_t* __restrict__ tickets) {
+    using C = Cfg<MP>;
+    constexpr int S = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Barriers<MP>* bars = reinterpret_cast<Barriers<MP>*>(smem + S * C::kStageBytes);
+    const uint32_t base = smem_u32(smem);
+    auto st_w = [&](int s) { return base + s * C::kStageBytes; };
+    auto st_x = [&](int s) { return base + s * C::kStageBytes + C::kABytes; };
+    auto st_sw = [&](int s) { return base + s * C::kStageBytes + C::kABytes + C::kXBytes; };
+    auto st_sx = [&](int s) { return st_sw(s) + 2 * kScaleTile; };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int num_m = (M + MP - 1) / MP, num_n = (N + BN - 1) / BN;
+    const int kt_total = (K + kStepK - 1) / kStepK, groups = (K + 127) >> 7;
+    const int G = gridDim.x;
+    const long long U = static_cast<long long>(num_m) * num_n * kt_total;
+    const long long u_begin = first_unit(blockIdx.x, U, G), u_end = first_unit(blockIdx.x + 1ll, U, G);
+    const Abort ab{&bars->abort, 0u, ~0u};
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&bars->full[s]), 1);
+            mbar_init(smem_u32(&bars->empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&bars->tfull[a]), 1);
+            mbar_init(smem_u32(&bars->tempty[a]), 4);
+        }
+        mbar_init(smem_u32(&bars->drain), 1);
+        bars->abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tw);
+        tma_prefetch_desc(&tx);
+        tma_prefetch_desc(&tsw);
+        tma_prefetch_desc(&tsx);
+    }
+    if (warp == 2) tmem_alloc(smem_u32(&bars->tmem_base), C::kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    griddep_launch_dependents();
+    griddep_wait();
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            long long j = 0;
+            bool ok = true;
+            for (long long u = u_begin; u < u_end; ++u, ++j) {
+                const long long t = u / kt_total;
+                const int kt = static_cast<int>(u - t * kt_total);
+                const int m_blk = static_cast<int>(t % num_m), n_blk = static_cast<int>(t / num_m);
+                const int s = static_cast<int>(j % S);
+                if (!wait_bar(smem_u32(&bars->empty[s]), (static_cast<uint32_t>(j / S) & 1u) ^ 1u, ab)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb = smem_u32(&bars->full[s]);
+                mbar_arrive_expect_tx(fb, C::kStageBytes);
+                tma_load_2d(st_w(s), &tw, kt * static_cast<int>(kRowBytes), n_blk * BN, fb);
+                tma_load_2d(st_x(s), &tx, kt * static_cast<int>(kRowBytes), m_blk * MP, fb);
+                tma_load_2d(st_sw(s), &tsw, 0, n_blk * groups + 2 * kt, fb);
+                tma_load_2d(st_sx(s), &tsx, 0, m_blk * groups + 2 * kt, fb);
+            }
+            drain_ring(bars->full, S, j);
+            drain_ring(bars->empty, S, j);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ exponent copies and MMAs
+        if (lane == 0) {
+            constexpr uint32_t kIdesc0 = umma_idesc_mxf4(BN, MP, 0), kIdesc1 = umma_idesc_mxf4(BN, MP, 1);
+            long long j = 0;
+            int seg = 0;
+            bool ok = true;
+            for (long long u = u_begin; u < u_end && ok; ++seg) {
+                const long long t = u / kt_total;
+                const int k0 = static_cast<int>(u - t * kt_total);
+                const int k1 = static_cast<int>(std::min<long long>(kt_total, k0 + (u_end - u)));
+                const int acc = seg & 1;
+                if (!wait_bar(smem_u32(&bars->tempty[acc]), ((seg >> 1) & 1) ^ 1, ab)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d = tmem + acc * C::kAccCols;
+                for (int kt = k0; kt < k1; ++kt, ++j) {
+                    const int s = static_cast<int>(j % S);
+                    if (!wait_bar(smem_u32(&bars->full[s]), static_cast<uint32_t>(j / S) & 1u, ab)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    // one exponent buffer per stage: the MMAs that read it retired before the stage was refilled
+                    const uint32_t sfw = tmem + C::kScaleCol + 16 * s, sfx = sfw + 8;
+                    const int ng = step_groups(groups, kt), nk = step_mmas(K, kt);
+                    for (int gq = 0; gq < ng; ++gq) {
+                        tmem_cp_scales(sfw + 4 * gq, scale_copy_desc(st_sw(s) + gq * kScaleTile));
+                        tmem_cp_scales(sfx + 4 * gq, scale_copy_desc(st_sx(s) + gq * kScaleTile));
+                    }
+                    const uint64_t wdesc = sw128_kmajor_desc(st_w(s)), xdesc = sw128_kmajor_desc(st_x(s));
+                    for (int kk = 0; kk < nk; ++kk)
+                        umma_mxf4(d, wdesc + 2u * kk, xdesc + 2u * kk, (kk & 1) ? kIdesc1 : kIdesc0,
+                                  sfw + 4 * (kk >> 1), sfx + 4 * (kk >> 1), kt != k0 || kk != 0);
+                    umma_commit(smem_u32(&bars->empty[s]));
+                }
+                if (!ok) break;
+                umma_commit(smem_u32(&bars->tfull[acc]));
+                u += k1 - k0;
+            }
+            umma_commit(smem_u32(&bars->drain));
+            drain_ring(&bars->drain, 1, 1);
+        }
+    } else if (warp >= kEpiWarp0) {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+        int seg = 0;
+        for (long long u = u_begin; u < u_end; ++seg) {
+            const long long t = u / kt_total;
+            const int k0 = static_cast<int>(u - t * kt_total);
+            const int k1 = static_cast<int>(std::min<long long>(kt_total, k0 + (u_end - u)));
+            u += k1 - k0;
+            const int acc = seg & 1;
+            if (!warp_wait_bar(smem_u32(&bars->tfull[acc]), (seg >> 1) & 1, ab, lane)) break;
+            tc_fence_after();
+            const int m0 = static_cast<int>(t % num_m) * MP;
+            const int mc = min(MP, M - m0);                              // rows of A of this tile
+            const int n = static_cast<int>(t / num_m) * BN + q * 32 + lane;
+            const bool whole = k0 == 0 && k1 == kt_total;
+            // slot 1: the tile begins here; slot 0: an earlier CTA began it
+            float* part = partials + (static_cast<size_t>(blockIdx.x) * 2 + (k0 == 0 ? 1 : 0)) * kSlotFloats + q * 32 + lane;
+#pragma unroll 1
+            for (int ch = 0; ch * 32 < mc; ++ch) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(tmem + lanes + acc * C::kAccCols + ch * 32, r);
+                tmem_wait_ld();
+                if (whole) {
+                    if (n < N) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (ch * 32 + i < mc)
+                                store1<kOut>(y, static_cast<size_t>(m0 + ch * 32 + i) * N + n, __uint_as_float(r[i]));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (ch * 32 + i < mc) __stcg(part + (ch * 32 + i) * 128, __uint_as_float(r[i]));
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc]));
+            if (whole) continue;
+            const long long first = t * kt_total;
+            const int b_lo = unit_owner(first, U, G), b_hi = unit_owner(first + kt_total - 1, U, G);
+            __threadfence();
+            __syncwarp();
+            uint32_t last = 0;
+            if (lane == 0) last = atomicAdd(tickets + 4 * t + q, 1u) == static_cast<unsigned>(b_hi - b_lo);
+            last = __shfl_sync(0xffffffffu, last, 0);
+            if (!last) continue;
+            __threadfence();
+            if (n < N) {
+                const float* lo = partials + (static_cast<size_t>(b_lo) * 2 + 1) * kSlotFloats + q * 32 + lane;
+                for (int c = 0; c < mc; c += 16) {
+                    float sum[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum[i] = c + i < mc ? __ldcg(lo + (c + i) * 128) : 0.f;
+                    for (int b = b_lo + 1; b <= b_hi; ++b) {
+                        const float* src = partials + static_cast<size_t>(b) * 2 * kSlotFloats + q * 32 + lane;
+                        float v[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = c + i < mc ? __ldcg(src + (c + i) * 128) : 0.f;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) sum[i] += v[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c + i < mc) store1<kOut>(y, static_cast<size_t>(m0 + c + i) * N + n, sum[i]);
+                }
+            }
+            if (lane == 0) tickets[4 * t + q] = 0u;
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+}  // namespace rows
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// Codes [rows, K/2 bytes]: boxes of one K step by `box_rows` rows.
+bool encode_codes(CUtensorMap* map, const uint32_t* codes, int rows, int K, int box_rows) {
+    return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, static_cast<uint64_t>(K / 2),
+                     static_cast<uint64_t>(rows), static_cast<uint64_t>(K / 2), kRowBytes,
+                     static_cast<uint32_t>(box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Exponent tiles as rows of 128 words: boxes of two tiles (one K step of 128 rows).
+bool encode_scales(CUtensorMap* map, const uint8_t* es, int rows, int K) {
+    const uint64_t n = static_cast<uint64_t>((rows + 127) / 128) * ((K + 127) / 128);
+    return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_INT32, es, 128, n, kScaleTile, 128, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+template <int kOut>
+int resident_pairs(const DeviceProps& dp) {
+    static std::mutex mu;
+    static int cached[64] = {0};
+    const int dev = (dp.device >= 0 && dp.device < 64) ? dp.device : 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!cached[dev]) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * (dp.sms / 2));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = pair::kSmemBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, pair::pair_kernel<kOut>, &cfg) != cudaSuccess || n <= 0) {
+            (void)cudaGetLastError();
+            n = dp.sms / 2;
+        }
+        cached[dev] = n;
+    }
+    return cached[dev];
+}
+
+template <int kOut>
+cudaError_t launch_pair(const MxMatmulArgs& a, const DeviceProps& dp, cudaStream_t s) {
+    auto kern = pair::pair_kernel<kOut>;
+    if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), dp.device, pair::kSmemBytes);
+        e != cudaSuccess)
+        return e;
+    CUtensorMap ta, tb, tsa, tsb;
+    if (!encode_codes(&ta, a.a, a.M, a.K, pair::CM) || !encode_codes(&tb, a.b, a.N, a.K, pair::CN) ||
+        !encode_scales(&tsa, a.ea, a.M, a.K) || !encode_scales(&tsb, a.eb, a.N, a.K))
+        return cudaErrorInvalidValue;
+    const long long tiles = static_cast<long long>((a.M + pair::BM - 1) / pair::BM) * ((a.N + pair::BN - 1) / pair::BN);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::max<long long>(1, std::min<long long>(tiles, resident_pairs<kOut>(dp)))));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = pair::kSmemBytes;
+    cfg.stream = s;
+    // An ordinary launch: with programmatic serialization on both this kernel and
+    // the quantisation before it, a queue of about a hundred such pairs stopped
+    // making progress (every wait in the kernel is bounded, and the same calls one
+    // at a time were right), for a gain of about 1 % on a call of 0.37 ms.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, ta, tb, tsa, tsb, a.y, a.M, a.N, a.K);
+}
+
+template <int kOut, int MP>
+cudaError_t launch_rows(const MxMatmulArgs& a, float* partials, uint32_t* tickets, const DeviceProps& dp,
+                        cudaStream_t s) {
+    auto kern = rows::rows_kernel<kOut, MP>;
+    constexpr size_t kSmem = rows::smem_bytes<MP>();
+    static_assert(kSmem <= 227 * 1024, "shared memory budget");
+    if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), dp.device, kSmem); e != cudaSuccess)
+        return e;
+    CUtensorMap tw, tx, tsw, tsx;
+    if (!encode_codes(&tw, a.b, a.N, a.K, rows::BN) || !encode_codes(&tx, a.a, a.M, a.K, MP) ||
+        !encode_scales(&tsw, a.eb, a.N, a.K) || !encode_scales(&tsx, a.ea, a.M, a.K))
+        return cudaErrorInvalidValue;
+    const long long units = static_cast<long long>((a.M + MP - 1) / MP) * ((a.N + rows::BN - 1) / rows::BN) *
+                            ((a.K + kStepK - 1) / kStepK);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(units, dp.sms)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, tw, tx, tsw, tsx, a.y, a.M, a.N, a.K, partials, tickets);
+}
+
+// The pair kernel needs tiles for most of the GPU's CTA pairs; below that the
+// stream-K kernel spreads the same work evenly.
+bool uses_pairs(long long M, long long N, const DeviceProps& dp) {
+    if (M <= 128) return false;
+    const long long tiles = ((M + pair::BM - 1) / pair::BM) * ((N + pair::BN - 1) / pair::BN);
+    return tiles * 2 >= dp.sms;
+}
+
+size_t partial_bytes(const DeviceProps& dp) {
+    return static_cast<size_t>(dp.sms) * 2 * rows::kSlotFloats * sizeof(float);
+}
+
+template <int kOut>
+cudaError_t launch_typed(const MxMatmulArgs& a, void* workspace, const DeviceProps& dp, cudaStream_t s) {
+    if (uses_pairs(a.M, a.N, dp)) return launch_pair<kOut>(a, dp, s);
+    float* partials = static_cast<float*>(workspace);
+    uint32_t* tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + partial_bytes(dp));
+    if (a.M <= 16) return launch_rows<kOut, 16>(a, partials, tickets, dp, s);
+    if (a.M <= 32) return launch_rows<kOut, 32>(a, partials, tickets, dp, s);
+    if (a.M <= 64) return launch_rows<kOut, 64>(a, partials, tickets, dp, s);
+    return launch_rows<kOut, 128>(a, partials, tickets, dp, s);
+}
+
+}  // namespace
+
+size_t mx_matmul_workspace_bytes(int64_t M, int64_t N, const DeviceProps& dp) {
+    if (uses_pairs(M, N, dp)) return 0;
+    const size_t tiles = static_cast<size_t>((M + 127) / 128) * ((N + rows::BN - 1) / rows::BN);
+    return partial_bytes(dp) + ((tiles * 4 * sizeof(uint32_t) + 255) & ~size_t(255));
+}
+
+cudaError_t launch_mx_matmul(const MxMatmulArgs& a, int out_type, void* workspace, const DeviceProps& dp,
+                             cudaStream_t s) {
+    if (out_type == kF16) return launch_typed<kF16>(a, workspace, dp, s);
+    if (out_type == kBf16) return launch_typed<kBf16>(a, workspace, dp, s);
+    return launch_typed<kF32>(a, workspace, dp, s);
+}
+
+cudaError_t read_and_clear_mx_matmul_error(uint32_t* out) {
+    uint32_t v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_mx_matmul_error, sizeof(v));
+    if (e != cudaSuccess) return e;
+    if (v) {
+        const uint32_t zero = 0;
+        e = cudaMemcpyToSymbol(g_mx_matmul_error, &zero, sizeof(zero));
+    }
+    *out = v;
+    return e;
+}
+
+}  // namespace w4a16
