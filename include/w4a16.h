@@ -436,6 +436,56 @@ w4a16_status w4a16_mxfp4_matmul(const int32_t* a, const uint8_t* ea, const int32
                                 size_t workspace_bytes, w4a16_stream stream);
 
 /*
+ * w4a16_mxfp4_moe -- a mixture-of-experts layer with MXFP4 expert weights for
+ * 1..64 tokens, in one kernel. ("Add BF16xFP4 MoE GEMM stage1 kernel" is the
+ * gate/up product alone, with the routing done outside.)
+ *
+ *     p[t, :]   = softmax(x[t, :] . router^T) over the E experts
+ *     chosen(t) = the top_k experts of largest logit, ties to the lower index;
+ *                 with `renormalize` their p is divided by its sum
+ *     h_e[t, :] = silu(x W1_e) * (x W3_e),     silu(v) = v / (1 + exp(-v))
+ *     y[t, :]   = sum over chosen e of p[t, e] * (h_e[t, :] W2_e)
+ *
+ * x       bf16 [T, H]; router bf16 [E, H], one expert per row
+ * w13     int32 [E, H/8, 2 I], e13 uint8 [E, H/32, 2 I]: every expert's
+ *         [W1 | W3] in the weight layout above, gate columns [0, I), up
+ *         columns [I, 2 I) (w4a16_mxfp4_quantize with dim 0 on the stack
+ *         [E * H, 2 I])
+ * w2      int32 [E, I/8, H], e2 uint8 [E, I/32, H]
+ * y       bf16 [T, H], written (not accumulated into)
+ *
+ * Logits, softmax, the products' sums and the weighted sum are FP32. x and h
+ * enter the products as fp16 scaled by powers of two (x per token, h per 32
+ * columns): x converts exactly where it is within 2^-29 of its token's largest
+ * magnitude, h is rounded to 11 bits. Weights of a chosen expert are read once
+ * per 16 tokens that chose it; experts nobody chose are not read. A token's y
+ * does not depend on the other tokens, except that tokens beyond 16 of one
+ * expert are taken in further groups; the result is deterministic. A token with
+ * an infinity or NaN in x or in a chosen expert's block yields NaN there and
+ * leaves other tokens alone.
+ *
+ * workspace: at least w4a16_mxfp4_moe_workspace_bytes(...) bytes with the
+ * ownership and zero-fill rules of w4a16_gemv's (the words that must be zero
+ * are the first 262400 bytes, left zero, bar a counter, by every call, so one
+ * workspace serves calls of any shape it is large enough for). Two calls that
+ * may run at the same time must not share one. After a W4A16_ERR_TIMEOUT
+ * reported by w4a16_device_status, zero it again.
+ *
+ * Launched cooperatively (its thread blocks wait for one another at two
+ * points); it can be captured in a CUDA graph.
+ * Limits: 1 <= T <= 64, 1 <= E <= 256, 1 <= top_k <= min(E, 16), H and I
+ * multiples of 32, H <= 65536.
+ * Errors: NULL, SHAPE, ALIGN, WORKSPACE, DEVICE, CUDA.
+ */
+w4a16_status w4a16_mxfp4_moe(const void* x, const void* router, const int32_t* w13, const uint8_t* e13,
+                             const int32_t* w2, const uint8_t* e2, void* y, int64_t T, int64_t E, int64_t top_k,
+                             int64_t H, int64_t I, int renormalize, void* workspace, size_t workspace_bytes,
+                             w4a16_stream stream);
+
+/* Bytes of workspace w4a16_mxfp4_moe needs; 0 for shapes it rejects. */
+size_t w4a16_mxfp4_moe_workspace_bytes(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I);
+
+/*
  * w4a16_device_status -- synchronise `stream`, then read and clear the
  * device-side error word of the current device. Every wait on an mbarrier
  * inside the GEMM pipeline gives up after about two seconds; the kernel then

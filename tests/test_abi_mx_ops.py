@@ -78,3 +78,26 @@ def test_matmul_rejections(lib):
     assert matmul(lib, N=(1 << 31) - 8, K=(1 << 31) - 32) == w4.ERR_SHAPE
     assert matmul(lib, ws=None) == w4.ERR_WORKSPACE      # M <= 128 always needs one
     assert matmul(lib, ws=MIS) == w4.ERR_WORKSPACE
+
+
+def moe(lib, **kw):
+    a = dict(x=P, r=P, w13=P, e13=P, w2=P, e2=P, y=P, T=3, E=8, k=2, H=64, I=32, ws=P, n=1 << 40)
+    a.update(kw)
+    return lib.w4a16_mxfp4_moe(a["x"], a["r"], a["w13"], a["e13"], a["w2"], a["e2"], a["y"], a["T"], a["E"], a["k"],
+                               a["H"], a["I"], 1, a["ws"], a["n"], None)
+
+
+def test_moe_rejections(lib):
+    for name in ("x", "r", "w13", "e13", "w2", "e2", "y"):
+        assert moe(lib, **{name: None}) == w4.ERR_NULL
+        assert moe(lib, **{name: MIS}) == w4.ERR_ALIGN
+    for bad in (dict(T=0), dict(T=65), dict(E=0), dict(E=257), dict(k=0), dict(k=9), dict(k=17, E=32), dict(H=48),
+                dict(H=0), dict(H=65568), dict(I=40), dict(I=-32), dict(I=1 << 31)):
+        assert moe(lib, **bad) == w4.ERR_SHAPE, bad
+        shape = dict(T=3, E=8, k=2, H=64, I=32, **{}) | bad
+        assert lib.w4a16_mxfp4_moe_workspace_bytes(shape["T"], shape["E"], shape["k"], shape["H"], shape["I"]) == 0
+    assert moe(lib, ws=None) == w4.ERR_WORKSPACE
+    assert moe(lib, ws=MIS) == w4.ERR_WORKSPACE
+    need = lib.w4a16_mxfp4_moe_workspace_bytes(3, 8, 2, 64, 32)
+    assert need > 0
+    assert moe(lib, n=need - 1) == w4.ERR_WORKSPACE

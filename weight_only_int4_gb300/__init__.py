@@ -60,6 +60,8 @@ SIGNATURES = {
     "w4a16_mxfp4_dequant_rows": (_INT, [_VP, _VP, _VP, _I64, _I64, _VP]),
     "w4a16_mxfp4_tile_scales": (_INT, [_VP, _VP, _I64, _I64, _VP]),
     "w4a16_mxfp4_matmul": (_INT, [_VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _INT, _VP, _SZ, _VP]),
+    "w4a16_mxfp4_moe": (_INT, [_VP] * 7 + [_I64] * 5 + [_INT, _VP, _SZ, _VP]),
+    "w4a16_mxfp4_moe_workspace_bytes": (_SZ, [_I64] * 5),
     "w4a16_status_string": (ctypes.c_char_p, [_INT]),
     "w4a16_abi_version": (_INT, []),
 }
@@ -499,6 +501,43 @@ def mxfp4_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, workspace=Non
     _check("w4a16_mxfp4_matmul", lib.w4a16_mxfp4_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(),
                                                         b_scale.data_ptr(), out.data_ptr(), M, N, K, dt, ws_ptr,
                                                         ws_bytes, _stream_ptr(stream)))
+    return out
+
+
+def mxfp4_moe(x, router, w13, e13, w2, e2, top_k: int, renormalize: bool = True, out=None, workspace=None,
+              stream=None):
+    """Mixture-of-experts layer with MXFP4 expert weights for 1..64 tokens, in one
+    kernel: router product, softmax, the top_k experts of each token (their
+    weights divided by their sum where `renormalize`), gate and up products,
+    SwiGLU, down product and the weighted sum.
+
+    x bf16 [T, H], router bf16 [E, H]; w13 int32 [E, H/8, 2 I] with e13 uint8
+    [E, H/32, 2 I] (gate columns, then up columns) and w2 int32 [E, I/8, H] with
+    e2 uint8 [E, I/32, H], as mxfp4_quantize(w, 0) makes them of [E, H, 2 I] and
+    [E, I, H]. Returns y bf16 [T, H]."""
+    torch = _torch()
+    for name, t, dtype, dims in (("x", x, torch.bfloat16, 2), ("router", router, torch.bfloat16, 2),
+                                 ("w13", w13, torch.int32, 3), ("e13", e13, torch.uint8, 3),
+                                 ("w2", w2, torch.int32, 3), ("e2", e2, torch.uint8, 3)):
+        _cuda_contig(name, t)
+        if t.dim() != dims or t.dtype != dtype:
+            raise TypeError(f"{name} must be a {dims}-D {dtype} tensor, got {t.dim()}-D {t.dtype}")
+    T, H = x.shape
+    E, I = w2.shape[0], w2.shape[1] * 8
+    for name, t, shape in (("router", router, (E, H)), ("w13", w13, (E, H // 8, 2 * I)),
+                           ("e13", e13, (E, H // 32, 2 * I)), ("w2", w2, (E, I // 8, H)), ("e2", e2, (E, I // 32, H))):
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} shape {tuple(t.shape)} does not match {shape}")
+    lib = load_library()
+    out = _out("out", out, (T, H), torch.bfloat16, x.device, stream)
+    if workspace is None:
+        need = lib.w4a16_mxfp4_moe_workspace_bytes(T, E, top_k, H, I)
+        workspace = _cached_workspace(need, x.device, stream, "mxfp4_moe") if need else None
+    ws_ptr, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(),
+                                                          workspace.numel() * workspace.element_size())
+    _check("w4a16_mxfp4_moe", lib.w4a16_mxfp4_moe(x.data_ptr(), router.data_ptr(), w13.data_ptr(), e13.data_ptr(),
+                                                  w2.data_ptr(), e2.data_ptr(), out.data_ptr(), T, E, top_k, H, I,
+                                                  1 if renormalize else 0, ws_ptr, ws_bytes, _stream_ptr(stream)))
     return out
 
 

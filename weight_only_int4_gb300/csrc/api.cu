@@ -129,6 +129,15 @@ w4a16_status check_mx_product(int64_t M, int64_t N, int64_t K) {
     return W4A16_OK;
 }
 
+w4a16_status check_moe_shape(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
+    if (T < 1 || T > w4a16::kMoeMaxTokens || E < 1 || E > w4a16::kMoeMaxExperts) return W4A16_ERR_SHAPE;
+    if (k < 1 || k > w4a16::kMoeMaxTopK || k > E) return W4A16_ERR_SHAPE;
+    if (H < 32 || H > w4a16::kMoeMaxHidden || H % 32 != 0) return W4A16_ERR_SHAPE;
+    // the stacked rows E I / 8 and the 2 I columns are 32-bit coordinates
+    if (I < 32 || I % 32 != 0 || I > kMaxDim / 512) return W4A16_ERR_SHAPE;
+    return W4A16_OK;
+}
+
 w4a16_status from_cuda(cudaError_t e) { return e == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA; }
 
 }  // namespace
@@ -256,12 +265,12 @@ w4a16_status w4a16_device_status(w4a16_stream stream) {
     DeviceProps dp;
     w4a16_status st = device_gate(&dp);
     if (st != W4A16_OK) return st;
-    uint32_t v = 0, u = 0, k = 0, p = 0;
+    uint32_t v = 0, u = 0, k = 0, p = 0, m = 0;
     if (w4a16::read_and_clear_device_error(&v, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess ||
         w4a16::read_and_clear_gemv_error(&u) != cudaSuccess || w4a16::read_and_clear_skinny_error(&k) != cudaSuccess ||
-        w4a16::read_and_clear_mx_matmul_error(&p) != cudaSuccess)
+        w4a16::read_and_clear_mx_matmul_error(&p) != cudaSuccess || w4a16::read_and_clear_mx_moe_error(&m) != cudaSuccess)
         return W4A16_ERR_CUDA;
-    return (v | u | k | p) ? W4A16_ERR_TIMEOUT : W4A16_OK;
+    return (v | u | k | p | m) ? W4A16_ERR_TIMEOUT : W4A16_OK;
 }
 
 w4a16_status w4a16_dequant(const int32_t* qweight, const void* scales, const int32_t* qzeros, void* w, int64_t N,
@@ -386,6 +395,34 @@ w4a16_status w4a16_mxfp4_matmul(const int32_t* a, const uint8_t* ea, const int32
                                    (int)M, (int)N, (int)K};
     return from_cuda(w4a16::launch_mx_matmul(args, static_cast<int>(dt), workspace, dp,
                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t w4a16_mxfp4_moe_workspace_bytes(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I) {
+    if (check_moe_shape(T, E, top_k, H, I) != W4A16_OK) return 0;
+    return w4a16::mx_moe_workspace_bytes((int)T, (int)E, (int)top_k, (int)H, (int)I);
+}
+
+w4a16_status w4a16_mxfp4_moe(const void* x, const void* router, const int32_t* w13, const uint8_t* e13,
+                             const int32_t* w2, const uint8_t* e2, void* y, int64_t T, int64_t E, int64_t top_k,
+                             int64_t H, int64_t I, int renormalize, void* workspace, size_t workspace_bytes,
+                             w4a16_stream stream) {
+    if (!x || !router || !w13 || !e13 || !w2 || !e2 || !y) return W4A16_ERR_NULL;
+    w4a16_status st = check_moe_shape(T, E, top_k, H, I);
+    if (st != W4A16_OK) return st;
+    if (!aligned16(x) || !aligned16(router) || !aligned16(w13) || !aligned16(e13) || !aligned16(w2) || !aligned16(e2) ||
+        !aligned16(y))
+        return W4A16_ERR_ALIGN;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < w4a16::mx_moe_workspace_bytes((int)T, (int)E, (int)top_k, (int)H, (int)I))
+        return W4A16_ERR_WORKSPACE;
+    DeviceProps dp;
+    if ((st = device_gate(&dp)) != W4A16_OK) return st;
+    const w4a16::MxMoeArgs args{x,       router,   reinterpret_cast<const uint32_t*>(w13),
+                                e13,     reinterpret_cast<const uint32_t*>(w2),
+                                e2,      y,        (int)T,
+                                (int)E,  (int)top_k, (int)H,
+                                (int)I,  renormalize != 0};
+    return from_cuda(w4a16::launch_mx_moe(args, workspace, dp, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 w4a16_status w4a16_selftest_wait_timeout(w4a16_stream stream) {

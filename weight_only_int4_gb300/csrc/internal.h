@@ -153,6 +153,26 @@ cudaError_t launch_mx_matmul(const MxMatmulArgs& a, int out_type, void* workspac
                              cudaStream_t s);
 cudaError_t read_and_clear_mx_matmul_error(uint32_t* out);
 
+// Mixture-of-experts layer for a few tokens, MXFP4 expert weights.
+constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 256, kMoeMaxHidden = 65536;
+// Barrier words and one ticket per 64 columns of y and token: the same size for
+// every shape, zero before the first call, and no call writes data below it.
+constexpr size_t kMoeControlBytes = 256 + size_t(kMoeMaxHidden / 64) * kMoeMaxTokens * 4;
+struct MxMoeArgs {
+    const void* x;
+    const void* router;
+    const uint32_t* w13;
+    const uint8_t* e13;
+    const uint32_t* w2;
+    const uint8_t* e2;
+    void* y;
+    int T, E, k, H, I;
+    bool renormalize;
+};
+size_t mx_moe_workspace_bytes(int T, int E, int k, int H, int I);
+cudaError_t launch_mx_moe(const MxMoeArgs& a, void* workspace, const DeviceProps& dp, cudaStream_t s);
+cudaError_t read_and_clear_mx_moe_error(uint32_t* out);
+
 // Workspace of the GEMV entry points (w4a16_mxfp4_gemv runs either the GEMV
 // kernel or, for 5..16 rows of a large layer, the few-row tensor-core kernel):
 // both kernels' partial-sum regions (sizes fixed per device), then one ticket
