@@ -14,26 +14,30 @@
 //      as fp16 with one power-of-two factor per token
 //      -- grid barrier --
 //   1  every CTA picks the experts itself (a warp per token) and lists the
-//      tokens of each expert in groups of up to 16
+//      tokens of each expert in groups of up to 8 or 16
 //   2  items (group, 32 gate columns and their 32 up columns): products, SwiGLU,
 //      h as fp16 with one power of two per 32 columns
-//      -- grid barrier (the first weights of phase 3 are already on their way) --
+//      -- grid barrier (weights of phase 3 are already on their way) --
 //   3  items (group, 64 columns of y): products; the last of a token's k experts
 //      to finish a column block adds the k parts in order: deterministic
 //
-// A CTA is one producer warp and sixteen consumer warps around a ring of
-// stages. A stage is 256 rows of K by 64 columns of codes (two TMA boxes of 32
-// columns, 128-byte swizzle), their exponent bytes and the same 256 elements of
-// the group's activation rows. Two sets of eight warps, each with a ring of its
-// own, take alternate stages of an item (which set takes the first depends on
-// the column block alone, so a token's sums are formed in the same order
-// whatever else the call holds); a warp converts one 32-row block: a lane's 16-byte load holds eight consecutive
-// codes of each of four columns, which become fp16 pairs by the hardware's
-// exact conversion and serve as the A operand of warp-level MMAs (columns of W
-// as MMA rows, tokens as MMA columns), x as B; K is permuted alike on both
-// sides, so neither needs a shuffle. The block's FP32 products are scaled by
-// the columns' 2^(e - 127) as they are added up. The sixteen warps' sums meet
-// in shared memory once per item.
+// A CTA is two producer warps, sixteen consumer warps and two epilogue warps.
+// Weights pass through a ring of stages: 512 rows of K by 64 columns of codes
+// (two TMA boxes of 32 columns, 128-byte swizzle) and their exponent bytes; the
+// producers fill it without regard to phases or barriers. Two sets of eight
+// consumer warps, each with a producer and half of the ring, take alternate
+// stages of an item (which set takes the first depends on the column block
+// alone, so a token's sums are formed in the same order whatever else the call
+// holds). A warp converts four 32-row blocks of one box: a lane's 16-byte load
+// holds eight consecutive codes of each of four columns, which become fp16
+// pairs by the hardware's exact conversion and serve as the A operand of
+// warp-level MMAs (columns of W as MMA rows, tokens as MMA columns), x as B; K
+// is permuted alike on both sides, so neither needs a shuffle. The activations
+// come straight from global memory (L2) into B fragments, loaded before the wait
+// for the stage's weights. A block's FP32 products are scaled by the columns'
+// 2^(e - 127) as they are added up. At the end of an item the warps leave their
+// sums in one of two buffers and go on; the buffer's epilogue warp adds the
+// eight parts in order and finishes the item beside the next ones.
 //
 // Activations in fp16: a token's x is multiplied by the power of two that
 // brings its largest magnitude just below 2^15, a run of 32 h values likewise
@@ -50,6 +54,7 @@
 #include "tmap.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace w4a16 {
 
@@ -57,83 +62,93 @@ __device__ unsigned int g_mx_moe_error = 0;
 
 namespace {
 
-constexpr int kConsumerWarps = 16;
+constexpr int kConsumerWarps = 16, kEpilogues = 2, kProducers = 2;
 constexpr int kConsumers = kConsumerWarps * 32;
-constexpr int kThreads = kConsumers + 32;
-constexpr int kSetStages = 3;            // ring of each set of warps
-constexpr int kStages = 2 * kSetStages;
-constexpr int kStepK = 256;              // rows of K per stage: one 32-row block per warp of a set
+constexpr int kThreads = kConsumers + (kEpilogues + kProducers) * 32;
+constexpr int kStepK = 512;              // rows of K per stage
 constexpr int kBlocks = kStepK / 32;
-constexpr int kGroup = 16;               // tokens of an expert taken together
+constexpr int kWarpBlocks = 4;           // consecutive 32-row blocks of a box that a warp converts
+constexpr int kSlices = kBlocks / kWarpBlocks;
 constexpr int kMaxExperts = kMoeMaxExperts;
 constexpr int kMaxSlots = kMoeMaxTokens * kMoeMaxTopK;
-constexpr uint32_t kBoxBytes = 32 * 128;             // 32 word rows x 32 columns
+constexpr uint32_t kBoxBytes = kStepK / 8 * 128;     // 64 word rows x 32 columns
 constexpr uint32_t kScaleBoxBytes = kBlocks * 32;
-constexpr uint32_t kXStride = 704;       // 8 records of 80 bytes, padded so that two rows' 64 bytes hit different banks
-constexpr uint32_t kStageBytes = 2 * kBoxBytes + 2 * kScaleBoxBytes + kGroup * kXStride;
-static_assert(kStageBytes % 128 == 0, "stages stay 128-byte aligned");
-constexpr uint32_t kStagePitch = (kStageBytes + 1023) & ~1023u;   // swizzled boxes start 1024-byte aligned
+constexpr uint32_t kStageBytes = 2 * kBoxBytes + 2 * kScaleBoxBytes;
+static_assert(kStageBytes % 1024 == 0, "swizzled boxes start 1024-byte aligned");
+constexpr int kSetStages = 4;            // half of the ring
+constexpr int kStages = 2 * kSetStages;
 constexpr int kRedPitch = 33;            // floats per slot of a warp's partial sums
-constexpr int kRedSlots = 32;            // [token parity of an 8-token tile, tile][box][column % 4]
 constexpr uint32_t kSuspendNs = 20000;
 constexpr unsigned long long kWaitLimitCycles = 4000000000ull;   // ~2 s at 2 GHz
 constexpr unsigned int kErrTimeout = 9u;
-constexpr int kHRecord = 80;             // 32 fp16 values, the run's shift, padding to 16 bytes
 
+// kGroup: tokens of an expert taken together, 8 or 16.
+template <int kGroup>
 struct __align__(16) Shared {
-    float red[kConsumerWarps][kRedSlots][kRedPitch];
+    static constexpr int kTiles = kGroup / 8;            // 8-token MMA tiles
+    static constexpr int kRedSlots = kTiles * 8;         // [tile][token parity][column % 4]
+    float red[kEpilogues][kConsumerWarps][kRedSlots][kRedPitch];
     uint64_t full[kStages];
     uint64_t empty[kStages];
+    uint64_t sums[kEpilogues];           // a buffer of partial sums is complete
+    uint64_t taken[kEpilogues];          // ... and has been read
     uint64_t phase3;                     // h of every CTA is visible
-    unsigned long long mask[kMaxExperts];
+    uint32_t mask[kMaxExperts][2];       // tokens of each expert
     float weight[kMaxSlots];             // of slot t * k + j
     uint32_t group[kMaxSlots];           // expert | count << 16
     uint16_t first[kMaxSlots];           // the group's first entry in `list`
     uint16_t list[kMaxSlots];            // slots, ordered by expert, then token
     uint16_t ids[kMaxSlots];             // expert of slot t * k + j
-    uint16_t offset[kMaxExperts], goffset[kMaxExperts];
+    uint16_t offset[kMaxExperts];
+    uint32_t scan[kMaxExperts / 32];
     int groups;
-    uint32_t generation;
+    uint32_t epoch;
     int abort;
 };
-constexpr size_t kSmemBytes = 1024 + kStages * kStagePitch + sizeof(Shared);
-static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+template <int kGroup>
+constexpr size_t smem_bytes() {
+    return 1024 + kStages * kStageBytes + sizeof(Shared<kGroup>);
+}
+static_assert(smem_bytes<16>() <= 227 * 1024, "shared memory budget");
 
 struct Params {
     const uint16_t* x;
     const uint16_t* router;
     uint16_t* y;
-    uint32_t* control;     // barrier count, barrier generation, then tickets
+    uint32_t* control;     // epoch, two pairs of barrier counts; from kTickets on, tickets
     float* logits;         // [T, E]
     uint16_t* x16;         // [T, H]
     float* xfactor;        // [T]
     int* hshift;           // [T k], smallest shift of the slot's runs
-    uint8_t* h;            // [T k, I / 32] records
+    uint16_t* h;           // [T k, I], runs of 32 values scaled by 2^shift
+    int* shift;            // [T k, pitch], the runs' shifts
     float* part;           // [T k, H]
     int T, E, k, H, I;
+    int pitch;             // I / 32, rounded up to whole stages
     int renormalize;
 };
+constexpr int kTickets = 8;   // word of `control`
 
-__device__ __forceinline__ void fail(Shared* sm) {
-    *reinterpret_cast<volatile int*>(&sm->abort) = 1;
+__device__ __forceinline__ void fail(volatile int* abort) {
+    *abort = 1;
     atomicOr(&g_mx_moe_error, 1u << kErrTimeout);
 }
 
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Shared* sm) {
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
     const uint32_t b = smem_u32(bar);
     const unsigned long long t0 = clock64();
     for (;;) {
         if (mbar_try_wait_suspend(b, parity, kSuspendNs)) return true;
-        if (*reinterpret_cast<volatile int*>(&sm->abort)) return false;
+        if (*abort) return false;
         if (clock64() - t0 > kWaitLimitCycles) {
-            fail(sm);
+            fail(abort);
             return false;
         }
     }
 }
-__device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, Shared* sm, int lane) {
+__device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, int lane) {
     int ok = 1;
-    if (lane == 0) ok = wait_bar(bar, parity, sm) ? 1 : 0;
+    if (lane == 0) ok = wait_bar(bar, parity, abort) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
     __syncwarp();
     return ok != 0;
@@ -144,24 +159,19 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
-// Grid barrier in two halves. control[0] counts arrivals, control[1] is the
-// generation; the last CTA to arrive resets the count and then advances it.
-__device__ __forceinline__ void grid_arrive(uint32_t* control) {
-    __threadfence();
-    if (atomicAdd(control, 1u) == gridDim.x - 1) {
-        control[0] = 0u;
-        __threadfence();
-        atomicAdd(control + 1, 1u);
-    }
+// Grid barriers. A call uses one of two pairs of counts, by the parity of the
+// call's epoch, and zeroes the other pair (the previous call's); the epoch
+// advances once every CTA has passed the first barrier, so all have read it.
+__device__ __forceinline__ void grid_arrive(uint32_t* count) {
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
 }
-__device__ __forceinline__ bool grid_wait(const uint32_t* control, uint32_t generation, Shared* sm) {
+__device__ __forceinline__ bool grid_wait(const uint32_t* count, volatile int* abort) {
     const unsigned long long t0 = clock64();
-    while (ld_acquire(control + 1) != generation) {
-        if (*reinterpret_cast<volatile int*>(&sm->abort)) return false;
+    while (ld_acquire(count) != gridDim.x) {
+        if (*abort) return false;
         if (clock64() - t0 > kWaitLimitCycles) {
-            fail(sm);
+            fail(abort);
             return false;
         }
     }
@@ -169,13 +179,6 @@ __device__ __forceinline__ bool grid_wait(const uint32_t* control, uint32_t gene
 }
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
-
-// Untiled copy of `bytes` (a multiple of 16), global to shared.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-                 : "memory");
-}
 
 // D = A * B on fp16 (FP32 result), accumulators starting at zero or at D.
 __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -216,7 +219,7 @@ __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 // ---------------------------------------------------------------------------
 // Logits of 16 experts x 8 tokens: the consumer warps take 32-element blocks of
 // H in turn and their sums meet in shared memory.
-__device__ void router_tile(const Params& p, Shared* sm, int e0, int t0, int warp, int lane) {
+__device__ void router_tile(const Params& p, float (*scratch)[4][32], int e0, int t0, int warp, int lane) {
     const int g = lane >> 2, t = lane & 3;
     const int blocks = p.H >> 5;
     const bool ok0 = e0 + g < p.E, ok1 = e0 + g + 8 < p.E, okx = t0 + g < p.T;
@@ -243,13 +246,13 @@ __device__ void router_tile(const Params& p, Shared* sm, int e0, int t0, int war
         }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sm->red[warp][i][lane] = d[i];
+    for (int i = 0; i < 4; ++i) scratch[warp][i][lane] = d[i];
     consumer_sync();
     const int i = warp;   // 4 warps finish one register of the fragment each
     if (i < 4) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kConsumerWarps; ++w) s += sm->red[w][i][lane];
+        for (int w = 0; w < kConsumerWarps; ++w) s += scratch[w][i][lane];
         const int e = e0 + g + (i >> 1) * 8, tok = t0 + 2 * t + (i & 1);
         if (e < p.E && tok < p.T) __stcg(p.logits + static_cast<size_t>(tok) * p.E + e, s);
     }
@@ -257,7 +260,7 @@ __device__ void router_tile(const Params& p, Shared* sm, int e0, int t0, int war
 }
 
 // One token's x as fp16, scaled by a power of two.
-__device__ void convert_token(const Params& p, Shared* sm, int tok, int warp, int lane) {
+__device__ void convert_token(const Params& p, float (*scratch)[4][32], int tok, int warp, int lane) {
     const uint4* src = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(tok) * p.H);
     const int n = p.H >> 3, tid = warp * 32 + lane;
     uint32_t m = 0;
@@ -268,9 +271,9 @@ __device__ void convert_token(const Params& p, Shared* sm, int tok, int warp, in
         for (int j = 0; j < 4; ++j) m = max(m, max((w[j] >> 7) & 0xFFu, (w[j] >> 23) & 0xFFu));
     }
     m = __reduce_max_sync(0xffffffffu, m);
-    if (lane == 0) sm->red[warp][0][0] = __uint_as_float(m);
+    if (lane == 0) scratch[warp][0][0] = __uint_as_float(m);
     consumer_sync();
-    for (int w = 0; w < kConsumerWarps; ++w) m = max(m, __float_as_uint(sm->red[w][0][0]));
+    for (int w = 0; w < kConsumerWarps; ++w) m = max(m, __float_as_uint(scratch[w][0][0]));
     const int c = mx::x_shift(m);
     uint4* dst = reinterpret_cast<uint4*>(p.x16 + static_cast<size_t>(tok) * p.H);
     for (int i = tid; i < n; i += kConsumers) {
@@ -291,178 +294,181 @@ __device__ void convert_token(const Params& p, Shared* sm, int tok, int warp, in
 // ---------------------------------------------------------------------------
 // phase 1
 // ---------------------------------------------------------------------------
-// One token's experts, by one warp: k rounds of a warp-wide maximum. Every
-// round takes an expert not taken before whatever the logits hold (NaN too).
-__device__ void pick_experts(const Params& p, Shared* sm, int tok, int lane) {
-    constexpr int kPer = kMaxExperts / 32;
+// FP32 to unsigned keys of the same order, never 0, and back. (-0 counts as 0;
+// a NaN sorts above every number or below, by its sign.)
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __float_as_uint(v == 0.f ? 0.f : v);
+    return max((b >> 31) ? ~b : (b | 0x80000000u), 1u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float((k >> 31) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+// One token's experts, by one warp. Each lane sorts the logits it holds (experts
+// lane, lane + 32, ...), then k rounds take the largest head of the 32 lists,
+// the lower expert where heads are equal. Every round takes an expert that was
+// not taken before, whatever the logits hold.
+template <int kPer, int kGroup>
+__device__ __forceinline__ void pick_experts(const Params& p, Shared<kGroup>* sm, int tok, int lane) {
     const float* row = p.logits + static_cast<size_t>(tok) * p.E;
-    float v[kPer];
-    uint32_t key[kPer];   // ordered as the logits are; 0: absent or taken
+    uint32_t key[kPer], id[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int e = lane + 32 * i;
-        v[i] = e < p.E ? __ldcg(row + e) : 0.f;
-        const uint32_t b = __float_as_uint(v[i] == 0.f ? 0.f : v[i]);   // -0 equals 0
-        key[i] = e < p.E ? max((b >> 31) ? ~b : (b | 0x80000000u), 1u) : 0u;
+        id[i] = lane + 32 * i;
+        key[i] = id[i] < static_cast<uint32_t>(p.E) ? order_key(__ldcg(row + id[i])) : 0u;   // 0: absent
     }
-    float top = 0.f, sum = 0.f, mine = 0.f;
-    for (int j = 0; j < p.k; ++j) {
-        uint32_t best = 0;
-        int at = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (key[i] > best) best = key[i], at = i;
-        const uint32_t high = __reduce_max_sync(0xffffffffu, best);
-        const uint32_t e = __reduce_min_sync(0xffffffffu, best == high ? static_cast<uint32_t>(lane + 32 * at) : ~0u);
-        float l = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (e == static_cast<uint32_t>(lane + 32 * i)) {
-                l = v[i];
-                key[i] = 0;
-            }
-        l = __shfl_sync(0xffffffffu, l, e & 31);
-        if (j == 0) top = l;
-        const float ex = expf(l - top);
-        sum += ex;
-        if (lane == j) mine = ex;
-        if (lane == 0) {
-            sm->ids[tok * p.k + j] = static_cast<uint16_t>(e);
-            atomicOr(&sm->mask[e], 1ull << tok);
-        }
-    }
+    float total = 0.f;
     if (!p.renormalize) {
-        sum = 0.f;
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) m = max(m, key[i]);
+        const float top = key_value(__reduce_max_sync(0xffffffffu, m));
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-            if (lane + 32 * i < p.E) sum += expf(v[i] - top);
+            if (key[i]) total += expf(key_value(key[i]) - top);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     }
-    if (lane < p.k) sm->weight[tok * p.k + lane] = mine / sum;
-}
-
-// Prefix sums over the experts of their tokens and groups (one warp).
-__device__ void number_groups(const Params& p, Shared* sm, int lane) {
-    constexpr int kPer = kMaxExperts / 32;
-    int n[kPer], tokens = 0, groups = 0;
+    // neighbours exchange only where the later one is larger: equal keys keep their order
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = lane * kPer + i;
-        n[i] = e < p.E ? __popcll(sm->mask[e]) : 0;
-        tokens += n[i];
-        groups += (n[i] + kGroup - 1) / kGroup;
-    }
-    int at = tokens, ga = groups;
+    for (int r = 0; r < kPer; ++r)
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, at, o), b = __shfl_up_sync(0xffffffffu, ga, o);
-        if (lane >= o) at += a, ga += b;
-    }
-    if (lane == 31) sm->groups = ga;
-    at -= tokens;
-    ga -= groups;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = lane * kPer + i;
-        if (e < p.E) {
-            sm->offset[e] = static_cast<uint16_t>(at);
-            for (int q = 0; q < n[i]; q += kGroup, ++ga) {
-                sm->group[ga] = static_cast<uint32_t>(e) | static_cast<uint32_t>(min(kGroup, n[i] - q)) << 16;
-                sm->first[ga] = static_cast<uint16_t>(at + q);
-            }
+        for (int i = r & 1; i + 1 < kPer; i += 2) {
+            const bool swap = key[i + 1] > key[i];
+            const uint32_t k0 = key[i], i0 = id[i];
+            key[i] = swap ? key[i + 1] : k0;
+            id[i] = swap ? id[i + 1] : i0;
+            key[i + 1] = swap ? k0 : key[i + 1];
+            id[i + 1] = swap ? i0 : id[i + 1];
         }
-        at += n[i];
+    uint32_t won = 0, expert = 0;
+    for (int j = 0; j < p.k; ++j) {
+        const uint32_t high = __reduce_max_sync(0xffffffffu, key[0]);
+        const bool tied = key[0] == high;
+        const uint32_t who = __ballot_sync(0xffffffffu, tied);
+        uint32_t e = __shfl_sync(0xffffffffu, id[0], __ffs(who) - 1);
+        if (who & (who - 1)) e = __reduce_min_sync(0xffffffffu, tied ? id[0] : ~0u);
+        if (tied && id[0] == e) {
+#pragma unroll
+            for (int i = 0; i + 1 < kPer; ++i) key[i] = key[i + 1], id[i] = id[i + 1];
+            key[kPer - 1] = 0;
+        }
+        if (lane == j) won = high, expert = e;
+    }
+    // lane j holds the token's j-th choice
+    const float top = __shfl_sync(0xffffffffu, key_value(won), 0);
+    const float ex = lane < p.k ? expf(key_value(won) - top) : 0.f;
+    float sum = ex;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane < p.k) {
+        sm->weight[tok * p.k + lane] = ex / (p.renormalize ? sum : total);
+        sm->ids[tok * p.k + lane] = static_cast<uint16_t>(expert);
+        atomicOr(&sm->mask[expert][tok >> 5], 1u << (tok & 31));
     }
 }
 
+// Tokens and groups of every expert, numbered in the experts' order: one thread
+// per expert, prefix sums over packed counts (tokens | groups << 16). All
+// threads of the CTA.
+template <int kGroup>
+__device__ __forceinline__ void number_groups(const Params& p, Shared<kGroup>* sm) {
+    const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
+    int n = 0;
+    uint32_t own = 0, at = 0;
+    if (e < kMaxExperts) {
+        n = e < p.E ? __popc(sm->mask[e][0]) + __popc(sm->mask[e][1]) : 0;
+        own = at = static_cast<uint32_t>(n) | static_cast<uint32_t>((n + kGroup - 1) / kGroup) << 16;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at += v;
+        }
+        if (lane == 31) sm->scan[warp] = at;
+    }
+    __syncthreads();
+    if (e < kMaxExperts) {
+#pragma unroll
+        for (int w = 0; w < kMaxExperts / 32; ++w)
+            if (w < warp) at += sm->scan[w];
+        if (e == kMaxExperts - 1) sm->groups = static_cast<int>(at >> 16);
+        at -= own;
+        sm->offset[e] = static_cast<uint16_t>(at & 0xFFFFu);
+        int gi = static_cast<int>(at >> 16);
+        for (int q = 0; q < n; q += kGroup, ++gi) {
+            sm->group[gi] = static_cast<uint32_t>(e) | static_cast<uint32_t>(min(kGroup, n - q)) << 16;
+            sm->first[gi] = static_cast<uint16_t>((at & 0xFFFFu) + q);
+        }
+    }
+    __syncthreads();
+    // a slot's place among its expert's: the tokens before it
+    for (int s = threadIdx.x; s < p.T * p.k; s += kThreads) {
+        const int ex = sm->ids[s], tok = s / p.k;
+        const unsigned long long m = sm->mask[ex][0] | static_cast<unsigned long long>(sm->mask[ex][1]) << 32;
+        sm->list[sm->offset[ex] + __popcll(m & ((1ull << tok) - 1))] = static_cast<uint16_t>(s);
+    }
+    __syncthreads();
+}
+
 // ---------------------------------------------------------------------------
-// phases 2 and 3: the stream of stages
+// phases 2 and 3
 // ---------------------------------------------------------------------------
-// A 32-row block of 64 columns against the group's rows, added to acc
-// [8-token tile][16-column tile][fragment]. kH: the rows are runs of h with
-// shifts of their own, `align` holds the rows' common shift.
-template <bool kH>
-__device__ __forceinline__ void block_products(float (&acc)[2][4][4], uint32_t stage, int c, bool two, int g, int t,
-                                               const int (&align)[2]) {
+// Whether one of four bytes is 0 or 255.
+__device__ __forceinline__ bool has_edge_byte(uint32_t v) {
+    return (__vcmpeq4(v, 0u) | __vcmpeq4(v, 0xFFFFFFFFu)) != 0u;
+}
+
+// Block c (32 rows) of one box of a stage against the group's rows in b, added
+// to acc [8-token tile][16-column tile][fragment].
+template <int kTiles>
+__device__ __forceinline__ void block_products(float (&acc)[kTiles][2][4], uint32_t box, uint32_t scales, int c,
+                                               int tiles, int g, int t, const uint4 (&b)[kTiles]) {
     const int row = 4 * c + t;
-    const uint32_t chunk = static_cast<uint32_t>((g >> 1) | ((g & 1) << 2));
-    const uint32_t waddr = stage + row * 128 + ((chunk ^ (row & 7)) << 4);
-    const uint32_t saddr = stage + 2 * kBoxBytes + c * 32 + chunk * 4;
-    const uint32_t xaddr = stage + 2 * kBoxBytes + 2 * kScaleBoxBytes + g * kXStride + c * (kH ? kHRecord : 64) + t * 16;
-    uint32_t b[2][4];
+    const uint32_t chunk = static_cast<uint32_t>((g >> 1) | ((g & 1) << 2));   // quarter-warps hit every bank once
+    const uint4 w = ld_shared_v4(box + row * 128 + ((chunk ^ (row & 7)) << 4));
+    const uint32_t e4 = ld_shared_u32(scales + c * 32 + chunk * 4);
+    // 2^(e - 127): the byte as an FP32 exponent field, right for 1..254
+    float scale[4];
+    scale[0] = __uint_as_float((e4 & 0xFFu) << 23);
+    scale[1] = __uint_as_float((e4 & 0xFF00u) << 15);
+    scale[2] = __uint_as_float((e4 & 0xFF0000u) << 7);
+    scale[3] = __uint_as_float((e4 >> 24) << 23);
+    // 0 is the subnormal 2^-127, 255 NaN: rare
+    if (has_edge_byte(e4)) {
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        if (n == 1 && !two) break;
-        const uint4 v = ld_shared_v4(xaddr + n * 8 * kXStride);
-        b[n][0] = v.x, b[n][1] = v.y, b[n][2] = v.z, b[n][3] = v.w;
-        if constexpr (kH) {
-            const int shift = static_cast<int>(ld_shared_u32(xaddr + n * 8 * kXStride - t * 16 + 64));
-            const uint32_t f = pow2_f16x2(min(align[n] - shift, 0));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[n][i] = hmul2(b[n][i], f);
-        }
+        for (int i = 0; i < 4; ++i) scale[i] = mx::scale_f32((e4 >> (8 * i)) & 0xFFu);
     }
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int box = 0; box < 2; ++box) {
-        const uint4 w = ld_shared_v4(waddr + box * kBoxBytes);
-        const uint32_t e4 = ld_shared_u32(saddr + box * kScaleBoxBytes);
-        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    for (int m = 0; m < 2; ++m) {
+        uint32_t lo[4], hi[4];
+        mx::e2m1x8_to_f16x2(words[2 * m], lo);
+        mx::e2m1x8_to_f16x2(words[2 * m + 1], hi);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            uint32_t lo[4], hi[4];
-            mx::e2m1x8_to_f16x2(words[2 * m], lo);
-            mx::e2m1x8_to_f16x2(words[2 * m + 1], hi);
-            const float s0 = mx::scale_f32((e4 >> (16 * m)) & 0xFFu), s1 = mx::scale_f32((e4 >> (16 * m + 8)) & 0xFFu);
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                if (n == 1 && !two) break;
-                float d[4];
-                mma_f16_zero(d, lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
-                mma_m16n8k16<false>(d, lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
-                float(&a)[4] = acc[n][2 * box + m];
-                a[0] = fmaf(d[0], s0, a[0]);
-                a[1] = fmaf(d[1], s0, a[1]);
-                a[2] = fmaf(d[2], s1, a[2]);
-                a[3] = fmaf(d[3], s1, a[3]);
-            }
+        for (int n = 0; n < kTiles; ++n) {
+            if (n > 0 && n >= tiles) break;
+            float d[4];
+            mma_f16_zero(d, lo[0], hi[0], lo[1], hi[1], b[n].x, b[n].y);
+            mma_m16n8k16<false>(d, lo[2], hi[2], lo[3], hi[3], b[n].z, b[n].w);
+            float(&a)[4] = acc[n][m];
+            a[0] = fmaf(d[0], scale[2 * m], a[0]);
+            a[1] = fmaf(d[1], scale[2 * m], a[1]);
+            a[2] = fmaf(d[2], scale[2 * m + 1], a[2]);
+            a[3] = fmaf(d[3], scale[2 * m + 1], a[3]);
         }
     }
 }
 
-// A warp's sums to shared memory: slot [tile][token parity][box][column % 4],
-// at the lane that holds them.
-__device__ __forceinline__ void store_sums(Shared* sm, const float (&acc)[2][4][4], bool two, int warp, int lane) {
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        if (n == 1 && !two) break;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)       // 16-column tile: box q >> 1, columns 2 (q & 1) and + 1 of every four
-#pragma unroll
-            for (int i = 0; i < 4; ++i)   // fragment: column i >> 1, token parity i & 1
-                sm->red[warp][n * 16 + (i & 1) * 8 + (q >> 1) * 4 + (q & 1) * 2 + (i >> 1)][lane] = acc[n][q][i];
-    }
-}
-
-// The sum over the warps of token n, column `col` (0..31) of box `box`.
-__device__ __forceinline__ float load_sum(const Shared* sm, int n, int box, int col) {
-    const int chunk = col >> 2;
-    const int g = ((chunk & 3) << 1) | (chunk >> 2);
-    const int slot = (n >> 3) * 16 + (n & 1) * 8 + box * 4 + (col & 3);
-    const int at = g * 4 + ((n & 7) >> 1);
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < kConsumerWarps; ++w) s += sm->red[w][slot][at];
-    return s;
-}
-
+template <int kGroup>
 __global__ void __launch_bounds__(kThreads, 1)
 moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUtensorMap te13,
            const __grid_constant__ CUtensorMap tw2, const __grid_constant__ CUtensorMap te2, const Params p) {
+    constexpr int kTiles = Shared<kGroup>::kTiles;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Shared* sm = reinterpret_cast<Shared*>(ring + kStages * kStagePitch);
+    Shared<kGroup>* sm = reinterpret_cast<Shared<kGroup>*>(ring + kStages * kStageBytes);
     const uint32_t ring_base = smem_u32(ring);
+    volatile int* abort = &sm->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int grid = gridDim.x, cta = blockIdx.x;
 
@@ -471,262 +477,320 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
             mbar_init(smem_u32(&sm->full[s]), 1);
             mbar_init(smem_u32(&sm->empty[s]), kConsumerWarps / 2);
         }
+        for (int b = 0; b < kEpilogues; ++b) {
+            mbar_init(smem_u32(&sm->sums[b]), kConsumerWarps);
+            mbar_init(smem_u32(&sm->taken[b]), 1);
+        }
         mbar_init(smem_u32(&sm->phase3), 1);
-        sm->abort = 0;
-        sm->generation = ld_acquire(p.control + 1);
+        *abort = 0;
+        sm->epoch = ld_acquire(p.control);
         fence_mbar_init();
         tma_prefetch_desc(&tw13);
         tma_prefetch_desc(&te13);
         tma_prefetch_desc(&tw2);
         tma_prefetch_desc(&te2);
     }
-    for (int e = threadIdx.x; e < kMaxExperts; e += kThreads) sm->mask[e] = 0ull;
+    if (threadIdx.x < kMaxExperts) sm->mask[threadIdx.x][0] = sm->mask[threadIdx.x][1] = 0u;
     __syncthreads();
+    uint32_t* counts = p.control + 1 + 2 * (sm->epoch & 1u);
 
     // ---------------------------------------------------------------- phase 0
     if (warp < kConsumerWarps) {
+        float(*scratch)[4][32] = reinterpret_cast<float(*)[4][32]>(&sm->red[0][0][0][0]);
         const int etiles = (p.E + 15) >> 4, tiles = etiles * ((p.T + 7) >> 3);
         for (int u = cta; u < tiles + p.T; u += grid) {
             if (u < tiles)
-                router_tile(p, sm, (u % etiles) * 16, (u / etiles) * 8, warp, lane);
+                router_tile(p, scratch, (u % etiles) * 16, (u / etiles) * 8, warp, lane);
             else
-                convert_token(p, sm, u - tiles, warp, lane);
+                convert_token(p, scratch, u - tiles, warp, lane);
         }
-        fence_proxy_async_global();   // x16 is read by bulk copies
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        grid_arrive(p.control);
-        grid_wait(p.control, sm->generation + 1, sm);
+        grid_arrive(counts);
+        grid_wait(counts, abort);
+        if (cta == 0) {
+            uint32_t* other = p.control + 1 + 2 * ((sm->epoch & 1u) ^ 1u);
+            other[0] = other[1] = 0u;
+            p.control[0] = sm->epoch + 1u;
+        }
     }
     __syncthreads();
 
     // ---------------------------------------------------------------- phase 1
-    const bool alive = *reinterpret_cast<volatile int*>(&sm->abort) == 0;
+    const bool alive = *abort == 0;
     if (alive) {
-        for (int tok = warp; tok < p.T; tok += kThreads / 32) pick_experts(p, sm, tok, lane);
-        __syncthreads();
-        if (warp == 0) number_groups(p, sm, lane);
-        __syncthreads();
-        for (int s = threadIdx.x; s < p.T * p.k; s += kThreads) {
-            const int e = sm->ids[s];
-            sm->list[sm->offset[e] + __popcll(sm->mask[e] & ((1ull << (s / p.k)) - 1))] = static_cast<uint16_t>(s);
+        for (int tok = warp; tok < p.T; tok += kThreads / 32) {
+            if (p.E <= 64)
+                pick_experts<2>(p, sm, tok, lane);
+            else if (p.E <= 128)
+                pick_experts<4>(p, sm, tok, lane);
+            else
+                pick_experts<kMaxExperts / 32>(p, sm, tok, lane);
         }
         __syncthreads();
+        number_groups(p, sm);
     }
+    // Items, column blocks fastest: CTAs next to one another read neighbouring columns of an expert
     const int groups = alive ? sm->groups : 0;
-    const int items2 = groups * (p.I >> 5), items3 = groups * ((p.H + 63) >> 6);
+    const int cols2 = p.I >> 5, cols3 = (p.H + 63) >> 6;                 // column blocks
+    const int items2 = groups * cols2, items3 = groups * cols3;
     const int blocks2 = p.H >> 5, blocks3 = p.I >> 5;                    // 32-row blocks of K
     const int steps2 = (blocks2 + kBlocks - 1) / kBlocks, steps3 = (blocks3 + kBlocks - 1) / kBlocks;
 
-    if (warp == kConsumerWarps) {
-        // ------------------------------------------------------------ producer
-        fence_proxy_async_global();
-        bool ok = true;
-        // the CTA's stages of a phase in order, and how many each set's ring has seen
-        struct Cursor {
-            int item, ks;
-            uint32_t used[2];
-        };
-        auto set_of = [&](const Cursor& u) { return (u.ks + u.item / groups) & 1; };
-        auto slot_of = [&](const Cursor& u) {
-            const int q = set_of(u);
-            return q * kSetStages + static_cast<int>(u.used[q] % kSetStages);
-        };
-        auto advance = [&](Cursor& u, int steps) {
-            ++u.used[set_of(u)];
-            if (++u.ks == steps) u.ks = 0, u.item += grid;
-        };
-        // weights of one stage (lane 0; waits for the stage to be free and announces all its bytes)
-        auto weights = [&](bool second, const Cursor& u) {
-            const int s = slot_of(u);
-            if (!warp_wait_bar(&sm->empty[s], (u.used[set_of(u)] / kSetStages & 1u) ^ 1u, sm, lane)) return false;
-            if (lane == 0) {
-                const uint32_t gr = sm->group[u.item % groups];
-                const int e = gr & 0xFFFFu, n = gr >> 16, cb = u.item / groups;
-                const int nb = min(kBlocks, (second ? blocks3 : blocks2) - u.ks * kBlocks);
-                const uint32_t bar = smem_u32(&sm->full[s]), dst = ring_base + s * kStagePitch;
-                mbar_arrive_expect_tx(bar, 2 * kBoxBytes + 2 * kScaleBoxBytes + n * nb * (second ? kHRecord : 64));
-                const int c0 = second ? cb * 64 : cb * 32, c1 = second ? cb * 64 + 32 : p.I + cb * 32;
-                const int kb = e * (second ? blocks3 : blocks2) + u.ks * kBlocks;   // 32-row block of the stack
+    if (warp >= kConsumerWarps + kEpilogues) {
+        // ------------------------------------------------------------ producers: the weights of one set's stages
+        if (lane == 0) {
+            const int set = warp - kConsumerWarps - kEpilogues;
+            int slot = 0, seen = 0;
+            uint32_t parity = 1u;
+            bool ok = true;
+            for (int second = 0; second < 2 && ok; ++second) {
+                const int items = second ? items3 : items2, cols = second ? cols3 : cols2;
+                const int blocks = second ? blocks3 : blocks2, steps = second ? steps3 : steps2;
                 const CUtensorMap* tw = second ? &tw2 : &tw13;
                 const CUtensorMap* te = second ? &te2 : &te13;
-                tma_load_2d(dst, tw, c0, kb * 4, bar);
-                tma_load_2d(dst + kBoxBytes, tw, c1, kb * 4, bar);
-                tma_load_2d(dst + 2 * kBoxBytes, te, c0, kb, bar);
-                tma_load_2d(dst + 2 * kBoxBytes + kScaleBoxBytes, te, c1, kb, bar);
-            }
-            return true;
-        };
-        // activation rows of the stage, one copy per lane
-        auto rows = [&](bool second, const Cursor& u) {
-            const int s = slot_of(u), gi = u.item % groups;
-            if (lane < static_cast<int>(sm->group[gi] >> 16)) {
-                const int slot = sm->list[sm->first[gi] + lane];
-                const int nb = min(kBlocks, (second ? blocks3 : blocks2) - u.ks * kBlocks);
-                const uint32_t dst =
-                    ring_base + s * kStagePitch + 2 * kBoxBytes + 2 * kScaleBoxBytes + lane * kXStride;
-                if (second)
-                    bulk_load(dst, p.h + (static_cast<size_t>(slot) * blocks3 + u.ks * kBlocks) * kHRecord,
-                              nb * kHRecord, smem_u32(&sm->full[s]));
-                else
-                    bulk_load(dst, p.x16 + static_cast<size_t>(slot / p.k) * p.H + u.ks * kStepK, nb * 64,
-                              smem_u32(&sm->full[s]));
-            }
-        };
-        Cursor u{cta, 0, {0u, 0u}};
-        while (u.item < items2 && ok) {
-            ok = weights(false, u);
-            if (!ok) break;
-            rows(false, u);
-            advance(u, steps2);
-        }
-        // the rings' worth of phase 3 weights before the barrier, their rows after it
-        u.item = cta;
-        u.ks = 0;
-        const Cursor start = u;
-        while (u.item < items3 && ok) {
-            const int q = set_of(u);
-            if (u.used[q] - start.used[q] == kSetStages) break;
-            ok = weights(true, u);
-            if (ok) advance(u, steps3);
-        }
-        if (ok && alive) {
-            int go = 1;
-            if (lane == 0) go = grid_wait(p.control, sm->generation + 2, sm) ? 1 : 0;
-            go = __shfl_sync(0xffffffffu, go, 0);
-            __syncwarp();
-            ok = go != 0;
-            fence_proxy_async_global();
-            if (lane == 0 && ok) mbar_arrive(smem_u32(&sm->phase3));
-        }
-        if (ok)
-            for (Cursor v = start; v.item != u.item || v.ks != u.ks; advance(v, steps3)) rows(true, v);
-        while (u.item < items3 && ok) {
-            ok = weights(true, u);
-            if (!ok) break;
-            rows(true, u);
-            advance(u, steps3);
-        }
-        // copies in flight land before the CTA's shared memory is given back
-        if (lane == 0) {
-            const unsigned long long t0 = clock64();
-            for (int q = 0; q < 2; ++q)
-                for (uint32_t i = u.used[q] > kSetStages ? u.used[q] - kSetStages : 0; i < u.used[q]; ++i)
-                    while (!mbar_try_wait(smem_u32(&sm->full[q * kSetStages + i % kSetStages]), i / kSetStages & 1u) &&
-                           clock64() - t0 < kWaitLimitCycles) {
+                for (int item = cta; item < items && ok; item += grid) {
+                    const int gi = item / cols, cb = item - gi * cols;
+                    const int c0 = second ? cb * 64 : cb * 32, c1 = second ? c0 + 32 : p.I + c0;
+                    const int kb0 = static_cast<int>(sm->group[gi] & 0xFFFFu) * blocks;   // 32-row block of the stack
+                    for (int ks = (cb ^ set) & 1; ks < steps; ks += 2) {
+                        const int s = set * kSetStages + slot, kb = kb0 + ks * kBlocks;
+                        if (!wait_bar(&sm->empty[s], parity, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t bar = smem_u32(&sm->full[s]), dst = ring_base + s * kStageBytes;
+                        mbar_arrive_expect_tx(bar, kStageBytes);
+                        tma_load_2d(dst, tw, c0, kb * 4, bar);
+                        tma_load_2d(dst + kBoxBytes, tw, c1, kb * 4, bar);
+                        tma_load_2d(dst + 2 * kBoxBytes, te, c0, kb, bar);
+                        tma_load_2d(dst + 2 * kBoxBytes + kScaleBoxBytes, te, c1, kb, bar);
+                        ++seen;
+                        if (++slot == kSetStages) slot = 0, parity ^= 1u;
                     }
+                }
+            }
+            // copies in flight land before the CTA's shared memory is given back
+            const unsigned long long t0 = clock64();
+            for (int i = max(0, seen - kSetStages); i < seen; ++i)
+                while (!mbar_try_wait(smem_u32(&sm->full[set * kSetStages + i % kSetStages]), i / kSetStages & 1) &&
+                       clock64() - t0 < kWaitLimitCycles) {
+                }
         }
-    } else {
+    } else if (warp < kConsumerWarps) {
         // ------------------------------------------------------------ consumers
         const int g = lane >> 2, t = lane & 3;
-        const int set = warp >> 3, c = warp & 7;
-        uint32_t used = 0;   // stages of the set's ring so far
+        const int set = warp >> 3, box = (warp >> 2) & 1, c0 = (warp & 3) * kWarpBlocks;
+        uint32_t used = 0;    // stages of the set's half of the ring so far
+        uint32_t count = 0;   // items so far
         bool ok = alive;
-        const int no_align[2] = {0, 0};
-
-        // ---- phase 2
-        for (int item = cta; item < items2; item += grid) {
-            const int gi = item % groups, cb = item / groups;
-            const int n = sm->group[gi] >> 16;
-            float acc[2][4][4];
+        auto phase = [&](auto second) {
+            constexpr bool kH = decltype(second)::value;
+            const int items = kH ? items3 : items2, cols = kH ? cols3 : cols2;
+            const int blocks = kH ? blocks3 : blocks2, steps = kH ? steps3 : steps2;
+            for (int item = cta; item < items; item += grid, ++count) {
+                const int gi = item / cols, cb = item - gi * cols;
+                const int n = sm->group[gi] >> 16, tiles = (n + 7) >> 3;
+                // the rows of tokens g and g + 8, from element 8 t of every block
+                const uint16_t* row[kTiles];
+                const int* shift[kTiles];
+                int align[kTiles];
+                float acc[kTiles][2][4];
 #pragma unroll
-            for (int a = 0; a < 2; ++a)
+                for (int a = 0; a < kTiles; ++a) {
+                    row[a] = nullptr;
+                    shift[a] = nullptr;
+                    align[a] = 0;
+                    if (ok && g + 8 * a < n) {
+                        const int slot = sm->list[sm->first[gi] + g + 8 * a];
+                        row[a] = (kH ? p.h + static_cast<size_t>(slot) * p.I
+                                     : p.x16 + static_cast<size_t>(slot / p.k) * p.H) + c0 * 32 + 8 * t;
+                        if constexpr (kH) {
+                            shift[a] = p.shift + static_cast<size_t>(slot) * p.pitch + c0;
+                            align[a] = __ldcg(p.hshift + slot);
+                        }
+                    }
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[a][b][i] = 0.f;
-            for (int ks = (cb ^ set) & 1; ks < steps2; ks += 2, ++used) {
-                const int s = set * kSetStages + static_cast<int>(used % kSetStages);
-                if (!ok || !warp_wait_bar(&sm->full[s], used / kSetStages & 1u, sm, lane)) {
-                    ok = false;
-                    continue;
+                        for (int i = 0; i < 4; ++i) acc[a][m][i] = 0.f;
                 }
-                if (ks * kBlocks + c < blocks2)
-                    block_products<false>(acc, ring_base + s * kStagePitch, c, n > 8, g, t, no_align);
+                for (int ks = (cb ^ set) & 1; ks < steps; ks += 2, ++used) {
+                    const int here = blocks - ks * kBlocks - c0;   // of the warp's blocks, those that exist
+                    uint4 x[kWarpBlocks][kTiles];
+#pragma unroll
+                    for (int i = 0; i < kWarpBlocks; ++i)
+#pragma unroll
+                        for (int a = 0; a < kTiles; ++a) {
+                            x[i][a] = make_uint4(0, 0, 0, 0);
+                            if (i < here && row[a])
+                                x[i][a] = __ldcg(reinterpret_cast<const uint4*>(row[a] + ks * kStepK + i * 32));
+                        }
+                    int4 sh[kTiles];
+                    if constexpr (kH) {
+#pragma unroll
+                        for (int a = 0; a < kTiles; ++a) {
+                            sh[a] = make_int4(0, 0, 0, 0);
+                            if (here > 0 && row[a]) sh[a] = __ldcg(reinterpret_cast<const int4*>(shift[a] + ks * kBlocks));
+                        }
+                    }
+                    const int s = set * kSetStages + static_cast<int>(used % kSetStages);
+                    if (!ok || !warp_wait_bar(&sm->full[s], used / kSetStages & 1u, abort, lane)) {
+                        ok = false;
+                        continue;
+                    }
+                    const uint32_t stage = ring_base + s * kStageBytes;
+#pragma unroll
+                    for (int i = 0; i < kWarpBlocks; ++i) {
+                        if (i >= here) break;
+                        if constexpr (kH) {
+                            // every run of h to its row's common shift
+#pragma unroll
+                            for (int a = 0; a < kTiles; ++a) {
+                                const int si = i == 0 ? sh[a].x : i == 1 ? sh[a].y : i == 2 ? sh[a].z : sh[a].w;
+                                const uint32_t f = pow2_f16x2(min(align[a] - si, 0));
+                                x[i][a] = make_uint4(hmul2(x[i][a].x, f), hmul2(x[i][a].y, f), hmul2(x[i][a].z, f),
+                                                     hmul2(x[i][a].w, f));
+                            }
+                        }
+                        block_products<kTiles>(acc, stage + box * kBoxBytes,
+                                               stage + 2 * kBoxBytes + box * kScaleBoxBytes, c0 + i, tiles, g, t, x[i]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm->empty[s]));
+                }
+                // sums to the item's buffer: slot [tile][token parity][column % 4], at the lane that holds them
+                const int b = static_cast<int>(count % kEpilogues);
+                if (ok) ok = warp_wait_bar(&sm->taken[b], (count / kEpilogues & 1u) ^ 1u, abort, lane);
+#pragma unroll
+                for (int a = 0; a < kTiles; ++a) {
+                    if (a > 0 && a >= tiles) break;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)       // columns 2 m and 2 m + 1 of every four
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)   // fragment: column i >> 1, token parity i & 1
+                            sm->red[b][warp][a * 8 + (i & 1) * 4 + m * 2 + (i >> 1)][lane] = acc[a][m][i];
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sm->empty[s]));
+                if (lane == 0) mbar_arrive(smem_u32(&sm->sums[b]));
             }
-            consumer_sync();   // the previous item's sums have been read
-            store_sums(sm, acc, n > 8, warp, lane);
-            consumer_sync();
-            if (warp < n && ok) {
-                const int slot = sm->list[sm->first[gi] + warp];
-                const float f = __ldcg(p.xfactor + slot / p.k);
-                const float gate = load_sum(sm, warp, 0, lane) * f, up = load_sum(sm, warp, 1, lane) * f;
+        };
+        phase(std::false_type{});
+        if (ok) ok = warp_wait_bar(&sm->phase3, 0, abort, lane);
+        phase(std::true_type{});
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int b = warp - kConsumerWarps;   // this warp's buffer: every other item
+        uint32_t count = 0;
+        bool ok = alive;
+        // token n of the group, column `lane` of box `box`: the warps' parts in order
+        auto total = [&](int n, int box) {
+            const int chunk = lane >> 2, slot = (n >> 3) * 8 + (n & 1) * 4 + (lane & 3);
+            const int from = (((chunk & 3) << 1) | (chunk >> 2)) * 4 + ((n & 7) >> 1);
+            float s = 0.f;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int w = 0; w < kSlices; ++w) s += sm->red[b][q * 8 + box * 4 + w][slot][from];
+            return s;
+        };
+        for (int item = cta; item < items2; item += grid, ++count) {
+            if (count % kEpilogues != static_cast<uint32_t>(b)) continue;
+            const int gi = item / cols2, cb = item - gi * cols2, n = sm->group[gi] >> 16;
+            int slot = 0;
+            float f = 0.f;
+            if (lane < n) {
+                slot = sm->list[sm->first[gi] + lane];
+                f = __ldcg(p.xfactor + slot / p.k);
+            }
+            if (!ok || !warp_wait_bar(&sm->sums[b], count / kEpilogues & 1u, abort, lane)) {
+                ok = false;
+                continue;
+            }
+            int low = 127;   // lane i: token i's shift
+            for (int i = 0; i < n; ++i) {
+                const int si = __shfl_sync(0xffffffffu, slot, i);
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+                const float gate = total(i, 0) * fi, up = total(i, 1) * fi;
                 const float h = silu(gate) * up;
-                const int shift = mx::x_shift(__reduce_max_sync(0xffffffffu, (__float_as_uint(h) >> 23) & 0xFFu));
-                uint8_t* rec = p.h + (static_cast<size_t>(slot) * blocks3 + cb) * kHRecord;
-                const float scaled = h * __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
-                __stcg(reinterpret_cast<unsigned short*>(rec) + lane, __half_as_ushort(__float2half_rn(scaled)));
-                if (lane == 0) {
-                    __stcg(reinterpret_cast<int*>(rec + 64), shift);
-                    atomicMin(p.hshift + slot, shift);
-                }
+                const int sh = mx::x_shift(__reduce_max_sync(0xffffffffu, (__float_as_uint(h) >> 23) & 0xFFu));
+                const float scaled = h * __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
+                __stcg(p.h + static_cast<size_t>(si) * p.I + cb * 32 + lane, __half_as_ushort(__float2half_rn(scaled)));
+                if (lane == i) low = sh;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm->taken[b]));
+            if (lane < n) {
+                __stcg(p.shift + static_cast<size_t>(slot) * p.pitch + cb, low);
+                atomicMin(p.hshift + slot, low);
             }
         }
-        fence_proxy_async_global();   // h is read by bulk copies
-        consumer_sync();
-        if (threadIdx.x == 0 && alive) grid_arrive(p.control);
+        asm volatile("bar.sync 2, %0;" ::"n"(kEpilogues * 32) : "memory");
+        if (b == 0 && lane == 0 && alive) {
+            grid_arrive(counts + 1);
+            if (grid_wait(counts + 1, abort)) mbar_arrive(smem_u32(&sm->phase3));
+        }
+        __syncwarp();
 
-        // ---- phase 3
-        if (ok) ok = warp_wait_bar(&sm->phase3, 0, sm, lane);
-        for (int item = cta; item < items3; item += grid) {
-            const int gi = item % groups, cb = item / groups;
-            const int n = sm->group[gi] >> 16;
-            int align[2] = {0, 0};
-#pragma unroll
-            for (int a = 0; a < 2; ++a)
-                if (ok && g + 8 * a < n) align[a] = __ldcg(p.hshift + sm->list[sm->first[gi] + g + 8 * a]);
-            float acc[2][4][4];
-#pragma unroll
-            for (int a = 0; a < 2; ++a)
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[a][b][i] = 0.f;
-            for (int ks = (cb ^ set) & 1; ks < steps3; ks += 2, ++used) {
-                const int s = set * kSetStages + static_cast<int>(used % kSetStages);
-                if (!ok || !warp_wait_bar(&sm->full[s], used / kSetStages & 1u, sm, lane)) {
-                    ok = false;
-                    continue;
-                }
-                if (ks * kBlocks + c < blocks3)
-                    block_products<true>(acc, ring_base + s * kStagePitch, c, n > 8, g, t, align);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sm->empty[s]));
+        if (ok) ok = warp_wait_bar(&sm->phase3, 0, abort, lane);
+        for (int item = cta; item < items3; item += grid, ++count) {
+            if (count % kEpilogues != static_cast<uint32_t>(b)) continue;
+            const int gi = item / cols3, cb = item - gi * cols3, n = sm->group[gi] >> 16;
+            int slot = 0;
+            float f = 0.f;
+            if (ok && lane < n) {
+                slot = sm->list[sm->first[gi] + lane];
+                f = mx::x_unshift(__ldcg(p.hshift + slot));
             }
-            consumer_sync();
-            store_sums(sm, acc, n > 8, warp, lane);
-            consumer_sync();
-            if (warp < n && ok) {
-                const int slot = sm->list[sm->first[gi] + warp], tok = slot / p.k;
-                const float f = mx::x_unshift(__ldcg(p.hshift + slot)), pw = sm->weight[slot];
-                float* part = p.part + static_cast<size_t>(slot) * p.H + cb * 64;
+            const float pw = lane < n ? sm->weight[slot] : 0.f;
+            if (!ok || !warp_wait_bar(&sm->sums[b], count / kEpilogues & 1u, abort, lane)) {
+                ok = false;
+                continue;
+            }
+            const bool right = cb * 64 + 32 < p.H;   // H % 64 may be 32
+            for (int i = 0; i < n; ++i) {
+                const int si = __shfl_sync(0xffffffffu, slot, i);
+                const float fi = __shfl_sync(0xffffffffu, f, i), wi = __shfl_sync(0xffffffffu, pw, i);
+                float* part = p.part + static_cast<size_t>(si) * p.H + cb * 64 + lane;
+                __stcg(part, total(i, 0) * fi * wi);
+                if (right) __stcg(part + 32, total(i, 1) * fi * wi);
+            }
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm->taken[b]));
+            // a ticket per token and column block: the last of its k experts adds the parts in order
+            const int tok = slot / p.k;
+            uint32_t* ticket = p.control + kTickets + static_cast<size_t>(cb) * kMoeMaxTokens + tok;
+            const bool last = lane < n && atomicAdd(ticket, 1u) == static_cast<uint32_t>(p.k - 1);
+            if (last) *ticket = 0u;
+            uint32_t todo = __ballot_sync(0xffffffffu, last);
+            if (todo) __threadfence();
+            // two tokens at a time, four columns a lane
+            const int half = lane >> 4, col = cb * 64 + 4 * (lane & 15);
+            while (todo) {
+                const int a = __ffs(todo) - 1;
+                todo &= todo - 1;
+                const int c = todo ? __ffs(todo) - 1 : a;
+                const bool live = (half == 0 || c != a) && col < p.H;
+                todo &= todo - 1;   // stays 0 when it is 0
+                const int mine = __shfl_sync(0xffffffffu, tok, half ? c : a);
+                if (live) {
+                    const float* src = p.part + static_cast<size_t>(mine) * p.k * p.H + col;
+                    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int q0 = 0; q0 < p.k; q0 += 8) {
+                        float4 v[8];
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    if (cb * 64 + b * 32 < p.H)
-                        __stcg(part + b * 32 + lane, load_sum(sm, warp, b, lane) * f * pw);
-                __threadfence();
-                __syncwarp();
-                uint32_t* ticket = p.control + 2 + static_cast<size_t>(cb) * kMoeMaxTokens + tok;
-                uint32_t last = 0;
-                if (lane == 0) last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(p.k - 1);
-                last = __shfl_sync(0xffffffffu, last, 0);
-                if (last) {
-                    __threadfence();
-                    const float* src = p.part + static_cast<size_t>(tok) * p.k * p.H + cb * 64 + lane;
-                    float sum[2] = {0.f, 0.f};
-                    for (int q = 0; q < p.k; ++q)
+                        for (int q = 0; q < 8; ++q)
+                            v[q] = q0 + q < p.k
+                                       ? __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(q0 + q) * p.H))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                        for (int b = 0; b < 2; ++b)
-                            if (cb * 64 + b * 32 < p.H) sum[b] += __ldcg(src + static_cast<size_t>(q) * p.H + b * 32);
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-                        if (cb * 64 + b * 32 < p.H)
-                            p.y[static_cast<size_t>(tok) * p.H + cb * 64 + b * 32 + lane] =
-                                __bfloat16_as_ushort(__float2bfloat16_rn(sum[b]));
-                    if (lane == 0) *ticket = 0u;
+                        for (int q = 0; q < 8; ++q) s.x += v[q].x, s.y += v[q].y, s.z += v[q].z, s.w += v[q].w;
+                    }
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+                    *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(mine) * p.H + col) = make_uint2(
+                        *reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
                 }
             }
         }
@@ -736,7 +800,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
 struct Layout {
-    size_t logits, x16, xfactor, hshift, h, part, total;
+    size_t logits, x16, xfactor, hshift, h, shift, part, total;
+    int pitch;
 };
 Layout layout(int T, int E, int k, int H, int I) {
     Layout l;
@@ -751,10 +816,38 @@ Layout layout(int T, int E, int k, int H, int I) {
     l.x16 = take(static_cast<size_t>(T) * H * 2);
     l.xfactor = take(static_cast<size_t>(T) * 4);
     l.hshift = take(slots * 4);
-    l.h = take(slots * (I / 32) * kHRecord);
+    l.pitch = (I / 32 + kBlocks - 1) / kBlocks * kBlocks;
+    l.h = take(slots * I * 2);
+    l.shift = take(slots * l.pitch * 4);
     l.part = take(slots * H * 4);
     l.total = at;
     return l;
+}
+
+// Whether the experts have more than `n` tokens each on average.
+bool slots_per_expert_over(const MxMoeArgs& a, int n) { return static_cast<long long>(a.T) * a.k > static_cast<long long>(n) * a.E; }
+
+template <int kGroup>
+cudaError_t launch_group(const CUtensorMap (&maps)[4], const Params& p, const DeviceProps& dp, cudaStream_t s) {
+    auto kern = moe_kernel<kGroup>;
+    if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), dp.device, smem_bytes<kGroup>());
+        e != cudaSuccess)
+        return e;
+    // no more CTAs than the larger of the two expert phases can use
+    const long long slots = static_cast<long long>(p.T) * p.k;
+    const long long want = slots * std::max<long long>(p.I / 32, (p.H + 63) / 64);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(want, dp.sms)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<kGroup>();
+    cfg.stream = s;
+    // the CTAs wait for one another at the grid barriers: all of them are resident together or the launch fails
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p);
 }
 
 }  // namespace
@@ -762,18 +855,15 @@ Layout layout(int T, int E, int k, int H, int I) {
 size_t mx_moe_workspace_bytes(int T, int E, int k, int H, int I) { return layout(T, E, k, H, I).total; }
 
 cudaError_t launch_mx_moe(const MxMoeArgs& a, void* workspace, const DeviceProps& dp, cudaStream_t s) {
-    if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(moe_kernel), dp.device, kSmemBytes);
-        e != cudaSuccess)
-        return e;
-    CUtensorMap tw13, te13, tw2, te2;
+    CUtensorMap maps[4];
     const uint64_t E = a.E, H = a.H, I = a.I;
-    if (!encode_2d(&tw13, CU_TENSOR_MAP_DATA_TYPE_INT32, a.w13, 2 * I, E * (H / 8), 2 * I * 4, 32, kStepK / 8,
+    if (!encode_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_INT32, a.w13, 2 * I, E * (H / 8), 2 * I * 4, 32, kStepK / 8,
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_2d(&te13, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.e13, 2 * I, E * (H / 32), 2 * I, 32, kBlocks,
+        !encode_2d(&maps[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.e13, 2 * I, E * (H / 32), 2 * I, 32, kBlocks,
                    CU_TENSOR_MAP_SWIZZLE_NONE) ||
-        !encode_2d(&tw2, CU_TENSOR_MAP_DATA_TYPE_INT32, a.w2, H, E * (I / 8), H * 4, 32, kStepK / 8,
+        !encode_2d(&maps[2], CU_TENSOR_MAP_DATA_TYPE_INT32, a.w2, H, E * (I / 8), H * 4, 32, kStepK / 8,
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_2d(&te2, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.e2, H, E * (I / 32), H, 32, kBlocks,
+        !encode_2d(&maps[3], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.e2, H, E * (I / 32), H, 32, kBlocks,
                    CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -787,7 +877,9 @@ cudaError_t launch_mx_moe(const MxMoeArgs& a, void* workspace, const DeviceProps
     p.x16 = reinterpret_cast<uint16_t*>(ws + l.x16);
     p.xfactor = reinterpret_cast<float*>(ws + l.xfactor);
     p.hshift = reinterpret_cast<int*>(ws + l.hshift);
-    p.h = ws + l.h;
+    p.h = reinterpret_cast<uint16_t*>(ws + l.h);
+    p.shift = reinterpret_cast<int*>(ws + l.shift);
+    p.pitch = l.pitch;
     p.part = reinterpret_cast<float*>(ws + l.part);
     p.T = a.T;
     p.E = a.E;
@@ -795,21 +887,9 @@ cudaError_t launch_mx_moe(const MxMoeArgs& a, void* workspace, const DeviceProps
     p.H = a.H;
     p.I = a.I;
     p.renormalize = a.renormalize ? 1 : 0;
-    // no more CTAs than the larger of the two expert phases can use
-    const long long slots = static_cast<long long>(a.T) * a.k;
-    const long long want = slots * std::max<long long>(a.I / 32, (a.H + 63) / 64);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::max<long long>(1, std::min<long long>(want, dp.sms))));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = s;
-    // the CTAs wait for one another at the grid barriers: all of them are resident together or the launch fails
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, moe_kernel, tw13, te13, tw2, te2, p);
+    // Groups of 16 cost ring stages; they pay where experts have more than 8 tokens (6 on average, and more) to read
+    // their weights once for.
+    return a.T > 8 && slots_per_expert_over(a, 6) ? launch_group<16>(maps, p, dp, s) : launch_group<8>(maps, p, dp, s);
 }
 
 cudaError_t read_and_clear_mx_moe_error(uint32_t* out) {
