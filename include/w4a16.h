@@ -465,13 +465,14 @@ w4a16_status w4a16_mxfp4_matmul(const int32_t* a, const uint8_t* ea, const int32
  * leaves other tokens alone.
  *
  * workspace: at least w4a16_mxfp4_moe_workspace_bytes(...) bytes with the
- * ownership and zero-fill rules of w4a16_gemv's (the words that must be zero
- * are the first 262400 bytes, left zero, bar a counter, by every call, so one
- * workspace serves calls of any shape it is large enough for). Two calls that
+ * ownership and zero-fill rules of w4a16_gemv's (what must start at zero are
+ * barrier words in its first 256 bytes, which every call leaves as the next
+ * needs them: one workspace serves calls of any shape it is large enough for,
+ * and is not zeroed again between them). Two calls that
  * may run at the same time must not share one. After a W4A16_ERR_TIMEOUT
  * reported by w4a16_device_status, zero it again.
  *
- * Launched cooperatively (its thread blocks wait for one another at two
+ * Launched cooperatively (its thread blocks wait for one another at three
  * points); it can be captured in a CUDA graph.
  * Limits: 1 <= T <= 64, 1 <= E <= 256, 1 <= top_k <= min(E, 16), H and I
  * multiples of 32, H <= 65536.

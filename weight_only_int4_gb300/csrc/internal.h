@@ -155,9 +155,9 @@ cudaError_t read_and_clear_mx_matmul_error(uint32_t* out);
 
 // Mixture-of-experts layer for a few tokens, MXFP4 expert weights.
 constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 256, kMoeMaxHidden = 65536;
-// Barrier words and one ticket per 64 columns of y and token: the same size for
-// every shape, zero before the first call, and no call writes data below it.
-constexpr size_t kMoeControlBytes = 256 + size_t(kMoeMaxHidden / 64) * kMoeMaxTokens * 4;
+// Barrier words, before everything else in the workspace: zero before the first
+// call, and no call writes data there.
+constexpr size_t kMoeControlBytes = 256;
 struct MxMoeArgs {
     const void* x;
     const void* router;

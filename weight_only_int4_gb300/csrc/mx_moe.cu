@@ -18,8 +18,10 @@
 //   2  items (group, 32 gate columns and their 32 up columns): products, SwiGLU,
 //      h as fp16 with one power of two per 32 columns
 //      -- grid barrier (weights of phase 3 are already on their way) --
-//   3  items (group, 64 columns of y): products; the last of a token's k experts
-//      to finish a column block adds the k parts in order: deterministic
+//   3  items (group, 64 columns of y): products, each token's part from each of
+//      its k experts to global memory (L2)
+//      -- grid barrier --
+//   4  the k parts of every y added in order: deterministic
 //
 // A CTA is two producer warps, sixteen consumer warps and two epilogue warps.
 // Weights pass through a ring of stages: 512 rows of K by 64 columns of codes
@@ -36,8 +38,8 @@
 // come straight from global memory (L2) into B fragments, loaded before the wait
 // for the stage's weights. A block's FP32 products are scaled by the columns'
 // 2^(e - 127) as they are added up. At the end of an item the warps leave their
-// sums in one of two buffers and go on; the buffer's epilogue warp adds the
-// eight parts in order and finishes the item beside the next ones.
+// sums in one of two buffers and go on; the epilogue warps, two tokens each at
+// a time, add the eight parts in order and finish the item beside the next ones.
 //
 // Activations in fp16: a token's x is multiplied by the power of two that
 // brings its largest magnitude just below 2^15, a run of 32 h values likewise
@@ -63,6 +65,7 @@ __device__ unsigned int g_mx_moe_error = 0;
 namespace {
 
 constexpr int kConsumerWarps = 16, kEpilogues = 2, kProducers = 2;
+constexpr int kBuffers = 2;              // of partial sums
 constexpr int kConsumers = kConsumerWarps * 32;
 constexpr int kThreads = kConsumers + (kEpilogues + kProducers) * 32;
 constexpr int kStepK = 512;              // rows of K per stage
@@ -78,7 +81,6 @@ static_assert(kStageBytes % 1024 == 0, "swizzled boxes start 1024-byte aligned")
 constexpr int kSetStages = 4;            // half of the ring
 constexpr int kStages = 2 * kSetStages;
 constexpr int kRedPitch = 33;            // floats per slot of a warp's partial sums
-constexpr uint32_t kSuspendNs = 20000;
 constexpr unsigned long long kWaitLimitCycles = 4000000000ull;   // ~2 s at 2 GHz
 constexpr unsigned int kErrTimeout = 9u;
 
@@ -87,12 +89,13 @@ template <int kGroup>
 struct __align__(16) Shared {
     static constexpr int kTiles = kGroup / 8;            // 8-token MMA tiles
     static constexpr int kRedSlots = kTiles * 8;         // [tile][token parity][column % 4]
-    float red[kEpilogues][kConsumerWarps][kRedSlots][kRedPitch];
+    float red[kBuffers][kConsumerWarps][kRedSlots][kRedPitch];
     uint64_t full[kStages];
     uint64_t empty[kStages];
-    uint64_t sums[kEpilogues];           // a buffer of partial sums is complete
-    uint64_t taken[kEpilogues];          // ... and has been read
+    uint64_t sums[kBuffers];             // a buffer of partial sums is complete
+    uint64_t taken[kBuffers];            // ... and has been read
     uint64_t phase3;                     // h of every CTA is visible
+    uint64_t phase4;                     // the parts of y are
     uint32_t mask[kMaxExperts][2];       // tokens of each expert
     float weight[kMaxSlots];             // of slot t * k + j
     uint32_t group[kMaxSlots];           // expert | count << 16
@@ -115,7 +118,7 @@ struct Params {
     const uint16_t* x;
     const uint16_t* router;
     uint16_t* y;
-    uint32_t* control;     // epoch, two pairs of barrier counts; from kTickets on, tickets
+    uint32_t* control;     // epoch, then two sets of barrier counts
     float* logits;         // [T, E]
     uint16_t* x16;         // [T, H]
     float* xfactor;        // [T]
@@ -127,7 +130,7 @@ struct Params {
     int pitch;             // I / 32, rounded up to whole stages
     int renormalize;
 };
-constexpr int kTickets = 8;   // word of `control`
+constexpr int kBarriers = 3;
 
 __device__ __forceinline__ void fail(volatile int* abort) {
     *abort = 1;
@@ -138,7 +141,9 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
     const uint32_t b = smem_u32(bar);
     const unsigned long long t0 = clock64();
     for (;;) {
-        if (mbar_try_wait_suspend(b, parity, kSuspendNs)) return true;
+        // a few polls between looks at the clock; a thread suspended in its wait woke up microseconds late
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(b, parity)) return true;
         if (*abort) return false;
         if (clock64() - t0 > kWaitLimitCycles) {
             fail(abort);
@@ -160,8 +165,8 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
     return v;
 }
 
-// Grid barriers. A call uses one of two pairs of counts, by the parity of the
-// call's epoch, and zeroes the other pair (the previous call's); the epoch
+// Grid barriers. A call uses one of two sets of counts, by the parity of the
+// call's epoch, and zeroes the other set (the previous call's); the epoch
 // advances once every CTA has passed the first barrier, so all have read it.
 __device__ __forceinline__ void grid_arrive(uint32_t* count) {
     asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
@@ -418,43 +423,51 @@ __device__ __forceinline__ bool has_edge_byte(uint32_t v) {
     return (__vcmpeq4(v, 0u) | __vcmpeq4(v, 0xFFFFFFFFu)) != 0u;
 }
 
-// Block c (32 rows) of one box of a stage against the group's rows in b, added
-// to acc [8-token tile][16-column tile][fragment].
-template <int kTiles>
-__device__ __forceinline__ void block_products(float (&acc)[kTiles][2][4], uint32_t box, uint32_t scales, int c,
-                                               int tiles, int g, int t, const uint4 (&b)[kTiles]) {
-    const int row = 4 * c + t;
+// kCount 32-row blocks of one box of a stage, from block c on, against the
+// group's rows in b, added to acc [8-token tile][16-column tile][fragment].
+// kEdge: a byte of 0 or 255 may be among the exponents.
+template <bool kEdge, int kCount, int kTiles>
+__device__ __forceinline__ void block_products(float (&acc)[kTiles][2][4], uint32_t box, const uint32_t (&e4)[4],
+                                               int c, int first, int tiles, int g, int t, const uint4 (&b)[4][kTiles]) {
     const uint32_t chunk = static_cast<uint32_t>((g >> 1) | ((g & 1) << 2));   // quarter-warps hit every bank once
-    const uint4 w = ld_shared_v4(box + row * 128 + ((chunk ^ (row & 7)) << 4));
-    const uint32_t e4 = ld_shared_u32(scales + c * 32 + chunk * 4);
-    // 2^(e - 127): the byte as an FP32 exponent field, right for 1..254
-    float scale[4];
-    scale[0] = __uint_as_float((e4 & 0xFFu) << 23);
-    scale[1] = __uint_as_float((e4 & 0xFF00u) << 15);
-    scale[2] = __uint_as_float((e4 & 0xFF0000u) << 7);
-    scale[3] = __uint_as_float((e4 >> 24) << 23);
-    // 0 is the subnormal 2^-127, 255 NaN: rare
-    if (has_edge_byte(e4)) {
+    uint4 w[kCount];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) scale[i] = mx::scale_f32((e4 >> (8 * i)) & 0xFFu);
+    for (int j = 0; j < kCount; ++j) {
+        const int row = 4 * (c + first + j) + t;
+        w[j] = ld_shared_v4(box + row * 128 + ((chunk ^ (row & 7)) << 4));
     }
-    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-        uint32_t lo[4], hi[4];
-        mx::e2m1x8_to_f16x2(words[2 * m], lo);
-        mx::e2m1x8_to_f16x2(words[2 * m + 1], hi);
+    for (int j = 0; j < kCount; ++j) {
+        const uint32_t words[4] = {w[j].x, w[j].y, w[j].z, w[j].w}, e = e4[first + j];
+        // 2^(e - 127): the byte as an FP32 exponent field, right for 1..254
+        float scale[4];
+        if constexpr (kEdge) {
 #pragma unroll
-        for (int n = 0; n < kTiles; ++n) {
-            if (n > 0 && n >= tiles) break;
-            float d[4];
-            mma_f16_zero(d, lo[0], hi[0], lo[1], hi[1], b[n].x, b[n].y);
-            mma_m16n8k16<false>(d, lo[2], hi[2], lo[3], hi[3], b[n].z, b[n].w);
-            float(&a)[4] = acc[n][m];
-            a[0] = fmaf(d[0], scale[2 * m], a[0]);
-            a[1] = fmaf(d[1], scale[2 * m], a[1]);
-            a[2] = fmaf(d[2], scale[2 * m + 1], a[2]);
-            a[3] = fmaf(d[3], scale[2 * m + 1], a[3]);
+            for (int i = 0; i < 4; ++i) scale[i] = mx::scale_f32((e >> (8 * i)) & 0xFFu);
+        } else {
+            scale[0] = __uint_as_float((e & 0xFFu) << 23);
+            scale[1] = __uint_as_float((e & 0xFF00u) << 15);
+            scale[2] = __uint_as_float((e & 0xFF0000u) << 7);
+            scale[3] = __uint_as_float((e >> 24) << 23);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            uint32_t lo[4], hi[4];
+            mx::e2m1x8_to_f16x2(words[2 * m], lo);
+            mx::e2m1x8_to_f16x2(words[2 * m + 1], hi);
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) {
+                if (n > 0 && n >= tiles) break;
+                const uint4 x = b[first + j][n];
+                float d[4];
+                mma_f16_zero(d, lo[0], hi[0], lo[1], hi[1], x.x, x.y);
+                mma_m16n8k16<false>(d, lo[2], hi[2], lo[3], hi[3], x.z, x.w);
+                float(&a)[4] = acc[n][m];
+                a[0] = fmaf(d[0], scale[2 * m], a[0]);
+                a[1] = fmaf(d[1], scale[2 * m], a[1]);
+                a[2] = fmaf(d[2], scale[2 * m + 1], a[2]);
+                a[3] = fmaf(d[3], scale[2 * m + 1], a[3]);
+            }
         }
     }
 }
@@ -477,11 +490,12 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
             mbar_init(smem_u32(&sm->full[s]), 1);
             mbar_init(smem_u32(&sm->empty[s]), kConsumerWarps / 2);
         }
-        for (int b = 0; b < kEpilogues; ++b) {
+        for (int b = 0; b < kBuffers; ++b) {
             mbar_init(smem_u32(&sm->sums[b]), kConsumerWarps);
-            mbar_init(smem_u32(&sm->taken[b]), 1);
+            mbar_init(smem_u32(&sm->taken[b]), kEpilogues);
         }
         mbar_init(smem_u32(&sm->phase3), 1);
+        mbar_init(smem_u32(&sm->phase4), 1);
         *abort = 0;
         sm->epoch = ld_acquire(p.control);
         fence_mbar_init();
@@ -492,7 +506,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
     }
     if (threadIdx.x < kMaxExperts) sm->mask[threadIdx.x][0] = sm->mask[threadIdx.x][1] = 0u;
     __syncthreads();
-    uint32_t* counts = p.control + 1 + 2 * (sm->epoch & 1u);
+    uint32_t* counts = p.control + 1 + kBarriers * (sm->epoch & 1u);
 
     // ---------------------------------------------------------------- phase 0
     if (warp < kConsumerWarps) {
@@ -510,8 +524,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
         grid_arrive(counts);
         grid_wait(counts, abort);
         if (cta == 0) {
-            uint32_t* other = p.control + 1 + 2 * ((sm->epoch & 1u) ^ 1u);
-            other[0] = other[1] = 0u;
+            uint32_t* other = p.control + 1 + kBarriers * ((sm->epoch & 1u) ^ 1u);
+            for (int i = 0; i < kBarriers; ++i) other[i] = 0u;
             p.control[0] = sm->epoch + 1u;
         }
     }
@@ -640,29 +654,41 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                         ok = false;
                         continue;
                     }
-                    const uint32_t stage = ring_base + s * kStageBytes;
+                    const uint32_t stage = ring_base + s * kStageBytes, weights = stage + box * kBoxBytes;
+                    uint32_t e4[kWarpBlocks];
 #pragma unroll
-                    for (int i = 0; i < kWarpBlocks; ++i) {
-                        if (i >= here) break;
-                        if constexpr (kH) {
-                            // every run of h to its row's common shift
+                    for (int i = 0; i < kWarpBlocks; ++i)
+                        e4[i] = ld_shared_u32(stage + 2 * kBoxBytes + box * kScaleBoxBytes + (c0 + i) * 32 +
+                                              ((g >> 1) | ((g & 1) << 2)) * 4);
+                    if constexpr (kH) {
+                        // every run of h to its row's common shift
 #pragma unroll
-                            for (int a = 0; a < kTiles; ++a) {
-                                const int si = i == 0 ? sh[a].x : i == 1 ? sh[a].y : i == 2 ? sh[a].z : sh[a].w;
-                                const uint32_t f = pow2_f16x2(min(align[a] - si, 0));
+                        for (int a = 0; a < kTiles; ++a) {
+                            const int si[4] = {sh[a].x, sh[a].y, sh[a].z, sh[a].w};
+#pragma unroll
+                            for (int i = 0; i < kWarpBlocks; ++i) {
+                                const uint32_t f = pow2_f16x2(min(align[a] - si[i], 0));
                                 x[i][a] = make_uint4(hmul2(x[i][a].x, f), hmul2(x[i][a].y, f), hmul2(x[i][a].z, f),
                                                      hmul2(x[i][a].w, f));
                             }
                         }
-                        block_products<kTiles>(acc, stage + box * kBoxBytes,
-                                               stage + 2 * kBoxBytes + box * kScaleBoxBytes, c0 + i, tiles, g, t, x[i]);
+                    }
+                    // the usual stage without a branch, so that its blocks overlap; else one block at a time
+                    const bool edge =
+                        has_edge_byte(e4[0]) | has_edge_byte(e4[1]) | has_edge_byte(e4[2]) | has_edge_byte(e4[3]);
+                    if (here >= kWarpBlocks && !__any_sync(0xffffffffu, edge)) {
+                        block_products<false, kWarpBlocks, kTiles>(acc, weights, e4, c0, 0, tiles, g, t, x);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kWarpBlocks; ++i)
+                            if (i < here) block_products<true, 1, kTiles>(acc, weights, e4, c0, i, tiles, g, t, x);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sm->empty[s]));
                 }
                 // sums to the item's buffer: slot [tile][token parity][column % 4], at the lane that holds them
-                const int b = static_cast<int>(count % kEpilogues);
-                if (ok) ok = warp_wait_bar(&sm->taken[b], (count / kEpilogues & 1u) ^ 1u, abort, lane);
+                const int b = static_cast<int>(count % kBuffers);
+                if (ok) ok = warp_wait_bar(&sm->taken[b], (count / kBuffers & 1u) ^ 1u, abort, lane);
 #pragma unroll
                 for (int a = 0; a < kTiles; ++a) {
                     if (a > 0 && a >= tiles) break;
@@ -681,11 +707,11 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
         phase(std::true_type{});
     } else {
         // ------------------------------------------------------------ epilogue
-        const int b = warp - kConsumerWarps;   // this warp's buffer: every other item
+        const int half = warp - kConsumerWarps;   // tokens 4 i + 2 half and the next of a group
         uint32_t count = 0;
         bool ok = alive;
         // token n of the group, column `lane` of box `box`: the warps' parts in order
-        auto total = [&](int n, int box) {
+        auto total = [&](int b, int n, int box) {
             const int chunk = lane >> 2, slot = (n >> 3) * 8 + (n & 1) * 4 + (lane & 3);
             const int from = (((chunk & 3) << 1) | (chunk >> 2)) * 4 + ((n & 7) >> 1);
             float s = 0.f;
@@ -696,38 +722,51 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
             return s;
         };
         for (int item = cta; item < items2; item += grid, ++count) {
-            if (count % kEpilogues != static_cast<uint32_t>(b)) continue;
             const int gi = item / cols2, cb = item - gi * cols2, n = sm->group[gi] >> 16;
+            const int b = static_cast<int>(count % kBuffers);
             int slot = 0;
             float f = 0.f;
             if (lane < n) {
                 slot = sm->list[sm->first[gi] + lane];
                 f = __ldcg(p.xfactor + slot / p.k);
             }
-            if (!ok || !warp_wait_bar(&sm->sums[b], count / kEpilogues & 1u, abort, lane)) {
+            if (!ok || !warp_wait_bar(&sm->sums[b], count / kBuffers & 1u, abort, lane)) {
                 ok = false;
                 continue;
             }
             int low = 127;   // lane i: token i's shift
-            for (int i = 0; i < n; ++i) {
-                const int si = __shfl_sync(0xffffffffu, slot, i);
-                const float fi = __shfl_sync(0xffffffffu, f, i);
-                const float gate = total(i, 0) * fi, up = total(i, 1) * fi;
-                const float h = silu(gate) * up;
-                const int sh = mx::x_shift(__reduce_max_sync(0xffffffffu, (__float_as_uint(h) >> 23) & 0xFFu));
-                const float scaled = h * __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
-                __stcg(p.h + static_cast<size_t>(si) * p.I + cb * 32 + lane, __half_as_ushort(__float2half_rn(scaled)));
-                if (lane == i) low = sh;
+            for (int i0 = 2 * half; i0 < n; i0 += 2 * kEpilogues) {
+                float h[2];
+                int sh[2];
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    const float fi = __shfl_sync(0xffffffffu, f, i0 + d);   // 0 past the last token
+                    const float gate = total(b, i0 + d, 0) * fi, up = total(b, i0 + d, 1) * fi;
+                    h[d] = silu(gate) * up;
+                }
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+                    sh[d] = mx::x_shift(__reduce_max_sync(0xffffffffu, (__float_as_uint(h[d]) >> 23) & 0xFFu));
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    const int si = __shfl_sync(0xffffffffu, slot, i0 + d);
+                    const float scaled = h[d] * __uint_as_float(static_cast<uint32_t>(sh[d] + 127) << 23);
+                    if (i0 + d < n)
+                        __stcg(p.h + static_cast<size_t>(si) * p.I + cb * 32 + lane,
+                               __half_as_ushort(__float2half_rn(scaled)));
+                    if (lane == i0 + d) low = sh[d];
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm->taken[b]));
-            if (lane < n) {
+            if (lane < n && ((lane >> 1) & 1) == half) {
                 __stcg(p.shift + static_cast<size_t>(slot) * p.pitch + cb, low);
                 atomicMin(p.hshift + slot, low);
             }
         }
-        asm volatile("bar.sync 2, %0;" ::"n"(kEpilogues * 32) : "memory");
-        if (b == 0 && lane == 0 && alive) {
+        auto epilogue_sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(kEpilogues * 32) : "memory"); };
+        epilogue_sync();
+        if (half == 0 && lane == 0 && alive) {
             grid_arrive(counts + 1);
             if (grid_wait(counts + 1, abort)) mbar_arrive(smem_u32(&sm->phase3));
         }
@@ -735,8 +774,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
 
         if (ok) ok = warp_wait_bar(&sm->phase3, 0, abort, lane);
         for (int item = cta; item < items3; item += grid, ++count) {
-            if (count % kEpilogues != static_cast<uint32_t>(b)) continue;
             const int gi = item / cols3, cb = item - gi * cols3, n = sm->group[gi] >> 16;
+            const int b = static_cast<int>(count % kBuffers);
             int slot = 0;
             float f = 0.f;
             if (ok && lane < n) {
@@ -744,56 +783,54 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                 f = mx::x_unshift(__ldcg(p.hshift + slot));
             }
             const float pw = lane < n ? sm->weight[slot] : 0.f;
-            if (!ok || !warp_wait_bar(&sm->sums[b], count / kEpilogues & 1u, abort, lane)) {
+            if (!ok || !warp_wait_bar(&sm->sums[b], count / kBuffers & 1u, abort, lane)) {
                 ok = false;
                 continue;
             }
             const bool right = cb * 64 + 32 < p.H;   // H % 64 may be 32
-            for (int i = 0; i < n; ++i) {
-                const int si = __shfl_sync(0xffffffffu, slot, i);
-                const float fi = __shfl_sync(0xffffffffu, f, i), wi = __shfl_sync(0xffffffffu, pw, i);
-                float* part = p.part + static_cast<size_t>(si) * p.H + cb * 64 + lane;
-                __stcg(part, total(i, 0) * fi * wi);
-                if (right) __stcg(part + 32, total(i, 1) * fi * wi);
-            }
-            __threadfence();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm->taken[b]));
-            // a ticket per token and column block: the last of its k experts adds the parts in order
-            const int tok = slot / p.k;
-            uint32_t* ticket = p.control + kTickets + static_cast<size_t>(cb) * kMoeMaxTokens + tok;
-            const bool last = lane < n && atomicAdd(ticket, 1u) == static_cast<uint32_t>(p.k - 1);
-            if (last) *ticket = 0u;
-            uint32_t todo = __ballot_sync(0xffffffffu, last);
-            if (todo) __threadfence();
-            // two tokens at a time, four columns a lane
-            const int half = lane >> 4, col = cb * 64 + 4 * (lane & 15);
-            while (todo) {
-                const int a = __ffs(todo) - 1;
-                todo &= todo - 1;
-                const int c = todo ? __ffs(todo) - 1 : a;
-                const bool live = (half == 0 || c != a) && col < p.H;
-                todo &= todo - 1;   // stays 0 when it is 0
-                const int mine = __shfl_sync(0xffffffffu, tok, half ? c : a);
-                if (live) {
-                    const float* src = p.part + static_cast<size_t>(mine) * p.k * p.H + col;
-                    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int q0 = 0; q0 < p.k; q0 += 8) {
-                        float4 v[8];
+            for (int i0 = 2 * half; i0 < n; i0 += 2 * kEpilogues) {
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            v[q] = q0 + q < p.k
-                                       ? __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(q0 + q) * p.H))
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) s.x += v[q].x, s.y += v[q].y, s.z += v[q].z, s.w += v[q].w;
+                for (int d = 0; d < 2; ++d) {
+                    const int si = __shfl_sync(0xffffffffu, slot, i0 + d);
+                    const float fi = __shfl_sync(0xffffffffu, f, i0 + d), wi = __shfl_sync(0xffffffffu, pw, i0 + d);
+                    const float s0 = total(b, i0 + d, 0) * fi * wi, s1 = total(b, i0 + d, 1) * fi * wi;
+                    if (i0 + d < n) {
+                        float* part = p.part + static_cast<size_t>(si) * p.H + cb * 64 + lane;
+                        __stcg(part, s0);
+                        if (right) __stcg(part + 32, s1);
                     }
-                    const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
-                    *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(mine) * p.H + col) = make_uint2(
-                        *reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm->taken[b]));
         }
+        epilogue_sync();
+        if (half == 0 && lane == 0 && alive) {
+            grid_arrive(counts + 2);
+            if (grid_wait(counts + 2, abort)) mbar_arrive(smem_u32(&sm->phase4));
+        }
+    }
+
+    // ---------------------------------------------------------------- phase 4
+    __syncwarp();   // single-lane roles rejoin their warp
+    if (!alive || !warp_wait_bar(&sm->phase4, 0, abort, lane)) return;
+    const int quads = p.H >> 2;
+    for (int i = cta * kThreads + static_cast<int>(threadIdx.x); i < p.T * quads; i += grid * kThreads) {
+        const int tok = i / quads, col = (i - tok * quads) * 4;
+        const float* src = p.part + static_cast<size_t>(tok) * p.k * p.H + col;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q0 = 0; q0 < p.k; q0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                v[q] = q0 + q < p.k ? __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(q0 + q) * p.H))
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) s.x += v[q].x, s.y += v[q].y, s.z += v[q].z, s.w += v[q].w;
+        }
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+        *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(tok) * p.H + col) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
 }
 
