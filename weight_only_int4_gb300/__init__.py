@@ -102,15 +102,25 @@ def abi_version() -> int:
     return load_library().w4a16_abi_version()
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_ptr(stream=None) -> int:
+    """Raw handle of `stream`, or of the current stream of the current device."""
+    if stream is not None:
+        return int(stream.cuda_stream)
     torch = _torch()
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    # the stream object that torch.cuda.current_stream() builds costs 3 us a call
+    return int(torch.cuda.current_stream().cuda_stream) if raw is None else raw(torch.cuda.current_device())
 
 
 def _check(fn: str, status: int) -> None:
@@ -204,10 +214,14 @@ def _cached_workspace(nbytes: int, device, stream, op: int):
     through an earlier call may still replay into it."""
     torch = _torch()
     dev = device.index if device.index is not None else torch.cuda.current_device()
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    key = (dev, int(s.cuda_stream), op)
+    if stream is None and dev == torch.cuda.current_device():
+        handle = _stream_ptr()
+    else:
+        handle = int((torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream)
+    key = (dev, handle, op)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
+        s = torch.cuda.current_stream(dev) if stream is None else stream
         with torch.cuda.stream(s):
             fresh = new_workspace(nbytes, device)
         if ws is not None:
@@ -418,37 +432,38 @@ def mxfp4_quantize(x, dim: int, out=None, stream=None):
     torch = _torch()
     _cuda_contig("x", x)
     dt = _dtype_code(x.dtype)
-    if dim not in (0, 1):
-        raise ValueError(f"dim must be 0 or 1, got {dim}")
-    if not (x.dim() == 2 or (x.dim() == 3 and dim == 0)):
-        raise ValueError("x must be 2-D (or 3-D with dim 0)")
-    K = x.shape[-2] if dim == 0 else x.shape[-1]
-    if K % 32 or not x.numel():
-        raise ValueError(f"x must hold whole blocks of 32 along dim {dim}, got shape {tuple(x.shape)}")
-    if dim == 0:
-        lead, cols = tuple(x.shape[:-2]), x.shape[-1]
-        rows = x.numel() // cols
-        shapes = (*lead, K // 8, cols), (*lead, K // 32, cols)
-    else:
-        rows, cols = x.shape
+    shape = x.shape
+    if dim == 1 and len(shape) == 2:
+        rows, cols = shape
+        K = cols
         shapes = (rows, K // 8), mxfp4_scale_shape(rows, cols)
+    elif dim == 0 and len(shape) in (2, 3):
+        K, cols = shape[-2:]
+        rows = K if len(shape) == 2 else shape[0] * K
+        shapes = (*shape[:-2], K // 8, cols), (*shape[:-2], K // 32, cols)
+    else:
+        raise ValueError(f"x must be 2-D (or 3-D with dim 0) and dim 0 or 1, got {len(shape)}-D and dim {dim}")
+    if K % 32 or not rows or not cols:
+        raise ValueError(f"x must hold whole blocks of 32 along dim {dim}, got shape {tuple(shape)}")
     codes, escale = (None, None) if out is None else out
-    sp = _stream_ptr(stream)
-    codes = _out("codes", codes, shapes[0], torch.int32, x.device, stream)
-    escale = _out("escale", escale, shapes[1], torch.uint8, x.device, stream)
-    _check("w4a16_mxfp4_quantize", load_library().w4a16_mxfp4_quantize(x.data_ptr(), codes.data_ptr(),
-                                                                        escale.data_ptr(), rows, cols, dim, dt, sp))
+    device = x.device
+    codes = _out("codes", codes, shapes[0], torch.int32, device, stream)
+    escale = _out("escale", escale, shapes[1], torch.uint8, device, stream)
+    st = load_library().w4a16_mxfp4_quantize(x.data_ptr(), codes.data_ptr(), escale.data_ptr(), rows, cols, dim, dt,
+                                             _stream_ptr(stream))
+    _check("w4a16_mxfp4_quantize", st)
     return codes, escale
 
 
 def _mx_rows(name: str, codes, escale):
     """Checks a row-layout operand, returns its rows and K."""
     torch = _torch()
-    for n, t in ((name, codes), (f"{name} scales", escale)):
-        _cuda_contig(n, t)
-    if codes.dim() != 2 or codes.dtype != torch.int32:
+    _cuda_contig(name, codes)
+    _cuda_contig(name + " scales", escale)
+    shape = codes.shape
+    if len(shape) != 2 or codes.dtype != torch.int32:
         raise TypeError(f"{name} must be a 2-D torch.int32 tensor of codes")
-    R, K = codes.shape[0], codes.shape[1] * 8
+    R, K = shape[0], shape[1] * 8
     if escale.dtype != torch.uint8 or tuple(escale.shape) != mxfp4_scale_shape(R, K):
         raise ValueError(f"{name} scales must be torch.uint8 {mxfp4_scale_shape(R, K)}, got {escale.dtype} "
                          f"{tuple(escale.shape)}")
@@ -457,11 +472,11 @@ def _mx_rows(name: str, codes, escale):
 
 def mxfp4_dequant_rows(codes, escale, out=None, stream=None):
     """Dense bf16 copy [R, K] of the row layout."""
-    torch = _torch()
     R, K = _mx_rows("codes", codes, escale)
-    out = _out("out", out, (R, K), torch.bfloat16, codes.device, stream)
-    _check("w4a16_mxfp4_dequant_rows", load_library().w4a16_mxfp4_dequant_rows(
-        codes.data_ptr(), escale.data_ptr(), out.data_ptr(), R, K, _stream_ptr(stream)))
+    out = _out("out", out, (R, K), _torch().bfloat16, codes.device, stream)
+    st = load_library().w4a16_mxfp4_dequant_rows(codes.data_ptr(), escale.data_ptr(), out.data_ptr(), R, K,
+                                                 _stream_ptr(stream))
+    _check("w4a16_mxfp4_dequant_rows", st)
     return out
 
 
@@ -473,9 +488,18 @@ def mxfp4_tile_scales(escale, out=None, stream=None):
         raise TypeError("escale must be a 2-D torch.uint8 tensor")
     R, K = escale.shape[0], escale.shape[1] * 32
     out = _out("out", out, mxfp4_scale_shape(R, K), torch.uint8, escale.device, stream)
-    _check("w4a16_mxfp4_tile_scales", load_library().w4a16_mxfp4_tile_scales(escale.data_ptr(), out.data_ptr(), R, K,
-                                                                              _stream_ptr(stream)))
+    st = load_library().w4a16_mxfp4_tile_scales(escale.data_ptr(), out.data_ptr(), R, K, _stream_ptr(stream))
+    _check("w4a16_mxfp4_tile_scales", st)
     return out
+
+
+def _workspace(given, need: int, device, stream, op):
+    """(address, bytes) of the caller's workspace or the binding's own."""
+    if given is None:
+        if not need:
+            return 0, 0
+        given = _cached_workspace(need, device, stream, op)
+    return given.data_ptr(), given.numel() * given.element_size()
 
 
 def mxfp4_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, workspace=None, stream=None):
@@ -483,24 +507,21 @@ def mxfp4_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, workspace=Non
     mxfp4_quantize(x, 1)) and B [N, K] (a weight, one output feature per row).
     4-bit tensor-core product, FP32 sums; returns y [M, N] in `out_dtype`
     (bfloat16 unless given; float16 and float32 too)."""
-    torch = _torch()
     M, K = _mx_rows("a", a, a_scale)
     N, Kb = _mx_rows("b", b, b_scale)
     if K != Kb:
         raise ValueError(f"a has K = {K}, b has K = {Kb}")
     if out_dtype is None:
-        out_dtype = torch.bfloat16 if out is None else out.dtype
+        out_dtype = _torch().bfloat16 if out is None else out.dtype
     dt = _dtype_code(out_dtype)
     lib = load_library()
-    out = _out("out", out, (M, N), out_dtype, a.device, stream)
-    if workspace is None:
-        need = lib.w4a16_workspace_bytes(OP_MXFP4_MATMUL, M, N, K, 32)
-        workspace = _cached_workspace(need, a.device, stream, OP_MXFP4_MATMUL) if need else None
-    ws_ptr, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(),
-                                                          workspace.numel() * workspace.element_size())
-    _check("w4a16_mxfp4_matmul", lib.w4a16_mxfp4_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(),
-                                                        b_scale.data_ptr(), out.data_ptr(), M, N, K, dt, ws_ptr,
-                                                        ws_bytes, _stream_ptr(stream)))
+    device = a.device
+    out = _out("out", out, (M, N), out_dtype, device, stream)
+    need = lib.w4a16_workspace_bytes(OP_MXFP4_MATMUL, M, N, K, 32) if workspace is None else 0
+    ws_ptr, ws_bytes = _workspace(workspace, need, device, stream, OP_MXFP4_MATMUL)
+    st = lib.w4a16_mxfp4_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr(),
+                                M, N, K, dt, ws_ptr, ws_bytes, _stream_ptr(stream))
+    _check("w4a16_mxfp4_matmul", st)
     return out
 
 
@@ -516,9 +537,9 @@ def mxfp4_moe(x, router, w13, e13, w2, e2, top_k: int, renormalize: bool = True,
     e2 uint8 [E, I/32, H], as mxfp4_quantize(w, 0) makes them of [E, H, 2 I] and
     [E, I, H]. Returns y bf16 [T, H]."""
     torch = _torch()
-    for name, t, dtype, dims in (("x", x, torch.bfloat16, 2), ("router", router, torch.bfloat16, 2),
-                                 ("w13", w13, torch.int32, 3), ("e13", e13, torch.uint8, 3),
-                                 ("w2", w2, torch.int32, 3), ("e2", e2, torch.uint8, 3)):
+    bf16, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+    for name, t, dtype, dims in (("x", x, bf16, 2), ("router", router, bf16, 2), ("w13", w13, i32, 3),
+                                 ("e13", e13, u8, 3), ("w2", w2, i32, 3), ("e2", e2, u8, 3)):
         _cuda_contig(name, t)
         if t.dim() != dims or t.dtype != dtype:
             raise TypeError(f"{name} must be a {dims}-D {dtype} tensor, got {t.dim()}-D {t.dtype}")
@@ -526,18 +547,17 @@ def mxfp4_moe(x, router, w13, e13, w2, e2, top_k: int, renormalize: bool = True,
     E, I = w2.shape[0], w2.shape[1] * 8
     for name, t, shape in (("router", router, (E, H)), ("w13", w13, (E, H // 8, 2 * I)),
                            ("e13", e13, (E, H // 32, 2 * I)), ("w2", w2, (E, I // 8, H)), ("e2", e2, (E, I // 32, H))):
-        if tuple(t.shape) != shape:
+        if t.shape != shape:
             raise ValueError(f"{name} shape {tuple(t.shape)} does not match {shape}")
     lib = load_library()
-    out = _out("out", out, (T, H), torch.bfloat16, x.device, stream)
-    if workspace is None:
-        need = lib.w4a16_mxfp4_moe_workspace_bytes(T, E, top_k, H, I)
-        workspace = _cached_workspace(need, x.device, stream, "mxfp4_moe") if need else None
-    ws_ptr, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(),
-                                                          workspace.numel() * workspace.element_size())
-    _check("w4a16_mxfp4_moe", lib.w4a16_mxfp4_moe(x.data_ptr(), router.data_ptr(), w13.data_ptr(), e13.data_ptr(),
-                                                  w2.data_ptr(), e2.data_ptr(), out.data_ptr(), T, E, top_k, H, I,
-                                                  1 if renormalize else 0, ws_ptr, ws_bytes, _stream_ptr(stream)))
+    device = x.device
+    out = _out("out", out, (T, H), bf16, device, stream)
+    need = lib.w4a16_mxfp4_moe_workspace_bytes(T, E, top_k, H, I) if workspace is None else 0
+    ws_ptr, ws_bytes = _workspace(workspace, need, device, stream, "mxfp4_moe")
+    st = lib.w4a16_mxfp4_moe(x.data_ptr(), router.data_ptr(), w13.data_ptr(), e13.data_ptr(), w2.data_ptr(),
+                             e2.data_ptr(), out.data_ptr(), T, E, top_k, H, I, 1 if renormalize else 0, ws_ptr,
+                             ws_bytes, _stream_ptr(stream))
+    _check("w4a16_mxfp4_moe", st)
     return out
 
 
