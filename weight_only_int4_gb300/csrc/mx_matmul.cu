@@ -41,7 +41,6 @@ constexpr uint32_t kRowBytes = kStepK / 2;  // codes of one row of a step
 constexpr uint32_t kScaleTile = 512;        // exponent bytes of 128 rows x 128 elements
 constexpr int kThreads = 256;
 constexpr int kEpiWarp0 = 4;                // warps 4..7: one tensor-memory lane quarter each
-constexpr uint32_t kSuspendNs = 20000;
 constexpr unsigned long long kWaitLimitCycles = 4000000000ull;   // ~2 s at 2 GHz
 constexpr unsigned int kErrTimeout = 9u;
 
@@ -57,7 +56,9 @@ struct Abort {
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Abort& ab) {
     const unsigned long long t0 = clock64();
     for (;;) {
-        if (mbar_try_wait_suspend(bar, parity, kSuspendNs)) return true;
+        // a few polls between looks at the clock; a thread suspended in its wait wakes up late
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
         if (*ab.flag) return false;
         if (clock64() - t0 > kWaitLimitCycles) {
             *ab.flag = 1;
@@ -140,11 +141,15 @@ __device__ __forceinline__ int step_groups(int groups, int kt) { return min(2, g
 // even CTA's barrier; its MMA thread copies the exponents to tensor memory in
 // both CTAs and issues the pair's MMAs.
 //
-// Tensor memory (512 columns): two 256-column accumulators that overlap by 64
-// columns, [0, 256) and [192, 448), and two exponent buffers of 32 columns. The
-// epilogue reads the shared 64 columns first and then lets the next tile's
+// Tensor memory (512 columns): two 256-column accumulators that overlap by 96
+// columns, [0, 256) and [160, 416), and four exponent buffers of 24 columns.
+// The epilogue reads the shared 96 columns first and then lets the next tile's
 // MMAs start into the other accumulator, so only that read, not the whole
 // epilogue, separates two tiles' MMAs.
+//
+// The MMAs of a step take about 220 ns (measured with the copies left out);
+// what the single threads that feed them do per step has to stay below that, so
+// codes and exponents have a producer thread each and no thread divides.
 namespace pair {
 
 constexpr int BM = 256, BN = 256, CM = 128, CN = 128;
@@ -153,8 +158,12 @@ constexpr uint32_t kABytes = CM * kRowBytes, kBBytes = CN * kRowBytes;
 constexpr uint32_t kSfaBytes = 2 * kScaleTile, kSfbBytes = 4 * kScaleTile;
 constexpr uint32_t kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
 static_assert(kStageBytes % 1024 == 0, "operand tiles stay 1024-byte aligned");
-constexpr uint32_t kAcc1 = 192, kScaleCol = 448, kScaleCols = 32;
+constexpr uint32_t kAcc1 = 160, kScaleCol = kAcc1 + 256, kScaleCols = 24;
+constexpr int kScaleBufs = 4;
+constexpr int kShared = (256 - kAcc1) / 32;   // 32-column chunks of an accumulator that the other one overlaps
 constexpr uint32_t kTmemCols = 512;
+static_assert(kScaleCol + kScaleBufs * kScaleCols == kTmemCols, "tensor memory budget");
+static_assert(kStages > kScaleBufs, "the MMAs that read an exponent buffer retire before their stage's barrier turns twice");
 
 struct __align__(8) Barriers {
     uint64_t full[kStages];     // even CTA: both CTAs' copies landed
@@ -188,7 +197,7 @@ pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
     const int pair_id = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     const int num_m = (M + BM - 1) / BM, num_n = (N + BN - 1) / BN;
     const long long tiles = static_cast<long long>(num_m) * num_n;
-    const int kt_total = (K + kStepK - 1) / kStepK, groups = (K + 127) >> 7;
+    const int kt_total = (K + kStepK - 1) / kStepK;
     const Abort ab{&bars->abort, smem_u32(&bars->abort), rank ^ 1u};
 
     if (threadIdx.x == 0) {
@@ -213,70 +222,89 @@ pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ producer
+    if (warp == 0 || warp == 3) {
+        // ------------------------------------------------------------ producers: codes (warp 0), exponents (warp 3)
         if (lane == 0) {
-            long long j = 0;
+            const int r = static_cast<int>(rank);
+            const uint32_t even = map_to_cta(smem_u32(&bars->full[0]), 0);
+            int s = 0, steps = 0;
+            uint32_t parity = 1u;
             bool ok = true;
             for (long long t = pair_id; t < tiles && ok; t += npairs) {
                 const int m_blk = static_cast<int>(t % num_m), n_blk = static_cast<int>(t / num_m);
-                for (int kt = 0; kt < kt_total; ++kt, ++j) {
-                    const int s = static_cast<int>(j % kStages);
-                    const uint32_t ph = static_cast<uint32_t>(j / kStages) & 1u;
-                    if (!wait_bar(smem_u32(&bars->empty[s]), ph ^ 1u, ab)) { ok = false; break; }
-                    const uint32_t fb = smem_u32(&bars->full[s]);
-                    if (rank == 0) mbar_arrive_expect_tx(fb, 2 * kStageBytes);
-                    const uint32_t even = map_to_cta(fb, 0);
-                    const int r = static_cast<int>(rank);
-                    tma_load_2d_pair(st_a(s), &ta, kt * static_cast<int>(kRowBytes), m_blk * BM + r * CM, even);
-                    tma_load_2d_pair(st_b(s), &tb, kt * static_cast<int>(kRowBytes), n_blk * BN + r * CN, even);
-                    tma_load_2d_pair(st_sfa(s), &tsa, 0, (m_blk * 2 + r) * groups + 2 * kt, even);
-                    tma_load_2d_pair(st_sfb(s), &tsb, 0, n_blk * 2 * groups + 2 * kt, even);
-                    tma_load_2d_pair(st_sfb(s) + 2 * kScaleTile, &tsb, 0, (n_blk * 2 + 1) * groups + 2 * kt, even);
+                const int m0 = m_blk * BM + r * CM, n0 = n_blk * BN + r * CN;
+                for (int kt = 0; kt < kt_total; ++kt) {
+                    if (!wait_bar(smem_u32(&bars->empty[s]), parity, ab)) { ok = false; break; }
+                    const uint32_t bar = even + 8u * s;
+                    if (warp == 0) {
+                        if (r == 0) mbar_arrive_expect_tx(smem_u32(&bars->full[s]), 2 * kStageBytes);
+                        tma_load_2d_pair(st_a(s), &ta, kt * static_cast<int>(kRowBytes), m0, bar);
+                        tma_load_2d_pair(st_b(s), &tb, kt * static_cast<int>(kRowBytes), n0, bar);
+                    } else {
+                        tma_load_3d_pair(st_sfa(s), &tsa, 0, 2 * kt, m_blk * 2 + r, bar);
+                        tma_load_3d_pair(st_sfb(s), &tsb, 0, 2 * kt, n_blk * 2, bar);
+                    }
+                    ++steps;
+                    if (++s == kStages) s = 0, parity ^= 1u;
                 }
             }
             // every step's copies (counted in the even CTA) and commits have arrived
-            if (rank == 0) drain_ring(bars->full, kStages, j);
-            drain_ring(bars->empty, kStages, j);
+            if (rank == 0) drain_ring(bars->full, kStages, steps);
+            drain_ring(bars->empty, kStages, steps);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ exponent copies and MMAs (even CTA)
         if (rank == 0 && lane == 0) {
             constexpr uint32_t kIdesc0 = umma_idesc_mxf4(BM, BN, 0), kIdesc1 = umma_idesc_mxf4(BM, BN, 1);
             constexpr uint16_t kPair = 0x3;
-            long long j = 0;
-            int it = 0;
+            const uint64_t desc_a = sw128_kmajor_desc(st_a(0)), desc_b = sw128_kmajor_desc(st_b(0));
+            const uint64_t desc_sf = scale_copy_desc(st_sfa(0));
+            int s = 0, buf = 0, behind = 0, it = 0;   // behind: the stage used kScaleBufs steps ago
+            uint32_t parity = 0, behind_parity = 0, steps = 0;
             bool ok = true;
             for (long long t = pair_id; t < tiles && ok; t += npairs, ++it) {
                 if (it > 0 && !wait_bar(smem_u32(&bars->tempty), (it - 1) & 1, ab)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem + ((it & 1) ? kAcc1 : 0u);
-                for (int kt = 0; kt < kt_total; ++kt, ++j) {
-                    const int s = static_cast<int>(j % kStages);
-                    if (!wait_bar(smem_u32(&bars->full[s]), static_cast<uint32_t>(j / kStages) & 1u, ab)) {
-                        ok = false;
-                        break;
+                for (int kt = 0; kt < kt_total; ++kt) {
+                    // the MMAs that read this exponent buffer before have retired
+                    if (steps >= kScaleBufs) {
+                        if (!wait_bar(smem_u32(&bars->empty[behind]), behind_parity, ab)) { ok = false; break; }
+                        if (++behind == kStages) behind = 0, behind_parity ^= 1u;
+                    } else {
+                        ++steps;
                     }
-                    // the MMAs that read this exponent buffer two steps ago have retired
-                    if (j >= 2 && !wait_bar(smem_u32(&bars->empty[(j - 2) % kStages]),
-                                            static_cast<uint32_t>((j - 2) / kStages) & 1u, ab)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!wait_bar(smem_u32(&bars->full[s]), parity, ab)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t sfa = tmem + kScaleCol + static_cast<uint32_t>(j & 1) * kScaleCols, sfb = sfa + 8;
-                    const int ng = step_groups(groups, kt), nk = step_mmas(K, kt);
-                    for (int gq = 0; gq < ng; ++gq) {
-                        tmem_cp_scales_pair(sfa + 4 * gq, scale_copy_desc(st_sfa(s) + gq * kScaleTile));
-                        tmem_cp_scales_pair(sfb + 8 * gq, scale_copy_desc(st_sfb(s) + gq * kScaleTile));
-                        tmem_cp_scales_pair(sfb + 8 * gq + 4, scale_copy_desc(st_sfb(s) + (2 + gq) * kScaleTile));
-                    }
-                    const uint64_t adesc = sw128_kmajor_desc(st_a(s)), bdesc = sw128_kmajor_desc(st_b(s));
+                    const uint32_t sfa = tmem + kScaleCol + buf * kScaleCols, sfb = sfa + 8;
+                    const uint64_t off = static_cast<uint64_t>(s) * (kStageBytes >> 4);
+                    const uint64_t a = desc_a + off, b = desc_b + off, sf = desc_sf + off;
+                    // exponent tiles of a stage: A's two groups of 128 along K, then the groups of B's rows 0..127
+                    // and 128..255
+                    constexpr uint32_t kTile = kScaleTile >> 4;
+                    auto copy = [&](int gq) {
+                        tmem_cp_scales_pair(sfa + 4 * gq, sf + gq * kTile);
+                        tmem_cp_scales_pair(sfb + 8 * gq, sf + (2 + gq) * kTile);
+                        tmem_cp_scales_pair(sfb + 8 * gq + 4, sf + (4 + gq) * kTile);
+                    };
                     // 64 elements (32 bytes) further along K inside the swizzle atom
-                    for (int kk = 0; kk < nk; ++kk)
-                        umma_mxf4_pair(d, adesc + 2u * kk, bdesc + 2u * kk, (kk & 1) ? kIdesc1 : kIdesc0,
-                                       sfa + 4 * (kk >> 1), sfb + 8 * (kk >> 1), (kt | kk) != 0);
+                    auto mma = [&](int kk) {
+                        umma_mxf4_pair(d, a + 2u * kk, b + 2u * kk, (kk & 1) ? kIdesc1 : kIdesc0, sfa + 4 * (kk >> 1),
+                                       sfb + 8 * (kk >> 1), (kt | kk) != 0);
+                    };
+                    const int nk = step_mmas(K, kt);
+                    copy(0);
+                    if (nk == 4) {
+                        copy(1);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) mma(kk);
+                    } else {
+                        if (nk > 2) copy(1);
+                        for (int kk = 0; kk < nk; ++kk) mma(kk);
+                    }
                     umma_commit_pair_mc(smem_u32(&bars->empty[s]), kPair);
+                    if (++s == kStages) s = 0, parity ^= 1u;
+                    if (++buf == kScaleBufs) buf = 0;
                 }
                 if (!ok) break;
                 umma_commit_pair_mc(smem_u32(&bars->tfull[it & 1]), kPair);
@@ -297,24 +325,24 @@ pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
             const int m = m_blk * BM + static_cast<int>(rank) * CM + q * 32 + lane;
             const size_t row_at = static_cast<size_t>(m) * N;
             const int n0 = n_blk * BN;
-            // columns shared with the other accumulator first: the last 64 of the even one, the first 64 of the odd
-            const int c0 = (it & 1) ? 0 : 6;
+            // columns shared with the other accumulator first: the last of the even one, the first of the odd
+            const int c0 = (it & 1) ? 0 : 8 - kShared;
             {
-                uint32_t r0[32], r1[32];
-                tmem_ld_32x32b_x32(d + c0 * 32, r0);
-                tmem_ld_32x32b_x32(d + c0 * 32 + 32, r1);
+                uint32_t r[kShared][32];
+#pragma unroll
+                for (int i = 0; i < kShared; ++i) tmem_ld_32x32b_x32(d + (c0 + i) * 32, r[i]);
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(smem_u32(&bars->tempty), 0);
                 if (m < M) {
-                    store_row32<kOut>(y, row_at, n0 + c0 * 32, N, r0);
-                    store_row32<kOut>(y, row_at, n0 + c0 * 32 + 32, N, r1);
+#pragma unroll
+                    for (int i = 0; i < kShared; ++i) store_row32<kOut>(y, row_at, n0 + (c0 + i) * 32, N, r[i]);
                 }
             }
 #pragma unroll 1
-            for (int i = 0; i < 6; ++i) {
-                const int ch = (it & 1) ? i + 2 : i;
+            for (int i = 0; i < 8 - kShared; ++i) {
+                const int ch = (it & 1) ? i + kShared : i;
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(d + ch * 32, r);
                 tmem_wait_ld();
@@ -448,8 +476,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
                 mbar_arrive_expect_tx(fb, C::kStageBytes);
                 tma_load_2d(st_w(s), &tw, kt * static_cast<int>(kRowBytes), n_blk * BN, fb);
                 tma_load_2d(st_x(s), &tx, kt * static_cast<int>(kRowBytes), m_blk * MP, fb);
-                tma_load_2d(st_sw(s), &tsw, 0, n_blk * groups + 2 * kt, fb);
-                tma_load_2d(st_sx(s), &tsx, 0, m_blk * groups + 2 * kt, fb);
+                tma_load_3d(st_sw(s), &tsw, 0, 2 * kt, n_blk, fb);
+                tma_load_3d(st_sx(s), &tsx, 0, 2 * kt, m_blk, fb);
             }
             drain_ring(bars->full, S, j);
             drain_ring(bars->empty, S, j);
@@ -589,10 +617,11 @@ bool encode_codes(CUtensorMap* map, const uint32_t* codes, int rows, int K, int 
                      static_cast<uint64_t>(rows), static_cast<uint64_t>(K / 2), kRowBytes,
                      static_cast<uint32_t>(box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// Exponent tiles as rows of 128 words: boxes of two tiles (one K step of 128 rows).
-bool encode_scales(CUtensorMap* map, const uint8_t* es, int rows, int K) {
-    const uint64_t n = static_cast<uint64_t>((rows + 127) / 128) * ((K + 127) / 128);
-    return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_INT32, es, 128, n, kScaleTile, 128, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+// Exponent tiles [row tile, group of 128 along K, 128 words]: boxes of one K step (two groups) by `tiles` row tiles.
+bool encode_scales(CUtensorMap* map, const uint8_t* es, int rows, int K, int tiles) {
+    const uint64_t groups = static_cast<uint64_t>((K + 127) / 128);
+    return encode_3d(map, CU_TENSOR_MAP_DATA_TYPE_INT32, es, 128, groups, static_cast<uint64_t>((rows + 127) / 128),
+                     kScaleTile, groups * kScaleTile, 128, 2, static_cast<uint32_t>(tiles), CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 template <int kOut>
@@ -631,7 +660,7 @@ cudaError_t launch_pair(const MxMatmulArgs& a, const DeviceProps& dp, cudaStream
         return e;
     CUtensorMap ta, tb, tsa, tsb;
     if (!encode_codes(&ta, a.a, a.M, a.K, pair::CM) || !encode_codes(&tb, a.b, a.N, a.K, pair::CN) ||
-        !encode_scales(&tsa, a.ea, a.M, a.K) || !encode_scales(&tsb, a.eb, a.N, a.K))
+        !encode_scales(&tsa, a.ea, a.M, a.K, 1) || !encode_scales(&tsb, a.eb, a.N, a.K, 2))
         return cudaErrorInvalidValue;
     const long long tiles = static_cast<long long>((a.M + pair::BM - 1) / pair::BM) * ((a.N + pair::BN - 1) / pair::BN);
     cudaLaunchConfig_t cfg = {};
@@ -663,7 +692,7 @@ cudaError_t launch_rows(const MxMatmulArgs& a, float* partials, uint32_t* ticket
         return e;
     CUtensorMap tw, tx, tsw, tsx;
     if (!encode_codes(&tw, a.b, a.N, a.K, rows::BN) || !encode_codes(&tx, a.a, a.M, a.K, MP) ||
-        !encode_scales(&tsw, a.eb, a.N, a.K) || !encode_scales(&tsx, a.ea, a.M, a.K))
+        !encode_scales(&tsw, a.eb, a.N, a.K, 1) || !encode_scales(&tsx, a.ea, a.M, a.K, 1))
         return cudaErrorInvalidValue;
     const long long units = static_cast<long long>((a.M + MP - 1) / MP) * ((a.N + rows::BN - 1) / rows::BN) *
                             ((a.K + kStepK - 1) / kStepK);

@@ -38,4 +38,18 @@ inline bool encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [outer, middle, inner] tensor with its strides in bytes; zero fill as above.
+inline bool encode_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t middle,
+                      uint64_t outer, uint64_t middle_bytes, uint64_t outer_bytes, uint32_t box_inner,
+                      uint32_t box_middle, uint32_t box_outer, CUtensorMapSwizzle swz) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {inner, middle, outer};
+    const cuuint64_t strides[2] = {middle_bytes, outer_bytes};
+    const cuuint32_t box[3] = {box_inner, box_middle, box_outer};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace w4a16
