@@ -53,20 +53,38 @@ struct Abort {
     uint32_t peer;   // cluster rank of the peer, or ~0
 };
 
+__device__ __noinline__ bool give_up(const Abort& ab) {
+    *ab.flag = 1;
+    if (ab.peer != ~0u) st_cluster_u32(ab.addr, ab.peer, 1u);
+    atomicOr(&g_mx_matmul_error, 1u << kErrTimeout);
+    return false;
+}
+
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Abort& ab) {
+    if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = clock64();
     for (;;) {
         // a few polls between looks at the clock; a thread suspended in its wait wakes up late
         for (int i = 0; i < 32; ++i)
             if (mbar_try_wait(bar, parity)) return true;
         if (*ab.flag) return false;
-        if (clock64() - t0 > kWaitLimitCycles) {
-            *ab.flag = 1;
-            if (ab.peer != ~0u) st_cluster_u32(ab.addr, ab.peer, 1u);
-            atomicOr(&g_mx_matmul_error, 1u << kErrTimeout);
-            return false;
-        }
+        if (clock64() - t0 > kWaitLimitCycles) return give_up(ab);
     }
+}
+
+// The same for a converged warp that goes on together: one lane polls and a vote
+// spreads the verdict, which the compiler knows to be uniform. The warp that
+// issues tensor-core instructions waits this way, so that their operands stay in
+// uniform registers: under a single-lane branch every instruction moves its
+// operands there first, 65 cycles each (measured), more than the copies and
+// MMAs themselves take.
+__device__ __forceinline__ bool uniform_wait_bar(uint32_t bar, uint32_t parity, const Abort& ab, bool leader) {
+    bool done = true;
+    if (leader) done = mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, done)) return true;
+    bool ok = true;
+    if (leader) ok = wait_bar(bar, parity, ab);
+    return __all_sync(0xffffffffu, ok);
 }
 
 // Lane 0 waits; the shuffle orders the other lanes' accesses after its acquire.
@@ -128,9 +146,8 @@ __device__ __forceinline__ void store_row32(void* y, size_t row_at, int n, int N
     }
 }
 
-// MMAs (64 deep) and exponent tiles (128 deep) of a K step.
+// MMAs (64 deep) of a K step.
 __device__ __forceinline__ int step_mmas(int K, int kt) { return min(4, (K - kt * kStepK + 63) >> 6); }
-__device__ __forceinline__ int step_groups(int groups, int kt) { return min(2, groups - 2 * kt); }
 
 // ---------------------------------------------------------------------------
 // CTA pairs, 256 x 256 tiles
@@ -148,8 +165,9 @@ __device__ __forceinline__ int step_groups(int groups, int kt) { return min(2, g
 // epilogue, separates two tiles' MMAs.
 //
 // The MMAs of a step take about 220 ns (measured with the copies left out);
-// what the single threads that feed them do per step has to stay below that, so
-// codes and exponents have a producer thread each and no thread divides.
+// what the warps that feed them do per step has to stay below that, so codes
+// and exponents have a producer thread each, no thread divides, and the MMA warp
+// stays converged (uniform_wait_bar).
 namespace pair {
 
 constexpr int BM = 256, BN = 256, CM = 128, CN = 128;
@@ -254,27 +272,29 @@ pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ exponent copies and MMAs (even CTA)
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             constexpr uint32_t kIdesc0 = umma_idesc_mxf4(BM, BN, 0), kIdesc1 = umma_idesc_mxf4(BM, BN, 1);
             constexpr uint16_t kPair = 0x3;
+            const bool leader = elect_one();
             const uint64_t desc_a = sw128_kmajor_desc(st_a(0)), desc_b = sw128_kmajor_desc(st_b(0));
             const uint64_t desc_sf = scale_copy_desc(st_sfa(0));
+            const uint32_t bar_full = smem_u32(&bars->full[0]), bar_empty = smem_u32(&bars->empty[0]);
             int s = 0, buf = 0, behind = 0, it = 0;   // behind: the stage used kScaleBufs steps ago
             uint32_t parity = 0, behind_parity = 0, steps = 0;
             bool ok = true;
             for (long long t = pair_id; t < tiles && ok; t += npairs, ++it) {
-                if (it > 0 && !wait_bar(smem_u32(&bars->tempty), (it - 1) & 1, ab)) { ok = false; break; }
+                if (it > 0 && !uniform_wait_bar(smem_u32(&bars->tempty), (it - 1) & 1, ab, leader)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem + ((it & 1) ? kAcc1 : 0u);
                 for (int kt = 0; kt < kt_total; ++kt) {
                     // the MMAs that read this exponent buffer before have retired
                     if (steps >= kScaleBufs) {
-                        if (!wait_bar(smem_u32(&bars->empty[behind]), behind_parity, ab)) { ok = false; break; }
+                        if (!uniform_wait_bar(bar_empty + 8 * behind, behind_parity, ab, leader)) { ok = false; break; }
                         if (++behind == kStages) behind = 0, behind_parity ^= 1u;
                     } else {
                         ++steps;
                     }
-                    if (!wait_bar(smem_u32(&bars->full[s]), parity, ab)) { ok = false; break; }
+                    if (!uniform_wait_bar(bar_full + 8 * s, parity, ab, leader)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t sfa = tmem + kScaleCol + buf * kScaleCols, sfb = sfa + 8;
                     const uint64_t off = static_cast<uint64_t>(s) * (kStageBytes >> 4);
@@ -282,35 +302,35 @@ pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
                     // exponent tiles of a stage: A's two groups of 128 along K, then the groups of B's rows 0..127
                     // and 128..255
                     constexpr uint32_t kTile = kScaleTile >> 4;
-                    auto copy = [&](int gq) {
-                        tmem_cp_scales_pair(sfa + 4 * gq, sf + gq * kTile);
-                        tmem_cp_scales_pair(sfb + 8 * gq, sf + (2 + gq) * kTile);
-                        tmem_cp_scales_pair(sfb + 8 * gq + 4, sf + (4 + gq) * kTile);
-                    };
-                    // 64 elements (32 bytes) further along K inside the swizzle atom
-                    auto mma = [&](int kk) {
-                        umma_mxf4_pair(d, a + 2u * kk, b + 2u * kk, (kk & 1) ? kIdesc1 : kIdesc0, sfa + 4 * (kk >> 1),
-                                       sfb + 8 * (kk >> 1), (kt | kk) != 0);
-                    };
                     const int nk = step_mmas(K, kt);
-                    copy(0);
-                    if (nk == 4) {
-                        copy(1);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) mma(kk);
-                    } else {
-                        if (nk > 2) copy(1);
-                        for (int kk = 0; kk < nk; ++kk) mma(kk);
+                    if (leader) {
+                        tmem_cp_scales_pair(sfa, sf);
+                        tmem_cp_scales_pair(sfb, sf + 2 * kTile);
+                        tmem_cp_scales_pair(sfb + 4, sf + 4 * kTile);
+                        if (nk > 2) {
+                            tmem_cp_scales_pair(sfa + 4, sf + kTile);
+                            tmem_cp_scales_pair(sfb + 8, sf + 3 * kTile);
+                            tmem_cp_scales_pair(sfb + 12, sf + 5 * kTile);
+                        }
+                        // 64 elements (32 bytes) further along K inside the swizzle atom
+                        umma_mxf4_pair(d, a, b, kIdesc0, sfa, sfb, kt != 0);
+                        if (nk > 1) umma_mxf4_pair(d, a + 2, b + 2, kIdesc1, sfa, sfb, 1);
+                        if (nk > 2) umma_mxf4_pair(d, a + 4, b + 4, kIdesc0, sfa + 4, sfb + 8, 1);
+                        if (nk > 3) umma_mxf4_pair(d, a + 6, b + 6, kIdesc1, sfa + 4, sfb + 8, 1);
+                        umma_commit_pair_mc(bar_empty + 8 * s, kPair);
                     }
-                    umma_commit_pair_mc(smem_u32(&bars->empty[s]), kPair);
+                    __syncwarp();
                     if (++s == kStages) s = 0, parity ^= 1u;
                     if (++buf == kScaleBufs) buf = 0;
                 }
                 if (!ok) break;
-                umma_commit_pair_mc(smem_u32(&bars->tfull[it & 1]), kPair);
+                if (leader) umma_commit_pair_mc(smem_u32(&bars->tfull[it & 1]), kPair);
+                __syncwarp();
             }
-            umma_commit_pair(smem_u32(&bars->drain));
-            drain_ring(&bars->drain, 1, 1);
+            if (leader) {
+                umma_commit_pair(smem_u32(&bars->drain));
+                drain_ring(&bars->drain, 1, 1);
+            }
         }
     } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------------ epilogue
@@ -427,7 +447,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int num_m = (M + MP - 1) / MP, num_n = (N + BN - 1) / BN;
-    const int kt_total = (K + kStepK - 1) / kStepK, groups = (K + 127) >> 7;
+    const int kt_total = (K + kStepK - 1) / kStepK;
     const int G = gridDim.x;
     const long long U = static_cast<long long>(num_m) * num_n * kt_total;
     const long long u_begin = first_unit(blockIdx.x, U, G), u_end = first_unit(blockIdx.x + 1ll, U, G);
@@ -461,66 +481,78 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
-            long long j = 0;
+            int s = 0, steps = 0;
+            uint32_t parity = 1u;
             bool ok = true;
-            for (long long u = u_begin; u < u_end; ++u, ++j) {
-                const long long t = u / kt_total;
-                const int kt = static_cast<int>(u - t * kt_total);
-                const int m_blk = static_cast<int>(t % num_m), n_blk = static_cast<int>(t / num_m);
-                const int s = static_cast<int>(j % S);
-                if (!wait_bar(smem_u32(&bars->empty[s]), (static_cast<uint32_t>(j / S) & 1u) ^ 1u, ab)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t fb = smem_u32(&bars->full[s]);
-                mbar_arrive_expect_tx(fb, C::kStageBytes);
-                tma_load_2d(st_w(s), &tw, kt * static_cast<int>(kRowBytes), n_blk * BN, fb);
-                tma_load_2d(st_x(s), &tx, kt * static_cast<int>(kRowBytes), m_blk * MP, fb);
-                tma_load_3d(st_sw(s), &tsw, 0, 2 * kt, n_blk, fb);
-                tma_load_3d(st_sx(s), &tsx, 0, 2 * kt, m_blk, fb);
-            }
-            drain_ring(bars->full, S, j);
-            drain_ring(bars->empty, S, j);
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ exponent copies and MMAs
-        if (lane == 0) {
-            constexpr uint32_t kIdesc0 = umma_idesc_mxf4(BN, MP, 0), kIdesc1 = umma_idesc_mxf4(BN, MP, 1);
-            long long j = 0;
-            int seg = 0;
-            bool ok = true;
-            for (long long u = u_begin; u < u_end && ok; ++seg) {
+            for (long long u = u_begin; u < u_end && ok;) {
                 const long long t = u / kt_total;
                 const int k0 = static_cast<int>(u - t * kt_total);
                 const int k1 = static_cast<int>(std::min<long long>(kt_total, k0 + (u_end - u)));
-                const int acc = seg & 1;
-                if (!wait_bar(smem_u32(&bars->tempty[acc]), ((seg >> 1) & 1) ^ 1, ab)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t d = tmem + acc * C::kAccCols;
-                for (int kt = k0; kt < k1; ++kt, ++j) {
-                    const int s = static_cast<int>(j % S);
-                    if (!wait_bar(smem_u32(&bars->full[s]), static_cast<uint32_t>(j / S) & 1u, ab)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    // one exponent buffer per stage: the MMAs that read it retired before the stage was refilled
-                    const uint32_t sfw = tmem + C::kScaleCol + 16 * s, sfx = sfw + 8;
-                    const int ng = step_groups(groups, kt), nk = step_mmas(K, kt);
-                    for (int gq = 0; gq < ng; ++gq) {
-                        tmem_cp_scales(sfw + 4 * gq, scale_copy_desc(st_sw(s) + gq * kScaleTile));
-                        tmem_cp_scales(sfx + 4 * gq, scale_copy_desc(st_sx(s) + gq * kScaleTile));
-                    }
-                    const uint64_t wdesc = sw128_kmajor_desc(st_w(s)), xdesc = sw128_kmajor_desc(st_x(s));
-                    for (int kk = 0; kk < nk; ++kk)
-                        umma_mxf4(d, wdesc + 2u * kk, xdesc + 2u * kk, (kk & 1) ? kIdesc1 : kIdesc0,
-                                  sfw + 4 * (kk >> 1), sfx + 4 * (kk >> 1), kt != k0 || kk != 0);
-                    umma_commit(smem_u32(&bars->empty[s]));
+                const int m_blk = static_cast<int>(t % num_m), n_blk = static_cast<int>(t / num_m);
+                for (int kt = k0; kt < k1; ++kt) {
+                    if (!wait_bar(smem_u32(&bars->empty[s]), parity, ab)) { ok = false; break; }
+                    const uint32_t fb = smem_u32(&bars->full[s]);
+                    mbar_arrive_expect_tx(fb, C::kStageBytes);
+                    tma_load_2d(st_w(s), &tw, kt * static_cast<int>(kRowBytes), n_blk * BN, fb);
+                    tma_load_2d(st_x(s), &tx, kt * static_cast<int>(kRowBytes), m_blk * MP, fb);
+                    tma_load_3d(st_sw(s), &tsw, 0, 2 * kt, n_blk, fb);
+                    tma_load_3d(st_sx(s), &tsx, 0, 2 * kt, m_blk, fb);
+                    ++steps;
+                    if (++s == S) s = 0, parity ^= 1u;
                 }
-                if (!ok) break;
-                umma_commit(smem_u32(&bars->tfull[acc]));
                 u += k1 - k0;
             }
+            drain_ring(bars->full, S, steps);
+            drain_ring(bars->empty, S, steps);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ exponent copies and MMAs
+        constexpr uint32_t kIdesc0 = umma_idesc_mxf4(BN, MP, 0), kIdesc1 = umma_idesc_mxf4(BN, MP, 1);
+        const bool leader = elect_one();
+        const uint64_t desc_w = sw128_kmajor_desc(st_w(0)), desc_x = sw128_kmajor_desc(st_x(0));
+        const uint64_t desc_sf = scale_copy_desc(st_sw(0));
+        const uint32_t bar_full = smem_u32(&bars->full[0]), bar_empty = smem_u32(&bars->empty[0]);
+        int s = 0, seg = 0;
+        uint32_t parity = 0;
+        bool ok = true;
+        for (long long u = u_begin; u < u_end && ok; ++seg) {
+            const int k0 = static_cast<int>(u % kt_total);
+            const int k1 = static_cast<int>(std::min<long long>(kt_total, k0 + (u_end - u)));
+            const int acc = seg & 1;
+            if (!uniform_wait_bar(smem_u32(&bars->tempty[acc]), ((seg >> 1) & 1) ^ 1, ab, leader)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t d = tmem + acc * C::kAccCols;
+            for (int kt = k0; kt < k1; ++kt) {
+                if (!uniform_wait_bar(bar_full + 8 * s, parity, ab, leader)) { ok = false; break; }
+                tc_fence_after();
+                // one exponent buffer per stage: the MMAs that read it retired before the stage was refilled
+                const uint32_t sfw = tmem + C::kScaleCol + 16 * s, sfx = sfw + 8;
+                const uint64_t off = static_cast<uint64_t>(s) * (C::kStageBytes >> 4);
+                const uint64_t w = desc_w + off, x = desc_x + off, sf = desc_sf + off;
+                constexpr uint32_t kTile = kScaleTile >> 4;
+                const int nk = step_mmas(K, kt);
+                if (leader) {
+                    tmem_cp_scales(sfw, sf);
+                    tmem_cp_scales(sfx, sf + 2 * kTile);
+                    if (nk > 2) {
+                        tmem_cp_scales(sfw + 4, sf + kTile);
+                        tmem_cp_scales(sfx + 4, sf + 3 * kTile);
+                    }
+                    umma_mxf4(d, w, x, kIdesc0, sfw, sfx, kt != k0);
+                    if (nk > 1) umma_mxf4(d, w + 2, x + 2, kIdesc1, sfw, sfx, 1);
+                    if (nk > 2) umma_mxf4(d, w + 4, x + 4, kIdesc0, sfw + 4, sfx + 4, 1);
+                    if (nk > 3) umma_mxf4(d, w + 6, x + 6, kIdesc1, sfw + 4, sfx + 4, 1);
+                    umma_commit(bar_empty + 8 * s);
+                }
+                __syncwarp();
+                if (++s == S) s = 0, parity ^= 1u;
+            }
+            if (!ok) break;
+            if (leader) umma_commit(smem_u32(&bars->tfull[acc]));
+            __syncwarp();
+            u += k1 - k0;
+        }
+        if (leader) {
             umma_commit(smem_u32(&bars->drain));
             drain_ring(&bars->drain, 1, 1);
         }

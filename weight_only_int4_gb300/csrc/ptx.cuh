@@ -57,6 +57,13 @@ __device__ __forceinline__ bool mbar_try_wait_suspend(uint32_t bar, uint32_t par
     return ok != 0;
 }
 
+// One lane of a converged warp (the same on every call).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 // ---------------------------------------------------------------------------
 // TMA (tiled tensor copies, global -> shared, completion on an mbarrier)
 // ---------------------------------------------------------------------------
