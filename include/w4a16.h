@@ -417,13 +417,13 @@ w4a16_status w4a16_mxfp4_tile_scales(const uint8_t* src, uint8_t* dst, int64_t r
  * 255 makes every y of its row (of A) or column (of B) NaN. Exponents whose
  * product leaves the FP32 range overflow to infinity or flush to zero.
  *
- * Many tiles of 256 x 256 run on CTA pairs; otherwise (always for M <= 128) a
- * kernel with 128 rows of B per tile splits its K steps evenly over the SMs and
- * needs a workspace of w4a16_workspace_bytes(W4A16_OP_MXFP4_MATMUL, M, N, K, 32)
- * bytes, with the ownership and zero-fill rules of w4a16_gemv's; a workspace of
- * this op serves this op only. Tiles shared by several CTAs are summed in a
- * fixed order: the result is deterministic. After a W4A16_ERR_TIMEOUT reported
- * by w4a16_device_status, zero the workspace again.
+ * Large products run on CTA pairs (256 x 256 tiles); the others (always for
+ * M <= 128) on a kernel with 128 rows of B per tile that may split tiles between
+ * CTAs and takes a workspace of w4a16_workspace_bytes(W4A16_OP_MXFP4_MATMUL, M,
+ * N, K, 32) bytes (0: none needed), with the ownership and zero-fill rules of
+ * w4a16_gemv's; a workspace of this op serves this op only. Split tiles are
+ * summed in a fixed order: the result is deterministic. After a
+ * W4A16_ERR_TIMEOUT reported by w4a16_device_status, zero the workspace again.
  *
  * M >= 1, N % 8 == 0, K % 32 == 0. Launched with programmatic stream
  * serialization: its prologue (barriers, tensor memory) may overlap the end of

@@ -68,16 +68,25 @@ def test_few_rows(M, dtype):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 8, 32), (1, 128, 64), (3, 136, 96), (16, 16, 128), (5, 264, 160), (130, 8, 224),
-                                   (2, 40, 256), (1, 2048, 4128), (20, 20480, 288)])
+                                   (2, 40, 256), (1, 2048, 4128), (20, 20480, 288), (9, 43008, 512),
+                                   (40, 30000, 320), (500, 4096, 160)])
 def test_small_and_odd(M, N, K):
     check(Operand(M, K, 3), Operand(N, K, 4), torch.float32, (M, N, K))
+
+
+@pytest.mark.parametrize("dtype", list(ULP))
+@pytest.mark.parametrize("M,N,K", [(1, 1000, 8224), (16, 2048, 5376), (17, 5376, 4128), (50, 264, 12000),
+                                   (100, 1288, 9120), (200, 640, 6176)])
+def test_few_tiles_of_a_long_k(M, N, K, dtype):
+    """K split over the CTAs of a cluster, in equal and unequal parts, for every row template."""
+    check(Operand(M, K, 16), Operand(N, K, 17), dtype, (M, N, K))
 
 
 @pytest.mark.parametrize("dtype", list(ULP))
 @pytest.mark.parametrize("M,N,K", [(2560, 2560, 512), (1032, 5000, 288), (513, 8008, 1056), (4100, 1288, 64),
                                    (2300, 4360, 2080)])
 def test_many_tiles(M, N, K, dtype):
-    """Enough 256 x 256 tiles for CTA pairs: one and several tiles per pair, tails in M, N and K, an odd number of 128-row tiles."""
+    """256 x 256 tiles for most CTA pairs: one and several per pair, tails in M, N and K, odd numbers of 128-row tiles."""
     check(Operand(M, K, 5), Operand(N, K, 6), dtype, (M, N, K))
 
 

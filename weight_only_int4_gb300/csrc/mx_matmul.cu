@@ -16,8 +16,10 @@
 //
 // Two kernels:
 //   pair_kernel  CTA pairs own 256 x 256 tiles of y (cta_group::2).
-//   rows_kernel  128 rows of B against 16..128 rows of A, its work split
-//                stream-K over (tile, K step) units: what has few tiles.
+//   rows_kernel  128 rows of B against 16..128 rows of A per CTA: what has few
+//                tiles of that size. K is split over a cluster, or the (tile, K
+//                step) units over all CTAs, where whole tiles would leave SMs
+//                idle.
 //
 // Every mbarrier wait is bounded (about two seconds). On expiry the kernel
 // records the timeout in a device word, raises the abort flag, every role
@@ -181,7 +183,7 @@ constexpr int kScaleBufs = 4;
 constexpr int kShared = (256 - kAcc1) / 32;   // 32-column chunks of an accumulator that the other one overlaps
 constexpr uint32_t kTmemCols = 512;
 static_assert(kScaleCol + kScaleBufs * kScaleCols == kTmemCols, "tensor memory budget");
-static_assert(kStages > kScaleBufs, "the MMAs that read an exponent buffer retire before their stage's barrier turns twice");
+static_assert(kStages > kScaleBufs, "a stage's barrier turns once between the uses of an exponent buffer");
 
 struct __align__(8) Barriers {
     uint64_t full[kStages];     // even CTA: both CTAs' copies landed
@@ -283,7 +285,10 @@ pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
             uint32_t parity = 0, behind_parity = 0, steps = 0;
             bool ok = true;
             for (long long t = pair_id; t < tiles && ok; t += npairs, ++it) {
-                if (it > 0 && !uniform_wait_bar(smem_u32(&bars->tempty), (it - 1) & 1, ab, leader)) { ok = false; break; }
+                if (it > 0 && !uniform_wait_bar(smem_u32(&bars->tempty), (it - 1) & 1, ab, leader)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
                 const uint32_t d = tmem + ((it & 1) ? kAcc1 : 0u);
                 for (int kt = 0; kt < kt_total; ++kt) {
@@ -386,10 +391,16 @@ pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
 // few rows of A: 128 rows of B per tile, stream-K
 // ---------------------------------------------------------------------------
 // The tile's 128 rows of B are the MMA's M, MP rows of A its N: with few rows
-// of A the kernel streams B and is bound by HBM bandwidth, so every SM gets the
-// same number of K steps whatever the number of tiles. A tile shared by several
-// CTAs is finished by the last of them (a ticket per tile and epilogue warp),
-// which adds their FP32 partial tiles in ascending CTA order: deterministic.
+// of A the kernel streams B and is bound by HBM bandwidth, or by the latency of
+// a tile's K steps (about 0.29 us each, with a ring of 6..10 steps) where few
+// tiles leave SMs idle. Three ways to hand out the work:
+//   whole tiles, one or more per CTA;
+//   split > 1: a cluster of `split` CTAs per tile, each a part of K; the parts
+//     are added from the CTAs' shared memory, in the order of K;
+//   share: equal ranges of (tile, K step) units; a tile shared by several CTAs
+//     is finished by the last of them (a ticket per tile and epilogue warp),
+//     which adds their FP32 parts from global memory in ascending CTA order.
+// All three are deterministic.
 namespace rows {
 
 constexpr int BN = 128;
@@ -423,7 +434,7 @@ constexpr size_t smem_bytes() {
     return 1024 + Cfg<MP>::kStages * Cfg<MP>::kStageBytes + sizeof(Barriers<MP>);
 }
 
-// CTA b of G owns units [b U / G, (b + 1) U / G); the owner of unit u.
+// CTA b of G owns units [b U / G, (b + 1) U / G) (tiles where none are shared); the owner of unit u.
 __device__ __forceinline__ long long first_unit(long long b, long long U, int G) { return b * U / G; }
 __device__ __forceinline__ int unit_owner(long long u, long long U, int G) {
     return static_cast<int>(((u + 1) * G - 1) / U);
@@ -433,7 +444,8 @@ template <int kOut, int MP>
 __global__ void __launch_bounds__(kThreads, 1)
 rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
             const __grid_constant__ CUtensorMap tsw, const __grid_constant__ CUtensorMap tsx, void* __restrict__ y,
-            int M, int N, int K, float* __restrict__ partials, uint32_t* __restrict__ tickets) {
+            int M, int N, int K, int split, int share, float* __restrict__ partials,
+            uint32_t* __restrict__ tickets) {
     using C = Cfg<MP>;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -444,13 +456,25 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
     auto st_x = [&](int s) { return base + s * C::kStageBytes + C::kABytes; };
     auto st_sw = [&](int s) { return base + s * C::kStageBytes + C::kABytes + C::kXBytes; };
     auto st_sx = [&](int s) { return st_sw(s) + 2 * kScaleTile; };
+    // split > 1: this CTA's part, [row of A][128], once the ring is idle
+    float* parts = reinterpret_cast<float*>(smem);
+    static_assert(MP * 128 * 4 <= S * C::kStageBytes, "a part fits the ring");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int num_m = (M + MP - 1) / MP, num_n = (N + BN - 1) / BN;
     const int kt_total = (K + kStepK - 1) / kStepK;
     const int G = gridDim.x;
-    const long long U = static_cast<long long>(num_m) * num_n * kt_total;
-    const long long u_begin = first_unit(blockIdx.x, U, G), u_end = first_unit(blockIdx.x + 1ll, U, G);
+    const long long T = static_cast<long long>(num_m) * num_n, U = T * kt_total;
+    const int part_k = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    long long u_begin, u_end;
+    if (split > 1) {
+        const long long first = static_cast<long long>(blockIdx.x / split) * kt_total;
+        u_begin = first + static_cast<long long>(part_k) * kt_total / split;
+        u_end = first + static_cast<long long>(part_k + 1) * kt_total / split;
+    } else {
+        u_begin = share ? first_unit(blockIdx.x, U, G) : first_unit(blockIdx.x, T, G) * kt_total;
+        u_end = share ? first_unit(blockIdx.x + 1ll, U, G) : first_unit(blockIdx.x + 1ll, T, G) * kt_total;
+    }
     const Abort ab{&bars->abort, 0u, ~0u};
 
     if (threadIdx.x == 0) {
@@ -496,7 +520,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
                     tma_load_2d(st_w(s), &tw, kt * static_cast<int>(kRowBytes), n_blk * BN, fb);
                     tma_load_2d(st_x(s), &tx, kt * static_cast<int>(kRowBytes), m_blk * MP, fb);
                     tma_load_3d(st_sw(s), &tsw, 0, 2 * kt, n_blk, fb);
-                    tma_load_3d(st_sx(s), &tsx, 0, 2 * kt, m_blk, fb);
+                    tma_load_3d(st_sx(s), &tsx, 0, 2 * kt, m_blk * MP / 128, fb);
                     ++steps;
                     if (++s == S) s = 0, parity ^= 1u;
                 }
@@ -519,9 +543,15 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
             const int k0 = static_cast<int>(u % kt_total);
             const int k1 = static_cast<int>(std::min<long long>(kt_total, k0 + (u_end - u)));
             const int acc = seg & 1;
-            if (!uniform_wait_bar(smem_u32(&bars->tempty[acc]), ((seg >> 1) & 1) ^ 1, ab, leader)) { ok = false; break; }
+            if (!uniform_wait_bar(smem_u32(&bars->tempty[acc]), ((seg >> 1) & 1) ^ 1, ab, leader)) {
+                ok = false;
+                break;
+            }
             tc_fence_after();
             const uint32_t d = tmem + acc * C::kAccCols;
+            // exponents of 32 rows per column: where the tile's rows begin in their 128-row exponent tile (fewer
+            // than 32 rows of A per tile only come as the first)
+            const uint32_t x_col = static_cast<uint32_t>(u / kt_total % num_m) * MP % 128 / 32;
             for (int kt = k0; kt < k1; ++kt) {
                 if (!uniform_wait_bar(bar_full + 8 * s, parity, ab, leader)) { ok = false; break; }
                 tc_fence_after();
@@ -538,10 +568,11 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
                         tmem_cp_scales(sfw + 4, sf + kTile);
                         tmem_cp_scales(sfx + 4, sf + 3 * kTile);
                     }
-                    umma_mxf4(d, w, x, kIdesc0, sfw, sfx, kt != k0);
-                    if (nk > 1) umma_mxf4(d, w + 2, x + 2, kIdesc1, sfw, sfx, 1);
-                    if (nk > 2) umma_mxf4(d, w + 4, x + 4, kIdesc0, sfw + 4, sfx + 4, 1);
-                    if (nk > 3) umma_mxf4(d, w + 6, x + 6, kIdesc1, sfw + 4, sfx + 4, 1);
+                    const uint32_t x0 = sfx + x_col, x1 = x0 + 4;
+                    umma_mxf4(d, w, x, kIdesc0, sfw, x0, kt != k0);
+                    if (nk > 1) umma_mxf4(d, w + 2, x + 2, kIdesc1, sfw, x0, 1);
+                    if (nk > 2) umma_mxf4(d, w + 4, x + 4, kIdesc0, sfw + 4, x1, 1);
+                    if (nk > 3) umma_mxf4(d, w + 6, x + 6, kIdesc1, sfw + 4, x1, 1);
                     umma_commit(bar_empty + 8 * s);
                 }
                 __syncwarp();
@@ -574,13 +605,19 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
             const int n = static_cast<int>(t / num_m) * BN + q * 32 + lane;
             const bool whole = k0 == 0 && k1 == kt_total;
             // slot 1: the tile begins here; slot 0: an earlier CTA began it
-            float* part = partials + (static_cast<size_t>(blockIdx.x) * 2 + (k0 == 0 ? 1 : 0)) * kSlotFloats + q * 32 + lane;
+            float* part =
+                partials + (static_cast<size_t>(blockIdx.x) * 2 + (k0 == 0 ? 1 : 0)) * kSlotFloats + q * 32 + lane;
 #pragma unroll 1
             for (int ch = 0; ch * 32 < mc; ++ch) {
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(tmem + lanes + acc * C::kAccCols + ch * 32, r);
                 tmem_wait_ld();
-                if (whole) {
+                if (split > 1) {
+                    // the ring is idle: this CTA's copies have landed and its MMAs have read them
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (ch * 32 + i < mc) parts[(ch * 32 + i) * 128 + q * 32 + lane] = __uint_as_float(r[i]);
+                } else if (whole) {
                     if (n < N) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -596,7 +633,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc]));
-            if (whole) continue;
+            if (whole || split > 1) continue;
             const long long first = t * kt_total;
             const int b_lo = unit_owner(first, U, G), b_hi = unit_owner(first + kt_total - 1, U, G);
             __threadfence();
@@ -631,7 +668,25 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
 
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    if (split > 1) {
+        cluster_sync();   // every part of the tile is in its CTA's shared memory
+        const long long t = blockIdx.x / split;
+        const int m0 = static_cast<int>(t % num_m) * MP, mc = min(MP, M - m0);
+        const int col = threadIdx.x & 127, n = static_cast<int>(t / num_m) * BN + col;
+        const uint32_t at = smem_u32(parts) + 4u * col;
+        for (int m = 2 * part_k + (threadIdx.x >> 7); m < mc; m += 2 * split) {
+            float v[8], sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] = c < split ? ld_cluster_f32(at + 512u * m, c) : 0.f;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < split) sum += v[c];
+            if (n < N) store1<kOut>(y, static_cast<size_t>(m0 + m) * N + n, sum);
+        }
+        cluster_sync();   // no CTA leaves while another may read its part
+    } else {
+        __syncthreads();
+    }
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
@@ -654,6 +709,33 @@ bool encode_scales(CUtensorMap* map, const uint8_t* es, int rows, int K, int til
     const uint64_t groups = static_cast<uint64_t>((K + 127) / 128);
     return encode_3d(map, CU_TENSOR_MAP_DATA_TYPE_INT32, es, 128, groups, static_cast<uint64_t>((rows + 127) / 128),
                      kScaleTile, groups * kScaleTile, 128, 2, static_cast<uint32_t>(tiles), CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+struct Plan {
+    int mp;       // rows of A per tile; 0: the pair kernel
+    int split;    // CTAs of a cluster per tile
+    bool share;   // tiles split between CTAs by units
+};
+
+// Measured on 152 SMs (us; whole tiles unless said):
+//   pair kernel against 128-row tiles: 1024 x 2560 x 5376 (160 tiles) 14.4 / 17.1, 200 x 16384 x 5376 (256) 14.8 /
+//     17.5, 512 x 4096 x 4096 (128) 11.8 / 9.3, 700 x 2560 x 5376 (120) 14.1 / 10.6: the pair kernel where 128-row
+//     tiles need a second wave;
+//   64-row against 128-row tiles: 300 x 2600 x 2080 (63 tiles of 128) 6.6 / 7.6, 128 x 6144 x 2048 (48) 6.3 / 6.6,
+//     512 x 4096 x 4096 (128) 13.5 / 9.3: 64 where both kinds fit one wave;
+//   shared units against whole tiles: 16 x 43008 x 5376 (336 tiles) 26.0 / 28.0, 32 rows 27.3 / 27.9, but 64 rows
+//     31.2 / 27.7 and everything that fits one wave slower: up to 32 rows, where the last wave is mostly idle.
+Plan plan(long long M, long long N, long long K, const DeviceProps& dp) {
+    const long long cols = (N + rows::BN - 1) / rows::BN, steps = (K + kStepK - 1) / kStepK;
+    const long long tiles128 = ((M + 127) / 128) * cols;
+    if (M > 128 && tiles128 > dp.sms) return {0, 1, false};
+    const int mp = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 || 2 * tiles128 <= dp.sms ? 64 : 128;
+    const long long tiles = ((M + mp - 1) / mp) * cols;
+    // a step saved is worth about 0.29 us, a cluster's sum and its ordinary launch cost about 3 us
+    const long long split = std::min<long long>({8, dp.sms / tiles, steps / 4});
+    if (split > 1 && steps - steps / split >= 12) return {mp, static_cast<int>(split), false};
+    const long long waves = (tiles + dp.sms - 1) / dp.sms;
+    return {mp, 1, mp <= 32 && tiles > dp.sms && waves * dp.sms * 100 > tiles * 115};
 }
 
 template <int kOut>
@@ -696,7 +778,8 @@ cudaError_t launch_pair(const MxMatmulArgs& a, const DeviceProps& dp, cudaStream
         return cudaErrorInvalidValue;
     const long long tiles = static_cast<long long>((a.M + pair::BM - 1) / pair::BM) * ((a.N + pair::BN - 1) / pair::BN);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::max<long long>(1, std::min<long long>(tiles, resident_pairs<kOut>(dp)))));
+    const long long pairs = std::max<long long>(1, std::min<long long>(tiles, resident_pairs<kOut>(dp)));
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = pair::kSmemBytes;
     cfg.stream = s;
@@ -715,8 +798,8 @@ cudaError_t launch_pair(const MxMatmulArgs& a, const DeviceProps& dp, cudaStream
 }
 
 template <int kOut, int MP>
-cudaError_t launch_rows(const MxMatmulArgs& a, float* partials, uint32_t* tickets, const DeviceProps& dp,
-                        cudaStream_t s) {
+cudaError_t launch_rows(const MxMatmulArgs& a, const Plan& pl, float* partials, uint32_t* tickets,
+                        const DeviceProps& dp, cudaStream_t s) {
     auto kern = rows::rows_kernel<kOut, MP>;
     constexpr size_t kSmem = rows::smem_bytes<MP>();
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -726,27 +809,28 @@ cudaError_t launch_rows(const MxMatmulArgs& a, float* partials, uint32_t* ticket
     if (!encode_codes(&tw, a.b, a.N, a.K, rows::BN) || !encode_codes(&tx, a.a, a.M, a.K, MP) ||
         !encode_scales(&tsw, a.eb, a.N, a.K, 1) || !encode_scales(&tsx, a.ea, a.M, a.K, 1))
         return cudaErrorInvalidValue;
-    const long long units = static_cast<long long>((a.M + MP - 1) / MP) * ((a.N + rows::BN - 1) / rows::BN) *
-                            ((a.K + kStepK - 1) / kStepK);
+    const long long tiles = static_cast<long long>((a.M + MP - 1) / MP) * ((a.N + rows::BN - 1) / rows::BN);
+    const long long units = tiles * ((a.K + kStepK - 1) / kStepK);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(units, dp.sms)));
+    cfg.gridDim = dim3(static_cast<unsigned>(pl.split > 1 ? tiles * pl.split
+                                                          : std::min<long long>(pl.share ? units : tiles, dp.sms)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    if (pl.split > 1) {   // an ordinary launch, as the pair kernel's
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(pl.split);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+    } else {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tw, tx, tsw, tsx, a.y, a.M, a.N, a.K, partials, tickets);
-}
-
-// The pair kernel needs tiles for most of the GPU's CTA pairs; below that the
-// stream-K kernel spreads the same work evenly.
-bool uses_pairs(long long M, long long N, const DeviceProps& dp) {
-    if (M <= 128) return false;
-    const long long tiles = ((M + pair::BM - 1) / pair::BM) * ((N + pair::BN - 1) / pair::BN);
-    return tiles * 2 >= dp.sms;
+    return cudaLaunchKernelEx(&cfg, kern, tw, tx, tsw, tsx, a.y, a.M, a.N, a.K, pl.split, pl.share ? 1 : 0,
+                              partials, tickets);
 }
 
 size_t partial_bytes(const DeviceProps& dp) {
@@ -755,20 +839,24 @@ size_t partial_bytes(const DeviceProps& dp) {
 
 template <int kOut>
 cudaError_t launch_typed(const MxMatmulArgs& a, void* workspace, const DeviceProps& dp, cudaStream_t s) {
-    if (uses_pairs(a.M, a.N, dp)) return launch_pair<kOut>(a, dp, s);
+    const Plan pl = plan(a.M, a.N, a.K, dp);
     float* partials = static_cast<float*>(workspace);
     uint32_t* tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + partial_bytes(dp));
-    if (a.M <= 16) return launch_rows<kOut, 16>(a, partials, tickets, dp, s);
-    if (a.M <= 32) return launch_rows<kOut, 32>(a, partials, tickets, dp, s);
-    if (a.M <= 64) return launch_rows<kOut, 64>(a, partials, tickets, dp, s);
-    return launch_rows<kOut, 128>(a, partials, tickets, dp, s);
+    switch (pl.mp) {
+        case 0: return launch_pair<kOut>(a, dp, s);
+        case 16: return launch_rows<kOut, 16>(a, pl, partials, tickets, dp, s);
+        case 32: return launch_rows<kOut, 32>(a, pl, partials, tickets, dp, s);
+        case 64: return launch_rows<kOut, 64>(a, pl, partials, tickets, dp, s);
+        default: return launch_rows<kOut, 128>(a, pl, partials, tickets, dp, s);
+    }
 }
 
 }  // namespace
 
-size_t mx_matmul_workspace_bytes(int64_t M, int64_t N, const DeviceProps& dp) {
-    if (uses_pairs(M, N, dp)) return 0;
-    const size_t tiles = static_cast<size_t>((M + 127) / 128) * ((N + rows::BN - 1) / rows::BN);
+size_t mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceProps& dp) {
+    const Plan pl = plan(M, N, K, dp);
+    if (pl.mp == 0) return 0;
+    const size_t tiles = static_cast<size_t>((M + pl.mp - 1) / pl.mp) * ((N + rows::BN - 1) / rows::BN);
     return partial_bytes(dp) + ((tiles * 4 * sizeof(uint32_t) + 255) & ~size_t(255));
 }
 

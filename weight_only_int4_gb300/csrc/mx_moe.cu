@@ -646,7 +646,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
 #pragma unroll
                         for (int a = 0; a < kTiles; ++a) {
                             sh[a] = make_int4(0, 0, 0, 0);
-                            if (here > 0 && row[a]) sh[a] = __ldcg(reinterpret_cast<const int4*>(shift[a] + ks * kBlocks));
+                            if (here > 0 && row[a])
+                                sh[a] = __ldcg(reinterpret_cast<const int4*>(shift[a] + ks * kBlocks));
                         }
                     }
                     const int s = set * kSetStages + static_cast<int>(used % kSetStages);
@@ -862,7 +863,9 @@ Layout layout(int T, int E, int k, int H, int I) {
 }
 
 // Whether the experts have more than `n` tokens each on average.
-bool slots_per_expert_over(const MxMoeArgs& a, int n) { return static_cast<long long>(a.T) * a.k > static_cast<long long>(n) * a.E; }
+bool slots_per_expert_over(const MxMoeArgs& a, int n) {
+    return static_cast<long long>(a.T) * a.k > static_cast<long long>(n) * a.E;
+}
 
 template <int kGroup>
 cudaError_t launch_group(const CUtensorMap (&maps)[4], const Params& p, const DeviceProps& dp, cudaStream_t s) {

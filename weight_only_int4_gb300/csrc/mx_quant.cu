@@ -38,7 +38,8 @@ struct Octet {
         for (auto& q : v) q = make_uint4(0, 0, 0, 0);
     }
     __device__ void load(const void* x, long long elem) {
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + elem * (kType == kF32 ? 4 : 2));
+        const uint8_t* at = static_cast<const uint8_t*>(x) + elem * (kType == kF32 ? 4 : 2);
+        const uint4* p = reinterpret_cast<const uint4*>(at);
 #pragma unroll
         for (int i = 0; i < (kType == kF32 ? 2 : 1); ++i)
             asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -129,7 +130,8 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const void* __rest
             kg[u] = it - row[u] * groups;
             valid[u] = it < items && static_cast<int>(kg[u]) * 16 + sub < words;
             v[u].zero();
-            if (valid[u]) v[u].load(x, static_cast<long long>(row[u]) * K + static_cast<long long>(kg[u]) * 128 + sub * 8);
+            if (valid[u])
+                v[u].load(x, static_cast<long long>(row[u]) * K + static_cast<long long>(kg[u]) * 128 + sub * 8);
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
@@ -302,7 +304,8 @@ cudaError_t quant_rows(const void* x, uint32_t* codes, uint8_t* es, long long M,
     if (one <= cap)
         return launch_pdl(quant_rows_kernel<kType, 1, unsigned>, one, s, x, codes, es, items, groups, K);
     const long long grid = std::min(cap, (one + 3) / 4);
-    if (items < kIndexLimit) return launch_pdl(quant_rows_kernel<kType, 4, unsigned>, grid, s, x, codes, es, items, groups, K);
+    if (items < kIndexLimit)
+        return launch_pdl(quant_rows_kernel<kType, 4, unsigned>, grid, s, x, codes, es, items, groups, K);
     return launch_pdl(quant_rows_kernel<kType, 4, unsigned long long>, grid, s, x, codes, es, items, groups, K);
 }
 
