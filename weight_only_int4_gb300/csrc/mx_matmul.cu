@@ -731,9 +731,11 @@ Plan plan(long long M, long long N, long long K, const DeviceProps& dp) {
     if (M > 128 && tiles128 > dp.sms) return {0, 1, false};
     const int mp = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 || 2 * tiles128 <= dp.sms ? 64 : 128;
     const long long tiles = ((M + mp - 1) / mp) * cols;
-    // a step saved is worth about 0.29 us, a cluster's sum and its ordinary launch cost about 3 us
-    const long long split = std::min<long long>({8, dp.sms / tiles, steps / 4});
-    if (split > 1 && steps - steps / split >= 12) return {mp, static_cast<int>(split), false};
+    // a step saved is worth 0.2..0.3 us, a cluster's sum and its ordinary launch cost about 2 us: 1 x 2048 x 4096 8.8
+    // (whole) / 5.3 (6 CTAs a tile), 1 x 5376 x 21504 27.4 / 15.7 (3), 100 x 1288 x 9120 13.6 / 8.5 (6). Clusters of 7
+    // and 8 do not all fit at once: 16 x 2048 x 8192 7.8 with 6, 13.0 with 7, 11.8 with 8
+    const long long split = std::min<long long>({6, dp.sms / tiles, steps / 2});
+    if (split > 1 && steps - steps / split >= 8) return {mp, static_cast<int>(split), false};
     const long long waves = (tiles + dp.sms - 1) / dp.sms;
     return {mp, 1, mp <= 32 && tiles > dp.sms && waves * dp.sms * 100 > tiles * 115};
 }
