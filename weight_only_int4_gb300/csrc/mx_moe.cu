@@ -137,11 +137,15 @@ __device__ __forceinline__ void fail(volatile int* abort) {
     atomicOr(&g_mx_moe_error, 1u << kErrTimeout);
 }
 
+// A poll takes 111 cycles (measured, phase complete). With one lane polling and
+// a shuffle of its verdict a wait took 266; the whole warp polling in one
+// instruction and voting takes 131.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
     const uint32_t b = smem_u32(bar);
+    if (mbar_try_wait(b, parity)) return true;
     const unsigned long long t0 = clock64();
     for (;;) {
-        // a few polls between looks at the clock; a thread suspended in its wait woke up microseconds late
+        // a few polls between looks at the clock
         for (int i = 0; i < 32; ++i)
             if (mbar_try_wait(b, parity)) return true;
         if (*abort) return false;
@@ -151,12 +155,19 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
         }
     }
 }
-__device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, int lane) {
-    int ok = 1;
-    if (lane == 0) ok = wait_bar(bar, parity, abort) ? 1 : 0;
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    __syncwarp();
-    return ok != 0;
+__device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    const uint32_t b = smem_u32(bar);
+    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+    const unsigned long long t0 = clock64();
+    for (;;) {
+        for (int i = 0; i < 32; ++i)
+            if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
+        if (__any_sync(0xffffffffu, clock64() - t0 > kWaitLimitCycles)) {
+            fail(abort);
+            return false;
+        }
+    }
 }
 
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
@@ -603,18 +614,18 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
             constexpr bool kH = decltype(second)::value;
             const int items = kH ? items3 : items2, cols = kH ? cols3 : cols2;
             const int blocks = kH ? blocks3 : blocks2, steps = kH ? steps3 : steps2;
-            for (int item = cta; item < items; item += grid, ++count) {
-                const int gi = item / cols, cb = item - gi * cols;
-                const int n = sm->group[gi] >> 16, tiles = (n + 7) >> 3;
-                // the rows of tokens g and g + 8, from element 8 t of every block
-                const uint16_t* row[kTiles];
-                const int* shift[kTiles];
-                int align[kTiles];
-                float acc[kTiles][2][4];
+            // An item's place and, for its tokens g and g + 8, the rows from element 8 t of the warp's first block.
+            int cb = 0, tiles = 0;
+            const uint16_t* row[kTiles];
+            const int* shift[kTiles];
+            int align[kTiles];
+            auto locate = [&](int item) {
+                const int gi = item / cols, n = sm->group[gi] >> 16;
+                cb = item - gi * cols;
+                tiles = (n + 7) >> 3;
 #pragma unroll
                 for (int a = 0; a < kTiles; ++a) {
                     row[a] = nullptr;
-                    shift[a] = nullptr;
                     align[a] = 0;
                     if (ok && g + 8 * a < n) {
                         const int slot = sm->list[sm->first[gi] + g + 8 * a];
@@ -625,33 +636,51 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                             align[a] = __ldcg(p.hshift + slot);
                         }
                     }
+                }
+            };
+            // The activations of a stage, loaded as soon as the stage before has used the registers (over an item's
+            // end too): their way from L2 is hidden by what lies between.
+            uint4 x[kWarpBlocks][kTiles];
+            int4 sh[kTiles];
+            auto load_rows = [&](int ks) {
+                const int here = blocks - ks * kBlocks - c0;
+#pragma unroll
+                for (int i = 0; i < kWarpBlocks; ++i)
+#pragma unroll
+                    for (int a = 0; a < kTiles; ++a) {
+                        x[i][a] = make_uint4(0, 0, 0, 0);
+                        if (i < here && row[a])
+                            x[i][a] = __ldcg(reinterpret_cast<const uint4*>(row[a] + ks * kStepK + i * 32));
+                    }
+                if constexpr (kH) {
+#pragma unroll
+                    for (int a = 0; a < kTiles; ++a) {
+                        sh[a] = make_int4(0, 0, 0, 0);
+                        if (here > 0 && row[a])
+                            sh[a] = __ldcg(reinterpret_cast<const int4*>(shift[a] + ks * kBlocks));
+                    }
+                }
+            };
+            auto begin = [&](int item) {
+                if (item >= items) return;
+                locate(item);
+                const int ks = (cb ^ set) & 1;
+                if (ks < steps) load_rows(ks);
+            };
+            begin(cta);
+            for (int item = cta; item < items; item += grid, ++count) {
+                const int now = tiles;
+                float acc[kTiles][2][4];
+#pragma unroll
+                for (int a = 0; a < kTiles; ++a)
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) acc[a][m][i] = 0.f;
-                }
                 for (int ks = (cb ^ set) & 1; ks < steps; ks += 2, ++used) {
                     const int here = blocks - ks * kBlocks - c0;   // of the warp's blocks, those that exist
-                    uint4 x[kWarpBlocks][kTiles];
-#pragma unroll
-                    for (int i = 0; i < kWarpBlocks; ++i)
-#pragma unroll
-                        for (int a = 0; a < kTiles; ++a) {
-                            x[i][a] = make_uint4(0, 0, 0, 0);
-                            if (i < here && row[a])
-                                x[i][a] = __ldcg(reinterpret_cast<const uint4*>(row[a] + ks * kStepK + i * 32));
-                        }
-                    int4 sh[kTiles];
-                    if constexpr (kH) {
-#pragma unroll
-                        for (int a = 0; a < kTiles; ++a) {
-                            sh[a] = make_int4(0, 0, 0, 0);
-                            if (here > 0 && row[a])
-                                sh[a] = __ldcg(reinterpret_cast<const int4*>(shift[a] + ks * kBlocks));
-                        }
-                    }
                     const int s = set * kSetStages + static_cast<int>(used % kSetStages);
-                    if (!ok || !warp_wait_bar(&sm->full[s], used / kSetStages & 1u, abort, lane)) {
+                    if (!ok || !warp_wait_bar(&sm->full[s], used / kSetStages & 1u, abort)) {
                         ok = false;
                         continue;
                     }
@@ -678,21 +707,23 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                     const bool edge =
                         has_edge_byte(e4[0]) | has_edge_byte(e4[1]) | has_edge_byte(e4[2]) | has_edge_byte(e4[3]);
                     if (here >= kWarpBlocks && !__any_sync(0xffffffffu, edge)) {
-                        block_products<false, kWarpBlocks, kTiles>(acc, weights, e4, c0, 0, tiles, g, t, x);
+                        block_products<false, kWarpBlocks, kTiles>(acc, weights, e4, c0, 0, now, g, t, x);
                     } else {
 #pragma unroll
                         for (int i = 0; i < kWarpBlocks; ++i)
-                            if (i < here) block_products<true, 1, kTiles>(acc, weights, e4, c0, i, tiles, g, t, x);
+                            if (i < here) block_products<true, 1, kTiles>(acc, weights, e4, c0, i, now, g, t, x);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sm->empty[s]));
+                    if (ks + 2 < steps) load_rows(ks + 2);
                 }
+                begin(item + grid);
                 // sums to the item's buffer: slot [tile][token parity][column % 4], at the lane that holds them
                 const int b = static_cast<int>(count % kBuffers);
-                if (ok) ok = warp_wait_bar(&sm->taken[b], (count / kBuffers & 1u) ^ 1u, abort, lane);
+                if (ok) ok = warp_wait_bar(&sm->taken[b], (count / kBuffers & 1u) ^ 1u, abort);
 #pragma unroll
                 for (int a = 0; a < kTiles; ++a) {
-                    if (a > 0 && a >= tiles) break;
+                    if (a > 0 && a >= now) break;
 #pragma unroll
                     for (int m = 0; m < 2; ++m)       // columns 2 m and 2 m + 1 of every four
 #pragma unroll
@@ -704,7 +735,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
             }
         };
         phase(std::false_type{});
-        if (ok) ok = warp_wait_bar(&sm->phase3, 0, abort, lane);
+        if (ok) ok = warp_wait_bar(&sm->phase3, 0, abort);
         phase(std::true_type{});
     } else {
         // ------------------------------------------------------------ epilogue
@@ -731,7 +762,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                 slot = sm->list[sm->first[gi] + lane];
                 f = __ldcg(p.xfactor + slot / p.k);
             }
-            if (!ok || !warp_wait_bar(&sm->sums[b], count / kBuffers & 1u, abort, lane)) {
+            if (!ok || !warp_wait_bar(&sm->sums[b], count / kBuffers & 1u, abort)) {
                 ok = false;
                 continue;
             }
@@ -773,7 +804,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
         }
         __syncwarp();
 
-        if (ok) ok = warp_wait_bar(&sm->phase3, 0, abort, lane);
+        if (ok) ok = warp_wait_bar(&sm->phase3, 0, abort);
         for (int item = cta; item < items3; item += grid, ++count) {
             const int gi = item / cols3, cb = item - gi * cols3, n = sm->group[gi] >> 16;
             const int b = static_cast<int>(count % kBuffers);
@@ -784,7 +815,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                 f = mx::x_unshift(__ldcg(p.hshift + slot));
             }
             const float pw = lane < n ? sm->weight[slot] : 0.f;
-            if (!ok || !warp_wait_bar(&sm->sums[b], count / kBuffers & 1u, abort, lane)) {
+            if (!ok || !warp_wait_bar(&sm->sums[b], count / kBuffers & 1u, abort)) {
                 ok = false;
                 continue;
             }
@@ -814,7 +845,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
 
     // ---------------------------------------------------------------- phase 4
     __syncwarp();   // single-lane roles rejoin their warp
-    if (!alive || !warp_wait_bar(&sm->phase4, 0, abort, lane)) return;
+    if (!alive || !warp_wait_bar(&sm->phase4, 0, abort)) return;
     const int quads = p.H >> 2;
     for (int i = cta * kThreads + static_cast<int>(threadIdx.x); i < p.T * quads; i += grid * kThreads) {
         const int tok = i / quads, col = (i - tok * quads) * 4;
