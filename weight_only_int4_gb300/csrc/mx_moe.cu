@@ -23,29 +23,28 @@
 //      -- grid barrier --
 //   4  the k parts of every y added in order: deterministic
 //
-// A CTA is two producer warps, sixteen consumer warps and two epilogue warps.
-// Weights pass through a ring of stages: 512 rows of K by 64 columns of codes
-// (two TMA boxes of 32 columns, 128-byte swizzle) and their exponent bytes; the
-// producers fill it without regard to phases or barriers. Two sets of eight
-// consumer warps, each with a producer and half of the ring, take alternate
-// stages of an item (which set takes the first depends on the column block
-// alone, so a token's sums are formed in the same order whatever else the call
-// holds). A warp converts four 32-row blocks of one box: a lane's 16-byte load
-// holds eight consecutive codes of each of four columns, which become fp16
-// pairs by the hardware's exact conversion and serve as the A operand of
-// warp-level MMAs (columns of W as MMA rows, tokens as MMA columns), x as B; K
-// is permuted alike on both sides, so neither needs a shuffle. The activations
-// come straight from global memory (L2) into B fragments, loaded before the wait
-// for the stage's weights. A block's FP32 products are scaled by the columns'
-// 2^(e - 127) as they are added up. At the end of an item the warps leave their
-// sums in one of two buffers and go on; the epilogue warps, two tokens each at
-// a time, add the eight parts in order and finish the item beside the next ones.
+// A CTA is two producer warps, sixteen consumer warps and two epilogue warps
+// around a ring of stages. A stage is 512 rows of K by 64 columns of codes (two
+// TMA boxes of 32 columns, 128-byte swizzle), their exponent bytes and the same
+// 512 elements of the group's activation rows. Two sets of eight consumer
+// warps, each with a producer and half of the ring, take alternate stages of an
+// item (which set takes the first depends on the column block alone, so a
+// token's sums are formed in the same order whatever else the call holds). A
+// warp converts four 32-row blocks of one box: a lane's 16-byte load holds eight
+// consecutive codes of each of four columns, which become fp16 pairs by the
+// hardware's exact conversion and serve as the A operand of warp-level MMAs
+// (columns of W as MMA rows, tokens as MMA columns), x as B; K is permuted alike
+// on both sides, so neither needs a shuffle. A block's FP32 products are scaled
+// by the columns' 2^(e - 127) as they are added up. At the end of an item the
+// warps leave their sums in a buffer and go on; the epilogue warps, two tokens
+// each at a time, add the eight parts in order and finish the item beside the
+// next ones.
 //
-// Activations in fp16: a token's x is multiplied by the power of two that
-// brings its largest magnitude just below 2^15, a run of 32 h values likewise
-// (then aligned to the run with the largest magnitude of its row, again by a
-// power of two). Values within 2^-29 of the largest convert exactly or, for h,
-// with fp16's 11 bits; smaller ones lose at most 2^-39 of the largest.
+// Activations in fp16: a token's x, and every run of 32 values of h, is
+// multiplied by the power of two that brings its largest magnitude just below
+// 2^15; the inverse goes into the FP32 scaling (per token at the end, per run
+// with the block's). Values within 2^-29 of the largest convert exactly or, for
+// h, with fp16's 11 bits; smaller ones lose at most 2^-39 of the largest.
 //
 // Waits are bounded (about two seconds); on expiry the kernel records the
 // timeout in a device word, every role stops, copies in flight are waited for
@@ -65,7 +64,6 @@ __device__ unsigned int g_mx_moe_error = 0;
 namespace {
 
 constexpr int kConsumerWarps = 16, kEpilogues = 2, kProducers = 2;
-constexpr int kBuffers = 2;              // of partial sums
 constexpr int kConsumers = kConsumerWarps * 32;
 constexpr int kThreads = kConsumers + (kEpilogues + kProducers) * 32;
 constexpr int kStepK = 512;              // rows of K per stage
@@ -76,24 +74,33 @@ constexpr int kMaxExperts = kMoeMaxExperts;
 constexpr int kMaxSlots = kMoeMaxTokens * kMoeMaxTopK;
 constexpr uint32_t kBoxBytes = kStepK / 8 * 128;     // 64 word rows x 32 columns
 constexpr uint32_t kScaleBoxBytes = kBlocks * 32;
-constexpr uint32_t kStageBytes = 2 * kBoxBytes + 2 * kScaleBoxBytes;
-static_assert(kStageBytes % 1024 == 0, "swizzled boxes start 1024-byte aligned");
-constexpr int kSetStages = 4;            // half of the ring
-constexpr int kStages = 2 * kSetStages;
+constexpr uint32_t kWeightBytes = 2 * kBoxBytes + 2 * kScaleBoxBytes;
+static_assert(kWeightBytes % 1024 == 0, "swizzled boxes start 1024-byte aligned");
+constexpr uint32_t kHRecord = 80;        // a run of h: 32 fp16 values, the FP32 factor 2^-shift, padding to 16 bytes
+constexpr uint32_t kXStride = kBlocks * kHRecord + 64;   // a row of a stage; two rows' 64 bytes hit different banks
 constexpr int kRedPitch = 33;            // floats per slot of a warp's partial sums
 constexpr unsigned long long kWaitLimitCycles = 4000000000ull;   // ~2 s at 2 GHz
 constexpr unsigned int kErrTimeout = 9u;
 
 // kGroup: tokens of an expert taken together, 8 or 16.
 template <int kGroup>
-struct __align__(16) Shared {
+struct Cfg {
     static constexpr int kTiles = kGroup / 8;            // 8-token MMA tiles
     static constexpr int kRedSlots = kTiles * 8;         // [tile][token parity][column % 4]
-    float red[kBuffers][kConsumerWarps][kRedSlots][kRedPitch];
-    uint64_t full[kStages];
-    uint64_t empty[kStages];
-    uint64_t sums[kBuffers];             // a buffer of partial sums is complete
-    uint64_t taken[kBuffers];            // ... and has been read
+    static constexpr int kBuffers = kGroup == 8 ? 2 : 1;   // of partial sums
+    static constexpr int kSetStages = kGroup == 8 ? 3 : 2;   // half of the ring
+    static constexpr int kStages = 2 * kSetStages;
+    static constexpr uint32_t kRowBytes = kGroup * kXStride;
+};
+
+template <int kGroup>
+struct __align__(16) Shared {
+    using C = Cfg<kGroup>;
+    float red[C::kBuffers][kConsumerWarps][C::kRedSlots][kRedPitch];
+    uint64_t full[C::kStages];
+    uint64_t empty[C::kStages];
+    uint64_t sums[C::kBuffers];          // a buffer of partial sums is complete
+    uint64_t taken[C::kBuffers];         // ... and has been read
     uint64_t phase3;                     // h of every CTA is visible
     uint64_t phase4;                     // the parts of y are
     uint32_t mask[kMaxExperts][2];       // tokens of each expert
@@ -110,9 +117,9 @@ struct __align__(16) Shared {
 };
 template <int kGroup>
 constexpr size_t smem_bytes() {
-    return 1024 + kStages * kStageBytes + sizeof(Shared<kGroup>);
+    return 1024 + Cfg<kGroup>::kStages * (kWeightBytes + Cfg<kGroup>::kRowBytes) + sizeof(Shared<kGroup>);
 }
-static_assert(smem_bytes<16>() <= 227 * 1024, "shared memory budget");
+static_assert(smem_bytes<8>() <= 227 * 1024 && smem_bytes<16>() <= 227 * 1024, "shared memory budget");
 
 struct Params {
     const uint16_t* x;
@@ -122,12 +129,9 @@ struct Params {
     float* logits;         // [T, E]
     uint16_t* x16;         // [T, H]
     float* xfactor;        // [T]
-    int* hshift;           // [T k], smallest shift of the slot's runs
-    uint16_t* h;           // [T k, I], runs of 32 values scaled by 2^shift
-    int* shift;            // [T k, pitch], the runs' shifts
+    uint8_t* h;            // [T k, I / 32] records
     float* part;           // [T k, H]
     int T, E, k, H, I;
-    int pitch;             // I / 32, rounded up to whole stages
     int renormalize;
 };
 constexpr int kBarriers = 3;
@@ -140,26 +144,12 @@ __device__ __forceinline__ void fail(volatile int* abort) {
 // A poll takes 111 cycles (measured, phase complete). With one lane polling and
 // a shuffle of its verdict a wait took 266; the whole warp polling in one
 // instruction and voting takes 131.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    const uint32_t b = smem_u32(bar);
-    if (mbar_try_wait(b, parity)) return true;
-    const unsigned long long t0 = clock64();
-    for (;;) {
-        // a few polls between looks at the clock
-        for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait(b, parity)) return true;
-        if (*abort) return false;
-        if (clock64() - t0 > kWaitLimitCycles) {
-            fail(abort);
-            return false;
-        }
-    }
-}
 __device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
     const uint32_t b = smem_u32(bar);
     if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
     const unsigned long long t0 = clock64();
     for (;;) {
+        // a few polls between looks at the clock
         for (int i = 0; i < 32; ++i)
             if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
         if (__any_sync(0xffffffffu, *abort != 0)) return false;
@@ -196,6 +186,15 @@ __device__ __forceinline__ bool grid_wait(const uint32_t* count, volatile int* a
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+// Untiled copy of `bytes` (a multiple of 16), global to shared.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // D = A * B on fp16 (FP32 result), accumulators starting at zero or at D.
 __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
@@ -203,18 +202,6 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_
         "{%10,%10,%10,%10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
-// fp16 2^d in both halves, d <= 0; zero below the fp16 subnormals.
-__device__ __forceinline__ uint32_t pow2_f16x2(int d) {
-    const uint32_t h = d >= -14 ? static_cast<uint32_t>(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
-    return h * 0x10001u;
 }
 
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
@@ -303,7 +290,6 @@ __device__ void convert_token(const Params& p, float (*scratch)[4][32], int tok,
         __stcg(dst + i, make_uint4(o[0], o[1], o[2], o[3]));
     }
     if (tid == 0) __stcg(p.xfactor + tok, mx::x_unshift(c));
-    for (int j = tid; j < p.k; j += kConsumers) __stcg(p.hshift + tok * p.k + j, 127);
     consumer_sync();
 }
 
@@ -435,17 +421,31 @@ __device__ __forceinline__ bool has_edge_byte(uint32_t v) {
 }
 
 // kCount 32-row blocks of one box of a stage, from block c on, against the
-// group's rows in b, added to acc [8-token tile][16-column tile][fragment].
-// kEdge: a byte of 0 or 255 may be among the exponents.
-template <bool kEdge, int kCount, int kTiles>
+// group's rows, added to acc [8-token tile][16-column tile][fragment]. rows: the
+// lane's first 16 bytes of its row g. kH: the rows are records of h, their
+// factors at `factors` for the lane's tokens 2 t and 2 t + 1. kEdge: a byte of 0
+// or 255 may be among the exponents e4.
+template <bool kH, bool kEdge, int kCount, int kTiles>
 __device__ __forceinline__ void block_products(float (&acc)[kTiles][2][4], uint32_t box, const uint32_t (&e4)[4],
-                                               int c, int first, int tiles, int g, int t, const uint4 (&b)[4][kTiles]) {
+                                               uint32_t rows, uint32_t factors, int c, int first, int tiles, int g,
+                                               int t) {
     const uint32_t chunk = static_cast<uint32_t>((g >> 1) | ((g & 1) << 2));   // quarter-warps hit every bank once
-    uint4 w[kCount];
+    constexpr uint32_t kRec = kH ? kHRecord : 64;
+    uint4 w[kCount], x[kCount][kTiles];
+    float f0[kCount][kTiles], f1[kCount][kTiles];
 #pragma unroll
     for (int j = 0; j < kCount; ++j) {
         const int row = 4 * (c + first + j) + t;
         w[j] = ld_shared_v4(box + row * 128 + ((chunk ^ (row & 7)) << 4));
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+            if (n > 0 && n >= tiles) break;
+            x[j][n] = ld_shared_v4(rows + (first + j) * kRec + n * 8 * kXStride);
+            if constexpr (kH) {
+                f0[j][n] = __uint_as_float(ld_shared_u32(factors + (first + j) * kRec + n * 8 * kXStride));
+                f1[j][n] = __uint_as_float(ld_shared_u32(factors + (first + j) * kRec + n * 8 * kXStride + kXStride));
+            }
+        }
     }
 #pragma unroll
     for (int j = 0; j < kCount; ++j) {
@@ -469,15 +469,22 @@ __device__ __forceinline__ void block_products(float (&acc)[kTiles][2][4], uint3
 #pragma unroll
             for (int n = 0; n < kTiles; ++n) {
                 if (n > 0 && n >= tiles) break;
-                const uint4 x = b[first + j][n];
                 float d[4];
-                mma_f16_zero(d, lo[0], hi[0], lo[1], hi[1], x.x, x.y);
-                mma_m16n8k16<false>(d, lo[2], hi[2], lo[3], hi[3], x.z, x.w);
+                mma_f16_zero(d, lo[0], hi[0], lo[1], hi[1], x[j][n].x, x[j][n].y);
+                mma_m16n8k16<false>(d, lo[2], hi[2], lo[3], hi[3], x[j][n].z, x[j][n].w);
                 float(&a)[4] = acc[n][m];
-                a[0] = fmaf(d[0], scale[2 * m], a[0]);
-                a[1] = fmaf(d[1], scale[2 * m], a[1]);
-                a[2] = fmaf(d[2], scale[2 * m + 1], a[2]);
-                a[3] = fmaf(d[3], scale[2 * m + 1], a[3]);
+                if constexpr (kH) {
+                    // d 2^-shift first: the size of h's products, whatever the exponents are
+                    a[0] = fmaf(d[0] * f0[j][n], scale[2 * m], a[0]);
+                    a[1] = fmaf(d[1] * f1[j][n], scale[2 * m], a[1]);
+                    a[2] = fmaf(d[2] * f0[j][n], scale[2 * m + 1], a[2]);
+                    a[3] = fmaf(d[3] * f1[j][n], scale[2 * m + 1], a[3]);
+                } else {
+                    a[0] = fmaf(d[0], scale[2 * m], a[0]);
+                    a[1] = fmaf(d[1], scale[2 * m], a[1]);
+                    a[2] = fmaf(d[2], scale[2 * m + 1], a[2]);
+                    a[3] = fmaf(d[3], scale[2 * m + 1], a[3]);
+                }
             }
         }
     }
@@ -487,11 +494,12 @@ template <int kGroup>
 __global__ void __launch_bounds__(kThreads, 1)
 moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUtensorMap te13,
            const __grid_constant__ CUtensorMap tw2, const __grid_constant__ CUtensorMap te2, const Params p) {
-    constexpr int kTiles = Shared<kGroup>::kTiles;
+    using C = Cfg<kGroup>;
+    constexpr int kTiles = C::kTiles, kBuffers = C::kBuffers, kSetStages = C::kSetStages, kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Shared<kGroup>* sm = reinterpret_cast<Shared<kGroup>*>(ring + kStages * kStageBytes);
-    const uint32_t ring_base = smem_u32(ring);
+    const uint32_t ring_base = smem_u32(ring), rows_base = ring_base + kStages * kWeightBytes;
+    Shared<kGroup>* sm = reinterpret_cast<Shared<kGroup>*>(ring + kStages * (kWeightBytes + C::kRowBytes));
     volatile int* abort = &sm->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int grid = gridDim.x, cta = blockIdx.x;
@@ -529,6 +537,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
             else
                 convert_token(p, scratch, u - tiles, warp, lane);
         }
+        fence_proxy_async_global();   // x16 is read by bulk copies
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -564,39 +573,81 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
     const int steps2 = (blocks2 + kBlocks - 1) / kBlocks, steps3 = (blocks3 + kBlocks - 1) / kBlocks;
 
     if (warp >= kConsumerWarps + kEpilogues) {
-        // ------------------------------------------------------------ producers: the weights of one set's stages
-        if (lane == 0) {
-            const int set = warp - kConsumerWarps - kEpilogues;
-            int slot = 0, seen = 0;
-            uint32_t parity = 1u;
-            bool ok = true;
-            for (int second = 0; second < 2 && ok; ++second) {
-                const int items = second ? items3 : items2, cols = second ? cols3 : cols2;
-                const int blocks = second ? blocks3 : blocks2, steps = second ? steps3 : steps2;
-                const CUtensorMap* tw = second ? &tw2 : &tw13;
-                const CUtensorMap* te = second ? &te2 : &te13;
-                for (int item = cta; item < items && ok; item += grid) {
-                    const int gi = item / cols, cb = item - gi * cols;
-                    const int c0 = second ? cb * 64 : cb * 32, c1 = second ? c0 + 32 : p.I + c0;
-                    const int kb0 = static_cast<int>(sm->group[gi] & 0xFFFFu) * blocks;   // 32-row block of the stack
-                    for (int ks = (cb ^ set) & 1; ks < steps; ks += 2) {
-                        const int s = set * kSetStages + slot, kb = kb0 + ks * kBlocks;
-                        if (!wait_bar(&sm->empty[s], parity, abort)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t bar = smem_u32(&sm->full[s]), dst = ring_base + s * kStageBytes;
-                        mbar_arrive_expect_tx(bar, kStageBytes);
+        // ------------------------------------------------------------ producers, one per set
+        const int set = warp - kConsumerWarps - kEpilogues;
+        int slot = 0, seen = 0;
+        uint32_t parity = 1u;
+        bool ok = alive;
+        fence_proxy_async_global();
+        auto phase = [&](auto second) {
+            constexpr bool kH = decltype(second)::value;
+            constexpr uint32_t kRec = kH ? kHRecord : 64;
+            const int items = kH ? items3 : items2, cols = kH ? cols3 : cols2;
+            const int blocks = kH ? blocks3 : blocks2, steps = kH ? steps3 : steps2;
+            const CUtensorMap* tw = kH ? &tw2 : &tw13;
+            const CUtensorMap* te = kH ? &te2 : &te13;
+            // Phase 3's first stages get their weights before h is complete and their rows after it.
+            bool open = !kH;
+            int held = 0, held_slot[kSetStages] = {};
+            uint32_t held_bytes[kSetStages] = {};
+            const uint8_t* held_src[kSetStages] = {};
+            auto rows = [&](int s, const uint8_t* src, uint32_t bytes) {   // one row per lane
+                if (src) bulk_load(rows_base + s * C::kRowBytes + lane * kXStride, src, bytes, smem_u32(&sm->full[s]));
+            };
+            auto release = [&] {
+                ok = ok && warp_wait_bar(&sm->phase3, 0, abort);
+                fence_proxy_async_global();
+#pragma unroll
+                for (int i = 0; i < kSetStages; ++i)
+                    if (ok && i < held) rows(held_slot[i], held_src[i], held_bytes[i]);
+                open = true;
+            };
+            for (int item = cta; item < items && ok; item += grid) {
+                const int gi = item / cols, cb = item - gi * cols;
+                const uint32_t gr = sm->group[gi];
+                const int n = gr >> 16, kb0 = static_cast<int>(gr & 0xFFFFu) * blocks;   // 32-row block of the stack
+                const int c0 = kH ? cb * 64 : cb * 32, c1 = kH ? c0 + 32 : p.I + c0;
+                const uint8_t* src = nullptr;
+                if (lane < n) {
+                    const int sl = sm->list[sm->first[gi] + lane];
+                    src = kH ? p.h + static_cast<size_t>(sl) * blocks * kHRecord
+                             : reinterpret_cast<const uint8_t*>(p.x16 + static_cast<size_t>(sl / p.k) * p.H);
+                }
+                for (int ks = (cb ^ set) & 1; ks < steps; ks += 2) {
+                    const int s = set * kSetStages + slot, kb = kb0 + ks * kBlocks;
+                    if (!warp_wait_bar(&sm->empty[s], parity, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bytes = min(kBlocks, blocks - ks * kBlocks) * kRec;
+                    if (lane == 0) {
+                        const uint32_t bar = smem_u32(&sm->full[s]), dst = ring_base + s * kWeightBytes;
+                        mbar_arrive_expect_tx(bar, kWeightBytes + n * bytes);
                         tma_load_2d(dst, tw, c0, kb * 4, bar);
                         tma_load_2d(dst + kBoxBytes, tw, c1, kb * 4, bar);
                         tma_load_2d(dst + 2 * kBoxBytes, te, c0, kb, bar);
                         tma_load_2d(dst + 2 * kBoxBytes + kScaleBoxBytes, te, c1, kb, bar);
-                        ++seen;
-                        if (++slot == kSetStages) slot = 0, parity ^= 1u;
                     }
+                    __syncwarp();
+                    const uint8_t* from = src ? src + static_cast<size_t>(ks) * kBlocks * kRec : nullptr;
+                    if (open) {
+                        rows(s, from, bytes);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kSetStages; ++i)
+                            if (i == held) held_slot[i] = s, held_src[i] = from, held_bytes[i] = bytes;
+                        if (++held == kSetStages) release();
+                    }
+                    ++seen;
+                    if (++slot == kSetStages) slot = 0, parity ^= 1u;
                 }
             }
-            // copies in flight land before the CTA's shared memory is given back
+            if (!open) release();
+        };
+        phase(std::false_type{});
+        phase(std::true_type{});
+        // copies in flight land before the CTA's shared memory is given back
+        if (lane == 0) {
             const unsigned long long t0 = clock64();
             for (int i = max(0, seen - kSetStages); i < seen; ++i)
                 while (!mbar_try_wait(smem_u32(&sm->full[set * kSetStages + i % kSetStages]), i / kSetStages & 1) &&
@@ -612,64 +663,12 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
         bool ok = alive;
         auto phase = [&](auto second) {
             constexpr bool kH = decltype(second)::value;
+            constexpr uint32_t kRec = kH ? kHRecord : 64;
             const int items = kH ? items3 : items2, cols = kH ? cols3 : cols2;
             const int blocks = kH ? blocks3 : blocks2, steps = kH ? steps3 : steps2;
-            // An item's place and, for its tokens g and g + 8, the rows from element 8 t of the warp's first block.
-            int cb = 0, tiles = 0;
-            const uint16_t* row[kTiles];
-            const int* shift[kTiles];
-            int align[kTiles];
-            auto locate = [&](int item) {
-                const int gi = item / cols, n = sm->group[gi] >> 16;
-                cb = item - gi * cols;
-                tiles = (n + 7) >> 3;
-#pragma unroll
-                for (int a = 0; a < kTiles; ++a) {
-                    row[a] = nullptr;
-                    align[a] = 0;
-                    if (ok && g + 8 * a < n) {
-                        const int slot = sm->list[sm->first[gi] + g + 8 * a];
-                        row[a] = (kH ? p.h + static_cast<size_t>(slot) * p.I
-                                     : p.x16 + static_cast<size_t>(slot / p.k) * p.H) + c0 * 32 + 8 * t;
-                        if constexpr (kH) {
-                            shift[a] = p.shift + static_cast<size_t>(slot) * p.pitch + c0;
-                            align[a] = __ldcg(p.hshift + slot);
-                        }
-                    }
-                }
-            };
-            // The activations of a stage, loaded as soon as the stage before has used the registers (over an item's
-            // end too): their way from L2 is hidden by what lies between.
-            uint4 x[kWarpBlocks][kTiles];
-            int4 sh[kTiles];
-            auto load_rows = [&](int ks) {
-                const int here = blocks - ks * kBlocks - c0;
-#pragma unroll
-                for (int i = 0; i < kWarpBlocks; ++i)
-#pragma unroll
-                    for (int a = 0; a < kTiles; ++a) {
-                        x[i][a] = make_uint4(0, 0, 0, 0);
-                        if (i < here && row[a])
-                            x[i][a] = __ldcg(reinterpret_cast<const uint4*>(row[a] + ks * kStepK + i * 32));
-                    }
-                if constexpr (kH) {
-#pragma unroll
-                    for (int a = 0; a < kTiles; ++a) {
-                        sh[a] = make_int4(0, 0, 0, 0);
-                        if (here > 0 && row[a])
-                            sh[a] = __ldcg(reinterpret_cast<const int4*>(shift[a] + ks * kBlocks));
-                    }
-                }
-            };
-            auto begin = [&](int item) {
-                if (item >= items) return;
-                locate(item);
-                const int ks = (cb ^ set) & 1;
-                if (ks < steps) load_rows(ks);
-            };
-            begin(cta);
             for (int item = cta; item < items; item += grid, ++count) {
-                const int now = tiles;
+                const int gi = item / cols, cb = item - gi * cols;
+                const int tiles = ((sm->group[gi] >> 16) + 7) >> 3;
                 float acc[kTiles][2][4];
 #pragma unroll
                 for (int a = 0; a < kTiles; ++a)
@@ -684,46 +683,34 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                         ok = false;
                         continue;
                     }
-                    const uint32_t stage = ring_base + s * kStageBytes, weights = stage + box * kBoxBytes;
+                    const uint32_t stage = ring_base + s * kWeightBytes, weights = stage + box * kBoxBytes;
+                    const uint32_t in = rows_base + s * C::kRowBytes + c0 * kRec;
+                    const uint32_t rows = in + g * kXStride + t * 16, factors = in + 2 * t * kXStride + 64;
                     uint32_t e4[kWarpBlocks];
 #pragma unroll
                     for (int i = 0; i < kWarpBlocks; ++i)
                         e4[i] = ld_shared_u32(stage + 2 * kBoxBytes + box * kScaleBoxBytes + (c0 + i) * 32 +
                                               ((g >> 1) | ((g & 1) << 2)) * 4);
-                    if constexpr (kH) {
-                        // every run of h to its row's common shift
-#pragma unroll
-                        for (int a = 0; a < kTiles; ++a) {
-                            const int si[4] = {sh[a].x, sh[a].y, sh[a].z, sh[a].w};
-#pragma unroll
-                            for (int i = 0; i < kWarpBlocks; ++i) {
-                                const uint32_t f = pow2_f16x2(min(align[a] - si[i], 0));
-                                x[i][a] = make_uint4(hmul2(x[i][a].x, f), hmul2(x[i][a].y, f), hmul2(x[i][a].z, f),
-                                                     hmul2(x[i][a].w, f));
-                            }
-                        }
-                    }
                     // the usual stage without a branch, so that its blocks overlap; else one block at a time
                     const bool edge =
                         has_edge_byte(e4[0]) | has_edge_byte(e4[1]) | has_edge_byte(e4[2]) | has_edge_byte(e4[3]);
                     if (here >= kWarpBlocks && !__any_sync(0xffffffffu, edge)) {
-                        block_products<false, kWarpBlocks, kTiles>(acc, weights, e4, c0, 0, now, g, t, x);
+                        block_products<kH, false, kWarpBlocks, kTiles>(acc, weights, e4, rows, factors, c0, 0, tiles, g, t);
                     } else {
 #pragma unroll
                         for (int i = 0; i < kWarpBlocks; ++i)
-                            if (i < here) block_products<true, 1, kTiles>(acc, weights, e4, c0, i, now, g, t, x);
+                            if (i < here)
+                                block_products<kH, true, 1, kTiles>(acc, weights, e4, rows, factors, c0, i, tiles, g, t);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sm->empty[s]));
-                    if (ks + 2 < steps) load_rows(ks + 2);
                 }
-                begin(item + grid);
                 // sums to the item's buffer: slot [tile][token parity][column % 4], at the lane that holds them
                 const int b = static_cast<int>(count % kBuffers);
                 if (ok) ok = warp_wait_bar(&sm->taken[b], (count / kBuffers & 1u) ^ 1u, abort);
 #pragma unroll
                 for (int a = 0; a < kTiles; ++a) {
-                    if (a > 0 && a >= now) break;
+                    if (a > 0 && a >= tiles) break;
 #pragma unroll
                     for (int m = 0; m < 2; ++m)       // columns 2 m and 2 m + 1 of every four
 #pragma unroll
@@ -735,7 +722,6 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
             }
         };
         phase(std::false_type{});
-        if (ok) ok = warp_wait_bar(&sm->phase3, 0, abort);
         phase(std::true_type{});
     } else {
         // ------------------------------------------------------------ epilogue
@@ -766,7 +752,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                 ok = false;
                 continue;
             }
-            int low = 127;   // lane i: token i's shift
+            float back = 0.f;   // lane i: token i's factor 2^-shift
             for (int i0 = 2 * half; i0 < n; i0 += 2 * kEpilogues) {
                 float h[2];
                 int sh[2];
@@ -784,18 +770,18 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                     const int si = __shfl_sync(0xffffffffu, slot, i0 + d);
                     const float scaled = h[d] * __uint_as_float(static_cast<uint32_t>(sh[d] + 127) << 23);
                     if (i0 + d < n)
-                        __stcg(p.h + static_cast<size_t>(si) * p.I + cb * 32 + lane,
+                        __stcg(reinterpret_cast<unsigned short*>(
+                                   p.h + (static_cast<size_t>(si) * blocks3 + cb) * kHRecord) + lane,
                                __half_as_ushort(__float2half_rn(scaled)));
-                    if (lane == i0 + d) low = sh[d];
+                    if (lane == i0 + d) back = mx::x_unshift(sh[d]);
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm->taken[b]));
-            if (lane < n && ((lane >> 1) & 1) == half) {
-                __stcg(p.shift + static_cast<size_t>(slot) * p.pitch + cb, low);
-                atomicMin(p.hshift + slot, low);
-            }
+            if (lane < n && ((lane >> 1) & 1) == half)
+                __stcg(reinterpret_cast<float*>(p.h + (static_cast<size_t>(slot) * blocks3 + cb) * kHRecord + 64), back);
         }
+        fence_proxy_async_global();   // h is read by bulk copies
         auto epilogue_sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(kEpilogues * 32) : "memory"); };
         epilogue_sync();
         if (half == 0 && lane == 0 && alive) {
@@ -804,16 +790,10 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
         }
         __syncwarp();
 
-        if (ok) ok = warp_wait_bar(&sm->phase3, 0, abort);
         for (int item = cta; item < items3; item += grid, ++count) {
             const int gi = item / cols3, cb = item - gi * cols3, n = sm->group[gi] >> 16;
             const int b = static_cast<int>(count % kBuffers);
-            int slot = 0;
-            float f = 0.f;
-            if (ok && lane < n) {
-                slot = sm->list[sm->first[gi] + lane];
-                f = mx::x_unshift(__ldcg(p.hshift + slot));
-            }
+            const int slot = lane < n ? sm->list[sm->first[gi] + lane] : 0;
             const float pw = lane < n ? sm->weight[slot] : 0.f;
             if (!ok || !warp_wait_bar(&sm->sums[b], count / kBuffers & 1u, abort)) {
                 ok = false;
@@ -824,8 +804,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
 #pragma unroll
                 for (int d = 0; d < 2; ++d) {
                     const int si = __shfl_sync(0xffffffffu, slot, i0 + d);
-                    const float fi = __shfl_sync(0xffffffffu, f, i0 + d), wi = __shfl_sync(0xffffffffu, pw, i0 + d);
-                    const float s0 = total(b, i0 + d, 0) * fi * wi, s1 = total(b, i0 + d, 1) * fi * wi;
+                    const float wi = __shfl_sync(0xffffffffu, pw, i0 + d);
+                    const float s0 = total(b, i0 + d, 0) * wi, s1 = total(b, i0 + d, 1) * wi;
                     if (i0 + d < n) {
                         float* part = p.part + static_cast<size_t>(si) * p.H + cb * 64 + lane;
                         __stcg(part, s0);
@@ -869,8 +849,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
 struct Layout {
-    size_t logits, x16, xfactor, hshift, h, shift, part, total;
-    int pitch;
+    size_t logits, x16, xfactor, h, part, total;
 };
 Layout layout(int T, int E, int k, int H, int I) {
     Layout l;
@@ -884,10 +863,7 @@ Layout layout(int T, int E, int k, int H, int I) {
     l.logits = take(static_cast<size_t>(T) * E * 4);
     l.x16 = take(static_cast<size_t>(T) * H * 2);
     l.xfactor = take(static_cast<size_t>(T) * 4);
-    l.hshift = take(slots * 4);
-    l.pitch = (I / 32 + kBlocks - 1) / kBlocks * kBlocks;
-    l.h = take(slots * I * 2);
-    l.shift = take(slots * l.pitch * 4);
+    l.h = take(slots * (I / 32) * kHRecord);
     l.part = take(slots * H * 4);
     l.total = at;
     return l;
@@ -947,10 +923,7 @@ cudaError_t launch_mx_moe(const MxMoeArgs& a, void* workspace, const DeviceProps
     p.logits = reinterpret_cast<float*>(ws + l.logits);
     p.x16 = reinterpret_cast<uint16_t*>(ws + l.x16);
     p.xfactor = reinterpret_cast<float*>(ws + l.xfactor);
-    p.hshift = reinterpret_cast<int*>(ws + l.hshift);
-    p.h = reinterpret_cast<uint16_t*>(ws + l.h);
-    p.shift = reinterpret_cast<int*>(ws + l.shift);
-    p.pitch = l.pitch;
+    p.h = ws + l.h;
     p.part = reinterpret_cast<float*>(ws + l.part);
     p.T = a.T;
     p.E = a.E;
