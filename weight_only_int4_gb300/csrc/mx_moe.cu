@@ -415,11 +415,6 @@ __device__ __forceinline__ void number_groups(const Params& p, Shared<kGroup>* s
 // ---------------------------------------------------------------------------
 // phases 2 and 3
 // ---------------------------------------------------------------------------
-// Whether one of four bytes is 0 or 255.
-__device__ __forceinline__ bool has_edge_byte(uint32_t v) {
-    return (__vcmpeq4(v, 0u) | __vcmpeq4(v, 0xFFFFFFFFu)) != 0u;
-}
-
 // kCount 32-row blocks of one box of a stage, from block c on, against the
 // group's rows, added to acc [8-token tile][16-column tile][fragment]. rows: the
 // lane's first 16 bytes of its row g. kH: the rows are records of h, their
@@ -691,10 +686,12 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                     for (int i = 0; i < kWarpBlocks; ++i)
                         e4[i] = ld_shared_u32(stage + 2 * kBoxBytes + box * kScaleBoxBytes + (c0 + i) * 32 +
                                               ((g >> 1) | ((g & 1) << 2)) * 4);
-                    // the usual stage without a branch, so that its blocks overlap; else one block at a time
-                    const bool edge =
-                        has_edge_byte(e4[0]) | has_edge_byte(e4[1]) | has_edge_byte(e4[2]) | has_edge_byte(e4[3]);
-                    if (here >= kWarpBlocks && !__any_sync(0xffffffffu, edge)) {
+                    // The usual stage without a branch, so that its blocks overlap: all four blocks, every exponent byte
+                    // in 64..191 (bits 7 and 6 differ; scales 2^-63..2^64), so none is 0 or 255. Else one at a time.
+                    uint32_t usual = 0x80808080u;
+#pragma unroll
+                    for (int i = 0; i < kWarpBlocks; ++i) usual &= e4[i] ^ (e4[i] << 1);
+                    if (here >= kWarpBlocks && __all_sync(0xffffffffu, usual == 0x80808080u)) {
                         block_products<kH, false, kWarpBlocks, kTiles>(acc, weights, e4, rows, factors, c0, 0, tiles, g, t);
                     } else {
 #pragma unroll
