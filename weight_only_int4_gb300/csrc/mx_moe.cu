@@ -10,8 +10,8 @@
 // bound by HBM bandwidth; small calls by the latency of their four dependent
 // phases, which is why they share one launch:
 //
-//   0  router logits (warp-level bf16 MMAs, 16 experts x 8 tokens a CTA) and x
-//      as fp16 with one power-of-two factor per token
+//   0  router logits (warp-level bf16 MMAs, 16 experts x 8 tokens and a part of
+//      H a CTA) and x as fp16 with one power-of-two factor per token
 //      -- grid barrier --
 //   1  every CTA picks the experts itself (a warp per token) and lists the
 //      tokens of each expert in groups of up to 8 or 16
@@ -126,15 +126,17 @@ struct Params {
     const uint16_t* router;
     uint16_t* y;
     uint32_t* control;     // epoch, then two sets of barrier counts
-    float* logits;         // [T, E]
+    float* logits;         // [splits, T, E], the parts of H in order
     uint16_t* x16;         // [T, H]
     float* xfactor;        // [T]
     uint8_t* h;            // [T k, I / 32] records
     float* part;           // [T k, H]
     int T, E, k, H, I;
+    int splits;            // parts of H in the router product
     int renormalize;
 };
 constexpr int kBarriers = 3;
+constexpr int kMaxSplits = 4;
 
 __device__ __forceinline__ void fail(volatile int* abort) {
     *abort = 1;
@@ -220,18 +222,20 @@ __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 // ---------------------------------------------------------------------------
 // phase 0
 // ---------------------------------------------------------------------------
-// Logits of 16 experts x 8 tokens: the consumer warps take 32-element blocks of
-// H in turn and their sums meet in shared memory.
-__device__ void router_tile(const Params& p, float (*scratch)[4][32], int e0, int t0, int warp, int lane) {
+// Logits of 16 experts x 8 tokens over part `part` of H: the consumer warps take
+// 32-element blocks in turn and their sums meet in shared memory. One CTA's
+// loads of a whole 16 x 4096 slice of the router took 5 us; in four parts they
+// are one round trip (16 tokens, 64 experts of 4096 x 1024: 87.0 -> 85.0 us).
+__device__ void router_tile(const Params& p, float (*scratch)[4][32], int e0, int t0, int part, int warp, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const int blocks = p.H >> 5;
+    const int all = p.H >> 5, first = all * part / p.splits, blocks = all * (part + 1) / p.splits;
     const bool ok0 = e0 + g < p.E, ok1 = e0 + g + 8 < p.E, okx = t0 + g < p.T;
     const uint4* r0 = reinterpret_cast<const uint4*>(p.router + static_cast<size_t>(ok0 ? e0 + g : 0) * p.H) + t;
     const uint4* r1 = reinterpret_cast<const uint4*>(p.router + static_cast<size_t>(ok1 ? e0 + g + 8 : 0) * p.H) + t;
     const uint4* xr = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(okx ? t0 + g : 0) * p.H) + t;
     float d[4] = {0.f, 0.f, 0.f, 0.f};
     constexpr int kBatch = 4;
-    for (int b = warp; b < blocks; b += kConsumerWarps * kBatch) {
+    for (int b = first + warp; b < blocks; b += kConsumerWarps * kBatch) {
         uint4 a0[kBatch], a1[kBatch], xb[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
@@ -257,7 +261,7 @@ __device__ void router_tile(const Params& p, float (*scratch)[4][32], int e0, in
 #pragma unroll
         for (int w = 0; w < kConsumerWarps; ++w) s += scratch[w][i][lane];
         const int e = e0 + g + (i >> 1) * 8, tok = t0 + 2 * t + (i & 1);
-        if (e < p.E && tok < p.T) __stcg(p.logits + static_cast<size_t>(tok) * p.E + e, s);
+        if (e < p.E && tok < p.T) __stcg(p.logits + (static_cast<size_t>(part) * p.T + tok) * p.E + e, s);
     }
     consumer_sync();
 }
@@ -317,7 +321,19 @@ __device__ __forceinline__ void pick_experts(const Params& p, Shared<kGroup>* sm
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         id[i] = lane + 32 * i;
-        key[i] = id[i] < static_cast<uint32_t>(p.E) ? order_key(__ldcg(row + id[i])) : 0u;   // 0: absent
+        key[i] = 0u;   // absent
+        if (id[i] < static_cast<uint32_t>(p.E)) {
+            float v = __ldcg(row + id[i]);
+            if (p.splits > 1) {
+                float part[kMaxSplits - 1];
+#pragma unroll
+                for (int q = 1; q < kMaxSplits; ++q)
+                    part[q - 1] = q < p.splits ? __ldcg(row + static_cast<size_t>(q) * p.T * p.E + id[i]) : 0.f;
+#pragma unroll
+                for (int q = 1; q < kMaxSplits; ++q) v += part[q - 1];
+            }
+            key[i] = order_key(v);
+        }
     }
     float total = 0.f;
     if (!p.renormalize) {
@@ -525,12 +541,13 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
     // ---------------------------------------------------------------- phase 0
     if (warp < kConsumerWarps) {
         float(*scratch)[4][32] = reinterpret_cast<float(*)[4][32]>(&sm->red[0][0][0][0]);
-        const int etiles = (p.E + 15) >> 4, tiles = etiles * ((p.T + 7) >> 3);
-        for (int u = cta; u < tiles + p.T; u += grid) {
-            if (u < tiles)
-                router_tile(p, scratch, (u % etiles) * 16, (u / etiles) * 8, warp, lane);
+        const int etiles = (p.E + 15) >> 4, tiles = etiles * ((p.T + 7) >> 3), units = tiles * p.splits;
+        for (int u = cta; u < units + p.T; u += grid) {
+            const int tile = u % tiles;
+            if (u < units)
+                router_tile(p, scratch, (tile % etiles) * 16, (tile / etiles) * 8, u / tiles, warp, lane);
             else
-                convert_token(p, scratch, u - tiles, warp, lane);
+                convert_token(p, scratch, u - units, warp, lane);
         }
         fence_proxy_async_global();   // x16 is read by bulk copies
     }
@@ -857,7 +874,7 @@ Layout layout(int T, int E, int k, int H, int I) {
         return here;
     };
     const size_t slots = static_cast<size_t>(T) * k;
-    l.logits = take(static_cast<size_t>(T) * E * 4);
+    l.logits = take(static_cast<size_t>(kMaxSplits) * T * E * 4);
     l.x16 = take(static_cast<size_t>(T) * H * 2);
     l.xfactor = take(static_cast<size_t>(T) * 4);
     l.h = take(slots * (I / 32) * kHRecord);
@@ -872,7 +889,7 @@ bool slots_per_expert_over(const MxMoeArgs& a, int n) {
 }
 
 template <int kGroup>
-cudaError_t launch_group(const CUtensorMap (&maps)[4], const Params& p, const DeviceProps& dp, cudaStream_t s) {
+cudaError_t launch_group(const CUtensorMap (&maps)[4], Params p, const DeviceProps& dp, cudaStream_t s) {
     auto kern = moe_kernel<kGroup>;
     if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), dp.device, smem_bytes<kGroup>());
         e != cudaSuccess)
@@ -881,7 +898,11 @@ cudaError_t launch_group(const CUtensorMap (&maps)[4], const Params& p, const De
     const long long slots = static_cast<long long>(p.T) * p.k;
     const long long want = slots * std::max<long long>(p.I / 32, (p.H + 63) / 64);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(want, dp.sms)));
+    const int grid = static_cast<int>(std::min<long long>(want, dp.sms));
+    // router: as many parts of H as leave one unit (tile and part, or token to convert) per CTA, 512 or more deep
+    const int tiles = (p.E + 15) / 16 * ((p.T + 7) / 8);
+    p.splits = std::max(1, std::min({kMaxSplits, (grid - p.T) / tiles, p.H / 512}));
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem_bytes<kGroup>();
     cfg.stream = s;
