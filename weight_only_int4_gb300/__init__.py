@@ -103,12 +103,16 @@ def abi_version() -> int:
 
 
 _torch_module = None
+_raw_stream = None   # device -> handle of its current stream; the object torch.cuda.current_stream() builds costs 3 us
+_dtype_codes = {}
 
 
 def _torch():
-    global _torch_module
+    global _torch_module, _raw_stream
     if _torch_module is None:
         import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _dtype_codes.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
         _torch_module = torch
     return _torch_module
 
@@ -117,10 +121,9 @@ def _stream_ptr(stream=None) -> int:
     """Raw handle of `stream`, or of the current stream of the current device."""
     if stream is not None:
         return int(stream.cuda_stream)
-    torch = _torch()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    # the stream object that torch.cuda.current_stream() builds costs 3 us a call
-    return int(torch.cuda.current_stream().cuda_stream) if raw is None else raw(torch.cuda.current_device())
+    if _raw_stream is None:
+        return int(_torch().cuda.current_stream().cuda_stream)
+    return _raw_stream(_torch_module.cuda.current_device())
 
 
 def _check(fn: str, status: int) -> None:
@@ -138,12 +141,11 @@ def _act_code(dtype) -> int:
 
 
 def _dtype_code(dtype) -> int:
-    torch = _torch()
-    if dtype == torch.float32:
-        return F32
-    if dtype in (torch.float16, torch.bfloat16):
-        return _act_code(dtype)
-    raise TypeError(f"dtype must be float16, bfloat16 or float32, got {dtype}")
+    _torch()
+    code = _dtype_codes.get(dtype)
+    if code is None:
+        raise TypeError(f"dtype must be float16, bfloat16 or float32, got {dtype}")
+    return code
 
 
 def _cuda_contig(name: str, t) -> None:
@@ -463,8 +465,9 @@ def _mx_rows(name: str, codes, escale):
     shape = codes.shape
     if len(shape) != 2 or codes.dtype != torch.int32:
         raise TypeError(f"{name} must be a 2-D torch.int32 tensor of codes")
-    R, K = shape[0], shape[1] * 8
-    if escale.dtype != torch.uint8 or tuple(escale.shape) != mxfp4_scale_shape(R, K):
+    R, words = shape
+    K = words * 8
+    if escale.dtype != torch.uint8 or escale.shape != (-(-R // 128), -(-K // 128), 32, 4, 4):
         raise ValueError(f"{name} scales must be torch.uint8 {mxfp4_scale_shape(R, K)}, got {escale.dtype} "
                          f"{tuple(escale.shape)}")
     return R, K

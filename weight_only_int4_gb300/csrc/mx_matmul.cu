@@ -443,7 +443,7 @@ __device__ __forceinline__ int unit_owner(long long u, long long U, int G) {
 template <int kOut, int MP>
 __global__ void __launch_bounds__(kThreads, 1)
 rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
-            const __grid_constant__ CUtensorMap tsw, const __grid_constant__ CUtensorMap tsx, void* __restrict__ y,
+            const uint8_t* __restrict__ ew, const uint8_t* __restrict__ ex, void* __restrict__ y,
             int M, int N, int K, int split, int share, float* __restrict__ partials,
             uint32_t* __restrict__ tickets) {
     using C = Cfg<MP>;
@@ -462,7 +462,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int num_m = (M + MP - 1) / MP, num_n = (N + BN - 1) / BN;
-    const int kt_total = (K + kStepK - 1) / kStepK;
+    const int kt_total = (K + kStepK - 1) / kStepK, groups = (K + 127) >> 7;
     const int G = gridDim.x;
     const long long T = static_cast<long long>(num_m) * num_n, U = T * kt_total;
     const int part_k = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -491,8 +491,6 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
         fence_mbar_init();
         tma_prefetch_desc(&tw);
         tma_prefetch_desc(&tx);
-        tma_prefetch_desc(&tsw);
-        tma_prefetch_desc(&tsx);
     }
     if (warp == 2) tmem_alloc(smem_u32(&bars->tmem_base), C::kTmemCols);
     tc_fence_before();
@@ -516,11 +514,14 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
                 for (int kt = k0; kt < k1; ++kt) {
                     if (!wait_bar(smem_u32(&bars->empty[s]), parity, ab)) { ok = false; break; }
                     const uint32_t fb = smem_u32(&bars->full[s]);
-                    mbar_arrive_expect_tx(fb, C::kStageBytes);
+                    // the exponent tiles of a row tile lie one after the other along K
+                    const uint32_t sf = min(2, groups - 2 * kt) * kScaleTile;
+                    mbar_arrive_expect_tx(fb, C::kABytes + C::kXBytes + 2 * sf);
                     tma_load_2d(st_w(s), &tw, kt * static_cast<int>(kRowBytes), n_blk * BN, fb);
                     tma_load_2d(st_x(s), &tx, kt * static_cast<int>(kRowBytes), m_blk * MP, fb);
-                    tma_load_3d(st_sw(s), &tsw, 0, 2 * kt, n_blk, fb);
-                    tma_load_3d(st_sx(s), &tsx, 0, 2 * kt, m_blk * MP / 128, fb);
+                    bulk_load(st_sw(s), ew + (static_cast<size_t>(n_blk) * groups + 2 * kt) * kScaleTile, sf, fb);
+                    bulk_load(st_sx(s), ex + (static_cast<size_t>(m_blk * MP / 128) * groups + 2 * kt) * kScaleTile, sf,
+                              fb);
                     ++steps;
                     if (++s == S) s = 0, parity ^= 1u;
                 }
@@ -807,9 +808,8 @@ cudaError_t launch_rows(const MxMatmulArgs& a, const Plan& pl, float* partials, 
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
     if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), dp.device, kSmem); e != cudaSuccess)
         return e;
-    CUtensorMap tw, tx, tsw, tsx;
-    if (!encode_codes(&tw, a.b, a.N, a.K, rows::BN) || !encode_codes(&tx, a.a, a.M, a.K, MP) ||
-        !encode_scales(&tsw, a.eb, a.N, a.K, 1) || !encode_scales(&tsx, a.ea, a.M, a.K, 1))
+    CUtensorMap tw, tx;
+    if (!encode_codes(&tw, a.b, a.N, a.K, rows::BN) || !encode_codes(&tx, a.a, a.M, a.K, MP))
         return cudaErrorInvalidValue;
     const long long tiles = static_cast<long long>((a.M + MP - 1) / MP) * ((a.N + rows::BN - 1) / rows::BN);
     const long long units = tiles * ((a.K + kStepK - 1) / kStepK);
@@ -831,7 +831,7 @@ cudaError_t launch_rows(const MxMatmulArgs& a, const Plan& pl, float* partials, 
     }
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tw, tx, tsw, tsx, a.y, a.M, a.N, a.K, pl.split, pl.share ? 1 : 0,
+    return cudaLaunchKernelEx(&cfg, kern, tw, tx, a.eb, a.ea, a.y, a.M, a.N, a.K, pl.split, pl.share ? 1 : 0,
                               partials, tickets);
 }
 
