@@ -76,7 +76,9 @@ constexpr uint32_t kBoxBytes = kStepK / 8 * 128;     // 64 word rows x 32 column
 constexpr uint32_t kScaleBoxBytes = kBlocks * 32;
 constexpr uint32_t kWeightBytes = 2 * kBoxBytes + 2 * kScaleBoxBytes;
 static_assert(kWeightBytes % 1024 == 0, "swizzled boxes start 1024-byte aligned");
-constexpr uint32_t kHRecord = 80;        // a run of h: 32 fp16 values, the FP32 factor 2^-shift, padding to 16 bytes
+// A run of h: 32 fp16 values, then the FP32 factor 2^-shift four times: lanes that read the factors of rows 0, 2, 4, 6
+// (or 1, 3, 5, 7), whose strides share a bank, take a copy each.
+constexpr uint32_t kHRecord = 80;
 constexpr uint32_t kXStride = kBlocks * kHRecord + 64;   // a row of a stage; two rows' 64 bytes hit different banks
 constexpr int kRedPitch = 33;            // floats per slot of a warp's partial sums
 constexpr unsigned long long kWaitLimitCycles = 4000000000ull;   // ~2 s at 2 GHz
@@ -690,7 +692,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                     }
                     const uint32_t stage = ring_base + s * kWeightBytes, weights = stage + box * kBoxBytes;
                     const uint32_t in = rows_base + s * C::kRowBytes + c0 * kRec;
-                    const uint32_t rows = in + g * kXStride + t * 16, factors = in + 2 * t * kXStride + 64;
+                    const uint32_t rows = in + g * kXStride + t * 16, factors = in + 2 * t * kXStride + 64 + 4 * t;
                     uint32_t e4[kWarpBlocks];
 #pragma unroll
                     for (int i = 0; i < kWarpBlocks; ++i)
@@ -786,7 +788,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm->taken[b]));
             if (lane < n && ((lane >> 1) & 1) == half)
-                __stcg(reinterpret_cast<float*>(p.h + (static_cast<size_t>(slot) * blocks3 + cb) * kHRecord + 64), back);
+                __stcg(reinterpret_cast<float4*>(p.h + (static_cast<size_t>(slot) * blocks3 + cb) * kHRecord + 64),
+                       make_float4(back, back, back, back));
         }
         fence_proxy_async_global();   // h is read by bulk copies
         auto epilogue_sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(kEpilogues * 32) : "memory"); };
