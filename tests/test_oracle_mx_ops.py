@@ -110,3 +110,12 @@ def test_one_expert_is_a_plain_gated_mlp():
     a = x @ (e2m1_decode(w13[0]) / 8)
     h = a[:, :inner] / (1 + np.exp(-a[:, :inner])) * a[:, inner:]
     assert np.allclose(y, h @ (e2m1_decode(w2[0]) / 4))
+
+
+def test_byte_counts():
+    from weight_only_int4_gb300.accounting import mx_matmul_bytes, mx_moe_bytes, mx_quantize_bytes
+    assert mx_quantize_bytes(64, 2) == 64 * 2 + 32 + 2
+    assert mx_matmul_bytes(2, 8, 64, 4) == 2 * 34 + 8 * 34 + 2 * 8 * 4
+    # one token reads its k experts; with k = E every expert is read
+    assert mx_moe_bytes(1, 8, 2, 64, 32) == 2 * 3 * 64 * 32 * 17 // 32 + 8 * 64 * 2 + 2 * 64 * 2
+    assert mx_moe_bytes(5, 4, 4, 64, 32) == 4 * 3 * 64 * 32 * 17 // 32 + 4 * 64 * 2 + 2 * 5 * 64 * 2

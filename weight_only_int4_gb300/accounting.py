@@ -70,5 +70,23 @@ def mx_dequant_bytes(N: int, K: int) -> LayerBytes:
     return LayerBytes(weights=b.weights, scales=b.scales, zeros=0, x=0, y=K * N * 2)
 
 
+def mx_quantize_bytes(elements: int, in_bytes: int = 2) -> int:
+    """Quantisation to MXFP4: the input once, 4-bit codes and one byte per 32 elements."""
+    return elements * in_bytes + elements // 2 + elements // 32
+
+
+def mx_matmul_bytes(M: int, N: int, K: int, out_bytes: int = 2) -> int:
+    """Product of two MXFP4 operands [M, K] and [N, K]: each once, and y [M, N]."""
+    return (M + N) * (K // 2 + K // 32) + M * N * out_bytes
+
+
+def mx_moe_bytes(T: int, E: int, top_k: int, H: int, I: int) -> int:
+    """Mixture-of-experts layer: router and x, y, and the weights of the experts
+    at least one of T tokens chooses, E (1 - (1 - k/E)^T) of them when all are
+    equally likely."""
+    active = E * (1.0 - (1.0 - top_k / E) ** T)
+    return int(active * 3 * H * I * (1 / 2 + 1 / 32)) + E * H * 2 + 2 * T * H * 2
+
+
 def layer_flops(M: int, N: int, K: int) -> int:
     return 2 * M * N * K
