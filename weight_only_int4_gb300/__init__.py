@@ -216,10 +216,10 @@ def _cached_workspace(nbytes: int, device, stream, op: int):
     through an earlier call may still replay into it."""
     torch = _torch()
     dev = device.index if device.index is not None else torch.cuda.current_device()
-    if stream is None and dev == torch.cuda.current_device():
-        handle = _stream_ptr()
+    if stream is not None:
+        handle = int(stream.cuda_stream)
     else:
-        handle = int((torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream)
+        handle = int(torch.cuda.current_stream(dev).cuda_stream) if _raw_stream is None else _raw_stream(dev)
     key = (dev, handle, op)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
@@ -496,9 +496,19 @@ def mxfp4_tile_scales(escale, out=None, stream=None):
     return out
 
 
-def _workspace(given, need: int, device, stream, op):
-    """(address, bytes) of the caller's workspace or the binding's own."""
+_workspace_needs = {}
+
+
+def _workspace(given, op, query, shape, device, stream):
+    """(address, bytes) of the caller's workspace or the binding's own, which
+    needs query(*shape) bytes; the sizes of the last few hundred shapes are kept."""
     if given is None:
+        key = (op, device.index, shape)
+        need = _workspace_needs.get(key)
+        if need is None:
+            if len(_workspace_needs) >= 512:
+                _workspace_needs.clear()
+            need = _workspace_needs[key] = int(query(*shape))
         if not need:
             return 0, 0
         given = _cached_workspace(need, device, stream, op)
@@ -520,8 +530,8 @@ def mxfp4_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, workspace=Non
     lib = load_library()
     device = a.device
     out = _out("out", out, (M, N), out_dtype, device, stream)
-    need = lib.w4a16_workspace_bytes(OP_MXFP4_MATMUL, M, N, K, 32) if workspace is None else 0
-    ws_ptr, ws_bytes = _workspace(workspace, need, device, stream, OP_MXFP4_MATMUL)
+    ws_ptr, ws_bytes = _workspace(workspace, OP_MXFP4_MATMUL, lib.w4a16_workspace_bytes,
+                                  (OP_MXFP4_MATMUL, M, N, K, 32), device, stream)
     st = lib.w4a16_mxfp4_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr(),
                                 M, N, K, dt, ws_ptr, ws_bytes, _stream_ptr(stream))
     _check("w4a16_mxfp4_matmul", st)
@@ -555,8 +565,8 @@ def mxfp4_moe(x, router, w13, e13, w2, e2, top_k: int, renormalize: bool = True,
     lib = load_library()
     device = x.device
     out = _out("out", out, (T, H), bf16, device, stream)
-    need = lib.w4a16_mxfp4_moe_workspace_bytes(T, E, top_k, H, I) if workspace is None else 0
-    ws_ptr, ws_bytes = _workspace(workspace, need, device, stream, "mxfp4_moe")
+    ws_ptr, ws_bytes = _workspace(workspace, "mxfp4_moe", lib.w4a16_mxfp4_moe_workspace_bytes, (T, E, top_k, H, I),
+                                  device, stream)
     st = lib.w4a16_mxfp4_moe(x.data_ptr(), router.data_ptr(), w13.data_ptr(), e13.data_ptr(), w2.data_ptr(),
                              e2.data_ptr(), out.data_ptr(), T, E, top_k, H, I, 1 if renormalize else 0, ws_ptr,
                              ws_bytes, _stream_ptr(stream))
