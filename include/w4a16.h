@@ -458,9 +458,9 @@ w4a16_status w4a16_mxfp4_matmul(const int32_t* a, const uint8_t* ea, const int32
  * enter the products as fp16 scaled by powers of two (x per token, h per 32
  * columns): x converts exactly where it is within 2^-29 of its token's largest
  * magnitude, h is rounded to 11 bits. Weights of a chosen expert are read once
- * per 16 tokens that chose it; experts nobody chose are not read. A token's y
- * does not depend on the other tokens, except that tokens beyond 16 of one
- * expert are taken in further groups; the result is deterministic. A token with
+ * per 8 tokens that chose it (again mostly from L2); experts nobody chose are not
+ * read. A token's y does not depend on the other tokens, bit for bit, and the
+ * result is deterministic. A token with
  * an infinity or NaN in x or in a chosen expert's block yields NaN there and
  * leaves other tokens alone.
  *

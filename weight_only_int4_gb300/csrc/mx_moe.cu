@@ -14,7 +14,7 @@
 //      H a CTA) and x as fp16 with one power-of-two factor per token
 //      -- grid barrier --
 //   1  every CTA picks the experts itself (a warp per token) and lists the
-//      tokens of each expert in groups of up to 8 or 16
+//      tokens of each expert in groups of up to 8
 //   2  items (group, 32 gate columns and their 32 up columns): products, SwiGLU,
 //      h as fp16 with one power of two per 32 columns
 //      -- grid barrier (weights of phase 3 are already on their way) --
@@ -84,25 +84,24 @@ constexpr int kRedPitch = 33;            // floats per slot of a warp's partial 
 constexpr unsigned long long kWaitLimitCycles = 4000000000ull;   // ~2 s at 2 GHz
 constexpr unsigned int kErrTimeout = 9u;
 
-// kGroup: tokens of an expert taken together, 8 or 16.
-template <int kGroup>
-struct Cfg {
-    static constexpr int kTiles = kGroup / 8;            // 8-token MMA tiles
-    static constexpr int kRedSlots = kTiles * 8;         // [tile][token parity][column % 4]
-    static constexpr int kBuffers = kGroup == 8 ? 2 : 1;   // of partial sums
-    static constexpr int kSetStages = kGroup == 8 ? 3 : 2;   // half of the ring
-    static constexpr int kStages = 2 * kSetStages;
-    static constexpr uint32_t kRowBytes = kGroup * kXStride;
-};
+// Tokens of an expert taken together: one MMA's columns. With groups of 16 the
+// ring falls from six stages to four and the accumulators spill: 64 tokens of
+// 2048 x 1024 took 174 us against 108 with 4 tokens per expert on average, 86
+// against 76 with 16 and 76 against 71 with 32, where the further groups' weights
+// come from L2.
+constexpr int kGroup = 8;
+constexpr int kRedSlots = 8;                     // [token parity][column % 4]
+constexpr int kBuffers = 2;                      // of partial sums
+constexpr int kSetStages = 3;                    // half of the ring
+constexpr int kStages = 2 * kSetStages;
+constexpr uint32_t kRowBytes = kGroup * kXStride;
 
-template <int kGroup>
 struct __align__(16) Shared {
-    using C = Cfg<kGroup>;
-    float red[C::kBuffers][kConsumerWarps][C::kRedSlots][kRedPitch];
-    uint64_t full[C::kStages];
-    uint64_t empty[C::kStages];
-    uint64_t sums[C::kBuffers];          // a buffer of partial sums is complete
-    uint64_t taken[C::kBuffers];         // ... and has been read
+    float red[kBuffers][kConsumerWarps][kRedSlots][kRedPitch];
+    uint64_t full[kStages];
+    uint64_t empty[kStages];
+    uint64_t sums[kBuffers];          // a buffer of partial sums is complete
+    uint64_t taken[kBuffers];         // ... and has been read
     uint64_t phase3;                     // h of every CTA is visible
     uint64_t phase4;                     // the parts of y are
     uint32_t mask[kMaxExperts][2];       // tokens of each expert
@@ -117,11 +116,8 @@ struct __align__(16) Shared {
     uint32_t epoch;
     int abort;
 };
-template <int kGroup>
-constexpr size_t smem_bytes() {
-    return 1024 + Cfg<kGroup>::kStages * (kWeightBytes + Cfg<kGroup>::kRowBytes) + sizeof(Shared<kGroup>);
-}
-static_assert(smem_bytes<8>() <= 227 * 1024 && smem_bytes<16>() <= 227 * 1024, "shared memory budget");
+constexpr size_t kSmemBytes = 1024 + kStages * (kWeightBytes + kRowBytes) + sizeof(Shared);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 
 struct Params {
     const uint16_t* x;
@@ -309,8 +305,8 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // lane, lane + 32, ...), then k rounds take the largest head of the 32 lists,
 // the lower expert where heads are equal. Every round takes an expert that was
 // not taken before, whatever the logits hold.
-template <int kPer, int kGroup>
-__device__ __forceinline__ void pick_experts(const Params& p, Shared<kGroup>* sm, int tok, int lane) {
+template <int kPer>
+__device__ __forceinline__ void pick_experts(const Params& p, Shared* sm, int tok, int lane) {
     const float* row = p.logits + static_cast<size_t>(tok) * p.E;
     uint32_t key[kPer], id[kPer];
 #pragma unroll
@@ -384,8 +380,7 @@ __device__ __forceinline__ void pick_experts(const Params& p, Shared<kGroup>* sm
 // Tokens and groups of every expert, numbered in the experts' order: one thread
 // per expert, prefix sums over packed counts (tokens | groups << 16). All
 // threads of the CTA.
-template <int kGroup>
-__device__ __forceinline__ void number_groups(const Params& p, Shared<kGroup>* sm) {
+__device__ __forceinline__ void number_groups(const Params& p, Shared* sm) {
     const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
     int n = 0;
     uint32_t own = 0, at = 0;
@@ -431,26 +426,21 @@ __device__ __forceinline__ void number_groups(const Params& p, Shared<kGroup>* s
 // lane's first 16 bytes of its row g. kH: the rows are records of h, their
 // factors at `factors` for the lane's tokens 2 t and 2 t + 1. kEdge: a byte of 0
 // or 255 may be among the exponents e4.
-template <bool kH, bool kEdge, int kCount, int kTiles>
-__device__ __forceinline__ void block_products(float (&acc)[kTiles][2][4], uint32_t box, const uint32_t (&e4)[4],
-                                               uint32_t rows, uint32_t factors, int c, int first, int tiles, int g,
-                                               int t) {
+template <bool kH, bool kEdge, int kCount>
+__device__ __forceinline__ void block_products(float (&acc)[2][4], uint32_t box, const uint32_t (&e4)[4],
+                                               uint32_t rows, uint32_t factors, int c, int first, int g, int t) {
     const uint32_t chunk = static_cast<uint32_t>((g >> 1) | ((g & 1) << 2));   // quarter-warps hit every bank once
     constexpr uint32_t kRec = kH ? kHRecord : 64;
-    uint4 w[kCount], x[kCount][kTiles];
-    float f0[kCount][kTiles], f1[kCount][kTiles];
+    uint4 w[kCount], x[kCount];
+    float f0[kCount], f1[kCount];
 #pragma unroll
     for (int j = 0; j < kCount; ++j) {
         const int row = 4 * (c + first + j) + t;
         w[j] = ld_shared_v4(box + row * 128 + ((chunk ^ (row & 7)) << 4));
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n) {
-            if (n > 0 && n >= tiles) break;
-            x[j][n] = ld_shared_v4(rows + (first + j) * kRec + n * 8 * kXStride);
-            if constexpr (kH) {
-                f0[j][n] = __uint_as_float(ld_shared_u32(factors + (first + j) * kRec + n * 8 * kXStride));
-                f1[j][n] = __uint_as_float(ld_shared_u32(factors + (first + j) * kRec + n * 8 * kXStride + kXStride));
-            }
+        x[j] = ld_shared_v4(rows + (first + j) * kRec);
+        if constexpr (kH) {
+            f0[j] = __uint_as_float(ld_shared_u32(factors + (first + j) * kRec));
+            f1[j] = __uint_as_float(ld_shared_u32(factors + (first + j) * kRec + kXStride));
         }
     }
 #pragma unroll
@@ -472,40 +462,33 @@ __device__ __forceinline__ void block_products(float (&acc)[kTiles][2][4], uint3
             uint32_t lo[4], hi[4];
             mx::e2m1x8_to_f16x2(words[2 * m], lo);
             mx::e2m1x8_to_f16x2(words[2 * m + 1], hi);
-#pragma unroll
-            for (int n = 0; n < kTiles; ++n) {
-                if (n > 0 && n >= tiles) break;
-                float d[4];
-                mma_f16_zero(d, lo[0], hi[0], lo[1], hi[1], x[j][n].x, x[j][n].y);
-                mma_m16n8k16<false>(d, lo[2], hi[2], lo[3], hi[3], x[j][n].z, x[j][n].w);
-                float(&a)[4] = acc[n][m];
-                if constexpr (kH) {
-                    // d 2^-shift first: the size of h's products, whatever the exponents are
-                    a[0] = fmaf(d[0] * f0[j][n], scale[2 * m], a[0]);
-                    a[1] = fmaf(d[1] * f1[j][n], scale[2 * m], a[1]);
-                    a[2] = fmaf(d[2] * f0[j][n], scale[2 * m + 1], a[2]);
-                    a[3] = fmaf(d[3] * f1[j][n], scale[2 * m + 1], a[3]);
-                } else {
-                    a[0] = fmaf(d[0], scale[2 * m], a[0]);
-                    a[1] = fmaf(d[1], scale[2 * m], a[1]);
-                    a[2] = fmaf(d[2], scale[2 * m + 1], a[2]);
-                    a[3] = fmaf(d[3], scale[2 * m + 1], a[3]);
-                }
+            float d[4];
+            mma_f16_zero(d, lo[0], hi[0], lo[1], hi[1], x[j].x, x[j].y);
+            mma_m16n8k16<false>(d, lo[2], hi[2], lo[3], hi[3], x[j].z, x[j].w);
+            float(&a)[4] = acc[m];
+            if constexpr (kH) {
+                // d 2^-shift first: the size of h's products, whatever the exponents are
+                a[0] = fmaf(d[0] * f0[j], scale[2 * m], a[0]);
+                a[1] = fmaf(d[1] * f1[j], scale[2 * m], a[1]);
+                a[2] = fmaf(d[2] * f0[j], scale[2 * m + 1], a[2]);
+                a[3] = fmaf(d[3] * f1[j], scale[2 * m + 1], a[3]);
+            } else {
+                a[0] = fmaf(d[0], scale[2 * m], a[0]);
+                a[1] = fmaf(d[1], scale[2 * m], a[1]);
+                a[2] = fmaf(d[2], scale[2 * m + 1], a[2]);
+                a[3] = fmaf(d[3], scale[2 * m + 1], a[3]);
             }
         }
     }
 }
 
-template <int kGroup>
 __global__ void __launch_bounds__(kThreads, 1)
 moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUtensorMap te13,
            const __grid_constant__ CUtensorMap tw2, const __grid_constant__ CUtensorMap te2, const Params p) {
-    using C = Cfg<kGroup>;
-    constexpr int kTiles = C::kTiles, kBuffers = C::kBuffers, kSetStages = C::kSetStages, kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t ring_base = smem_u32(ring), rows_base = ring_base + kStages * kWeightBytes;
-    Shared<kGroup>* sm = reinterpret_cast<Shared<kGroup>*>(ring + kStages * (kWeightBytes + C::kRowBytes));
+    Shared* sm = reinterpret_cast<Shared*>(ring + kStages * (kWeightBytes + kRowBytes));
     volatile int* abort = &sm->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int grid = gridDim.x, cta = blockIdx.x;
@@ -599,7 +582,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
             uint32_t held_bytes[kSetStages] = {};
             const uint8_t* held_src[kSetStages] = {};
             auto rows = [&](int s, const uint8_t* src, uint32_t bytes) {   // one row per lane
-                if (src) bulk_load(rows_base + s * C::kRowBytes + lane * kXStride, src, bytes, smem_u32(&sm->full[s]));
+                if (src) bulk_load(rows_base + s * kRowBytes + lane * kXStride, src, bytes, smem_u32(&sm->full[s]));
             };
             auto release = [&] {
                 ok = ok && warp_wait_bar(&sm->phase3, 0, abort);
@@ -675,14 +658,11 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
             const int blocks = kH ? blocks3 : blocks2, steps = kH ? steps3 : steps2;
             for (int item = cta; item < items; item += grid, ++count) {
                 const int gi = item / cols, cb = item - gi * cols;
-                const int tiles = ((sm->group[gi] >> 16) + 7) >> 3;
-                float acc[kTiles][2][4];
+                float acc[2][4];
 #pragma unroll
-                for (int a = 0; a < kTiles; ++a)
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[a][m][i] = 0.f;
+                    for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
                 for (int ks = (cb ^ set) & 1; ks < steps; ks += 2, ++used) {
                     const int here = blocks - ks * kBlocks - c0;   // of the warp's blocks, those that exist
                     const int s = set * kSetStages + static_cast<int>(used % kSetStages);
@@ -691,7 +671,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                         continue;
                     }
                     const uint32_t stage = ring_base + s * kWeightBytes, weights = stage + box * kBoxBytes;
-                    const uint32_t in = rows_base + s * C::kRowBytes + c0 * kRec;
+                    const uint32_t in = rows_base + s * kRowBytes + c0 * kRec;
                     const uint32_t rows = in + g * kXStride + t * 16, factors = in + 2 * t * kXStride + 64 + 4 * t;
                     uint32_t e4[kWarpBlocks];
 #pragma unroll
@@ -704,28 +684,24 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
 #pragma unroll
                     for (int i = 0; i < kWarpBlocks; ++i) usual &= e4[i] ^ (e4[i] << 1);
                     if (here >= kWarpBlocks && __all_sync(0xffffffffu, usual == 0x80808080u)) {
-                        block_products<kH, false, kWarpBlocks, kTiles>(acc, weights, e4, rows, factors, c0, 0, tiles, g, t);
+                        block_products<kH, false, kWarpBlocks>(acc, weights, e4, rows, factors, c0, 0, g, t);
                     } else {
 #pragma unroll
                         for (int i = 0; i < kWarpBlocks; ++i)
                             if (i < here)
-                                block_products<kH, true, 1, kTiles>(acc, weights, e4, rows, factors, c0, i, tiles, g, t);
+                                block_products<kH, true, 1>(acc, weights, e4, rows, factors, c0, i, g, t);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sm->empty[s]));
                 }
-                // sums to the item's buffer: slot [tile][token parity][column % 4], at the lane that holds them
+                // sums to the item's buffer: slot [token parity][column % 4], at the lane that holds them
                 const int b = static_cast<int>(count % kBuffers);
                 if (ok) ok = warp_wait_bar(&sm->taken[b], (count / kBuffers & 1u) ^ 1u, abort);
 #pragma unroll
-                for (int a = 0; a < kTiles; ++a) {
-                    if (a > 0 && a >= tiles) break;
+                for (int m = 0; m < 2; ++m)       // columns 2 m and 2 m + 1 of every four
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)       // columns 2 m and 2 m + 1 of every four
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)   // fragment: column i >> 1, token parity i & 1
-                            sm->red[b][warp][a * 8 + (i & 1) * 4 + m * 2 + (i >> 1)][lane] = acc[a][m][i];
-                }
+                    for (int i = 0; i < 4; ++i)   // fragment: column i >> 1, token parity i & 1
+                        sm->red[b][warp][(i & 1) * 4 + m * 2 + (i >> 1)][lane] = acc[m][i];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm->sums[b]));
             }
@@ -739,8 +715,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
         bool ok = alive;
         // token n of the group, column `lane` of box `box`: the warps' parts in order
         auto total = [&](int b, int n, int box) {
-            const int chunk = lane >> 2, slot = (n >> 3) * 8 + (n & 1) * 4 + (lane & 3);
-            const int from = (((chunk & 3) << 1) | (chunk >> 2)) * 4 + ((n & 7) >> 1);
+            const int chunk = lane >> 2, slot = (n & 1) * 4 + (lane & 3);
+            const int from = (((chunk & 3) << 1) | (chunk >> 2)) * 4 + (n >> 1);
             float s = 0.f;
 #pragma unroll
             for (int q = 0; q < 2; ++q)
@@ -879,15 +855,8 @@ Layout layout(int T, int E, int k, int H, int I) {
     return l;
 }
 
-// Whether the experts have more than `n` tokens each on average.
-bool slots_per_expert_over(const MxMoeArgs& a, int n) {
-    return static_cast<long long>(a.T) * a.k > static_cast<long long>(n) * a.E;
-}
-
-template <int kGroup>
-cudaError_t launch_group(const CUtensorMap (&maps)[4], Params p, const DeviceProps& dp, cudaStream_t s) {
-    auto kern = moe_kernel<kGroup>;
-    if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), dp.device, smem_bytes<kGroup>());
+cudaError_t launch_kernel(const CUtensorMap (&maps)[4], Params p, const DeviceProps& dp, cudaStream_t s) {
+    if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(moe_kernel), dp.device, kSmemBytes);
         e != cudaSuccess)
         return e;
     // no more CTAs than the larger of the two expert phases can use
@@ -900,7 +869,7 @@ cudaError_t launch_group(const CUtensorMap (&maps)[4], Params p, const DevicePro
     p.splits = std::max(1, std::min({kMaxSplits, (grid - p.T) / tiles, p.H / 512}));
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes<kGroup>();
+    cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = s;
     // the CTAs wait for one another at the grid barriers: all of them are resident together or the launch fails
     cudaLaunchAttribute attr[1];
@@ -908,7 +877,7 @@ cudaError_t launch_group(const CUtensorMap (&maps)[4], Params p, const DevicePro
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p);
+    return cudaLaunchKernelEx(&cfg, moe_kernel, maps[0], maps[1], maps[2], maps[3], p);
 }
 
 }  // namespace
@@ -945,9 +914,7 @@ cudaError_t launch_mx_moe(const MxMoeArgs& a, void* workspace, const DeviceProps
     p.H = a.H;
     p.I = a.I;
     p.renormalize = a.renormalize ? 1 : 0;
-    // Groups of 16 cost ring stages; they pay where experts have more than 8 tokens (6 on average, and more) to read
-    // their weights once for.
-    return a.T > 8 && slots_per_expert_over(a, 6) ? launch_group<16>(maps, p, dp, s) : launch_group<8>(maps, p, dp, s);
+    return launch_kernel(maps, p, dp, s);
 }
 
 cudaError_t read_and_clear_mx_moe_error(uint32_t* out) {
