@@ -72,6 +72,7 @@ constexpr int kWarpBlocks = 4;           // consecutive 32-row blocks of a box t
 constexpr int kSlices = kBlocks / kWarpBlocks;
 constexpr int kMaxExperts = kMoeMaxExperts;
 constexpr int kMaxSlots = kMoeMaxTokens * kMoeMaxTopK;
+static_assert(kMaxSlots <= 1 << 10 && kMoeMaxTokens <= 1 << 6, "a list entry's 16 bits");
 constexpr uint32_t kBoxBytes = kStepK / 8 * 128;     // 64 word rows x 32 columns
 constexpr uint32_t kScaleBoxBytes = kBlocks * 32;
 constexpr uint32_t kWeightBytes = 2 * kBoxBytes + 2 * kScaleBoxBytes;
@@ -108,7 +109,8 @@ struct __align__(16) Shared {
     float weight[kMaxSlots];             // of slot t * k + j
     uint32_t group[kMaxSlots];           // expert | count << 16
     uint16_t first[kMaxSlots];           // the group's first entry in `list`
-    uint16_t list[kMaxSlots];            // slots, ordered by expert, then token
+    uint16_t list[kMaxSlots];            // slot | token << 10, ordered by expert, then token
+    float xfactor[kMoeMaxTokens];
     uint16_t ids[kMaxSlots];             // expert of slot t * k + j
     uint16_t offset[kMaxExperts];
     uint32_t scan[kMaxExperts / 32];
@@ -208,7 +210,10 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
+// The fast division is within 2 units in the last place, and 0 where exp(-g) is
+// beyond 2^126 (silu below 2^-119); it has no branch, so that the epilogue's two
+// tokens overlap.
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + expf(-g)); }
 
 // ---------------------------------------------------------------------------
 // phase 0
@@ -413,7 +418,7 @@ __device__ __forceinline__ void number_groups(const Params& p, Shared* sm) {
     for (int s = threadIdx.x; s < p.T * p.k; s += kThreads) {
         const int ex = sm->ids[s], tok = s / p.k;
         const unsigned long long m = sm->mask[ex][0] | static_cast<unsigned long long>(sm->mask[ex][1]) << 32;
-        sm->list[sm->offset[ex] + __popcll(m & ((1ull << tok) - 1))] = static_cast<uint16_t>(s);
+        sm->list[sm->offset[ex] + __popcll(m & ((1ull << tok) - 1))] = static_cast<uint16_t>(s | tok << 10);
     }
     __syncthreads();
 }
@@ -421,31 +426,50 @@ __device__ __forceinline__ void number_groups(const Params& p, Shared* sm) {
 // ---------------------------------------------------------------------------
 // phases 2 and 3
 // ---------------------------------------------------------------------------
-// kCount 32-row blocks of one box of a stage, from block c on, against the
-// group's rows, added to acc [8-token tile][16-column tile][fragment]. rows: the
-// lane's first 16 bytes of its row g. kH: the rows are records of h, their
-// factors at `factors` for the lane's tokens 2 t and 2 t + 1. kEdge: a byte of 0
-// or 255 may be among the exponents e4.
-template <bool kH, bool kEdge, int kCount>
-__device__ __forceinline__ void block_products(float (&acc)[2][4], uint32_t box, const uint32_t (&e4)[4],
-                                               uint32_t rows, uint32_t factors, int c, int first, int g, int t) {
-    const uint32_t chunk = static_cast<uint32_t>((g >> 1) | ((g & 1) << 2));   // quarter-warps hit every bank once
-    constexpr uint32_t kRec = kH ? kHRecord : 64;
+// A CTA's items, every grid-th: group and column block without a division each.
+struct Walk {
+    int group, column, groups, columns, cols;
+    __device__ __forceinline__ Walk(int item, int grid, int cols)
+        : group(item / cols), column(item - group * cols), groups(grid / cols), columns(grid - groups * cols), cols(cols) {}
+    __device__ __forceinline__ void next() {
+        group += groups;
+        column += columns;
+        if (column >= cols) column -= cols, ++group;
+    }
+};
+
+// What a lane takes of kCount 32-row blocks of one box of a stage, from block
+// c + first on: words of codes, the 16 bytes of its row of activations at `rows`
+// and, where the rows are records of h (kH), the factors of its tokens 2 t and
+// 2 t + 1 at `factors`.
+template <bool kH, int kCount>
+struct Operands {
     uint4 w[kCount], x[kCount];
     float f0[kCount], f1[kCount];
+    __device__ __forceinline__ void load(uint32_t box, uint32_t rows, uint32_t factors, int c, int first, int g, int t) {
+        const uint32_t chunk = static_cast<uint32_t>((g >> 1) | ((g & 1) << 2));   // quarter-warps hit every bank once
+        constexpr uint32_t kRec = kH ? kHRecord : 64;
 #pragma unroll
-    for (int j = 0; j < kCount; ++j) {
-        const int row = 4 * (c + first + j) + t;
-        w[j] = ld_shared_v4(box + row * 128 + ((chunk ^ (row & 7)) << 4));
-        x[j] = ld_shared_v4(rows + (first + j) * kRec);
-        if constexpr (kH) {
-            f0[j] = __uint_as_float(ld_shared_u32(factors + (first + j) * kRec));
-            f1[j] = __uint_as_float(ld_shared_u32(factors + (first + j) * kRec + kXStride));
+        for (int j = 0; j < kCount; ++j) {
+            const int row = 4 * (c + first + j) + t;
+            w[j] = ld_shared_v4(box + row * 128 + ((chunk ^ (row & 7)) << 4));
+            x[j] = ld_shared_v4(rows + (first + j) * kRec);
+            if constexpr (kH) {
+                f0[j] = __uint_as_float(ld_shared_u32(factors + (first + j) * kRec));
+                f1[j] = __uint_as_float(ld_shared_u32(factors + (first + j) * kRec + kXStride));
+            }
         }
     }
+};
+
+// Their products added to acc [16-column tile][fragment]. kEdge: a byte of 0 or
+// 255 may be among the exponents e4.
+template <bool kEdge, bool kH, int kCount>
+__device__ __forceinline__ void add_products(float (&acc)[2][4], const Operands<kH, kCount>& o,
+                                             const uint32_t (&e4)[4], int first) {
 #pragma unroll
     for (int j = 0; j < kCount; ++j) {
-        const uint32_t words[4] = {w[j].x, w[j].y, w[j].z, w[j].w}, e = e4[first + j];
+        const uint32_t words[4] = {o.w[j].x, o.w[j].y, o.w[j].z, o.w[j].w}, e = e4[first + j];
         // 2^(e - 127): the byte as an FP32 exponent field, right for 1..254
         float scale[4];
         if constexpr (kEdge) {
@@ -463,15 +487,15 @@ __device__ __forceinline__ void block_products(float (&acc)[2][4], uint32_t box,
             mx::e2m1x8_to_f16x2(words[2 * m], lo);
             mx::e2m1x8_to_f16x2(words[2 * m + 1], hi);
             float d[4];
-            mma_f16_zero(d, lo[0], hi[0], lo[1], hi[1], x[j].x, x[j].y);
-            mma_m16n8k16<false>(d, lo[2], hi[2], lo[3], hi[3], x[j].z, x[j].w);
+            mma_f16_zero(d, lo[0], hi[0], lo[1], hi[1], o.x[j].x, o.x[j].y);
+            mma_m16n8k16<false>(d, lo[2], hi[2], lo[3], hi[3], o.x[j].z, o.x[j].w);
             float(&a)[4] = acc[m];
             if constexpr (kH) {
                 // d 2^-shift first: the size of h's products, whatever the exponents are
-                a[0] = fmaf(d[0] * f0[j], scale[2 * m], a[0]);
-                a[1] = fmaf(d[1] * f1[j], scale[2 * m], a[1]);
-                a[2] = fmaf(d[2] * f0[j], scale[2 * m + 1], a[2]);
-                a[3] = fmaf(d[3] * f1[j], scale[2 * m + 1], a[3]);
+                a[0] = fmaf(d[0] * o.f0[j], scale[2 * m], a[0]);
+                a[1] = fmaf(d[1] * o.f1[j], scale[2 * m], a[1]);
+                a[2] = fmaf(d[2] * o.f0[j], scale[2 * m + 1], a[2]);
+                a[3] = fmaf(d[3] * o.f1[j], scale[2 * m + 1], a[3]);
             } else {
                 a[0] = fmaf(d[0], scale[2 * m], a[0]);
                 a[1] = fmaf(d[1], scale[2 * m], a[1]);
@@ -544,6 +568,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
     // ---------------------------------------------------------------- phase 1
     const bool alive = *abort == 0;
     if (alive) {
+        if (threadIdx.x < p.T) sm->xfactor[threadIdx.x] = __ldcg(p.xfactor + threadIdx.x);
         for (int tok = warp; tok < p.T; tok += kThreads / 32) {
             if (p.E <= 64)
                 pick_experts<2>(p, sm, tok, lane);
@@ -566,6 +591,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
         // ------------------------------------------------------------ producers, one per set
         const int set = warp - kConsumerWarps - kEpilogues;
         int slot = 0, seen = 0;
+        uint32_t base = 0;   // the item's first stage among all of the CTA's
         uint32_t parity = 1u;
         bool ok = alive;
         fence_proxy_async_global();
@@ -592,18 +618,19 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                     if (ok && i < held) rows(held_slot[i], held_src[i], held_bytes[i]);
                 open = true;
             };
-            for (int item = cta; item < items && ok; item += grid) {
-                const int gi = item / cols, cb = item - gi * cols;
+            Walk at(cta, grid, cols);
+            for (int item = cta; item < items && ok; item += grid, at.next(), base += steps) {
+                const int gi = at.group, cb = at.column;
                 const uint32_t gr = sm->group[gi];
                 const int n = gr >> 16, kb0 = static_cast<int>(gr & 0xFFFFu) * blocks;   // 32-row block of the stack
                 const int c0 = kH ? cb * 64 : cb * 32, c1 = kH ? c0 + 32 : p.I + c0;
                 const uint8_t* src = nullptr;
                 if (lane < n) {
-                    const int sl = sm->list[sm->first[gi] + lane];
-                    src = kH ? p.h + static_cast<size_t>(sl) * blocks * kHRecord
-                             : reinterpret_cast<const uint8_t*>(p.x16 + static_cast<size_t>(sl / p.k) * p.H);
+                    const uint32_t sl = sm->list[sm->first[gi] + lane];
+                    src = kH ? p.h + static_cast<size_t>(sl & 1023u) * blocks * kHRecord
+                             : reinterpret_cast<const uint8_t*>(p.x16 + static_cast<size_t>(sl >> 10) * p.H);
                 }
-                for (int ks = (cb ^ set) & 1; ks < steps; ks += 2) {
+                for (int ks = (base ^ set) & 1; ks < steps; ks += 2) {
                     const int s = set * kSetStages + slot, kb = kb0 + ks * kBlocks;
                     if (!warp_wait_bar(&sm->empty[s], parity, abort)) {
                         ok = false;
@@ -648,25 +675,29 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
         // ------------------------------------------------------------ consumers
         const int g = lane >> 2, t = lane & 3;
         const int set = warp >> 3, box = (warp >> 2) & 1, c0 = (warp & 3) * kWarpBlocks;
-        uint32_t used = 0;    // stages of the set's half of the ring so far
+        uint32_t base = 0;    // the item's first stage among all of the CTA's: stage q is set q % 2's
         uint32_t count = 0;   // items so far
-        bool ok = alive;
+        uint32_t parity = 0;  // of the set's next stage
+        int slot = 0;         // ... its place in the set's half of the ring
+        bool ok = alive, next = false;   // next: it was complete when looked at beside the last one's products
         auto phase = [&](auto second) {
             constexpr bool kH = decltype(second)::value;
             constexpr uint32_t kRec = kH ? kHRecord : 64;
-            const int items = kH ? items3 : items2, cols = kH ? cols3 : cols2;
+            const int items = kH ? items3 : items2;
             const int blocks = kH ? blocks3 : blocks2, steps = kH ? steps3 : steps2;
-            for (int item = cta; item < items; item += grid, ++count) {
-                const int gi = item / cols, cb = item - gi * cols;
+            for (int item = cta; item < items; item += grid, ++count, base += steps) {
                 float acc[2][4];
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
-                for (int ks = (cb ^ set) & 1; ks < steps; ks += 2, ++used) {
+                const int b = static_cast<int>(count % kBuffers);
+                const uint32_t turn = (count / kBuffers & 1u) ^ 1u;
+                bool room = mbar_test_wait(smem_u32(&sm->taken[b]), turn);
+                for (int ks = (base ^ set) & 1; ks < steps; ks += 2) {
                     const int here = blocks - ks * kBlocks - c0;   // of the warp's blocks, those that exist
-                    const int s = set * kSetStages + static_cast<int>(used % kSetStages);
-                    if (!ok || !warp_wait_bar(&sm->full[s], used / kSetStages & 1u, abort)) {
+                    const int s = set * kSetStages + slot;
+                    if (!ok || !(__all_sync(0xffffffffu, next) || warp_wait_bar(&sm->full[s], parity, abort))) {
                         ok = false;
                         continue;
                     }
@@ -678,25 +709,40 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                     for (int i = 0; i < kWarpBlocks; ++i)
                         e4[i] = ld_shared_u32(stage + 2 * kBoxBytes + box * kScaleBoxBytes + (c0 + i) * 32 +
                                               ((g >> 1) | ((g & 1) << 2)) * 4);
+                    if (++slot == kSetStages) slot = 0, parity ^= 1u;
+                    const uint32_t empty = smem_u32(&sm->empty[s]);
+                    const uint32_t after = smem_u32(&sm->full[set * kSetStages + slot]);
                     // The usual stage without a branch, so that its blocks overlap: all four blocks, every exponent byte
-                    // in 64..191 (bits 7 and 6 differ; scales 2^-63..2^64), so none is 0 or 255. Else one at a time.
+                    // in 64..191 (bits 7 and 6 differ; scales 2^-63..2^64), so none is 0 or 255. It goes back to the
+                    // producer once the operands are in registers. Else one block at a time.
                     uint32_t usual = 0x80808080u;
 #pragma unroll
                     for (int i = 0; i < kWarpBlocks; ++i) usual &= e4[i] ^ (e4[i] << 1);
-                    if (here >= kWarpBlocks && __all_sync(0xffffffffu, usual == 0x80808080u)) {
-                        block_products<kH, false, kWarpBlocks>(acc, weights, e4, rows, factors, c0, 0, g, t);
+                    if (here >= kWarpBlocks) {
+                        Operands<kH, kWarpBlocks> o;
+                        o.load(weights, rows, factors, c0, 0, g, t);
+                        next = mbar_test_wait(after, parity);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(empty);
+                        if (__all_sync(0xffffffffu, usual == 0x80808080u))
+                            add_products<false>(acc, o, e4, 0);
+                        else
+                            add_products<true>(acc, o, e4, 0);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < kWarpBlocks; ++i)
-                            if (i < here)
-                                block_products<kH, true, 1>(acc, weights, e4, rows, factors, c0, i, g, t);
+                        for (int i = 0; i < kWarpBlocks - 1; ++i)
+                            if (i < here) {
+                                Operands<kH, 1> o;
+                                o.load(weights, rows, factors, c0, i, g, t);
+                                add_products<true>(acc, o, e4, i);
+                            }
+                        next = mbar_test_wait(after, parity);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(empty);
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sm->empty[s]));
                 }
                 // sums to the item's buffer: slot [token parity][column % 4], at the lane that holds them
-                const int b = static_cast<int>(count % kBuffers);
-                if (ok) ok = warp_wait_bar(&sm->taken[b], (count / kBuffers & 1u) ^ 1u, abort);
+                if (ok) ok = __all_sync(0xffffffffu, room) || warp_wait_bar(&sm->taken[b], turn, abort);
 #pragma unroll
                 for (int m = 0; m < 2; ++m)       // columns 2 m and 2 m + 1 of every four
 #pragma unroll
@@ -713,25 +759,29 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
         const int half = warp - kConsumerWarps;   // tokens 4 i + 2 half and the next of a group
         uint32_t count = 0;
         bool ok = alive;
-        // token n of the group, column `lane` of box `box`: the warps' parts in order
-        auto total = [&](int b, int n, int box) {
+        uint32_t base = 0;
+        // token n of the group, column `lane` of box `box`: the warps' parts, from the set of the item's first stage on:
+        // the same order whichever set that is
+        auto total = [&](int b, int n, int box, int start) {
             const int chunk = lane >> 2, slot = (n & 1) * 4 + (lane & 3);
             const int from = (((chunk & 3) << 1) | (chunk >> 2)) * 4 + (n >> 1);
             float s = 0.f;
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int w = 0; w < kSlices; ++w) s += sm->red[b][q * 8 + box * 4 + w][slot][from];
+                for (int w = 0; w < kSlices; ++w) s += sm->red[b][(q ^ start) * 8 + box * 4 + w][slot][from];
             return s;
         };
-        for (int item = cta; item < items2; item += grid, ++count) {
-            const int gi = item / cols2, cb = item - gi * cols2, n = sm->group[gi] >> 16;
-            const int b = static_cast<int>(count % kBuffers);
+        Walk at(cta, grid, cols2);
+        for (int item = cta; item < items2; item += grid, at.next(), ++count, base += steps2) {
+            const int gi = at.group, cb = at.column, n = sm->group[gi] >> 16;
+            const int b = static_cast<int>(count % kBuffers), start = static_cast<int>(base & 1u);
             int slot = 0;
             float f = 0.f;
             if (lane < n) {
-                slot = sm->list[sm->first[gi] + lane];
-                f = __ldcg(p.xfactor + slot / p.k);
+                const uint32_t sl = sm->list[sm->first[gi] + lane];
+                slot = sl & 1023u;
+                f = sm->xfactor[sl >> 10];
             }
             if (!ok || !warp_wait_bar(&sm->sums[b], count / kBuffers & 1u, abort)) {
                 ok = false;
@@ -744,7 +794,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
 #pragma unroll
                 for (int d = 0; d < 2; ++d) {
                     const float fi = __shfl_sync(0xffffffffu, f, i0 + d);   // 0 past the last token
-                    const float gate = total(b, i0 + d, 0) * fi, up = total(b, i0 + d, 1) * fi;
+                    const float gate = total(b, i0 + d, 0, start) * fi, up = total(b, i0 + d, 1, start) * fi;
                     h[d] = silu(gate) * up;
                 }
 #pragma unroll
@@ -776,10 +826,11 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
         }
         __syncwarp();
 
-        for (int item = cta; item < items3; item += grid, ++count) {
-            const int gi = item / cols3, cb = item - gi * cols3, n = sm->group[gi] >> 16;
-            const int b = static_cast<int>(count % kBuffers);
-            const int slot = lane < n ? sm->list[sm->first[gi] + lane] : 0;
+        at = Walk(cta, grid, cols3);
+        for (int item = cta; item < items3; item += grid, at.next(), ++count, base += steps3) {
+            const int gi = at.group, cb = at.column, n = sm->group[gi] >> 16;
+            const int b = static_cast<int>(count % kBuffers), start = static_cast<int>(base & 1u);
+            const int slot = lane < n ? sm->list[sm->first[gi] + lane] & 1023 : 0;
             const float pw = lane < n ? sm->weight[slot] : 0.f;
             if (!ok || !warp_wait_bar(&sm->sums[b], count / kBuffers & 1u, abort)) {
                 ok = false;
@@ -787,15 +838,19 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
             }
             const bool right = cb * 64 + 32 < p.H;   // H % 64 may be 32
             for (int i0 = 2 * half; i0 < n; i0 += 2 * kEpilogues) {
+                float sums[2][2];
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+#pragma unroll
+                    for (int box = 0; box < 2; ++box) sums[d][box] = total(b, i0 + d, box, start);
 #pragma unroll
                 for (int d = 0; d < 2; ++d) {
                     const int si = __shfl_sync(0xffffffffu, slot, i0 + d);
                     const float wi = __shfl_sync(0xffffffffu, pw, i0 + d);
-                    const float s0 = total(b, i0 + d, 0) * wi, s1 = total(b, i0 + d, 1) * wi;
                     if (i0 + d < n) {
                         float* part = p.part + static_cast<size_t>(si) * p.H + cb * 64 + lane;
-                        __stcg(part, s0);
-                        if (right) __stcg(part + 32, s1);
+                        __stcg(part, sums[d][0] * wi);
+                        if (right) __stcg(part + 32, sums[d][1] * wi);
                     }
                 }
             }
