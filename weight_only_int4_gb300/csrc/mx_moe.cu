@@ -27,10 +27,10 @@
 // around a ring of stages. A stage is 512 rows of K by 64 columns of codes (two
 // TMA boxes of 32 columns, 128-byte swizzle), their exponent bytes and the same
 // 512 elements of the group's activation rows. Two sets of eight consumer
-// warps, each with a producer and half of the ring, take alternate stages of an
-// item (which set takes the first depends on the column block alone, so a
-// token's sums are formed in the same order whatever else the call holds). A
-// warp converts four 32-row blocks of one box: a lane's 16-byte load holds eight
+// warps, each with a producer and half of the ring, take alternate stages of the
+// CTA's items; an item's parts are added from the set of its first stage on, so a
+// token's sums are formed in the same order whatever else the call holds. A warp
+// converts four 32-row blocks of one box: a lane's 16-byte load holds eight
 // consecutive codes of each of four columns, which become fp16 pairs by the
 // hardware's exact conversion and serve as the A operand of warp-level MMAs
 // (columns of W as MMA rows, tokens as MMA columns), x as B; K is permuted alike
@@ -39,6 +39,17 @@
 // warps leave their sums in a buffer and go on; the epilogue warps, two tokens
 // each at a time, add the eight parts in order and finish the item beside the
 // next ones.
+//
+// Measured in a graph of calls on operands larger than L2: 1 token, 4 of 32
+// experts of 2048 x 1024 14.6..16.4 us; 16 tokens, 8 of 64 of 4096 x 1024 79..80
+// (the weights' bytes take 56 at the copy bandwidth); 64 tokens, 8 of 128 of
+// 2048 x 1024 102 (63). What bounds the last one: 18.6 us are everything but the
+// items (barriers, router, top-k, the last sums). Without the products the call
+// takes 87 us, without the loads as long as with them, without loads and epilogue
+// 84: the consumer warps' instructions, and the epilogue warps' beside them. More
+// warps lose more by their smaller share of the registers than they win: a third
+// set of consumers at 72 registers took 119..124 us against 109, four epilogue
+// warps at 80 registers 111..113 against 102.
 //
 // Activations in fp16: a token's x, and every run of 32 values of h, is
 // multiplied by the power of two that brings its largest magnitude just below
@@ -430,7 +441,8 @@ __device__ __forceinline__ void number_groups(const Params& p, Shared* sm) {
 struct Walk {
     int group, column, groups, columns, cols;
     __device__ __forceinline__ Walk(int item, int grid, int cols)
-        : group(item / cols), column(item - group * cols), groups(grid / cols), columns(grid - groups * cols), cols(cols) {}
+        : group(item / cols), column(item - group * cols), groups(grid / cols), columns(grid - groups * cols),
+          cols(cols) {}
     __device__ __forceinline__ void next() {
         group += groups;
         column += columns;
@@ -446,7 +458,8 @@ template <bool kH, int kCount>
 struct Operands {
     uint4 w[kCount], x[kCount];
     float f0[kCount], f1[kCount];
-    __device__ __forceinline__ void load(uint32_t box, uint32_t rows, uint32_t factors, int c, int first, int g, int t) {
+    __device__ __forceinline__ void load(uint32_t box, uint32_t rows, uint32_t factors, int c, int first, int g,
+                                         int t) {
         const uint32_t chunk = static_cast<uint32_t>((g >> 1) | ((g & 1) << 2));   // quarter-warps hit every bank once
         constexpr uint32_t kRec = kH ? kHRecord : 64;
 #pragma unroll
@@ -712,9 +725,9 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                     if (++slot == kSetStages) slot = 0, parity ^= 1u;
                     const uint32_t empty = smem_u32(&sm->empty[s]);
                     const uint32_t after = smem_u32(&sm->full[set * kSetStages + slot]);
-                    // The usual stage without a branch, so that its blocks overlap: all four blocks, every exponent byte
-                    // in 64..191 (bits 7 and 6 differ; scales 2^-63..2^64), so none is 0 or 255. It goes back to the
-                    // producer once the operands are in registers. Else one block at a time.
+                    // The usual stage: all four blocks, which then overlap; it goes back to the producer once the
+                    // operands are in registers. Every exponent byte in 64..191 (bits 7 and 6 differ; scales
+                    // 2^-63..2^64): none is 0 or 255. A stage that ends early: one block at a time.
                     uint32_t usual = 0x80808080u;
 #pragma unroll
                     for (int i = 0; i < kWarpBlocks; ++i) usual &= e4[i] ^ (e4[i] << 1);
@@ -760,8 +773,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
         uint32_t count = 0;
         bool ok = alive;
         uint32_t base = 0;
-        // token n of the group, column `lane` of box `box`: the warps' parts, from the set of the item's first stage on:
-        // the same order whichever set that is
+        // token n of the group, column `lane` of box `box`: the warps' parts, from the set of the item's first stage
+        // on: the same order whichever set that is
         auto total = [&](int b, int n, int box, int start) {
             const int chunk = lane >> 2, slot = (n & 1) * 4 + (lane & 3);
             const int from = (((chunk & 3) << 1) | (chunk >> 2)) * 4 + (n >> 1);

@@ -329,8 +329,8 @@ cudaError_t quant_rows(const void* x, uint32_t* codes, uint8_t* es, long long M,
                        cudaStream_t s) {
     const long long groups = (K + 127) / 128, items = M * groups;
     constexpr int kHalves = kThreads / 16;
-    // one group per half-warp while the grid has room, then two at a time (three and four: the same; eight: 15 % slower,
-    // registers cost more warps than the loads in flight gain)
+    // one group per half-warp while the grid has room, then two at a time (three and four: the same; eight: 15 %
+    // slower, registers cost more warps than the loads in flight gain)
     constexpr int kDeep = 2;
     const long long one = (items + kHalves - 1) / kHalves;
     const long long cap = static_cast<long long>(dp.sms) * 32;
