@@ -181,6 +181,26 @@ def test_tokens_do_not_see_one_another():
     assert w4.device_status() == w4.OK
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [
+    (64, 128, 4, 2080, 64),      # many router tiles in one call, few in the other; three stages of K
+    (64, 12, 6, 1056, 544),      # several groups per expert, several items per thread block, 3 and 2 stages
+    (40, 24, 3, 544, 1056),
+])
+def test_a_token_alone_and_among_many(T, E, k, H, I):
+    """Bit for bit the same, whatever share of the call's work the token is."""
+    gen = torch.Generator().manual_seed(T + H)
+    rand = lambda *s: torch.randn(*s, generator=gen)
+    words = lambda *s: torch.randint(-2 ** 31, 2 ** 31 - 1, s, generator=gen, dtype=torch.int32).cuda()
+    scales = lambda *s: torch.randint(118, 122, s, generator=gen, dtype=torch.uint8).cuda()
+    x = rand(T, H).bfloat16().cuda()
+    rest = ((rand(E, H) / H ** 0.5).bfloat16().cuda(), words(E, H // 8, 2 * I), scales(E, H // 32, 2 * I),
+            words(E, I // 8, H), scales(E, I // 32, H), k)
+    full = w4.mxfp4_moe(x, *rest, renormalize=False)
+    assert bool(torch.isfinite(full).all())
+    for first, last in ((0, 1), (T // 2, T // 2 + 1), (T - 1, T), (5, 14), (3, T - 2)):
+        assert torch.equal(w4.mxfp4_moe(x[first:last].contiguous(), *rest, renormalize=False), full[first:last])
+
+
 def test_nan_scale_of_an_expert_stays_with_its_tokens():
     case = Case(12, 6, 2, 128, 64, seed=9)
     ref, bound = case.reference()

@@ -41,9 +41,9 @@
 // next ones.
 //
 // Measured in a graph of calls on operands larger than L2: 1 token, 4 of 32
-// experts of 2048 x 1024 14.6..16.4 us; 16 tokens, 8 of 64 of 4096 x 1024 79..80
+// experts of 2048 x 1024 14.6..16.9 us; 16 tokens, 8 of 64 of 4096 x 1024 79..81
 // (the weights' bytes take 56 at the copy bandwidth); 64 tokens, 8 of 128 of
-// 2048 x 1024 102 (63). What bounds the last one: 18.6 us are everything but the
+// 2048 x 1024 103 (63). What bounds the last one: 18.6 us are everything but the
 // items (barriers, router, top-k, the last sums). Without the products the call
 // takes 87 us, without the loads as long as with them, without loads and epilogue
 // 84: the consumer warps' instructions, and the epilogue warps' beside them. More
@@ -148,6 +148,7 @@ struct Params {
 };
 constexpr int kBarriers = 3;
 constexpr int kMaxSplits = 4;
+constexpr int kRouterDepth = 1024;   // elements of H in a part of the router product
 
 __device__ __forceinline__ void fail(volatile int* abort) {
     *abort = 1;
@@ -230,9 +231,11 @@ __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + expf
 // phase 0
 // ---------------------------------------------------------------------------
 // Logits of 16 experts x 8 tokens over part `part` of H: the consumer warps take
-// 32-element blocks in turn and their sums meet in shared memory. One CTA's
-// loads of a whole 16 x 4096 slice of the router took 5 us; in four parts they
-// are one round trip (16 tokens, 64 experts of 4096 x 1024: 87.0 -> 85.0 us).
+// 32-element blocks in turn and their sums meet in shared memory. Parts of 1024
+// (up to four): 16 tokens, 64 experts of 4096 x 1024 take 79.2 us against 79.8 in
+// parts of 2048 (undivided it cost 2 us more), 4 tokens, 128 experts of
+// 2048 x 768 32.7 against 33.6; only 64 tokens with 128 experts, whose tiles alone
+// fill the GPU, pay for it (103.1 against 102.3; 105.0 in parts of 512).
 __device__ void router_tile(const Params& p, float (*scratch)[4][32], int e0, int t0, int part, int warp, int lane) {
     const int g = lane >> 2, t = lane & 3;
     const int all = p.H >> 5, first = all * part / p.splits, blocks = all * (part + 1) / p.splits;
@@ -932,9 +935,9 @@ cudaError_t launch_kernel(const CUtensorMap (&maps)[4], Params p, const DevicePr
     const long long want = slots * std::max<long long>(p.I / 32, (p.H + 63) / 64);
     cudaLaunchConfig_t cfg = {};
     const int grid = static_cast<int>(std::min<long long>(want, dp.sms));
-    // router: as many parts of H as leave one unit (tile and part, or token to convert) per CTA, 512 or more deep
-    const int tiles = (p.E + 15) / 16 * ((p.T + 7) / 8);
-    p.splits = std::max(1, std::min({kMaxSplits, (grid - p.T) / tiles, p.H / 512}));
+    // The number of parts depends on H alone, and with it the order of a logit's sum: the other tokens of a call change
+    // nothing.
+    p.splits = std::min(kMaxSplits, (p.H + kRouterDepth - 1) / kRouterDepth);
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
