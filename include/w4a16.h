@@ -460,9 +460,8 @@ w4a16_status w4a16_mxfp4_matmul(const int32_t* a, const uint8_t* ea, const int32
  * magnitude, h is rounded to 11 bits. Weights of a chosen expert are read once
  * per 8 tokens that chose it (again mostly from L2); experts nobody chose are not
  * read. A token's y does not depend on the other tokens, bit for bit, and the
- * result is deterministic. A token with
- * an infinity or NaN in x or in a chosen expert's block yields NaN there and
- * leaves other tokens alone.
+ * result is deterministic. A token with an infinity or NaN in x or in a chosen
+ * expert's block yields NaN there and leaves other tokens alone.
  *
  * workspace: at least w4a16_mxfp4_moe_workspace_bytes(...) bytes with the
  * ownership and zero-fill rules of w4a16_gemv's (what must start at zero are
