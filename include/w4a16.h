@@ -133,6 +133,21 @@ w4a16_status w4a16_unpack(const int32_t* src, uint8_t* dst, int64_t rows, int64_
 size_t w4a16_workspace_bytes(w4a16_op op, int64_t M, int64_t N, int64_t K, int64_t g);
 
 /*
+ * w4a16_capture_id -- 0 while `stream` is not being captured into a CUDA graph,
+ * else a number that no other capture of the process has. (No counterpart on
+ * the pages this library follows.)
+ *
+ * A workspace has to be zero before the first kernel that uses it runs. A
+ * zero fill made while a stream is captured becomes a node of that graph and
+ * runs with it alone, so a workspace filled in one capture must not serve a
+ * second one: the second graph may be replayed first. Graphs that may run at
+ * the same time must not share a workspace either. With this number a caller
+ * that keeps workspaces gives each capture its own. Touches no device memory;
+ * 0 also where the query fails (such a stream takes no launch either).
+ */
+uint64_t w4a16_capture_id(w4a16_stream stream);
+
+/*
  * w4a16_gemv -- decode path, 1 <= M <= 16.
  *
  * One row (and two rows of a layer of at most 4 * 2^20 weights) is

@@ -47,6 +47,7 @@ SIGNATURES = {
     "w4a16_pack": (_INT, [_VP, _VP, _I64, _I64, _INT, _VP]),
     "w4a16_unpack": (_INT, [_VP, _VP, _I64, _I64, _INT, _VP]),
     "w4a16_workspace_bytes": (_SZ, [_INT, _I64, _I64, _I64, _I64]),
+    "w4a16_capture_id": (ctypes.c_uint64, [_VP]),
     "w4a16_gemv": (_INT, _LAYER_ARGS),
     "w4a16_gemm": (_INT, _LAYER_ARGS),
     "w4a16_gemv_noalloc": (_INT, [_VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _INT, _VP]),
@@ -204,6 +205,30 @@ def new_workspace(nbytes: int, device=None):
 _workspaces = {}
 _retired = []
 
+# Bytes of FP32 partial sums per SM with which an op's workspace begins, as include/w4a16.h lays it out; ticket words,
+# the part that must start at zero, follow.
+_PARTIALS_PER_SM = {OP_GEMV: 136 << 10, OP_GEMM: 128 << 10, OP_MXFP4_MATMUL: 128 << 10}
+_MOE_CONTROL_BYTES = 256   # mxfp4_moe: barrier words, at the start
+
+
+def _zero_range(op, nbytes: int, sms: int):
+    """(first, last + 1) of the bytes of a workspace that must start at zero."""
+    if op in _PARTIALS_PER_SM:
+        first = _PARTIALS_PER_SM[op] * sms
+        return (first if first < nbytes else 0), nbytes
+    return 0, min(_MOE_CONTROL_BYTES, nbytes)
+
+
+def _captured_workspace(nbytes: int, device, op, sms: int):
+    """A workspace whose zero fill will run on every replay of a graph: it covers
+    what must start at zero and no more (all 20 MB of a product's partial sums
+    would cost each replay 6 us)."""
+    torch = _torch()
+    ws = torch.empty(int(nbytes), dtype=torch.uint8, device=device)
+    first, last = _zero_range(op, int(nbytes), sms)
+    ws[first:last].zero_()
+    return ws
+
 
 def _cached_workspace(nbytes: int, device, stream, op: int):
     """One growing workspace per (device, stream, op): calls on one stream never
@@ -211,21 +236,29 @@ def _cached_workspace(nbytes: int, device, stream, op: int):
 
     The workspace is allocated and zero-filled on the stream the call runs on,
     so the zero fill is ordered before the kernel and the caching allocator
-    ties the memory to that stream. A workspace outgrown by a larger shape is
-    kept alive (not freed) until release_workspaces(): a CUDA graph captured
-    through an earlier call may still replay into it."""
+    ties the memory to that stream. While that stream is captured the fill
+    becomes a node of the graph, so every capture has workspaces of its own:
+    each graph carries the fill that its kernels rely on, whichever is replayed
+    first, and graphs replayed at the same time do not meet in one. A workspace
+    of a capture, or one outgrown by a larger shape, is kept alive (not freed)
+    until release_workspaces(): a graph may still replay into it."""
     torch = _torch()
     dev = device.index if device.index is not None else torch.cuda.current_device()
     if stream is not None:
         handle = int(stream.cuda_stream)
     else:
         handle = int(torch.cuda.current_stream(dev).cuda_stream) if _raw_stream is None else _raw_stream(dev)
-    key = (dev, handle, op)
+    capture = load_library().w4a16_capture_id(handle)
+    key = (dev, handle, op, capture)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         s = torch.cuda.current_stream(dev) if stream is None else stream
         with torch.cuda.stream(s):
-            fresh = new_workspace(nbytes, device)
+            if capture:
+                sms = torch.cuda.get_device_properties(dev).multi_processor_count
+                fresh = _captured_workspace(nbytes, device, op, sms)
+            else:
+                fresh = new_workspace(nbytes, device)
         if ws is not None:
             _retired.append(ws)
         _workspaces[key] = ws = fresh
@@ -234,7 +267,8 @@ def _cached_workspace(nbytes: int, device, stream, op: int):
 
 def release_workspaces() -> None:
     """Free the workspaces the binding allocated for calls made without one (one
-    per device, stream and op, plus any outgrown by larger shapes). Call it only
+    per device, stream and op, one more for each capture of the stream, plus any
+    outgrown by larger shapes). Call it only
     when no such call is in flight, and only after dropping every CUDA graph
     captured through such calls: a captured graph replays into the workspace
     address it saw at capture time. The next call allocates a fresh, zeroed
