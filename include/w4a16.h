@@ -394,8 +394,7 @@ w4a16_status w4a16_mxfp4_gemm(const void* x, const int32_t* qweight, const uint8
  * A block that holds an infinity or a NaN has e = 255 and codes 0: each of its
  * values reads as NaN. Values that MXFP4 represents exactly are kept exactly,
  * so quantising a dense copy gives its values back. Bit-exact; deterministic.
- * Streams each operand once; launched with programmatic stream serialization
- * (every read and write follows the completion of the kernel before it).
+ * Streams each operand once. An ordinary launch (no programmatic serialization).
  * Errors: NULL, DTYPE, SHAPE (non-positive, not a multiple as above, dim),
  * ALIGN (a pointer not 16-byte aligned), DEVICE, CUDA.
  */
@@ -440,10 +439,8 @@ w4a16_status w4a16_mxfp4_tile_scales(const uint8_t* src, uint8_t* dst, int64_t r
  * summed in a fixed order: the result is deterministic. After a
  * W4A16_ERR_TIMEOUT reported by w4a16_device_status, zero the workspace again.
  *
- * M >= 1, N % 8 == 0, K % 32 == 0. Launched with programmatic stream
- * serialization: its prologue (barriers, tensor memory) may overlap the end of
- * the kernel before it; every read and write of caller memory follows that
- * kernel's completion.
+ * M >= 1, N % 8 == 0, K % 32 == 0. An ordinary launch (no programmatic
+ * serialization).
  * Errors: NULL, DTYPE, SHAPE, ALIGN, WORKSPACE, DEVICE, CUDA.
  */
 w4a16_status w4a16_mxfp4_matmul(const int32_t* a, const uint8_t* ea, const int32_t* b, const uint8_t* eb, void* y,

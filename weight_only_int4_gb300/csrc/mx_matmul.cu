@@ -497,8 +497,6 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
-    griddep_launch_dependents();
-    griddep_wait();
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -786,10 +784,7 @@ cudaError_t launch_pair(const MxMatmulArgs& a, const DeviceProps& dp, cudaStream
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = pair::kSmemBytes;
     cfg.stream = s;
-    // An ordinary launch: with programmatic serialization on both this kernel and
-    // the quantisation before it, a queue of about a hundred such pairs stopped
-    // making progress (every wait in the kernel is bounded, and the same calls one
-    // at a time were right), for a gain of about 1 % on a call of 0.37 ms.
+    // no programmatic serialization: see launch_rows
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -819,18 +814,24 @@ cudaError_t launch_rows(const MxMatmulArgs& a, const Plan& pl, float* partials, 
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
+    // No kernel of this file or of mx_quant.cu is launched with programmatic
+    // serialization. With it on the quantisation and on the pair kernel, a queue of
+    // about a hundred calls stopped making progress; the calls were right one at a
+    // time, and reading gave no cause: every grid waits for earlier grids only, no
+    // two of these CTAs with tensor memory fit one SM, and the ring barriers are
+    // drained before a CTA leaves. What such a CTA does before its dependency wait
+    // is not bounded by a time limit either (tensor-memory allocation, the cluster
+    // barrier, the wait itself). So what follows one of these kernels starts when it
+    // has completed.
     cudaLaunchAttribute attr[1];
-    if (pl.split > 1) {   // an ordinary launch, as the pair kernel's
+    if (pl.split > 1) {
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = static_cast<unsigned>(pl.split);
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
-    } else {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
     }
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, tw, tx, a.eb, a.ea, a.y, a.M, a.N, a.K, pl.split, pl.share ? 1 : 0,
                               partials, tickets);
 }

@@ -128,8 +128,6 @@ template <int kType, int kUnroll, typename Index>
 __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const void* __restrict__ x, uint32_t* __restrict__ codes,
                                                               uint8_t* __restrict__ es, Index items, Index groups,
                                                               int K) {
-    griddep_launch_dependents();
-    griddep_wait();
     const int sub = threadIdx.x & 15;
     const Index half = static_cast<Index>((blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x) >> 4);
     const Index halves = static_cast<Index>((static_cast<long long>(gridDim.x) * kThreads) >> 4);
@@ -193,8 +191,6 @@ template <int kType, typename Index>
 __global__ void __launch_bounds__(kThreads) quant_cols_kernel(const void* __restrict__ x, uint32_t* __restrict__ codes,
                                                               uint8_t* __restrict__ es, Index items, int N) {
     constexpr int kCols = kType == kF32 ? 2 : 4;
-    griddep_launch_dependents();
-    griddep_wait();
     const Index per_block = static_cast<Index>(N / kCols);
     for (Index it = static_cast<Index>(blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x); it < items;
          it += static_cast<Index>(static_cast<long long>(gridDim.x) * kThreads)) {
@@ -255,8 +251,6 @@ __global__ void __launch_bounds__(kThreads) dequant_rows_kernel(const uint32_t* 
                                                                 const uint8_t* __restrict__ es,
                                                                 uint16_t* __restrict__ w, Index items, Index words,
                                                                 Index groups) {
-    griddep_launch_dependents();
-    griddep_wait();
     constexpr int kUnroll = 4;
     const Index step = static_cast<Index>(static_cast<long long>(gridDim.x) * kThreads);
     for (Index i0 = static_cast<Index>(blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x); i0 < items;
@@ -304,19 +298,13 @@ __global__ void __launch_bounds__(kThreads) tile_scales_kernel(const uint8_t* __
     }
 }
 
-// Launched with programmatic serialization: the launch itself overlaps the end
-// of the stream's previous kernel, every access follows that kernel's completion.
+// An ordinary launch (see launch_rows in mx_matmul.cu).
 template <typename... Params, typename... Args>
-cudaError_t launch_pdl(void (*kern)(Params...), long long blocks, cudaStream_t s, Args... args) {
+cudaError_t launch(void (*kern)(Params...), long long blocks, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
 }
 
@@ -335,11 +323,11 @@ cudaError_t quant_rows(const void* x, uint32_t* codes, uint8_t* es, long long M,
     const long long one = (items + kHalves - 1) / kHalves;
     const long long cap = static_cast<long long>(dp.sms) * 32;
     if (one <= cap)
-        return launch_pdl(quant_rows_kernel<kType, 1, unsigned>, one, s, x, codes, es, items, groups, K);
+        return launch(quant_rows_kernel<kType, 1, unsigned>, one, s, x, codes, es, items, groups, K);
     const long long grid = std::min(cap, (one + kDeep - 1) / kDeep);
     if (items < kIndexLimit)
-        return launch_pdl(quant_rows_kernel<kType, kDeep, unsigned>, grid, s, x, codes, es, items, groups, K);
-    return launch_pdl(quant_rows_kernel<kType, kDeep, unsigned long long>, grid, s, x, codes, es, items, groups, K);
+        return launch(quant_rows_kernel<kType, kDeep, unsigned>, grid, s, x, codes, es, items, groups, K);
+    return launch(quant_rows_kernel<kType, kDeep, unsigned long long>, grid, s, x, codes, es, items, groups, K);
 }
 
 template <int kType>
@@ -347,8 +335,8 @@ cudaError_t quant_cols(const void* x, uint32_t* codes, uint8_t* es, long long K,
                        cudaStream_t s) {
     const long long items = (K / 32) * (N / (kType == kF32 ? 2 : 4));
     const long long grid = std::min<long long>((items + kThreads - 1) / kThreads, static_cast<long long>(dp.sms) * 16);
-    if (items < kIndexLimit) return launch_pdl(quant_cols_kernel<kType, unsigned>, grid, s, x, codes, es, items, N);
-    return launch_pdl(quant_cols_kernel<kType, unsigned long long>, grid, s, x, codes, es, items, N);
+    if (items < kIndexLimit) return launch(quant_cols_kernel<kType, unsigned>, grid, s, x, codes, es, items, N);
+    return launch(quant_cols_kernel<kType, unsigned long long>, grid, s, x, codes, es, items, N);
 }
 
 }  // namespace
@@ -371,19 +359,18 @@ cudaError_t launch_mx_dequant_rows(const uint32_t* codes, const uint8_t* es, voi
     const long long grid =
         std::min<long long>((items + kThreads - 1) / kThreads, static_cast<long long>(dp.sms) * 8);
     if (items < kIndexLimit)
-        return launch_pdl(dequant_rows_kernel<unsigned>, grid, s, codes, es, static_cast<uint16_t*>(w), items, words,
+        return launch(dequant_rows_kernel<unsigned>, grid, s, codes, es, static_cast<uint16_t*>(w), items, words,
                           groups);
-    return launch_pdl(dequant_rows_kernel<unsigned long long>, grid, s, codes, es, static_cast<uint16_t*>(w), items,
+    return launch(dequant_rows_kernel<unsigned long long>, grid, s, codes, es, static_cast<uint16_t*>(w), items,
                       words, groups);
 }
 
 cudaError_t launch_mx_tile_scales(const uint8_t* src, uint8_t* dst, int64_t rows, int64_t cols, const DeviceProps& dp,
                                   cudaStream_t s) {
     const long long groups = (cols + 127) / 128, items = rows * groups;
-    const int grid = static_cast<int>(
-        std::min<long long>((items + kThreads - 1) / kThreads, static_cast<long long>(dp.sms) * 8));
-    tile_scales_kernel<<<grid, kThreads, 0, s>>>(src, dst, items, groups, cols / 32);
-    return cudaGetLastError();
+    const long long grid =
+        std::min<long long>((items + kThreads - 1) / kThreads, static_cast<long long>(dp.sms) * 8);
+    return launch(tile_scales_kernel, grid, s, src, dst, items, groups, cols / 32);
 }
 
 }  // namespace w4a16
