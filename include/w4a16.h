@@ -439,7 +439,7 @@ w4a16_status w4a16_mxfp4_tile_scales(const uint8_t* src, uint8_t* dst, int64_t r
  * summed in a fixed order: the result is deterministic. After a
  * W4A16_ERR_TIMEOUT reported by w4a16_device_status, zero the workspace again.
  *
- * M >= 1, N % 8 == 0, K % 32 == 0. An ordinary launch (no programmatic
+ * M >= 1, N % 8 == 0, K % 32 == 0, each at most 2^31 - 512. An ordinary launch (no programmatic
  * serialization).
  * Errors: NULL, DTYPE, SHAPE, ALIGN, WORKSPACE, DEVICE, CUDA.
  */

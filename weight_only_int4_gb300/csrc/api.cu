@@ -52,6 +52,8 @@ namespace {
 using w4a16::DeviceProps;
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+// Kernels that tile a dimension round it up to at most 512 in 32-bit arithmetic.
+constexpr int64_t kMaxProductDim = (int64_t(1) << 31) - 512;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -125,6 +127,7 @@ w4a16_status check_mx_product(int64_t M, int64_t N, int64_t K) {
     w4a16_status st = check_mx_rows(M, K);
     if (st == W4A16_OK) st = check_mx_rows(N, K);
     if (st != W4A16_OK) return st;
+    if (M > kMaxProductDim || N > kMaxProductDim || K > kMaxProductDim) return W4A16_ERR_SHAPE;
     if (N % 8 != 0 || ((M > N ? M : N) / 128 + 2) * (K / 128 + 2) > kMaxDim) return W4A16_ERR_SHAPE;
     return W4A16_OK;
 }
