@@ -42,7 +42,8 @@
  *   - The library runs only on compute capability 10.3 (GB300); any other
  *     device gives W4A16_ERR_DEVICE.
  *   - Shape limits: N % 8 == 0, K % g == 0, g in {32, 64, 128, 256}, all
- *     dimensions > 0 and < 2^31, base pointers 16-byte aligned. Products of
+ *     dimensions > 0 and < 2^31 (at most 2^31 - 512 in the layers and products,
+ *     whose tiles are counted in 32 bits), base pointers 16-byte aligned. Products of
  *     dimensions are not limited: every offset is computed in 64 bits, so
  *     tensors past 2^32 elements or 4 GiB are fine.
  */
@@ -439,7 +440,7 @@ w4a16_status w4a16_mxfp4_tile_scales(const uint8_t* src, uint8_t* dst, int64_t r
  * summed in a fixed order: the result is deterministic. After a
  * W4A16_ERR_TIMEOUT reported by w4a16_device_status, zero the workspace again.
  *
- * M >= 1, N % 8 == 0, K % 32 == 0, each at most 2^31 - 512. An ordinary launch (no programmatic
+ * M >= 1, N % 8 == 0, K % 32 == 0. An ordinary launch (no programmatic
  * serialization).
  * Errors: NULL, DTYPE, SHAPE, ALIGN, WORKSPACE, DEVICE, CUDA.
  */

@@ -84,7 +84,7 @@ w4a16_status check_layer_args(const void* x, const int32_t* qweight, const void*
     if (!x || !qweight || !scales || !y) return W4A16_ERR_NULL;
     if (dt != W4A16_F16 && dt != W4A16_BF16) return W4A16_ERR_DTYPE;
     if (M < 1 || N < 1 || K < 1 || g < 1) return W4A16_ERR_SHAPE;
-    if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return W4A16_ERR_SHAPE;
+    if (M > kMaxProductDim || N > kMaxProductDim || K > kMaxProductDim) return W4A16_ERR_SHAPE;
     if (max_m > 0 && M > max_m) return W4A16_ERR_SHAPE;
     if (N % 8 != 0 || K % g != 0) return W4A16_ERR_SHAPE;
     if (!supported_group(g)) return W4A16_ERR_UNSUPPORTED;
@@ -110,7 +110,8 @@ w4a16_status check_mx_args(const void* x, const int32_t* qweight, const uint8_t*
     if (!x || !y) return W4A16_ERR_NULL;
     w4a16_status st = check_mx_weights(qweight, escale, N, K);
     if (st != W4A16_OK) return st;
-    if (M < 1 || M > kMaxDim || (max_m > 0 && M > max_m)) return W4A16_ERR_SHAPE;
+    if (M < 1 || (max_m > 0 && M > max_m)) return W4A16_ERR_SHAPE;
+    if (M > kMaxProductDim || N > kMaxProductDim || K > kMaxProductDim) return W4A16_ERR_SHAPE;
     if (!aligned16(x) || !aligned16(y)) return W4A16_ERR_ALIGN;
     return W4A16_OK;
 }
@@ -187,8 +188,8 @@ w4a16_status w4a16_unpack(const int32_t* src, uint8_t* dst, int64_t rows, int64_
 
 size_t w4a16_workspace_bytes(w4a16_op op, int64_t M, int64_t N, int64_t K, int64_t g) {
     if (op != W4A16_OP_GEMV && op != W4A16_OP_GEMM && op != W4A16_OP_MXFP4_MATMUL) return 0;
-    if (M < 1 || N < 8 || N % 8 || K < 1 || K > kMaxDim || N > kMaxDim || M > kMaxDim || !supported_group(g) || K % g)
-        return 0;
+    if (M < 1 || N < 8 || N % 8 || K < 1 || !supported_group(g) || K % g) return 0;
+    if (M > kMaxProductDim || N > kMaxProductDim || K > kMaxProductDim) return 0;
     if (op == W4A16_OP_GEMV && M > 16) return 0;
     if (op == W4A16_OP_GEMM && M > w4a16::kSkinnyMaxM) return 0;
     DeviceProps dp;
