@@ -1,0 +1,66 @@
+"""Mixture-of-experts layers whose exponents lie far from the activations': the
+products of small activations with large weights, of large ones with small
+weights, and both kinds of blocks in one column, all with results in range.
+
+Tolerances and the FP64 reference are those of the layer's own tests: powers of
+two change no relative error as long as nothing leaves the FP32 range.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import weight_only_int4_gb300 as w4  # noqa: E402
+from test_gpu_mx_moe import Case, check  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def make(xscale, lo, hi, T=6, E=5, k=2, H=1120, I=96, seed=21):
+    """Gate and up exponent bytes in lo..hi, the down product's as usual. H: two whole stages and a short one."""
+    case = Case(T, E, k, H, I, seed=seed, xscale=xscale)
+    rng = np.random.default_rng([seed, lo, hi])
+    case.e13 = rng.integers(lo, hi + 1, size=case.e13.shape).astype(np.uint8)
+    return case
+
+
+@pytest.mark.parametrize("xscale,lo,hi", [
+    (2.0 ** -100, 236, 239),    # gate and up about 2^16: their sums without the factor 2^-114 pass 2^128
+    (2.0 ** -100, 219, 222),    # about 1/2
+    (2.0 ** -64, 186, 196),     # bytes on both sides of 191
+    (2.0 ** 24, 58, 70),        # ... and of 64
+    (2.0 ** 90, 30, 37),
+    (2.0 ** 110, 0, 17),        # byte 0 among them
+])
+def test_exponents_against_activations(xscale, lo, hi):
+    check(make(xscale, lo, hi), (xscale, lo, hi))
+
+
+@pytest.mark.parametrize("where", [0, 1, 15, 17, 34])
+def test_one_unusual_block(where):
+    """Every block of a column usual but one, wherever the stages put it: the sums before and after it still count."""
+    case = make(2.0 ** -100, 180, 184, seed=22)
+    case.e13[:, where] = np.where(case.e13[:, where] % 2, 236, 182).astype(np.uint8)
+    check(case, where)
+
+
+def test_crowded_experts_and_long_items():
+    """Groups of every size up to 8 tokens, several items per thread block, an unusual byte in some experts only."""
+    case = make(2.0 ** -100, 184, 190, T=64, E=6, k=2, H=2080, I=544, seed=23)
+    case.e13[1, 40] = 237
+    case.e13[4, 3, ::7] = 238
+    check(case)
+
+
+def test_a_token_does_not_see_its_neighbours_there():
+    case = make(2.0 ** -100, 188, 194, T=20, E=4, k=2, seed=24)
+    dev = case.device()
+    full = w4.mxfp4_moe(*dev, 2)
+    for t in (0, 9, 19):
+        assert torch.equal(w4.mxfp4_moe(dev[0][t:t + 1].contiguous(), *dev[1:], 2)[0], full[t])
+    big = dev[0].clone()
+    big[3] *= 2.0 ** 150
+    again = w4.mxfp4_moe(big, *dev[1:], 2)
+    keep = [t for t in range(20) if t != 3]
+    assert torch.equal(again[keep], full[keep])
+    assert w4.device_status() == w4.OK

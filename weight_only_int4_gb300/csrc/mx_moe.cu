@@ -57,6 +57,12 @@
 // with the block's). Values within 2^-29 of the largest convert exactly or, for
 // h, with fp16's 11 bits; smaller ones lose at most 2^-39 of the largest.
 //
+// The gate and up sums are kept without the token's factor as long as every
+// exponent byte is in 64..191: below 2^(23 + 64 + 11), they cannot overflow
+// whatever the factor is. From the first other byte on a warp keeps its sums of
+// the item in true units, factor and exponent applied to each block's products
+// in the order that stays in range, and marks them for the epilogue.
+//
 // Waits are bounded (about two seconds); on expiry the kernel records the
 // timeout in a device word, every role stops, copies in flight are waited for
 // (bounded) and the kernel returns.
@@ -110,6 +116,7 @@ constexpr uint32_t kRowBytes = kGroup * kXStride;
 
 struct __align__(16) Shared {
     float red[kBuffers][kConsumerWarps][kRedSlots][kRedPitch];
+    uint32_t factored[kBuffers][4];   // byte w: warp w's gate and up sums hold the token's factor
     uint64_t full[kStages];
     uint64_t empty[kStages];
     uint64_t sums[kBuffers];          // a buffer of partial sums is complete
@@ -478,11 +485,19 @@ struct Operands {
     }
 };
 
-// Their products added to acc [16-column tile][fragment]. kEdge: a byte of 0 or
-// 255 may be among the exponents e4.
+// d f s: what rounds or leaves the range in between does so in the result. A
+// factor above 1 belongs to large activations, one up to 1 to small ones.
+__device__ __forceinline__ float scaled_sum(float d, float f, float s, float acc) {
+    const bool large = f > 1.f;
+    return fmaf(d * (large ? s : f), large ? f : s, acc);
+}
+
+// Their products added to acc [16-column tile][fragment]. kEdge: any exponent
+// byte may be among e4, and f0 and f1 are factors of tokens 2 t and 2 t + 1 (1
+// where the sums are kept without them).
 template <bool kEdge, bool kH, int kCount>
 __device__ __forceinline__ void add_products(float (&acc)[2][4], const Operands<kH, kCount>& o,
-                                             const uint32_t (&e4)[4], int first) {
+                                             const uint32_t (&e4)[4], int first, float f0 = 1.f, float f1 = 1.f) {
 #pragma unroll
     for (int j = 0; j < kCount; ++j) {
         const uint32_t words[4] = {o.w[j].x, o.w[j].y, o.w[j].z, o.w[j].w}, e = e4[first + j];
@@ -512,6 +527,11 @@ __device__ __forceinline__ void add_products(float (&acc)[2][4], const Operands<
                 a[1] = fmaf(d[1] * o.f1[j], scale[2 * m], a[1]);
                 a[2] = fmaf(d[2] * o.f0[j], scale[2 * m + 1], a[2]);
                 a[3] = fmaf(d[3] * o.f1[j], scale[2 * m + 1], a[3]);
+            } else if constexpr (kEdge) {
+                a[0] = scaled_sum(d[0], f0, scale[2 * m], a[0]);
+                a[1] = scaled_sum(d[1], f1, scale[2 * m], a[1]);
+                a[2] = scaled_sum(d[2], f0, scale[2 * m + 1], a[2]);
+                a[3] = scaled_sum(d[3], f1, scale[2 * m + 1], a[3]);
             } else {
                 a[0] = fmaf(d[0], scale[2 * m], a[0]);
                 a[1] = fmaf(d[1], scale[2 * m], a[1]);
@@ -545,6 +565,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
         mbar_init(smem_u32(&sm->phase3), 1);
         mbar_init(smem_u32(&sm->phase4), 1);
         *abort = 0;
+        for (int b = 0; b < kBuffers; ++b)
+            for (int i = 0; i < 4; ++i) sm->factored[b][i] = 0u;
         sm->epoch = ld_acquire(p.control);
         fence_mbar_init();
         tma_prefetch_desc(&tw13);
@@ -695,6 +717,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
         uint32_t count = 0;   // items so far
         uint32_t parity = 0;  // of the set's next stage
         int slot = 0;         // ... its place in the set's half of the ring
+        bool ever = false;    // the warp has marked a buffer
         bool ok = alive, next = false;   // next: it was complete when looked at beside the last one's products
         auto phase = [&](auto second) {
             constexpr bool kH = decltype(second)::value;
@@ -702,6 +725,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
             const int items = kH ? items3 : items2;
             const int blocks = kH ? blocks3 : blocks2, steps = kH ? steps3 : steps2;
             for (int item = cta; item < items; item += grid, ++count, base += steps) {
+                uint32_t plain = 0x80808080u;   // 0: the sums hold the tokens' factors
                 float acc[2][4];
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
@@ -728,29 +752,52 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
                     if (++slot == kSetStages) slot = 0, parity ^= 1u;
                     const uint32_t empty = smem_u32(&sm->empty[s]);
                     const uint32_t after = smem_u32(&sm->full[set * kSetStages + slot]);
+                    // An unusual exponent byte: the sums take on the tokens' factors, if they have not yet
+                    auto use_factors = [&](float& f0, float& f1) {
+                        const int gi = item / cols2, n = sm->group[gi] >> 16;
+                        const uint16_t* list = sm->list + sm->first[gi];
+                        if (2 * t < n) f0 = sm->xfactor[list[2 * t] >> 10];
+                        if (2 * t + 1 < n) f1 = sm->xfactor[list[2 * t + 1] >> 10];
+                        if (!plain) return;
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) acc[m][0] *= f0, acc[m][1] *= f1, acc[m][2] *= f0, acc[m][3] *= f1;
+                        plain = 0u;
+                        ever = true;
+                    };
                     // The usual stage: all four blocks, which then overlap; it goes back to the producer once the
                     // operands are in registers. Every exponent byte in 64..191 (bits 7 and 6 differ; scales
                     // 2^-63..2^64): none is 0 or 255. A stage that ends early: one block at a time.
-                    uint32_t usual = 0x80808080u;
-#pragma unroll
-                    for (int i = 0; i < kWarpBlocks; ++i) usual &= e4[i] ^ (e4[i] << 1);
                     if (here >= kWarpBlocks) {
+                        uint32_t usual = plain;
+#pragma unroll
+                        for (int i = 0; i < kWarpBlocks; ++i) usual &= e4[i] ^ (e4[i] << 1);
                         Operands<kH, kWarpBlocks> o;
                         o.load(weights, rows, factors, c0, 0, g, t);
                         next = mbar_test_wait(after, parity);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(empty);
-                        if (__all_sync(0xffffffffu, usual == 0x80808080u))
+                        if (__all_sync(0xffffffffu, usual == 0x80808080u)) {
                             add_products<false>(acc, o, e4, 0);
-                        else
-                            add_products<true>(acc, o, e4, 0);
+                        } else {
+                            float f0 = 1.f, f1 = 1.f;
+                            if constexpr (!kH) use_factors(f0, f1);
+                            add_products<true>(acc, o, e4, 0, f0, f1);
+                        }
                     } else {
+                        float f0 = 1.f, f1 = 1.f;
+                        if constexpr (!kH) {
+                            uint32_t usual = plain;
+#pragma unroll
+                            for (int i = 0; i < kWarpBlocks - 1; ++i)
+                                if (i < here) usual &= e4[i] ^ (e4[i] << 1);
+                            if (!__all_sync(0xffffffffu, usual == 0x80808080u)) use_factors(f0, f1);
+                        }
 #pragma unroll
                         for (int i = 0; i < kWarpBlocks - 1; ++i)
                             if (i < here) {
                                 Operands<kH, 1> o;
                                 o.load(weights, rows, factors, c0, i, g, t);
-                                add_products<true>(acc, o, e4, i);
+                                add_products<true>(acc, o, e4, i, f0, f1);
                             }
                         next = mbar_test_wait(after, parity);
                         __syncwarp();
@@ -764,6 +811,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
 #pragma unroll
                     for (int i = 0; i < 4; ++i)   // fragment: column i >> 1, token parity i & 1
                         sm->red[b][warp][(i & 1) * 4 + m * 2 + (i >> 1)][lane] = acc[m][i];
+                if (!kH && ever && lane == 0) reinterpret_cast<volatile uint8_t*>(sm->factored[b])[warp] = plain ? 0 : 1;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm->sums[b]));
             }
@@ -776,16 +824,19 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
         uint32_t count = 0;
         bool ok = alive;
         uint32_t base = 0;
-        // token n of the group, column `lane` of box `box`: the warps' parts, from the set of the item's first stage
-        // on: the same order whichever set that is
-        auto total = [&](int b, int n, int box, int start) {
+        // token n of the group, column `lane`: warp w's part of it
+        auto part_of = [&](int b, int n, int w) {
             const int chunk = lane >> 2, slot = (n & 1) * 4 + (lane & 3);
             const int from = (((chunk & 3) << 1) | (chunk >> 2)) * 4 + (n >> 1);
+            return &sm->red[b][w][slot][from];
+        };
+        // and the sum of a box's parts, from the set of the item's first stage on: the same order whichever set that is
+        auto total = [&](int b, int n, int box, int start) {
             float s = 0.f;
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int w = 0; w < kSlices; ++w) s += sm->red[b][(q ^ start) * 8 + box * 4 + w][slot][from];
+                for (int w = 0; w < kSlices; ++w) s += *part_of(b, n, (q ^ start) * 8 + box * 4 + w);
             return s;
         };
         Walk at(cta, grid, cols2);
@@ -802,6 +853,16 @@ moe_kernel(const __grid_constant__ CUtensorMap tw13, const __grid_constant__ CUt
             if (!ok || !warp_wait_bar(&sm->sums[b], count / kBuffers & 1u, abort)) {
                 ok = false;
                 continue;
+            }
+            const uint32_t* has = sm->factored[b];
+            if (has[0] | has[1] | has[2] | has[3]) {
+                // some parts hold the factors: the others get them in place, by the lanes that will add them up
+                for (int n0 = 2 * half; n0 < n; n0 += (n0 & 1) ? 2 * kEpilogues - 1 : 1) {
+                    const float fi = __shfl_sync(0xffffffffu, f, n0);
+                    for (int w = 0; w < kConsumerWarps; ++w)
+                        if (!((has[w >> 2] >> (8 * (w & 3))) & 0xFFu)) *part_of(b, n0, w) *= fi;
+                }
+                f = 1.f;
             }
             float back = 0.f;   // lane i: token i's factor 2^-shift
             for (int i0 = 2 * half; i0 < n; i0 += 2 * kEpilogues) {
