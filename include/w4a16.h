@@ -126,9 +126,9 @@ w4a16_status w4a16_unpack(const int32_t* src, uint8_t* dst, int64_t rows, int64_
  * with M <= 128: FP32 partial slots of 128 KB per SM, followed by four 32-bit
  * tickets per 128 columns (rounded up to 256 bytes); 0 for the GEMM with
  * M > 128. The same sizes serve w4a16_mxfp4_gemv and w4a16_mxfp4_gemm with
- * g = 32. For the MXFP4 product (g = 32): FP32 partial tiles of 128 KB per SM,
- * then four 32-bit tickets per 128 x 128 tile of y (rounded up to 256 bytes);
- * 0 for shapes large enough for its CTA-pair kernel.
+ * g = 32. For the MXFP4 product (g = 32) with M <= 32: FP32 partial tiles of
+ * 128 KB per SM, then four 32-bit tickets per 128 columns of y (rounded up to
+ * 256 bytes); 0 for the product with M > 32.
  * Returns 0 for shapes the op rejects and when no GB300 is current.
  */
 size_t w4a16_workspace_bytes(w4a16_op op, int64_t M, int64_t N, int64_t K, int64_t g);
@@ -433,12 +433,14 @@ w4a16_status w4a16_mxfp4_tile_scales(const uint8_t* src, uint8_t* dst, int64_t r
  * product leaves the FP32 range overflow to infinity or flush to zero.
  *
  * Large products run on CTA pairs (256 x 256 tiles); the others (always for
- * M <= 128) on a kernel with 128 rows of B per tile that may split tiles between
- * CTAs and takes a workspace of w4a16_workspace_bytes(W4A16_OP_MXFP4_MATMUL, M,
- * N, K, 32) bytes (0: none needed), with the ownership and zero-fill rules of
- * w4a16_gemv's; a workspace of this op serves this op only. Split tiles are
- * summed in a fixed order: the result is deterministic. After a
- * W4A16_ERR_TIMEOUT reported by w4a16_device_status, zero the workspace again.
+ * M <= 128) on a kernel with 128 rows of B per tile, whose CTAs may split a
+ * tile's K among them. With M <= 32 it takes a workspace of
+ * w4a16_workspace_bytes(W4A16_OP_MXFP4_MATMUL, M, N, K, 32) bytes, with the
+ * ownership and zero-fill rules of w4a16_gemv's (one sized for the largest N
+ * serves every shape); a workspace of this op serves this op only. With M > 32 it
+ * uses none. Split tiles are summed in a fixed order: the result is
+ * deterministic. After a W4A16_ERR_TIMEOUT reported by w4a16_device_status, zero
+ * the workspace again.
  *
  * M >= 1, N % 8 == 0, K % 32 == 0. An ordinary launch (no programmatic
  * serialization).

@@ -564,8 +564,10 @@ def mxfp4_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, workspace=Non
     lib = load_library()
     device = a.device
     out = _out("out", out, (M, N), out_dtype, device, stream)
-    ws_ptr, ws_bytes = _workspace(workspace, OP_MXFP4_MATMUL, lib.w4a16_workspace_bytes,
-                                  (OP_MXFP4_MATMUL, M, N, K, 32), device, stream)
+    ws_ptr, ws_bytes = 0, 0
+    if M <= 32:   # tiles shared between thread blocks only there
+        ws_ptr, ws_bytes = _workspace(workspace, OP_MXFP4_MATMUL, lib.w4a16_workspace_bytes,
+                                      (OP_MXFP4_MATMUL, M, N, K, 32), device, stream)
     st = lib.w4a16_mxfp4_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr(),
                                 M, N, K, dt, ws_ptr, ws_bytes, _stream_ptr(stream))
     _check("w4a16_mxfp4_matmul", st)

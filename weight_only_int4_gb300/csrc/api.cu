@@ -195,7 +195,7 @@ size_t w4a16_workspace_bytes(w4a16_op op, int64_t M, int64_t N, int64_t K, int64
     DeviceProps dp;
     if (device_gate(&dp) != W4A16_OK) return 0;
     if (op == W4A16_OP_MXFP4_MATMUL)
-        return check_mx_product(M, N, K) == W4A16_OK ? w4a16::mx_matmul_workspace_bytes(M, N, K, dp) : 0;
+        return check_mx_product(M, N, K) == W4A16_OK ? w4a16::mx_matmul_workspace_bytes(M, N, dp) : 0;
     if (op == W4A16_OP_GEMM) return w4a16::skinny_workspace_bytes((int)N, dp);
     return w4a16::gemv_workspace(w4a16::plan_gemv((int)M, (int)N, (int)K, (int)g, dp), (int)N, dp).total();
 }
@@ -400,11 +400,10 @@ w4a16_status w4a16_mxfp4_matmul(const int32_t* a, const uint8_t* ea, const int32
     w4a16_status st = check_mx_product(M, N, K);
     if (st != W4A16_OK) return st;
     if (!aligned16(a) || !aligned16(ea) || !aligned16(b) || !aligned16(eb) || !aligned16(y)) return W4A16_ERR_ALIGN;
-    if (M <= 128 && (!workspace || !aligned16(workspace))) return W4A16_ERR_WORKSPACE;
+    if (M <= w4a16::kMxMatmulSharedMaxM && (!workspace || !aligned16(workspace))) return W4A16_ERR_WORKSPACE;
     DeviceProps dp;
     if ((st = device_gate(&dp)) != W4A16_OK) return st;
-    const size_t need = w4a16::mx_matmul_workspace_bytes(M, N, K, dp);
-    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+    if (workspace_bytes < w4a16::mx_matmul_workspace_bytes(M, N, dp)) return W4A16_ERR_WORKSPACE;
     const w4a16::MxMatmulArgs args{reinterpret_cast<const uint32_t*>(a), ea, reinterpret_cast<const uint32_t*>(b), eb, y,
                                    (int)M, (int)N, (int)K};
     return from_cuda(w4a16::launch_mx_matmul(args, static_cast<int>(dt), workspace, dp,

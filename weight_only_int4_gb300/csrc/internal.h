@@ -145,10 +145,12 @@ struct MxMatmulArgs {
     void* y;
     int M, N, K;
 };
-// 0 where the kernel for this shape needs none; else FP32 partial tiles (128 KB
-// per SM, a size fixed per device), then four ticket words per 128 x 128 tile
-// (zero before the first call; every call leaves them zero).
-size_t mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceProps& dp);
+// Up to this many rows of A (one row tile) tiles of y may be shared between
+// thread blocks. Their workspace: FP32 partial tiles (128 KB per SM, a size fixed
+// per device), then four ticket words per 128 columns of y (zero before the first
+// call; every call leaves them zero). 0 for more rows.
+constexpr int64_t kMxMatmulSharedMaxM = 32;
+size_t mx_matmul_workspace_bytes(int64_t M, int64_t N, const DeviceProps& dp);
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, int out_type, void* workspace, const DeviceProps& dp,
                              cudaStream_t s);
 cudaError_t read_and_clear_mx_matmul_error(uint32_t* out);

@@ -736,7 +736,7 @@ Plan plan(long long M, long long N, long long K, const DeviceProps& dp) {
     const long long split = std::min<long long>({6, dp.sms / tiles, steps / 2});
     if (split > 1 && steps - steps / split >= 8) return {mp, static_cast<int>(split), false};
     const long long waves = (tiles + dp.sms - 1) / dp.sms;
-    return {mp, 1, mp <= 32 && tiles > dp.sms && waves * dp.sms * 100 > tiles * 115};
+    return {mp, 1, M <= kMxMatmulSharedMaxM && tiles > dp.sms && waves * dp.sms * 100 > tiles * 115};
 }
 
 template <int kOut>
@@ -856,11 +856,10 @@ cudaError_t launch_typed(const MxMatmulArgs& a, void* workspace, const DevicePro
 
 }  // namespace
 
-size_t mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceProps& dp) {
-    const Plan pl = plan(M, N, K, dp);
-    if (pl.mp == 0) return 0;
-    const size_t tiles = static_cast<size_t>((M + pl.mp - 1) / pl.mp) * ((N + rows::BN - 1) / rows::BN);
-    return partial_bytes(dp) + ((tiles * 4 * sizeof(uint32_t) + 255) & ~size_t(255));
+size_t mx_matmul_workspace_bytes(int64_t M, int64_t N, const DeviceProps& dp) {
+    if (M > kMxMatmulSharedMaxM) return 0;
+    const size_t cols = static_cast<size_t>((N + rows::BN - 1) / rows::BN);
+    return partial_bytes(dp) + ((cols * 4 * sizeof(uint32_t) + 255) & ~size_t(255));
 }
 
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, int out_type, void* workspace, const DeviceProps& dp,
