@@ -524,6 +524,18 @@ w4a16_status w4a16_device_status(w4a16_stream stream);
  */
 w4a16_status w4a16_selftest_wait_timeout(w4a16_stream stream);
 
+/*
+ * w4a16_selftest_mxfp4_matmul_plan -- how w4a16_mxfp4_matmul would run a shape
+ * on a device of `sms` SMs, for tests that have to reach each way of running
+ * it. Host only. (No counterpart on the pages this library follows.)
+ * plan[0]  rows of A per tile (16, 32, 64 or 128), or 0: 256 x 256 tiles on CTA
+ *          pairs
+ * plan[1]  CTAs of a cluster that split a tile's K (1: not split)
+ * plan[2]  1 if tiles are shared between CTAs through the workspace
+ * Errors: NULL, SHAPE.
+ */
+w4a16_status w4a16_selftest_mxfp4_matmul_plan(int64_t M, int64_t N, int64_t K, int sms, int* plan);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* w4a16_status_string(w4a16_status status);
 

@@ -53,6 +53,7 @@ SIGNATURES = {
     "w4a16_gemv_noalloc": (_INT, [_VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _INT, _VP]),
     "w4a16_device_status": (_INT, [_VP]),
     "w4a16_selftest_wait_timeout": (_INT, [_VP]),
+    "w4a16_selftest_mxfp4_matmul_plan": (_INT, [_I64, _I64, _I64, _INT, ctypes.POINTER(_INT)]),
     "w4a16_dequant": (_INT, [_VP, _VP, _VP, _VP, _I64, _I64, _I64, _INT, _VP]),
     "w4a16_mxfp4_dequant": (_INT, [_VP, _VP, _VP, _I64, _I64, _VP]),
     "w4a16_mxfp4_gemv": (_INT, [_VP, _VP, _VP, _VP, _I64, _I64, _I64, _VP, _SZ, _VP]),

@@ -410,6 +410,17 @@ w4a16_status w4a16_mxfp4_matmul(const int32_t* a, const uint8_t* ea, const int32
                                              reinterpret_cast<cudaStream_t>(stream)));
 }
 
+w4a16_status w4a16_selftest_mxfp4_matmul_plan(int64_t M, int64_t N, int64_t K, int sms, int* plan) {
+    if (!plan) return W4A16_ERR_NULL;
+    const w4a16_status st = check_mx_product(M, N, K);
+    if (st != W4A16_OK) return st;
+    if (sms < 1) return W4A16_ERR_SHAPE;
+    int p[3];
+    w4a16::mx_matmul_plan(M, N, K, sms, p);
+    for (int i = 0; i < 3; ++i) plan[i] = p[i];
+    return W4A16_OK;
+}
+
 size_t w4a16_mxfp4_moe_workspace_bytes(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I) {
     if (check_moe_shape(T, E, top_k, H, I) != W4A16_OK) return 0;
     return w4a16::mx_moe_workspace_bytes((int)T, (int)E, (int)top_k, (int)H, (int)I);

@@ -151,6 +151,8 @@ struct MxMatmulArgs {
 // call; every call leaves them zero). 0 for more rows.
 constexpr int64_t kMxMatmulSharedMaxM = 32;
 size_t mx_matmul_workspace_bytes(int64_t M, int64_t N, const DeviceProps& dp);
+// {rows of A per tile (0: CTA pairs), CTAs of a cluster per tile, tiles shared} on a device of `sms` SMs.
+void mx_matmul_plan(int64_t M, int64_t N, int64_t K, int sms, int (&out)[3]);
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, int out_type, void* workspace, const DeviceProps& dp,
                              cudaStream_t s);
 cudaError_t read_and_clear_mx_matmul_error(uint32_t* out);

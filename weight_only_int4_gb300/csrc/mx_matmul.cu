@@ -417,6 +417,9 @@ struct Cfg {
     static constexpr uint32_t kScaleCol = 2 * kAccCols;       // 16 columns of exponents per stage
     static constexpr uint32_t kTmemCols = kScaleCol + 16 * kStages <= 256 ? 256 : 512;
     static_assert(kScaleCol + 16 * kStages <= 512, "tensor memory budget");
+    // What plan() never gives a template is not compiled into it: 128-row tiles are taken where more than half of the
+    // SMs have one, and tiles are shared only for one row tile.
+    static constexpr bool kSplits = MP < 128, kShares = MP <= kMxMatmulSharedMaxM;
 };
 
 template <int MP>
@@ -444,10 +447,12 @@ template <int kOut, int MP>
 __global__ void __launch_bounds__(kThreads, 1)
 rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
             const uint8_t* __restrict__ ew, const uint8_t* __restrict__ ex, void* __restrict__ y,
-            int M, int N, int K, int split, int share, float* __restrict__ partials,
+            int M, int N, int K, int split_by, int shared_units, float* __restrict__ partials,
             uint32_t* __restrict__ tickets) {
     using C = Cfg<MP>;
     constexpr int S = C::kStages;
+    const int split = C::kSplits ? split_by : 1;
+    const bool share = C::kShares && shared_units;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Barriers<MP>* bars = reinterpret_cast<Barriers<MP>*>(smem + S * C::kStageBytes);
@@ -602,7 +607,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
             const int m0 = static_cast<int>(t % num_m) * MP;
             const int mc = min(MP, M - m0);                              // rows of A of this tile
             const int n = static_cast<int>(t / num_m) * BN + q * 32 + lane;
-            const bool whole = k0 == 0 && k1 == kt_total;
+            const bool whole = !C::kShares || (k0 == 0 && k1 == kt_total);
             // slot 1: the tile begins here; slot 0: an earlier CTA began it
             float* part =
                 partials + (static_cast<size_t>(blockIdx.x) * 2 + (k0 == 0 ? 1 : 0)) * kSlotFloats + q * 32 + lane;
@@ -724,19 +729,19 @@ struct Plan {
 //     512 x 4096 x 4096 (128) 13.5 / 9.3: 64 where both kinds fit one wave;
 //   shared units against whole tiles: 16 x 43008 x 5376 (336 tiles) 26.0 / 28.0, 32 rows 27.3 / 27.9, but 64 rows
 //     31.2 / 27.7 and everything that fits one wave slower: up to 32 rows, where the last wave is mostly idle.
-Plan plan(long long M, long long N, long long K, const DeviceProps& dp) {
+Plan plan(long long M, long long N, long long K, int sms) {
     const long long cols = (N + rows::BN - 1) / rows::BN, steps = (K + kStepK - 1) / kStepK;
     const long long tiles128 = ((M + 127) / 128) * cols;
-    if (M > 128 && tiles128 > dp.sms) return {0, 1, false};
-    const int mp = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 || 2 * tiles128 <= dp.sms ? 64 : 128;
+    if (M > 128 && tiles128 > sms) return {0, 1, false};
+    const int mp = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 || 2 * tiles128 <= sms ? 64 : 128;
     const long long tiles = ((M + mp - 1) / mp) * cols;
     // a step saved is worth 0.2..0.3 us, a cluster's sum and its ordinary launch cost about 2 us: 1 x 2048 x 4096 8.8
     // (whole) / 5.3 (6 CTAs a tile), 1 x 5376 x 21504 27.4 / 15.7 (3), 100 x 1288 x 9120 13.6 / 8.5 (6). Clusters of 7
     // and 8 do not all fit at once: 16 x 2048 x 8192 7.8 with 6, 13.0 with 7, 11.8 with 8
-    const long long split = std::min<long long>({6, dp.sms / tiles, steps / 2});
+    const long long split = std::min<long long>({6, sms / tiles, steps / 2});
     if (split > 1 && steps - steps / split >= 8) return {mp, static_cast<int>(split), false};
-    const long long waves = (tiles + dp.sms - 1) / dp.sms;
-    return {mp, 1, M <= kMxMatmulSharedMaxM && tiles > dp.sms && waves * dp.sms * 100 > tiles * 115};
+    const long long waves = (tiles + sms - 1) / sms;
+    return {mp, 1, M <= kMxMatmulSharedMaxM && tiles > sms && waves * sms * 100 > tiles * 115};
 }
 
 template <int kOut>
@@ -842,7 +847,7 @@ size_t partial_bytes(const DeviceProps& dp) {
 
 template <int kOut>
 cudaError_t launch_typed(const MxMatmulArgs& a, void* workspace, const DeviceProps& dp, cudaStream_t s) {
-    const Plan pl = plan(a.M, a.N, a.K, dp);
+    const Plan pl = plan(a.M, a.N, a.K, dp.sms);
     float* partials = static_cast<float*>(workspace);
     uint32_t* tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + partial_bytes(dp));
     switch (pl.mp) {
@@ -855,6 +860,11 @@ cudaError_t launch_typed(const MxMatmulArgs& a, void* workspace, const DevicePro
 }
 
 }  // namespace
+
+void mx_matmul_plan(int64_t M, int64_t N, int64_t K, int sms, int (&out)[3]) {
+    const Plan pl = plan(M, N, K, sms);
+    out[0] = pl.mp, out[1] = pl.split, out[2] = pl.share ? 1 : 0;
+}
 
 size_t mx_matmul_workspace_bytes(int64_t M, int64_t N, const DeviceProps& dp) {
     if (M > kMxMatmulSharedMaxM) return 0;
