@@ -106,14 +106,16 @@ def abi_version() -> int:
 
 _torch_module = None
 _raw_stream = None   # device -> handle of its current stream; the object torch.cuda.current_stream() builds costs 3 us
+_current_device = None
 _dtype_codes = {}
 
 
 def _torch():
-    global _torch_module, _raw_stream
+    global _torch_module, _raw_stream, _current_device
     if _torch_module is None:
         import torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _dtype_codes.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
         _torch_module = torch
     return _torch_module
@@ -151,10 +153,28 @@ def _dtype_code(dtype) -> int:
 
 
 def _cuda_contig(name: str, t) -> None:
-    if not t.is_cuda:
+    """The kernels run on the current device and take raw pointers: every tensor has to be there, and dense."""
+    where = t.get_device()
+    if where < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if where != _current_device():
+        raise ValueError(f"{name} is on cuda:{where}, the current device is cuda:{_current_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _out(name: str, t, shape, dtype, device, stream=None):
+    """`t`, checked, or a new tensor that belongs to `stream` (the current one unless given)."""
+    torch = _torch()
+    if t is None:
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+    _cuda_contig(name, t)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t
 
 
 def pack(codes, dim: int, out=None, stream=None):
@@ -165,9 +185,7 @@ def pack(codes, dim: int, out=None, stream=None):
         raise TypeError("codes must be a 2-D torch.uint8 tensor")
     R, C = codes.shape
     shape = (R // 8, C) if dim == 0 else (R, C // 8)
-    if out is None:
-        out = torch.empty(shape, dtype=torch.int32, device=codes.device)
-    _cuda_contig("out", out)
+    out = _out("out", out, shape, torch.int32, codes.device)
     _check("w4a16_pack", load_library().w4a16_pack(codes.data_ptr(), out.data_ptr(), R, C, dim,
                                                    _stream_ptr(stream)))
     return out
@@ -181,9 +199,7 @@ def unpack(words, dim: int, out=None, stream=None):
         raise TypeError("words must be a 2-D torch.int32 tensor")
     W0, W1 = words.shape
     R, C = (W0 * 8, W1) if dim == 0 else (W0, W1 * 8)
-    if out is None:
-        out = torch.empty((R, C), dtype=torch.uint8, device=words.device)
-    _cuda_contig("out", out)
+    out = _out("out", out, (R, C), torch.uint8, words.device)
     _check("w4a16_unpack", load_library().w4a16_unpack(words.data_ptr(), out.data_ptr(), R, C, dim,
                                                        _stream_ptr(stream)))
     return out
@@ -266,6 +282,14 @@ def _cached_workspace(nbytes: int, device, stream, op: int):
     return ws
 
 
+def _workspace_args(ws):
+    """(address, bytes) of a workspace, or of none."""
+    if ws is None:
+        return 0, 0
+    _cuda_contig("workspace", ws)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def release_workspaces() -> None:
     """Free the workspaces the binding allocated for calls made without one (one
     per device, stream and op, one more for each capture of the stream, plus any
@@ -305,17 +329,14 @@ def _layer(fn_name: str, x, qweight, scales, qzeros, group_size: int, out=None, 
         if qzeros.shape != (K // group_size, N // 8):
             raise ValueError(f"qzeros shape {tuple(qzeros.shape)} does not match (K/g, N/8)")
         zp = qzeros.data_ptr()
-    if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
-    _cuda_contig("out", out)
+    out = _out("out", out, (M, N), x.dtype, x.device)
     lib = load_library()
     sp = _stream_ptr(stream)
     if workspace is None:
         op = OP_GEMV if fn_name == "w4a16_gemv" else OP_GEMM
         need = lib.w4a16_workspace_bytes(op, M, N, K, group_size)
         workspace = _cached_workspace(need, x.device, stream, op) if need else None
-    ws_ptr, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(),
-                                                          workspace.numel() * workspace.element_size())
+    ws_ptr, ws_bytes = _workspace_args(workspace)
     _check(fn_name, getattr(lib, fn_name)(x.data_ptr(), qweight.data_ptr(), scales.data_ptr(), zp,
                                           out.data_ptr(), M, N, K, group_size, dt, ws_ptr, ws_bytes, sp))
     return out
@@ -355,11 +376,7 @@ def dequant(qweight, scales, qzeros: Optional[object], group_size: int, out=None
         if qzeros.shape != (K // group_size, N // 8):
             raise ValueError(f"qzeros shape {tuple(qzeros.shape)} does not match (K/g, N/8)")
         zp = qzeros.data_ptr()
-    if out is None:
-        out = torch.empty((K, N), dtype=scales.dtype, device=scales.device)
-    _cuda_contig("out", out)
-    if out.shape != (K, N) or out.dtype != scales.dtype:
-        raise ValueError(f"out must be {scales.dtype} [K, N] = [{K}, {N}]")
+    out = _out("out", out, (K, N), scales.dtype, scales.device)
     _check("w4a16_dequant", load_library().w4a16_dequant(qweight.data_ptr(), scales.data_ptr(), zp, out.data_ptr(),
                                                          N, K, group_size, dt, _stream_ptr(stream)))
     return out
@@ -390,19 +407,14 @@ def _mx_layer(fn_name: str, x, qweight, escale, out, workspace, stream):
     M = x.shape[0]
     if x.shape[1] != K:
         raise ValueError(f"x has {x.shape[1]} columns, qweight holds K = {K} rows")
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    _cuda_contig("out", out)
-    if out.shape != (M, N) or out.dtype != torch.bfloat16:
-        raise ValueError(f"out must be bf16 [M, N] = [{M}, {N}]")
+    out = _out("out", out, (M, N), torch.bfloat16, x.device)
     lib = load_library()
     sp = _stream_ptr(stream)
     if workspace is None:
         op = OP_GEMM if fn_name == "w4a16_mxfp4_gemm" else OP_GEMV
         need = lib.w4a16_workspace_bytes(op, M, N, K, 32)
         workspace = _cached_workspace(need, x.device, stream, op) if need else None
-    ws_ptr, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(),
-                                                          workspace.numel() * workspace.element_size())
+    ws_ptr, ws_bytes = _workspace_args(workspace)
     if fn_name == "w4a16_mxfp4_gemm":
         _check(fn_name, lib.w4a16_mxfp4_gemm(x.data_ptr(), qweight.data_ptr(), escale.data_ptr(), out.data_ptr(),
                                               M, N, K, ws_ptr, ws_bytes, sp))
@@ -427,11 +439,7 @@ def mxfp4_dequant(qweight, escale, out=None, stream=None):
     """Dense bf16 copy W[k, n] = E2M1(q[k, n]) * 2^(e[k/32, n] - 127), [K, N]."""
     torch = _torch()
     K, N = _mx_weights(qweight, escale)
-    if out is None:
-        out = torch.empty((K, N), dtype=torch.bfloat16, device=qweight.device)
-    _cuda_contig("out", out)
-    if out.shape != (K, N) or out.dtype != torch.bfloat16:
-        raise ValueError(f"out must be bf16 [K, N] = [{K}, {N}]")
+    out = _out("out", out, (K, N), torch.bfloat16, qweight.device)
     _check("w4a16_mxfp4_dequant", load_library().w4a16_mxfp4_dequant(qweight.data_ptr(), escale.data_ptr(),
                                                                        out.data_ptr(), N, K, _stream_ptr(stream)))
     return out
@@ -441,20 +449,6 @@ def mxfp4_scale_shape(rows: int, cols: int):
     """Shape of the exponent bytes of a row-layout operand [rows, cols]: tiles of
     128 rows x 4 blocks, [row tile, block tile, row % 32, row // 32 % 4, block % 4]."""
     return (-(-rows // 128), -(-cols // 128), 32, 4, 4)
-
-
-def _out(name: str, t, shape, dtype, device, stream=None):
-    """`t`, checked, or a new tensor that belongs to the call's stream."""
-    torch = _torch()
-    if t is None:
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-    _cuda_contig(name, t)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    return t
 
 
 def mxfp4_quantize(x, dim: int, out=None, stream=None):
@@ -547,7 +541,8 @@ def _workspace(given, op, query, shape, device, stream):
         if not need:
             return 0, 0
         given = _cached_workspace(need, device, stream, op)
-    return given.data_ptr(), given.numel() * given.element_size()
+        return given.data_ptr(), given.numel()
+    return _workspace_args(given)
 
 
 def mxfp4_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, workspace=None, stream=None):
@@ -565,10 +560,11 @@ def mxfp4_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, workspace=Non
     lib = load_library()
     device = a.device
     out = _out("out", out, (M, N), out_dtype, device, stream)
-    ws_ptr, ws_bytes = 0, 0
     if M <= 32:   # tiles shared between thread blocks only there
         ws_ptr, ws_bytes = _workspace(workspace, OP_MXFP4_MATMUL, lib.w4a16_workspace_bytes,
                                       (OP_MXFP4_MATMUL, M, N, K, 32), device, stream)
+    else:
+        ws_ptr, ws_bytes = _workspace_args(workspace)
     st = lib.w4a16_mxfp4_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr(),
                                 M, N, K, dt, ws_ptr, ws_bytes, _stream_ptr(stream))
     _check("w4a16_mxfp4_matmul", st)
