@@ -90,3 +90,15 @@ def test_captured_fill_covers_what_must_start_at_zero(op, nbytes):
         assert (first, last) == ((partials if nbytes > partials else 0), nbytes)
     ws = w4._captured_workspace(nbytes, torch.device("cpu"), op, 152)
     assert ws.numel() == nbytes and not ws[first:last].any()
+
+
+def test_a_failed_size_query_is_not_remembered(monkeypatch):
+    """The library answers 0 where no GB300 is current: the next call of the shape asks again."""
+    answers = [0, 4096, 8192]
+    ws = types.SimpleNamespace(data_ptr=lambda: 0x10000, numel=lambda: 4096, element_size=lambda: 1)
+    monkeypatch.setattr(w4, "_workspace_needs", {})
+    monkeypatch.setattr(w4, "_cached_workspace", lambda nbytes, device, stream, op: ws)
+    ask = lambda: w4._workspace(None, "op", lambda *shape: answers.pop(0), (1, 2, 3), Device, None)
+    assert ask() == (0, 0)
+    assert ask() == (0x10000, 4096)
+    assert ask() == (0x10000, 4096) and answers == [8192]   # a size is

@@ -530,14 +530,18 @@ _workspace_needs = {}
 
 def _workspace(given, op, query, shape, device, stream):
     """(address, bytes) of the caller's workspace or the binding's own, which
-    needs query(*shape) bytes; the sizes of the last few hundred shapes are kept."""
+    needs query(*shape) bytes on the current device; the sizes of the last few
+    hundred shapes are kept. A size of 0 is not: the library also answers so
+    where the query itself fails."""
     if given is None:
         key = (op, device.index, shape)
         need = _workspace_needs.get(key)
         if need is None:
-            if len(_workspace_needs) >= 512:
-                _workspace_needs.clear()
-            need = _workspace_needs[key] = int(query(*shape))
+            need = int(query(*shape))
+            if need:
+                if len(_workspace_needs) >= 512:
+                    _workspace_needs.clear()
+                _workspace_needs[key] = need
         if not need:
             return 0, 0
         given = _cached_workspace(need, device, stream, op)
