@@ -29,6 +29,10 @@ PLANS = {
     (9, 38400, 800): (16, 1, 0),          # 300 tiles: whole ones, two a CTA
     (24, 2048, 1024): (32, 1, 0),
     (16, 2048, 5376): (16, 6, 0),
+    (16, 5376, 2048): (16, 3, 0),         # six of eight steps saved
+    (16, 5376, 1536): (16, 1, 0),         # four of six would be
+    (50, 5376, 2048): (64, 1, 0),
+    (1, 2048, 2048): (16, 4, 0),
     (17, 5376, 4128): (32, 3, 0),
     (70, 2000, 8192): (64, 4, 0),
     (700, 10240, 288): (0, 1, 0),

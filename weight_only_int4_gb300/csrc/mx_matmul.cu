@@ -721,25 +721,28 @@ struct Plan {
     bool share;   // tiles split between CTAs by units
 };
 
-// Measured on 152 SMs (us; whole tiles unless said):
-//   pair kernel against 128-row tiles: 1024 x 2560 x 5376 (160 tiles) 14.4 / 17.1, 200 x 16384 x 5376 (256) 14.8 /
-//     17.5, 512 x 4096 x 4096 (128) 11.8 / 9.3, 700 x 2560 x 5376 (120) 14.1 / 10.6: the pair kernel where 128-row
+// Measured on 152 SMs (us a call, whole tiles unless said):
+//   pair kernel against 128-row tiles: 1024 x 2560 x 5376 (160 tiles) 13.7 / 19.0, 200 x 16384 x 5376 (256) 16.2 /
+//     20.2, 512 x 4096 x 4096 (128) 11.7 / 11.1, 700 x 2560 x 5376 (120) 14.0 / 12.6: the pair kernel where 128-row
 //     tiles need a second wave;
-//   64-row against 128-row tiles: 300 x 2600 x 2080 (63 tiles of 128) 6.6 / 7.6, 128 x 6144 x 2048 (48) 6.3 / 6.6,
-//     512 x 4096 x 4096 (128) 13.5 / 9.3: 64 where both kinds fit one wave;
-//   shared units against whole tiles: 16 x 43008 x 5376 (336 tiles) 26.0 / 28.0, 32 rows 27.3 / 27.9, but 64 rows
-//     31.2 / 27.7 and everything that fits one wave slower: up to 32 rows, where the last wave is mostly idle.
+//   64-row against 128-row tiles: 300 x 2600 x 2080 (63 tiles of 128) 7.9 / 9.1, 128 x 6144 x 2048 (48) 7.8 / 8.7,
+//     512 x 4096 x 4096 (128) 15.0 / 11.1: 64 where both kinds fit one wave;
+//   shared units against whole tiles: 16 x 43008 x 5376 (336 tiles) 27.1 / 29.5, 32 rows 29.2 / 29.7, but 64 rows
+//     32.9 / 29.9 and what fits one wave slower (16 x 16384 x 5376 15.0 / 12.3): up to 32 rows, where the last wave
+//     is mostly idle.
 Plan plan(long long M, long long N, long long K, int sms) {
     const long long cols = (N + rows::BN - 1) / rows::BN, steps = (K + kStepK - 1) / kStepK;
     const long long tiles128 = ((M + 127) / 128) * cols;
     if (M > 128 && tiles128 > sms) return {0, 1, false};
     const int mp = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 || 2 * tiles128 <= sms ? 64 : 128;
     const long long tiles = ((M + mp - 1) / mp) * cols;
-    // a step saved is worth 0.2..0.3 us, a cluster's sum and its ordinary launch cost about 2 us: 1 x 2048 x 4096 8.8
-    // (whole) / 5.3 (6 CTAs a tile), 1 x 5376 x 21504 27.4 / 15.7 (3), 100 x 1288 x 9120 13.6 / 8.5 (6). Clusters of 7
-    // and 8 do not all fit at once: 16 x 2048 x 8192 7.8 with 6, 13.0 with 7, 11.8 with 8
+    // A step saved is worth 0.3 us; a cluster's sum costs 1 to 1.5 us with up to 32 rows and 2 with 64. Whole / split:
+    // 1 x 2048 x 4096 10.2 / 5.8 (6 CTAs a tile), 1 x 5376 x 21504 30.2 / 15.3 (3), 100 x 1288 x 9120 15.8 / 8.7 (6),
+    // 16 x 5376 x 2048 7.4 / 6.6 (3: 6 steps saved), 16 x 8192 x 2048 7.5 / 7.6 (2: 4 saved), 64 x 5376 x 2048 7.7 /
+    // 8.4 (3: 6 saved). Clusters of 7 and 8 do not all fit at once: 16 x 2048 x 8192 7.8 with 6, 13.2 with 7, 12.3
+    // with 8.
     const long long split = std::min<long long>({6, sms / tiles, steps / 2});
-    if (split > 1 && steps - steps / split >= 8) return {mp, static_cast<int>(split), false};
+    if (split > 1 && steps - steps / split >= (mp <= 32 ? 5 : 8)) return {mp, static_cast<int>(split), false};
     const long long waves = (tiles + sms - 1) / sms;
     return {mp, 1, M <= kMxMatmulSharedMaxM && tiles > sms && waves * sms * 100 > tiles * 115};
 }
