@@ -150,3 +150,11 @@ def test_quantised_outputs(lib):
     with pytest.raises(ValueError):
         w4.mxfp4_quantize(Tensor((5, 128), bf16, 1), 1, out=good)
     assert len(lib.launched) == 1
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_host_tensors_without_a_device(name):
+    """The same answer on a host that has no CUDA driver to ask."""
+    call, spec, _, _ = CALLS[name]
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
+        call({n: torch.zeros(s, dtype=d) for n, (s, d) in spec.items()})

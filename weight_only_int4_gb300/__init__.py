@@ -152,12 +152,13 @@ def _dtype_code(dtype) -> int:
     return code
 
 
-def _cuda_contig(name: str, t) -> None:
-    """The kernels run on the current device and take raw pointers: every tensor has to be there, and dense."""
+def _cuda_contig(name: str, t, current: Optional[int] = None) -> None:
+    """The kernels run on the current device (`current`, where the caller knows it)
+    and take raw pointers: every tensor has to be there, and dense."""
     where = t.get_device()
     if where < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if where != _current_device():
+    if where != (_current_device() if current is None else current):
         raise ValueError(f"{name} is on cuda:{where}, the current device is cuda:{_current_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -490,7 +491,7 @@ def _mx_rows(name: str, codes, escale):
     """Checks a row-layout operand, returns its rows and K."""
     torch = _torch()
     _cuda_contig(name, codes)
-    _cuda_contig(name + " scales", escale)
+    _cuda_contig(name + " scales", escale, codes.get_device())
     shape = codes.shape
     if len(shape) != 2 or codes.dtype != torch.int32:
         raise TypeError(f"{name} must be a 2-D torch.int32 tensor of codes")
@@ -588,9 +589,11 @@ def mxfp4_moe(x, router, w13, e13, w2, e2, top_k: int, renormalize: bool = True,
     [E, I, H]. Returns y bf16 [T, H]."""
     torch = _torch()
     bf16, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+    _cuda_contig("x", x)
+    current = x.get_device()
     for name, t, dtype, dims in (("x", x, bf16, 2), ("router", router, bf16, 2), ("w13", w13, i32, 3),
                                  ("e13", e13, u8, 3), ("w2", w2, i32, 3), ("e2", e2, u8, 3)):
-        _cuda_contig(name, t)
+        _cuda_contig(name, t, current)
         if t.dim() != dims or t.dtype != dtype:
             raise TypeError(f"{name} must be a {dims}-D {dtype} tensor, got {t.dim()}-D {t.dtype}")
     T, H = x.shape
