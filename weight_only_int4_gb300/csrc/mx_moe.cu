@@ -41,9 +41,9 @@
 // next ones.
 //
 // Measured in a graph of calls on operands larger than L2: 1 token, 4 of 32
-// experts of 2048 x 1024 14.6..16.9 us; 16 tokens, 8 of 64 of 4096 x 1024 79..81
+// experts of 2048 x 1024 14.5..17.0 us; 16 tokens, 8 of 64 of 4096 x 1024 80..82
 // (the weights' bytes take 56 at the copy bandwidth); 64 tokens, 8 of 128 of
-// 2048 x 1024 103 (63). What bounds the last one: 18.6 us are everything but the
+// 2048 x 1024 102..105 (63). What bounds the last one: 18.6 us are everything but the
 // items (barriers, router, top-k, the last sums). Without the products the call
 // takes 87 us, without the loads as long as with them, without loads and epilogue
 // 84: the consumer warps' instructions, and the epilogue warps' beside them. More
