@@ -44,6 +44,15 @@ def test_one_unusual_block(where):
     check(case, where)
 
 
+@pytest.mark.parametrize("I", [288, 512])
+def test_h_near_the_top_of_the_range(I):
+    """h about 2^122: 32 of its products with codes add up past 2^128 before the down weights' 2^-57 brings them
+    back."""
+    case = make(1.0, 182, 183, H=288, I=I, seed=25)
+    case.e2 = np.random.default_rng(25).integers(70, 74, size=case.e2.shape).astype(np.uint8)
+    check(case, I)
+
+
 def test_crowded_experts_and_long_items():
     """Groups of every size up to 8 tokens, several items per thread block, an unusual byte in some experts only."""
     case = make(2.0 ** -100, 184, 190, T=64, E=6, k=2, H=2080, I=544, seed=23)

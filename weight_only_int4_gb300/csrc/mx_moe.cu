@@ -521,12 +521,17 @@ __device__ __forceinline__ void add_products(float (&acc)[2][4], const Operands<
             mma_f16_zero(d, lo[0], hi[0], lo[1], hi[1], o.x[j].x, o.x[j].y);
             mma_m16n8k16<false>(d, lo[2], hi[2], lo[3], hi[3], o.x[j].z, o.x[j].w);
             float(&a)[4] = acc[m];
-            if constexpr (kH) {
-                // d 2^-shift first: the size of h's products, whatever the exponents are
-                a[0] = fmaf(d[0] * o.f0[j], scale[2 * m], a[0]);
-                a[1] = fmaf(d[1] * o.f1[j], scale[2 * m], a[1]);
-                a[2] = fmaf(d[2] * o.f0[j], scale[2 * m + 1], a[2]);
-                a[3] = fmaf(d[3] * o.f1[j], scale[2 * m + 1], a[3]);
+            if constexpr (kH && kEdge) {
+                a[0] = scaled_sum(d[0], o.f0[j], scale[2 * m], a[0]);
+                a[1] = scaled_sum(d[1], o.f1[j], scale[2 * m], a[1]);
+                a[2] = scaled_sum(d[2], o.f0[j], scale[2 * m + 1], a[2]);
+                a[3] = scaled_sum(d[3], o.f1[j], scale[2 * m + 1], a[3]);
+            } else if constexpr (kH) {
+                // with a usual exponent d scale is in range, whatever the factor is
+                a[0] = fmaf(d[0] * scale[2 * m], o.f0[j], a[0]);
+                a[1] = fmaf(d[1] * scale[2 * m], o.f1[j], a[1]);
+                a[2] = fmaf(d[2] * scale[2 * m + 1], o.f0[j], a[2]);
+                a[3] = fmaf(d[3] * scale[2 * m + 1], o.f1[j], a[3]);
             } else if constexpr (kEdge) {
                 a[0] = scaled_sum(d[0], f0, scale[2 * m], a[0]);
                 a[1] = scaled_sum(d[1], f1, scale[2 * m], a[1]);
