@@ -11,6 +11,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import weight_only_int4_gb300 as w4  # noqa: E402
+from oracle import mxfp4_ops_oracle as Q  # noqa: E402
 from test_gpu_mx_moe import Case, check  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -73,3 +74,32 @@ def test_a_token_does_not_see_its_neighbours_there():
     keep = [t for t in range(20) if t != 3]
     assert torch.equal(again[keep], full[keep])
     assert w4.device_status() == w4.OK
+
+
+@pytest.mark.parametrize("gate", [-40.0, -86.0, -88.0, -90.0, 88.0, 0.0])
+def test_silu_far_from_zero(gate):
+    """Every gate the same exact number, the up product large enough that silu of it matters.
+
+    Gate and up are single exact products, so h is off by the exponential (2 units of 2^-23), the addition, the
+    division (2) and two products: 2^-20 of itself; the exponential of -88 or -90 is below FP32's normal numbers, off by
+    2 units of 2^-149, which gate and up multiply. It is then rounded to 11 bits; the sums over I and the choices and the routing weights add (I / 32 + 32) 2^-23, the result
+    half a unit of 8 bits."""
+    T, E, k, H, I = 3, 4, 2, 64, 96
+    case = Case(T, E, k, H, I, seed=26)
+    case.x[:] = 0
+    case.x[:, 0], case.x[:, 1] = gate, 1.0
+    case.router[:] = 0
+    case.router[:, 1] = torch.tensor([0.5, 2.0, 1.0, 0.25])      # choices 1 and 2
+    case.c13[:] = 0
+    case.c13[:, 0, :I] = 2                                       # gate: 1.0 times x[0]
+    case.c13[:, 1, I:] = 2 + np.arange(I) % 4                    # up: 1, 1.5, 2 or 3 times 2^100
+    case.e13[:, :, :I], case.e13[:, :, I:] = 127, 227
+    y, _ = case.reference()
+    got = w4.mxfp4_moe(*case.device(), k, renormalize=True).double().cpu().numpy()
+    _, p = Q.route(case.logits(), k, True)
+    u = np.array([1.0, 1.5, 2.0, 3.0])[np.arange(I) % 4] * 2.0 ** 100
+    silu = gate / (1 + np.exp(-gate))
+    dh = np.abs(silu * u) * (2.0 ** -11 + 2.0 ** -20 + (I / 32 + 32) * 2.0 ** -23) + abs(gate) * 2.0 ** -148 * u
+    bound = sum(p[0, j] * (dh @ np.abs(Q.values(case.c2[e], case.e2[e], 0))) for j, e in enumerate((1, 2)))
+    assert np.all(np.abs(got - y) <= bound + 2.0 ** -8 * (np.abs(y) + bound) + 2.0 ** -134)
+    assert (np.abs(y).max() > 0) == (gate != 0)

@@ -229,10 +229,14 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
     return v;
 }
 
-// The fast division is within 2 units in the last place, and 0 where exp(-g) is
-// beyond 2^126 (silu below 2^-119); it has no branch, so that the epilogue's two
-// tokens overlap.
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + expf(-g)); }
+// g / (1 + exp(-g)), with the numerator and denominator multiplied by exp(g)
+// where g is negative: the divisor stays in [1, 2] (or NaN), where the fast
+// division is within 2 units in the last place. It has no branch, so that the
+// epilogue's two tokens overlap.
+__device__ __forceinline__ float silu(float g) {
+    const float t = expf(-fabsf(g));
+    return __fdividef(g < 0.f ? g * t : g, 1.f + t);
+}
 
 // ---------------------------------------------------------------------------
 // phase 0
