@@ -501,6 +501,117 @@ w4a16_status w4a16_mxfp4_moe(const void* x, const void* router, const int32_t* w
 size_t w4a16_mxfp4_moe_workspace_bytes(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I);
 
 /*
+ * 8-bit integer operands: rows of int8 codes with one FP32 scale per row, the
+ * value of an element being code * scale. (No counterpart on the pages this
+ * library follows.) Activations have a row per token, weights a row per output
+ * channel: [N, K] as they are stored before any packing.
+ *   codes   int8 [R, K]
+ *   scale   float [R]
+ */
+
+/*
+ * w4a16_int8_quantize -- codes and scales of the rows of x [rows, cols], dtype
+ * `dt` (F16, BF16 or F32), row-major. With amax the largest magnitude of a row,
+ *
+ *     scale = RN(amax / 127),   code = RN(127 x / amax), ties to even
+ *
+ * Both are decided exactly (the quotient is not rounded before the code is).
+ * Codes lie in -127..127. A row of zeros has scale 0 and codes 0. A row that
+ * holds an infinity or a NaN has scale NaN and codes 0: each of its values reads
+ * as NaN. Rows whose amax / 127 is below 2^-126 have a subnormal scale, with fewer
+ * bits. cols % 16 == 0. Bit-exact; deterministic.
+ * Errors: NULL, DTYPE, SHAPE (non-positive, cols % 16), ALIGN (a pointer not
+ * 16-byte aligned), DEVICE, CUDA.
+ */
+w4a16_status w4a16_int8_quantize(const void* x, int8_t* codes, float* scale, int64_t rows, int64_t cols,
+                                 w4a16_dtype dt, w4a16_stream stream);
+
+/*
+ * w4a16_int8_dequant -- dense copy y [rows, cols] of dtype `dt` (F16, BF16 or
+ * F32): code * scale in FP32, rounded to `dt`. Errors as w4a16_int8_quantize.
+ */
+w4a16_status w4a16_int8_dequant(const int8_t* codes, const float* scale, void* y, int64_t rows, int64_t cols,
+                                w4a16_dtype dt, w4a16_stream stream);
+
+/*
+ * w4a16_int8_matmul -- product of two int8 operands with a scale per row of each,
+ *
+ *     y[m, n] = (sum_k a[m, k] * b[n, k]) * a_scale[m] * b_scale[n]
+ *
+ * A [M, K]: activations quantised by w4a16_int8_quantize, a scale per token.
+ * B [N, K]: a weight quantised once, a scale per output channel. Any int8 value
+ * may occur, -128 too. Sums are exact while they are below 2^24 in magnitude
+ * (K <= 1024 always; K of any size for operands that are not nearly all of one
+ * sign and of full size), beyond that held in FP32 or wider. Both scales are
+ * applied in FP32, a_scale first, and the result is rounded once to `dt` (F16,
+ * BF16 or F32). A NaN scale makes every y of its row or column NaN.
+ *
+ * workspace: w4a16_int8_matmul_workspace_bytes(M, N, K) bytes with the ownership
+ * and zero-fill rules of w4a16_gemv's (what must start at zero are ticket words in
+ * its first 4096 bytes, which every call leaves at zero: one workspace serves calls
+ * of any shape it is large enough for). NULL where that is 0. Two calls that may run
+ * at the same time must not share one. After a W4A16_ERR_TIMEOUT reported by
+ * w4a16_device_status, zero it again.
+ *
+ * Deterministic. M >= 1, N % 8 == 0, K % 16 == 0, K <= 131056.
+ * Errors: NULL, DTYPE, SHAPE, ALIGN, WORKSPACE, DEVICE, CUDA.
+ */
+w4a16_status w4a16_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale, void* y,
+                               int64_t M, int64_t N, int64_t K, w4a16_dtype dt, void* workspace,
+                               size_t workspace_bytes, w4a16_stream stream);
+
+/*
+ * Bytes of workspace w4a16_int8_matmul needs on the current device; 0 where it
+ * needs none, for shapes it rejects, and when no GB300 is current.
+ */
+size_t w4a16_int8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* What the gate of w4a16_block_norm is given for. */
+typedef enum {
+    W4A16_GATE_CHANNEL = 0, /* [H]    */
+    W4A16_GATE_TOKEN = 1,   /* [T]    */
+    W4A16_GATE_ELEMENT = 2  /* [T, H] */
+} w4a16_gate;
+
+/*
+ * w4a16_block_norm -- the step between two blocks of a transformer: the norm
+ * after a block, its gate and the residual's scale, the residual update, the norm
+ * before the next block and, where asked for, its quantisation. (No counterpart on
+ * the pages this library follows.)
+ *
+ *     u  = h * rsqrt(mean(h^2) + eps) * after     (u = h where `after` is NULL)
+ *     r' = residual + scale * gate * u            (gate 1 where NULL; r' = residual where h is NULL)
+ *     y  = r' * rsqrt(mean(r'^2) + eps) * weight
+ *
+ * with the means over the H elements of a row. All in FP32; r' is normalised as
+ * it is before it is rounded to be stored.
+ *
+ * residual [T, H] dtype `residual_dt`; h, gate, after [H], weight [H], y [T, H]
+ * dtype `dt`. residual_dt is dt or F32.
+ *   residual_out  [T, H] dtype residual_dt, r'; may be `residual` itself. Required
+ *                 with h, NULL without (nothing would change).
+ *   weight        NULL: no norm before the next block; y, codes and code_scale
+ *                 are then NULL.
+ *   y             [T, H] dtype dt, or NULL:
+ *   codes         int8 [T, H] with code_scale float [T], y as w4a16_int8_quantize
+ *                 makes it of the unrounded y.
+ * One of h and weight at least; after and gate only with h. Outputs other than
+ * residual_out must not overlap the inputs or one another.
+ * scale finite, eps positive and finite (UNSUPPORTED otherwise). H % 16 == 0, H <= 16384.
+ * Magnitudes whose square leaves the FP32 range are normalised to zero, as the
+ * formula in FP32 gives it. A row with an infinity or a NaN yields NaN in that
+ * row (codes 0, scale NaN) and leaves other rows alone. Deterministic; a row does
+ * not depend on the others. An ordinary launch (no programmatic serialization).
+ * Errors: NULL (residual, or a pointer that another one asks for), DTYPE, SHAPE
+ * (T, H, the gate kind, a pointer given that must be NULL), UNSUPPORTED, ALIGN,
+ * DEVICE, CUDA.
+ */
+w4a16_status w4a16_block_norm(const void* residual, w4a16_dtype residual_dt, const void* h, const void* after,
+                              const void* gate, w4a16_gate gate_kind, float scale, void* residual_out,
+                              const void* weight, float eps, void* y, int8_t* codes, float* code_scale, int64_t T,
+                              int64_t H, w4a16_dtype dt, w4a16_stream stream);
+
+/*
  * w4a16_device_status -- synchronise `stream`, then read and clear the
  * device-side error word of the current device. Every wait on an mbarrier
  * inside the GEMM pipeline gives up after about two seconds; the kernel then

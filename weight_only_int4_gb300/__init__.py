@@ -39,6 +39,7 @@ OK, ERR_NULL, ERR_SHAPE, ERR_DTYPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_DEVICE, ERR_
     ERR_CUDA, ERR_TIMEOUT = range(10)
 F16, BF16, F32 = 0, 1, 2
 OP_GEMV, OP_GEMM, OP_MXFP4_MATMUL = 0, 1, 2
+GATE_CHANNEL, GATE_TOKEN, GATE_ELEMENT = 0, 1, 2
 
 # Every symbol include/w4a16.h declares, with (restype, argtypes).
 _VP, _I64, _SZ, _INT = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
@@ -64,6 +65,12 @@ SIGNATURES = {
     "w4a16_mxfp4_matmul": (_INT, [_VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _INT, _VP, _SZ, _VP]),
     "w4a16_mxfp4_moe": (_INT, [_VP] * 7 + [_I64] * 5 + [_INT, _VP, _SZ, _VP]),
     "w4a16_mxfp4_moe_workspace_bytes": (_SZ, [_I64] * 5),
+    "w4a16_int8_quantize": (_INT, [_VP, _VP, _VP, _I64, _I64, _INT, _VP]),
+    "w4a16_int8_dequant": (_INT, [_VP, _VP, _VP, _I64, _I64, _INT, _VP]),
+    "w4a16_int8_matmul": (_INT, [_VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _INT, _VP, _SZ, _VP]),
+    "w4a16_int8_matmul_workspace_bytes": (_SZ, [_I64] * 3),
+    "w4a16_block_norm": (_INT, [_VP, _INT, _VP, _VP, _VP, _INT, ctypes.c_float, _VP, _VP, ctypes.c_float, _VP, _VP,
+                                _VP, _I64, _I64, _INT, _VP]),
     "w4a16_status_string": (ctypes.c_char_p, [_INT]),
     "w4a16_abi_version": (_INT, []),
 }
@@ -226,7 +233,9 @@ _retired = []
 # Bytes of FP32 partial sums per SM with which an op's workspace begins, as include/w4a16.h lays it out; ticket words,
 # the part that must start at zero, follow.
 _PARTIALS_PER_SM = {OP_GEMV: 136 << 10, OP_GEMM: 128 << 10, OP_MXFP4_MATMUL: 128 << 10}
-_MOE_CONTROL_BYTES = 256   # mxfp4_moe: barrier words, at the start
+# What must start at zero at the beginning of the others': barrier words, ticket words.
+_MOE_CONTROL_BYTES = 256
+_CONTROL_BYTES = {"mxfp4_moe": _MOE_CONTROL_BYTES, "int8_matmul": 4096}
 
 
 def _zero_range(op, nbytes: int, sms: int):
@@ -234,7 +243,7 @@ def _zero_range(op, nbytes: int, sms: int):
     if op in _PARTIALS_PER_SM:
         first = _PARTIALS_PER_SM[op] * sms
         return (first if first < nbytes else 0), nbytes
-    return 0, min(_MOE_CONTROL_BYTES, nbytes)
+    return 0, min(_CONTROL_BYTES[op], nbytes)
 
 
 def _captured_workspace(nbytes: int, device, op, sms: int):
@@ -612,6 +621,143 @@ def mxfp4_moe(x, router, w13, e13, w2, e2, top_k: int, renormalize: bool = True,
                              ws_bytes, _stream_ptr(stream))
     _check("w4a16_mxfp4_moe", st)
     return out
+
+
+def int8_quantize(x, out=None, stream=None):
+    """Quantise the rows of x [R, K] (float16, bfloat16 or float32) to int8, with
+    one scale per row: scale = max |x| / 127, codes to nearest even. Returns
+    (codes int8 [R, K], scale float32 [R]); `out` may give both to write into.
+    Activations: a row per token. A weight: [N, K], a row per output channel."""
+    torch = _torch()
+    _cuda_contig("x", x)
+    dt = _dtype_code(x.dtype)
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D, got {x.dim()}-D")
+    R, K = x.shape
+    codes, scale = (None, None) if out is None else out
+    codes = _out("codes", codes, (R, K), torch.int8, x.device, stream)
+    scale = _out("scale", scale, (R,), torch.float32, x.device, stream)
+    st = load_library().w4a16_int8_quantize(x.data_ptr(), codes.data_ptr(), scale.data_ptr(), R, K, dt,
+                                            _stream_ptr(stream))
+    _check("w4a16_int8_quantize", st)
+    return codes, scale
+
+
+def _int8_rows(name: str, codes, scale):
+    """Checks int8 rows and their scales, returns rows and K."""
+    torch = _torch()
+    _cuda_contig(name, codes)
+    _cuda_contig(name + " scale", scale, codes.get_device())
+    if codes.dim() != 2 or codes.dtype != torch.int8:
+        raise TypeError(f"{name} must be a 2-D torch.int8 tensor of codes")
+    R, K = codes.shape
+    if scale.dtype != torch.float32 or scale.shape != (R,):
+        raise ValueError(f"{name} scale must be torch.float32 ({R},), got {scale.dtype} {tuple(scale.shape)}")
+    return R, K
+
+
+def int8_dequant(codes, scale, out_dtype=None, out=None, stream=None):
+    """Dense copy [R, K] of int8 rows: code * scale, in `out_dtype` (bfloat16
+    unless given; float16 and float32 too)."""
+    R, K = _int8_rows("codes", codes, scale)
+    if out_dtype is None:
+        out_dtype = _torch().bfloat16 if out is None else out.dtype
+    dt = _dtype_code(out_dtype)
+    out = _out("out", out, (R, K), out_dtype, codes.device, stream)
+    st = load_library().w4a16_int8_dequant(codes.data_ptr(), scale.data_ptr(), out.data_ptr(), R, K, dt,
+                                           _stream_ptr(stream))
+    _check("w4a16_int8_dequant", st)
+    return out
+
+
+def int8_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, workspace=None, stream=None):
+    """y = (A @ B.T) * a_scale[:, None] * b_scale of two int8 operands: A [M, K]
+    (activations through int8_quantize) and B [N, K] (a weight, one output channel
+    per row). Returns y [M, N] in `out_dtype` (bfloat16 unless given; float16 and
+    float32 too)."""
+    M, K = _int8_rows("a", a, a_scale)
+    N, Kb = _int8_rows("b", b, b_scale)
+    if K != Kb:
+        raise ValueError(f"a has K = {K}, b has K = {Kb}")
+    if out_dtype is None:
+        out_dtype = _torch().bfloat16 if out is None else out.dtype
+    dt = _dtype_code(out_dtype)
+    lib = load_library()
+    device = a.device
+    out = _out("out", out, (M, N), out_dtype, device, stream)
+    ws_ptr, ws_bytes = _workspace(workspace, "int8_matmul", lib.w4a16_int8_matmul_workspace_bytes, (M, N, K), device,
+                                  stream)
+    st = lib.w4a16_int8_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr(), M,
+                               N, K, dt, ws_ptr, ws_bytes, _stream_ptr(stream))
+    _check("w4a16_int8_matmul", st)
+    return out
+
+
+def block_norm(residual, weight=None, h=None, after=None, gate=None, scale: float = 1.0, eps: float = 1e-6,
+               quantize: bool = False, out=None, stream=None):
+    """The step between two blocks: norm after a block, gate, scaled residual
+    update, norm before the next block, in one kernel.
+
+        u  = h * rsqrt(mean(h^2) + eps) * after     (u = h without `after`)
+        r' = residual + scale * gate * u            (r' = residual without `h`)
+        y  = r' * rsqrt(mean(r'^2) + eps) * weight
+
+    residual [T, H] in h's dtype or float32; h, gate, after [H], weight [H] in one
+    dtype (float16, bfloat16 or float32); gate [H] (a factor per channel), [T, 1]
+    (per token) or [T, H]. Returns (r', y), with y in that dtype, or with `quantize`
+    (r', codes, scale), y as int8_quantize makes it. Without `weight` it returns
+    r' alone; without `h`, r' is `residual` itself. `out` may give the outputs to
+    write into, as a tuple in the order of the result (r' may be `residual`)."""
+    torch = _torch()
+    if h is None and weight is None:
+        raise ValueError("h or weight must be given")
+    if h is None and (after is not None or gate is not None):
+        raise ValueError("after and gate need h")
+    if quantize and weight is None:
+        raise ValueError("quantize needs weight")
+    _cuda_contig("residual", residual)
+    current = residual.get_device()
+    if residual.dim() != 2:
+        raise ValueError(f"residual must be 2-D, got {residual.dim()}-D")
+    T, H = residual.shape
+    dtype = (weight if h is None else h).dtype
+    dt, rdt = _dtype_code(dtype), _dtype_code(residual.dtype)
+    if rdt != dt and rdt != F32:
+        raise TypeError(f"residual must be {dtype} or float32, got {residual.dtype}")
+    kind = GATE_CHANNEL
+    if gate is not None:
+        kind = {(H,): GATE_CHANNEL, (T, H): GATE_ELEMENT, (T, 1): GATE_TOKEN}.get(tuple(gate.shape))
+        if kind is None:
+            raise ValueError(f"gate shape {tuple(gate.shape)} is none of {(H,)}, {(T, 1)}, {(T, H)}")
+    for name, t, shape in (("h", h, (T, H)), ("after", after, (H,)), ("gate", gate, None), ("weight", weight, (H,))):
+        if t is None:
+            continue
+        _cuda_contig(name, t, current)
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} shape {tuple(t.shape)} does not match {shape}")
+    device = residual.device
+    outs = [None] * 3 if out is None else list(out) if isinstance(out, (tuple, list)) else [out]
+    if out is not None and len(outs) != (1 if weight is None else 3 if quantize else 2):
+        raise ValueError(f"out holds {len(outs)} tensors")
+    new = residual if h is None else _out("residual out", outs[0], (T, H), residual.dtype, device, stream)
+    if h is None and outs[0] is not None and outs[0] is not residual:
+        raise ValueError("without h the residual is returned as it is")
+    y = codes = code_scale = None
+    if quantize:
+        codes = _out("codes", outs[1], (T, H), torch.int8, device, stream)
+        code_scale = _out("scale", outs[2], (T,), torch.float32, device, stream)
+    elif weight is not None:
+        y = _out("y", outs[1], (T, H), dtype, device, stream)
+    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    st = load_library().w4a16_block_norm(residual.data_ptr(), rdt, ptr(h), ptr(after), ptr(gate), kind, scale,
+                                         0 if h is None else new.data_ptr(), ptr(weight), eps, ptr(y), ptr(codes),
+                                         ptr(code_scale), T, H, dt, _stream_ptr(stream))
+    _check("w4a16_block_norm", st)
+    if weight is None:
+        return new
+    return (new, codes, code_scale) if quantize else (new, y)
 
 
 def device_status(stream=None) -> int:

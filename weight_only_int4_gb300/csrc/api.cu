@@ -4,6 +4,7 @@
 
 #include "internal.h"
 
+#include <cmath>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -140,6 +141,20 @@ w4a16_status check_moe_shape(int64_t T, int64_t E, int64_t k, int64_t H, int64_t
     // the stacked rows E I / 8 and the 2 I columns are 32-bit coordinates
     if (I < 32 || I % 32 != 0 || I > kMaxDim / 512) return W4A16_ERR_SHAPE;
     return W4A16_OK;
+}
+
+bool known_dtype(w4a16_dtype dt) { return dt == W4A16_F16 || dt == W4A16_BF16 || dt == W4A16_F32; }
+
+// Rows of int8 codes [rows, cols].
+w4a16_status check_int8_rows(int64_t rows, int64_t cols) {
+    if (rows < 1 || cols < 1 || rows > kMaxDim || cols > kMaxDim || cols % 16 != 0) return W4A16_ERR_SHAPE;
+    return W4A16_OK;
+}
+
+w4a16_status check_int8_product(int64_t M, int64_t N, int64_t K) {
+    if (M < 1 || N < 1 || K < 1 || M > kMaxProductDim || N > kMaxProductDim || K > w4a16::kInt8MaxK)
+        return W4A16_ERR_SHAPE;
+    return N % 8 == 0 && K % 16 == 0 ? W4A16_OK : W4A16_ERR_SHAPE;
 }
 
 w4a16_status from_cuda(cudaError_t e) { return e == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA; }
@@ -447,6 +462,82 @@ w4a16_status w4a16_mxfp4_moe(const void* x, const void* router, const int32_t* w
                                 (int)E,  (int)top_k, (int)H,
                                 (int)I,  renormalize != 0};
     return from_cuda(w4a16::launch_mx_moe(args, workspace, dp, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status w4a16_int8_quantize(const void* x, int8_t* codes, float* scale, int64_t rows, int64_t cols,
+                                 w4a16_dtype dt, w4a16_stream stream) {
+    if (!x || !codes || !scale) return W4A16_ERR_NULL;
+    if (!known_dtype(dt)) return W4A16_ERR_DTYPE;
+    w4a16_status st = check_int8_rows(rows, cols);
+    if (st != W4A16_OK) return st;
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scale)) return W4A16_ERR_ALIGN;
+    DeviceProps dp;
+    if ((st = device_gate(&dp)) != W4A16_OK) return st;
+    return from_cuda(w4a16::launch_int8_quantize(x, codes, scale, rows, cols, static_cast<int>(dt),
+                                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status w4a16_int8_dequant(const int8_t* codes, const float* scale, void* y, int64_t rows, int64_t cols,
+                                w4a16_dtype dt, w4a16_stream stream) {
+    if (!codes || !scale || !y) return W4A16_ERR_NULL;
+    if (!known_dtype(dt)) return W4A16_ERR_DTYPE;
+    w4a16_status st = check_int8_rows(rows, cols);
+    if (st != W4A16_OK) return st;
+    if (!aligned16(codes) || !aligned16(scale) || !aligned16(y)) return W4A16_ERR_ALIGN;
+    DeviceProps dp;
+    if ((st = device_gate(&dp)) != W4A16_OK) return st;
+    return from_cuda(w4a16::launch_int8_dequant(codes, scale, y, rows, cols, static_cast<int>(dt), dp,
+                                                reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t w4a16_int8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    DeviceProps dp;
+    if (check_int8_product(M, N, K) != W4A16_OK || device_gate(&dp) != W4A16_OK) return 0;
+    return w4a16::int8_matmul_workspace_bytes(M, N, K, dp);
+}
+
+w4a16_status w4a16_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale, void* y,
+                               int64_t M, int64_t N, int64_t K, w4a16_dtype dt, void* workspace,
+                               size_t workspace_bytes, w4a16_stream stream) {
+    if (!a || !a_scale || !b || !b_scale || !y) return W4A16_ERR_NULL;
+    if (!known_dtype(dt)) return W4A16_ERR_DTYPE;
+    w4a16_status st = check_int8_product(M, N, K);
+    if (st != W4A16_OK) return st;
+    if (!aligned16(a) || !aligned16(a_scale) || !aligned16(b) || !aligned16(b_scale) || !aligned16(y) ||
+        !aligned16(workspace))
+        return W4A16_ERR_ALIGN;
+    DeviceProps dp;
+    if ((st = device_gate(&dp)) != W4A16_OK) return st;
+    if ((workspace ? workspace_bytes : 0) < w4a16::int8_matmul_workspace_bytes(M, N, K, dp)) return W4A16_ERR_WORKSPACE;
+    const w4a16::Int8MatmulArgs args{a, a_scale, b, b_scale, y, (int)M, (int)N, (int)K};
+    return from_cuda(w4a16::launch_int8_matmul(args, static_cast<int>(dt), workspace, dp,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status w4a16_block_norm(const void* residual, w4a16_dtype residual_dt, const void* h, const void* after,
+                              const void* gate, w4a16_gate gate_kind, float scale, void* residual_out,
+                              const void* weight, float eps, void* y, int8_t* codes, float* code_scale, int64_t T,
+                              int64_t H, w4a16_dtype dt, w4a16_stream stream) {
+    if (!residual || (!h && !weight) || (h && !residual_out)) return W4A16_ERR_NULL;
+    if (weight && !y && (!codes || !code_scale)) return W4A16_ERR_NULL;
+    if (!known_dtype(dt) || (residual_dt != dt && residual_dt != W4A16_F32)) return W4A16_ERR_DTYPE;
+    if (T < 1 || T > kMaxDim || H < 16 || H > w4a16::kNormMaxHidden || H % 16 != 0) return W4A16_ERR_SHAPE;
+    if (!h && (after || gate || residual_out)) return W4A16_ERR_SHAPE;
+    if (weight ? y && (codes || code_scale) : y || codes || code_scale) return W4A16_ERR_SHAPE;
+    if (gate && gate_kind != W4A16_GATE_CHANNEL && gate_kind != W4A16_GATE_TOKEN && gate_kind != W4A16_GATE_ELEMENT)
+        return W4A16_ERR_SHAPE;
+    if (!std::isfinite(scale) || !std::isfinite(eps) || !(eps > 0.f)) return W4A16_ERR_UNSUPPORTED;
+    for (const void* p : {residual, h, after, gate, static_cast<const void*>(residual_out), weight,
+                          static_cast<const void*>(y), static_cast<const void*>(codes),
+                          static_cast<const void*>(code_scale)})
+        if (!aligned16(p)) return W4A16_ERR_ALIGN;
+    DeviceProps dp;
+    w4a16_status st = device_gate(&dp);
+    if (st != W4A16_OK) return st;
+    const w4a16::BlockNormArgs args{residual, h,   after,      gate,  residual_out, weight, y, codes,
+                                    code_scale, scale, eps, static_cast<int>(gate_kind), T, H};
+    return from_cuda(w4a16::launch_block_norm(args, static_cast<int>(dt), static_cast<int>(residual_dt),
+                                              reinterpret_cast<cudaStream_t>(stream)));
 }
 
 w4a16_status w4a16_selftest_wait_timeout(w4a16_stream stream) {

@@ -177,6 +177,47 @@ size_t mx_moe_workspace_bytes(int T, int E, int k, int H, int I);
 cudaError_t launch_mx_moe(const MxMoeArgs& a, void* workspace, const DeviceProps& dp, cudaStream_t s);
 cudaError_t read_and_clear_mx_moe_error(uint32_t* out);
 
+// Rows of int8 codes with one FP32 scale each; type as w4a16_dtype.
+cudaError_t launch_int8_quantize(const void* x, int8_t* codes, float* scales, int64_t rows, int64_t cols, int type,
+                                 cudaStream_t s);
+cudaError_t launch_int8_dequant(const int8_t* codes, const float* scales, void* y, int64_t rows, int64_t cols,
+                                int type, const DeviceProps& dp, cudaStream_t s);
+
+// Product of int8 rows, y [M, N] = (A [M, K] B [N, K]^T) * sa[m] * sb[n]. With
+// K at most this, no sum of K products of 8-bit integers leaves 32 bits.
+constexpr int64_t kInt8MaxK = 131056;
+struct Int8MatmulArgs {
+    const int8_t* a;
+    const float* sa;
+    const int8_t* b;
+    const float* sb;
+    void* y;
+    int M, N, K;
+};
+size_t int8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceProps& dp);
+cudaError_t launch_int8_matmul(const Int8MatmulArgs& a, int out_type, void* workspace, const DeviceProps& dp,
+                               cudaStream_t s);
+
+// Residual update and norms between two blocks; h, after, gate, weight, y of
+// one type, the residual of that type or FP32. A row is held by one thread block.
+constexpr int64_t kNormMaxHidden = 16384;
+enum : int { kGateChannel = 0, kGateToken = 1, kGateElement = 2 };
+struct BlockNormArgs {
+    const void* residual;
+    const void* h;        // or NULL: the residual as it is
+    const void* after;    // or NULL
+    const void* gate;     // or NULL
+    void* residual_out;   // with h
+    const void* weight;   // or NULL: the residual alone
+    void* y;              // with weight: this ...
+    int8_t* codes;        // ... or these
+    float* code_scales;
+    float scale, eps;
+    int gate_kind;
+    long long T, H;
+};
+cudaError_t launch_block_norm(const BlockNormArgs& a, int act_type, int residual_type, cudaStream_t s);
+
 // Workspace of the GEMV entry points (w4a16_mxfp4_gemv runs either the GEMV
 // kernel or, for 5..16 rows of a large layer, the few-row tensor-core kernel):
 // both kernels' partial-sum regions (sizes fixed per device), then one ticket
