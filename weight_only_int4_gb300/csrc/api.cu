@@ -294,12 +294,13 @@ w4a16_status w4a16_device_status(w4a16_stream stream) {
     DeviceProps dp;
     w4a16_status st = device_gate(&dp);
     if (st != W4A16_OK) return st;
-    uint32_t v = 0, u = 0, k = 0, p = 0, m = 0;
+    uint32_t v = 0, u = 0, k = 0, p = 0, m = 0, i = 0;
     if (w4a16::read_and_clear_device_error(&v, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess ||
         w4a16::read_and_clear_gemv_error(&u) != cudaSuccess || w4a16::read_and_clear_skinny_error(&k) != cudaSuccess ||
-        w4a16::read_and_clear_mx_matmul_error(&p) != cudaSuccess || w4a16::read_and_clear_mx_moe_error(&m) != cudaSuccess)
+        w4a16::read_and_clear_mx_matmul_error(&p) != cudaSuccess || w4a16::read_and_clear_mx_moe_error(&m) != cudaSuccess ||
+        w4a16::read_and_clear_int8_matmul_error(&i) != cudaSuccess)
         return W4A16_ERR_CUDA;
-    return (v | u | k | p | m) ? W4A16_ERR_TIMEOUT : W4A16_OK;
+    return (v | u | k | p | m | i) ? W4A16_ERR_TIMEOUT : W4A16_OK;
 }
 
 w4a16_status w4a16_dequant(const int32_t* qweight, const void* scales, const int32_t* qzeros, void* w, int64_t N,

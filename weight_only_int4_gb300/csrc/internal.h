@@ -198,6 +198,8 @@ size_t int8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, const Device
 cudaError_t launch_int8_matmul(const Int8MatmulArgs& a, int out_type, void* workspace, const DeviceProps& dp,
                                cudaStream_t s);
 
+cudaError_t read_and_clear_int8_matmul_error(uint32_t* out);
+
 // Residual update and norms between two blocks; h, after, gate, weight, y of
 // one type, the residual of that type or FP32. A row is held by one thread block.
 constexpr int64_t kNormMaxHidden = 16384;
