@@ -77,6 +77,24 @@ def test_sizes(M, N, K):
     run(M, N, K, torch.bfloat16)
 
 
+# On 152 SMs: 256 x 256 tiles on CTA pairs; 128-row tiles shared between CTAs; clusters of 2 to 6 CTAs per tile; eight
+# rows by dot products.
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [(129, 20488, 1040), (257, 10248, 16), (1030, 4104, 272), (300, 16392, 144),
+                                   (513, 5000, 2064), (16, 20488, 1040), (30, 43008, 272), (64, 24584, 400),
+                                   (128, 20488, 656), (100, 21000, 16), (12, 6400, 5376), (40, 264, 4112),
+                                   (8, 8192, 8192), (8, 8200, 8208), (6, 16392, 8192), (5, 520, 1040), (7, 40, 8208)])
+def test_plans(M, N, K, dtype):
+    run(M, N, K, dtype)
+
+
+def test_chunks_of_many_rows():
+    """More rows than are widened at a time, in both kernels that take widened rows."""
+    run(8200, 1032, 144, torch.bfloat16)
+    run(20000, 264, 272, torch.float32)
+    run(16500, 8200, 48, torch.float16)
+
+
 @pytest.mark.parametrize("M", [1, 8, 24, 100, 200, 600])
 def test_every_value_and_full_size(M):
     """-128 .. 127 in both operands, then sums far past 2^24: every code of one sign and size."""

@@ -11,8 +11,9 @@
 // widened to fp16 in the workspace by a kernel of their own before it.
 //
 // Three kernels:
-//   rows    one or two rows of a: dot products of four bytes (dp4a), exact in 32
-//           bits; streams b.
+//   rows    few rows of a: dot products of four bytes (dp4a), exact in 32 bits;
+//           streams b. The instruction's rate (about 18 lanes a cycle and SM, measured)
+//           bounds it from four rows on.
 //   tiles   128 rows of b against 16..128 rows of a per tile, tiles shared
 //           between CTAs by (tile, K step) units.
 //   pair    256 x 256 tiles on CTA pairs (cta_group::2).
@@ -26,7 +27,7 @@
 #include "tmap.h"
 
 #include <algorithm>
-#include <mutex>
+#include <atomic>
 
 namespace w4a16 {
 
@@ -87,12 +88,21 @@ __device__ __forceinline__ bool uniform_wait_bar(uint32_t bar, uint32_t parity, 
     return __all_sync(0xffffffffu, ok);
 }
 
-// Lane 0 waits; the shuffle orders the other lanes' accesses after its acquire.
-__device__ __forceinline__ bool warp_wait_bar(uint32_t bar, uint32_t parity, const Abort& ab, int lane) {
+// Several warps go on together once their first thread has seen up to two
+// phases complete: named barrier `id` spreads its verdict and orders the others'
+// accesses after its acquires. One thread polls, not one per warp: polls take
+// issue slots and shared-memory cycles from the warps at work (128-row tiles, 16
+// rows of a, steps of K measured at 0.47 us with 24 warps polling, 0.38 us so).
+__device__ __forceinline__ bool group_wait(int id, int threads, bool first, uint32_t bar0, uint32_t parity0,
+                                           uint32_t bar1, uint32_t parity1, const Abort& ab) {
     int ok = 1;
-    if (lane == 0) ok = wait_bar(bar, parity, ab) ? 1 : 0;
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    __syncwarp();
+    if (first) ok = wait_bar(bar0, parity0, ab) && (bar1 == 0u || wait_bar(bar1, parity1, ab));
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %0, 0;\n\t"
+        "barrier.cta.red.and.pred q, %1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "+r"(ok)
+        : "r"(id), "r"(threads)
+        : "memory");
     return ok != 0;
 }
 
@@ -135,6 +145,28 @@ __device__ __forceinline__ void widen_half_row(uint32_t tile, int row, int half,
     tmem_st_32x32b_x32(taddr, o);
 }
 
+// 16 codes (chunk c of row r of a 128-byte-swizzled tile [rows x 128]) widened to the fp16 operand tile: two boxes of 64
+// columns, `box` bytes each, 128-byte swizzle. Lanes of either box begin with another of their two stores, so the eight
+// lanes of a row reach different banks.
+__device__ __forceinline__ void widen_chunk(uint32_t codes, uint32_t wide, uint32_t box, int r, int c) {
+    uint32_t w[4], o[8];
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(codes + r * 128 + ((c ^ (r & 7)) << 4)));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) widen4(w[j], o[2 * j], o[2 * j + 1]);
+    const uint32_t row = wide + (c >> 2) * box + r * 128;
+    const bool second = c >> 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int h = second ? 1 - i : i;
+        const uint32_t at = row + (((2 * (c & 3) + h) ^ (r & 7)) << 4);
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(h ? o[4] : o[0]), "r"(h ? o[5] : o[1]),
+                     "r"(h ? o[6] : o[2]), "r"(h ? o[7] : o[3])
+                     : "memory");
+    }
+}
+
 // MMAs (16 deep) of a K step.
 __device__ __forceinline__ int step_mmas(int K, int kt) { return min(kStepK / 16, (K - kt * kStepK + 15) >> 4); }
 
@@ -154,7 +186,7 @@ __global__ void __launch_bounds__(256) widen_kernel(const int8_t* __restrict__ a
 }
 
 // ---------------------------------------------------------------------------
-// one or two rows of a
+// few rows of a
 // ---------------------------------------------------------------------------
 namespace rows {
 
@@ -173,25 +205,31 @@ __device__ __forceinline__ int dot16(uint4 a, uint4 b, int acc) {
     return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), acc);
 }
 
-// A warp takes four rows of b and MT of a; each lane 16 bytes of K at a time.
-constexpr int kWarps = 8, kRows = 4;
+// A warp takes kRows rows of b and MT of a, each lane 16 bytes of K at a time,
+// the loads of kDeep such chunks in flight. Blocks are small and many, so that the last
+// ones leave few SMs idle; registers are left to the loads (one resident block
+// asked for: with the compiler's own choice 39.1 us instead of 34.6 at
+// 1 x 43008 x 5376, less in flight).
+// 1 x 43008 x 5376 34.5 us (6.7 TB/s), 4 rows 38.7; 1 x 2048 x 2048 1.9.
+constexpr int kWarps = 4;
 
-template <int kOut, int MT>
-__global__ void __launch_bounds__(kWarps * 32) rows_kernel(const int8_t* __restrict__ a, const float* __restrict__ sa,
-                                                           const int8_t* __restrict__ b, const float* __restrict__ sb,
-                                                           void* __restrict__ y, int N, int K) {
+template <int kOut, int MT, int kRows, int kDeep>
+__global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const int8_t* __restrict__ a, const float* __restrict__ sa,
+                                                              const int8_t* __restrict__ b, const float* __restrict__ sb,
+                                                              void* __restrict__ y, int M, int N, int K) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long n0 = (blockIdx.x * static_cast<long long>(kWarps) + warp) * kRows;
     if (n0 >= N) return;
+    const int m0 = blockIdx.y * MT;
     int acc[MT][kRows] = {};
-#pragma unroll 2
+#pragma unroll kDeep
     for (int k = lane * 16; k < K; k += 512) {
         uint4 w[kRows];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) w[r] = load_weights(b + (n0 + r) * K + k);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(a + static_cast<long long>(m) * K + k));
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(a + static_cast<long long>(min(m0 + m, M - 1)) * K + k));
 #pragma unroll
             for (int r = 0; r < kRows; ++r) acc[m][r] = dot16(v, w[r], acc[m][r]);
         }
@@ -201,20 +239,35 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const int8_t* __restr
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
             const int sum = __reduce_add_sync(0xffffffffu, acc[m][r]);
-            if (lane == r)
-                store1<kOut>(y, static_cast<size_t>(m) * N + n0 + r,
-                             static_cast<float>(sum) * __ldg(sa + m) * __ldg(sb + n0 + r));
+            if (lane == r && m0 + m < M)
+                store1<kOut>(y, static_cast<size_t>(m0 + m) * N + n0 + r,
+                             static_cast<float>(sum) * __ldg(sa + m0 + m) * __ldg(sb + n0 + r));
         }
 }
 
-template <int kOut, int MT>
-cudaError_t launch(const Int8MatmulArgs& a, cudaStream_t s) {
+template <int kOut, int MT, int kRows, int kDeep>
+cudaError_t launch_mt(const Int8MatmulArgs& a, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     constexpr long long kBlock = kWarps * kRows;
-    cfg.gridDim = dim3(static_cast<unsigned>((a.N + kBlock - 1) / kBlock));
+    cfg.gridDim = dim3(static_cast<unsigned>((a.N + kBlock - 1) / kBlock), static_cast<unsigned>((a.M + MT - 1) / MT));
     cfg.blockDim = dim3(kWarps * 32);
     cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, rows_kernel<kOut, MT>, a.a, a.sa, a.b, a.sb, a.y, a.N, a.K);
+    return cudaLaunchKernelEx(&cfg, rows_kernel<kOut, MT, kRows, kDeep>, a.a, a.sa, a.b, a.sb, a.y, a.M, a.N, a.K);
+}
+
+// Rows of b per warp and chunks in flight (us, 1 x 43008 x 5376, 1 x 5376 x 21504 / 2 and 4 x 43008 x 5376): 2 rows, 4
+// chunks 34.5, 18.1 / 38.9, 53.7; 4 rows, 2 chunks 34.4, 20.1 / 35.5, 38.7.
+template <int kOut>
+cudaError_t launch(const Int8MatmulArgs& a, cudaStream_t s) {
+    switch (a.M) {
+        case 1: return launch_mt<kOut, 1, 2, 4>(a, s);
+        case 2: return launch_mt<kOut, 2, 4, 2>(a, s);
+        case 3: return launch_mt<kOut, 3, 4, 2>(a, s);
+        case 4: return launch_mt<kOut, 4, 4, 2>(a, s);
+        case 5:
+        case 6: return launch_mt<kOut, 6, 4, 2>(a, s);
+        default: return launch_mt<kOut, 8, 4, 2>(a, s);
+    }
 }
 
 }  // namespace rows
@@ -224,44 +277,58 @@ cudaError_t launch(const Int8MatmulArgs& a, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 // Warp roles, one CTA per SM:
 //   warp 0       producer: per K step TMA brings the tile's codes [128 x 128]
-//                and the fp16 rows of a [MP x 128] in two 64-column boxes, both
-//                with the 128-byte swizzle
-//   warps 8..23  two groups on alternate steps widen the codes into an operand
-//                stage of tensor memory (thread = row of b = lane, two threads a
-//                row)
+//                and MP rows of a, as codes (up to 64 rows) or widened before
+//                (128 rows: in two 64-column boxes), all with the 128-byte swizzle
+//   warps 12..27 four groups, steps in turn, widen the codes of b into an operand
+//                stage of tensor memory (thread = row of b = lane) and those of a
+//                into an operand tile in shared memory
 //   warp 1       issues the step's MMAs (M = 128, N = MP, A from tensor memory)
 //                into one of two accumulators
-//   warps 4..7   epilogue: scales, stores
+//   warps 4..11  epilogue, two warps per lane quarter, half the rows of a each
 //   warp 2       tensor memory
-// Units of (tile, K step), tile by tile, are cut into equal ranges, one per CTA.
-// A tile shared by several CTAs is finished, per epilogue warp, by the last of
-// them to arrive, which adds their FP32 parts in ascending CTA order.
+// Three ways to hand out the work:
+//   whole tiles, one or more per CTA;
+//   split > 1: a cluster of `split` CTAs per tile, each a part of K; the parts are
+//     added from the CTAs' shared memory, in the order of K;
+//   share: with more tiles than CTAs, equal ranges of (tile, K step) units, tile by
+//     tile. A tile that lies in two CTAs' ranges is finished by the later of them,
+//     which adds the two FP32 parts from global memory, the lower CTA's first.
+// All three are deterministic.
 namespace tiles {
 
 constexpr int BN = 128;
-constexpr int kThreads = 768;
-constexpr int kWidenWarp0 = 8, kGroups = 2, kGroupWarps = 8;
+constexpr int kThreads = 896;
+constexpr int kEpiWarps = 8, kWidenWarp0 = 12, kGroups = 4, kGroupWarps = 4;
 constexpr size_t kSlotFloats = 128 * 128;   // partial tile, [row of a][row of b]
 constexpr uint32_t kTmemCols = 512;
+constexpr int kMaxSplit = 6;
 
 template <int MP>
 struct Cfg {
+    // Up to 64 rows of a are widened here, by every CTA for itself: no kernel before this one, and half the bytes from
+    // L2. With 128 rows shared memory would have to carry more than the step's loads leave it time for.
+    static constexpr bool kInline = MP <= 64;
     static constexpr uint32_t kWBytes = BN * kStepK;
-    static constexpr uint32_t kXBytes = MP * kStepK * 2;
+    static constexpr uint32_t kXBytes = MP * kStepK * (kInline ? 1 : 2);   // rows of a as they are loaded
     static constexpr uint32_t kStageBytes = kWBytes + kXBytes;
     static constexpr int kStages = MP <= 32 ? 8 : MP == 64 ? 6 : 4;
-    static constexpr uint32_t kAccCols = MP < 32 ? 32 : MP;   // the epilogue reads 32 columns at a time
+    static constexpr uint32_t kAccCols = MP < 32 ? 32 : MP;   // the epilogue reads up to 32 columns at a time
     static constexpr uint32_t kOpCol0 = 2 * kAccCols;
     static constexpr int kOpStages = 4;
+    static constexpr uint32_t kWideBytes = MP * kStepK * 2, kBox = kWideBytes / 2;
+    static constexpr uint32_t kRingBytes = kStages * kStageBytes + (kInline ? kOpStages * kWideBytes : 0);
     static_assert(kOpCol0 + kOpStages * kOpCols <= kTmemCols, "tensor memory budget");
-    static_assert(kStages % kGroups == 0 && kOpStages % kGroups == 0, "each group owns whole ring stages");
-    static_assert(kStageBytes % 1024 == 0, "operand tiles stay 1024-byte aligned");
+    // A group takes loads from stages that other groups used in between. It waits for its operand stage first: then the
+    // MMAs of kOpStages steps before have retired, every step up to there had been widened, and the phase of the load
+    // stage that it skipped is complete.
+    static_assert(kStages >= kOpStages && kOpStages % kGroups == 0, "no group waits past an open phase");
+    static_assert(kStageBytes % 1024 == 0 && kWideBytes % 1024 == 0, "operand tiles stay 1024-byte aligned");
 };
 
 template <int MP>
 struct __align__(8) Barriers {
     uint64_t full[Cfg<MP>::kStages];        // codes and rows of a landed
-    uint64_t empty[Cfg<MP>::kStages];       // MMAs that read the rows of a retired (and the codes were widened before)
+    uint64_t empty[Cfg<MP>::kStages];       // widened; rows of a that came widened: the MMAs that read them retired
     uint64_t afull[Cfg<MP>::kOpStages];     // operand stage written
     uint64_t aempty[Cfg<MP>::kOpStages];    // MMAs that read it retired
     uint64_t tfull[2];
@@ -269,44 +336,74 @@ struct __align__(8) Barriers {
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
+    int last[2];
 };
 template <int MP>
 constexpr size_t smem_bytes() {
-    return 1024 + Cfg<MP>::kStages * Cfg<MP>::kStageBytes + sizeof(Barriers<MP>);
+    return 1024 + Cfg<MP>::kRingBytes + sizeof(Barriers<MP>);
 }
 
-// CTA b of G owns units [b U / G, (b + 1) U / G); the owner of unit u.
-__device__ __forceinline__ long long first_unit(long long b, long long U, int G) { return b * U / G; }
-__device__ __forceinline__ int unit_owner(long long u, long long U, int G) {
-    return static_cast<int>(((u + 1) * G - 1) / U);
-}
+struct Work {
+    int split;       // CTAs of a cluster per tile
+    int share;       // units shared
+    int each, more;  // units (share) or tiles per CTA, and how many of the first CTAs take one more
+};
 
 template <int kOut, int MP>
 __global__ void __launch_bounds__(kThreads, 1)
 tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
              const float* __restrict__ sa, const float* __restrict__ sb, void* __restrict__ y, int M, int N, int K,
-             float* __restrict__ partials, uint32_t* __restrict__ tickets) {
+             const Work work, float* __restrict__ partials, uint32_t* __restrict__ tickets) {
     using C = Cfg<MP>;
     constexpr int S = C::kStages, A = C::kOpStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Barriers<MP>* bars = reinterpret_cast<Barriers<MP>*>(smem + S * C::kStageBytes);
+    Barriers<MP>* bars = reinterpret_cast<Barriers<MP>*>(smem + C::kRingBytes);
     const uint32_t base = smem_u32(smem);
     auto st_w = [&](int s) { return base + s * C::kStageBytes; };
     auto st_x = [&](int s) { return base + s * C::kStageBytes + C::kWBytes; };
+    auto st_wide = [&](int s) { return base + S * C::kStageBytes + s * C::kWideBytes; };   // kInline
+
+    // split > 1: this CTA's part, [row of a][128], once the ring is idle
+    float* parts = reinterpret_cast<float*>(smem);
+    static_assert(MP * 128 * 4 <= C::kRingBytes, "a part fits the ring");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int num_m = (M + MP - 1) / MP, num_n = (N + BN - 1) / BN;
+    const int num_m = (M + MP - 1) / MP;
     const int kt_total = (K + kStepK - 1) / kStepK;
-    const int G = gridDim.x;
-    const long long U = static_cast<long long>(num_m) * num_n * kt_total;
-    const long long u_begin = first_unit(blockIdx.x, U, G), u_end = first_unit(blockIdx.x + 1ll, U, G);
+    // this CTA's units
+    const int split = work.split, share = work.share, b = blockIdx.x;
+    const int part_k = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    int u_begin, u_end;
+    if (split > 1) {
+        const int first = b / split * kt_total;
+        u_begin = first + part_k * kt_total / split;
+        u_end = first + (part_k + 1) * kt_total / split;
+    } else {
+        const int scale = share ? 1 : kt_total;
+        u_begin = (b * work.each + min(b, work.more)) * scale;
+        u_end = u_begin + (work.each + (b < work.more ? 1 : 0)) * scale;
+    }
+    const int t_begin = u_begin / kt_total, k_begin = u_begin - t_begin * kt_total;
     const Abort ab{&bars->abort, 0u, ~0u};
+
+    // the producer's place, and one step's copies
+    int fed = 0, at_k = k_begin, at_t = t_begin;
+    auto feed = [&](int s) {
+        const uint32_t fb = smem_u32(&bars->full[s]);
+        const int m0 = at_t % num_m * MP;
+        mbar_arrive_expect_tx(fb, C::kStageBytes);
+        tma_load_2d(st_w(s), &tw, at_k * kStepK, at_t / num_m * BN, fb);
+        tma_load_2d(st_x(s), &tx, at_k * kStepK, m0, fb);
+        if (!C::kInline) tma_load_2d(st_x(s) + C::kBox, &tx, at_k * kStepK + 64, m0, fb);
+        ++fed;
+        if (++at_k == kt_total) at_k = 0, ++at_t;
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(smem_u32(&bars->full[s]), 1);
-            mbar_init(smem_u32(&bars->empty[s]), 1);
+            mbar_init(smem_u32(&bars->empty[s]), C::kInline ? kGroupWarps : 1);
         }
         for (int s = 0; s < A; ++s) {
             mbar_init(smem_u32(&bars->afull[s]), kGroupWarps);
@@ -314,13 +411,15 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&bars->tfull[a]), 1);
-            mbar_init(smem_u32(&bars->tempty[a]), 4);
+            mbar_init(smem_u32(&bars->tempty[a]), kEpiWarps);
         }
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tw);
         tma_prefetch_desc(&tx);
+        // the ring is filled before the other warps are ready
+        for (int s = 0; s < min(S, u_end - u_begin); ++s) feed(s);
     }
     if (warp == 2) tmem_alloc(smem_u32(&bars->tmem_base), kTmemCols);
     tc_fence_before();
@@ -331,42 +430,28 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
-            int s = 0, steps = 0;
-            uint32_t parity = 1u;
-            bool ok = true;
-            for (long long u = u_begin; u < u_end && ok;) {
-                const long long t = u / kt_total;
-                const int k0 = static_cast<int>(u - t * kt_total);
-                const int k1 = static_cast<int>(std::min<long long>(kt_total, k0 + (u_end - u)));
-                const int m0 = static_cast<int>(t % num_m) * MP, n0 = static_cast<int>(t / num_m) * BN;
-                for (int kt = k0; kt < k1; ++kt) {
-                    if (!wait_bar(smem_u32(&bars->empty[s]), parity, ab)) { ok = false; break; }
-                    const uint32_t fb = smem_u32(&bars->full[s]);
-                    mbar_arrive_expect_tx(fb, C::kStageBytes);
-                    tma_load_2d(st_w(s), &tw, kt * kStepK, n0, fb);
-                    tma_load_2d(st_x(s), &tx, kt * kStepK, m0, fb);
-                    tma_load_2d(st_x(s) + C::kXBytes / 2, &tx, kt * kStepK + 64, m0, fb);
-                    ++steps;
-                    if (++s == S) s = 0, parity ^= 1u;
-                }
-                u += k1 - k0;
+            uint32_t parity = 0;
+            int s = 0;
+            for (int i = S; i < u_end - u_begin; ++i) {
+                if (!wait_bar(smem_u32(&bars->empty[s]), parity, ab)) break;
+                feed(s);
+                if (++s == S) s = 0, parity ^= 1u;
             }
-            drain_ring(bars->full, S, steps);
-            drain_ring(bars->empty, S, steps);
+            drain_ring(bars->full, S, fed);
+            if (!C::kInline) drain_ring(bars->empty, S, fed);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t kIdesc = umma_idesc_f16(BN, MP, false);
         const bool leader = elect_one();
-        const uint64_t desc_x = sw128_kmajor_desc(st_x(0));
+        const uint64_t desc_x = sw128_kmajor_desc(C::kInline ? st_wide(0) : st_x(0));
         const uint32_t bar_empty = smem_u32(&bars->empty[0]), bar_afull = smem_u32(&bars->afull[0]),
                        bar_aempty = smem_u32(&bars->aempty[0]);
         int s = 0, as = 0, seg = 0;
         uint32_t aparity = 0;
         bool ok = true;
-        for (long long u = u_begin; u < u_end && ok; ++seg) {
-            const int k0 = static_cast<int>(u % kt_total);
-            const int k1 = static_cast<int>(std::min<long long>(kt_total, k0 + (u_end - u)));
+        for (int u = u_begin, k0 = k_begin; u < u_end && ok; ++seg, k0 = 0) {
+            const int k1 = min(kt_total, k0 + (u_end - u));
             const int acc = seg & 1;
             if (!uniform_wait_bar(smem_u32(&bars->tempty[acc]), ((seg >> 1) & 1) ^ 1, ab, leader)) {
                 ok = false;
@@ -377,16 +462,17 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
                 // the group that wrote the stage had waited for the step's rows of a too
                 if (!uniform_wait_bar(bar_afull + 8 * as, aparity, ab, leader)) { ok = false; break; }
                 tc_fence_after();
-                const uint64_t x = desc_x + static_cast<uint64_t>(s) * (C::kStageBytes >> 4);
+                const uint64_t x = desc_x + (C::kInline ? static_cast<uint64_t>(as) * (C::kWideBytes >> 4)
+                                                        : static_cast<uint64_t>(s) * (C::kStageBytes >> 4));
                 const uint32_t a = tmem + C::kOpCol0 + as * kOpCols;
                 const int nk = step_mmas(K, kt);
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < kStepK / 16; ++kk)
                         if (kk < nk)
-                            umma_f16_ta(d, a + 8 * kk, x + (kk >> 2) * (C::kXBytes >> 5) + 2 * (kk & 3), kIdesc,
+                            umma_f16_ta(d, a + 8 * kk, x + (kk >> 2) * (C::kBox >> 4) + 2 * (kk & 3), kIdesc,
                                         kt != k0 || kk);
-                    umma_commit(bar_empty + 8 * s);
+                    if (!C::kInline) umma_commit(bar_empty + 8 * s);
                     umma_commit(bar_aempty + 8 * as);
                 }
                 __syncwarp();
@@ -403,19 +489,28 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
             drain_ring(&bars->drain, 1, 1);
         }
     } else if (warp >= kWidenWarp0) {
-        // ------------------------------------------------------------ codes to tensor memory
-        const int group = (warp - kWidenWarp0) / kGroupWarps, half = ((warp - kWidenWarp0) % kGroupWarps) >> 2;
+        // ------------------------------------------------------------ codes to operands
+        const int group = (warp - kWidenWarp0) / kGroupWarps, in_group = (warp - kWidenWarp0) % kGroupWarps;
         const int row = (warp & 3) * 32 + lane;
-        const uint32_t op = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kOpCol0 + half * 32;
-        const int steps = static_cast<int>(u_end - u_begin);
+        const uint32_t op = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kOpCol0;
+        const int steps = u_end - u_begin;
         int s = group, as = group;
         uint32_t parity = 0, aparity = 1u;
         for (int j = group; j < steps; j += kGroups) {
-            if (!warp_wait_bar(smem_u32(&bars->full[s]), parity, ab, lane) ||
-                !warp_wait_bar(smem_u32(&bars->aempty[as]), aparity, ab, lane))
+            if (!group_wait(1 + group, kGroupWarps * 32, in_group == 0 && lane == 0, smem_u32(&bars->aempty[as]), aparity,
+                            smem_u32(&bars->full[s]), parity, ab))
                 break;
             tc_fence_after();
-            widen_half_row(st_w(s), row, half, op + as * kOpCols);
+            widen_half_row(st_w(s), row, 0, op + as * kOpCols);
+            widen_half_row(st_w(s), row, 1, op + as * kOpCols + 32);
+            if constexpr (C::kInline) {
+#pragma unroll
+                for (int c = in_group * 32 + lane; c < MP * 8; c += kGroupWarps * 32)
+                    widen_chunk(st_x(s), st_wide(as), C::kBox, c >> 3, c & 7);
+                fence_proxy_async_smem();   // the MMAs read these stores
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->empty[s]));   // every lane's loads have returned
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -425,88 +520,126 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
         }
     } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------------ epilogue
-        const int q = warp & 3;
+        const int q = warp & 3, side = (warp - kEpiWarp0) >> 2;
+        constexpr int kCols = MP < 64 ? 16 : 32, kSide = MP / 2 < 16 ? 16 : MP / 2;   // rows of a at a time, per warp
         const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
         int seg = 0;
-        for (long long u = u_begin; u < u_end; ++seg) {
-            const long long t = u / kt_total;
-            const int k0 = static_cast<int>(u - t * kt_total);
-            const int k1 = static_cast<int>(std::min<long long>(kt_total, k0 + (u_end - u)));
+        for (int u = u_begin, t = t_begin, k0 = k_begin; u < u_end; ++seg, ++t, k0 = 0) {
+            const int k1 = min(kt_total, k0 + (u_end - u));
             u += k1 - k0;
             const int acc = seg & 1;
-            const int m0 = static_cast<int>(t % num_m) * MP, mc = min(MP, M - m0);
-            const int n = static_cast<int>(t / num_m) * BN + q * 32 + lane;
+            const int m0 = t % num_m * MP, mc = min(MP, M - m0);
+            const int n = t / num_m * BN + q * 32 + lane;
             const float tn = n < N ? __ldg(sb + n) : 0.f;
-            if (!warp_wait_bar(smem_u32(&bars->tfull[acc]), (seg >> 1) & 1, ab, lane)) break;
+            if (!group_wait(8, kEpiWarps * 32, threadIdx.x == kEpiWarp0 * 32, smem_u32(&bars->tfull[acc]), (seg >> 1) & 1, 0u,
+                            0u, ab))
+                break;
             tc_fence_after();
             const bool whole = k0 == 0 && k1 == kt_total;
             // slot 1: the tile begins here; slot 0: an earlier CTA began it
             float* part =
                 partials + (static_cast<size_t>(blockIdx.x) * 2 + (k0 == 0 ? 1 : 0)) * kSlotFloats + q * 32 + lane;
 #pragma unroll 1
-            for (int ch = 0; ch * 32 < mc; ++ch) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(tmem + lanes + acc * C::kAccCols + ch * 32, r);
+            for (int c = side * kSide; c < min(mc, (side + 1) * kSide); c += kCols) {
+                uint32_t r[kCols];
+                if constexpr (kCols == 32) tmem_ld_32x32b_x32(tmem + lanes + acc * C::kAccCols + c, r);
+                else tmem_ld_32x32b_x16(tmem + lanes + acc * C::kAccCols + c, r);
                 tmem_wait_ld();
-                if (whole) {
+                if (split > 1) {
+                    // the ring is idle: this CTA's copies have landed and its MMAs have read them
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i)
+                        if (c + i < mc) parts[(c + i) * 128 + q * 32 + lane] = __uint_as_float(r[i]);
+                } else if (whole) {
                     if (n < N) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (ch * 32 + i < mc)
-                                store1<kOut>(y, static_cast<size_t>(m0 + ch * 32 + i) * N + n,
-                                             __uint_as_float(r[i]) * __ldg(sa + m0 + ch * 32 + i) * tn);
+                        for (int i = 0; i < kCols; ++i)
+                            if (c + i < mc)
+                                store1<kOut>(y, static_cast<size_t>(m0 + c + i) * N + n,
+                                             __uint_as_float(r[i]) * __ldg(sa + m0 + c + i) * tn);
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (ch * 32 + i < mc) __stcg(part + (ch * 32 + i) * 128, __uint_as_float(r[i]));
+                    for (int i = 0; i < kCols; ++i)
+                        if (c + i < mc) __stcg(part + (c + i) * 128, __uint_as_float(r[i]));
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc]));
-            if (whole) continue;
-            const long long first = t * kt_total;
-            const int b_lo = unit_owner(first, U, G), b_hi = unit_owner(first + kt_total - 1, U, G);
-            // a CTA begins at most one tile that it does not end: the ticket goes by that CTA
-            __threadfence();
-            __syncwarp();
-            uint32_t last = 0;
-            if (lane == 0) last = atomicAdd(tickets + 4 * b_lo + q, 1u) == static_cast<unsigned>(b_hi - b_lo);
-            last = __shfl_sync(0xffffffffu, last, 0);
-            if (!last) continue;
-            __threadfence();
-            if (n < N) {
-                const float* lo = partials + (static_cast<size_t>(b_lo) * 2 + 1) * kSlotFloats + q * 32 + lane;
-                for (int c = 0; c < mc; c += 16) {
-                    float sum[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) sum[i] = c + i < mc ? __ldcg(lo + (c + i) * 128) : 0.f;
-                    for (int b = b_lo + 1; b <= b_hi; ++b) {
-                        const float* src = partials + static_cast<size_t>(b) * 2 * kSlotFloats + q * 32 + lane;
-                        float v[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = c + i < mc ? __ldcg(src + (c + i) * 128) : 0.f;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) sum[i] += v[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (c + i < mc)
-                            store1<kOut>(y, static_cast<size_t>(m0 + c + i) * N + n,
-                                         sum[i] * __ldg(sa + m0 + c + i) * tn);
-                }
-            }
-            if (lane == 0) tickets[4 * b_lo + q] = 0u;
         }
     }
 
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    if (split > 1) {
+        cluster_sync();   // every part of the tile is in its CTA's shared memory
+        const int t = b / split, m0 = t % num_m * MP, mc = min(MP, M - m0);
+        const int col = threadIdx.x & 127, n = t / num_m * BN + col;
+        const float tn = n < N ? __ldg(sb + n) : 0.f;
+        const uint32_t at = smem_u32(parts) + 4u * col;
+        for (int m = kThreads / 128 * part_k + (threadIdx.x >> 7); m < mc; m += kThreads / 128 * split) {
+            float v[kMaxSplit], sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < kMaxSplit; ++c) v[c] = c < split ? ld_cluster_f32(at + 512u * m, c) : 0.f;
+#pragma unroll
+            for (int c = 0; c < kMaxSplit; ++c)
+                if (c < split) sum += v[c];
+            if (n < N) store1<kOut>(y, static_cast<size_t>(m0 + m) * N + n, sum * __ldg(sa + m0 + m) * tn);
+        }
+        cluster_sync();   // no CTA leaves while another may read its part
+    } else {
+        __syncthreads();
+    }
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
+    }
+    if (!share) return;
+
+    // Shared tiles: the one that this CTA's range begins inside of and the one that it ends inside of. Every range is
+    // at least a tile long, so no tile lies in three.
+    const bool head = k_begin != 0;
+    const int t_end = u_end / kt_total;
+    const bool tail = u_end != t_end * kt_total;
+    if (threadIdx.x < 2) {
+        int last = 0;
+        if (threadIdx.x == 0 ? head : tail) {
+            uint32_t* ticket = tickets + (threadIdx.x == 0 ? b - 1 : b);   // the lower CTA's
+            __threadfence();   // the parts that this CTA's epilogue wrote before the barrier
+            last = atomicAdd(ticket, 1u) == 1u;
+            if (last) {
+                *ticket = 0u;
+                __threadfence();
+            }
+        }
+        bars->last[threadIdx.x] = last;
+    }
+    __syncthreads();
+    // half the threads for either tile
+    const int which = threadIdx.x >= kThreads / 2, thread = threadIdx.x - which * (kThreads / 2);
+    constexpr int kRowsAtOnce = kThreads / 2 / 128, kBatch = MP >= 64 ? 8 : MP >= 32 ? 4 : 2;
+    if (!bars->last[which] || thread >= kRowsAtOnce * 128) return;
+    const int t = which ? t_end : t_begin, lower = which ? b : b - 1;
+    const int m0 = t % num_m * MP, mc = min(MP, M - m0);
+    const int col = thread & 127, n = t / num_m * BN + col;
+    if (n >= N) return;
+    const float tn = __ldg(sb + n);
+    const float* lo = partials + (static_cast<size_t>(lower) * 2 + 1) * kSlotFloats + col;
+    const float* hi = partials + (static_cast<size_t>(lower) * 2 + 2) * kSlotFloats + col;
+    for (int c = thread >> 7; c < mc; c += kRowsAtOnce * kBatch) {
+        float p[kBatch], v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int m = min(c + j * kRowsAtOnce, mc - 1);
+            p[j] = __ldcg(lo + m * 128);
+            v[j] = __ldcg(hi + m * 128);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int m = c + j * kRowsAtOnce;
+            if (m < mc) store1<kOut>(y, static_cast<size_t>(m0 + m) * N + n, (p[j] + v[j]) * __ldg(sa + m0 + m) * tn);
+        }
     }
 }
 
@@ -719,7 +852,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
         }
     } else if (warp >= kWidenWarp0) {
         // ------------------------------------------------------------ codes to tensor memory
-        const int group = (warp - kWidenWarp0) / kGroupWarps;
+        const int group = (warp - kWidenWarp0) / kGroupWarps, in_group = (warp - kWidenWarp0) % kGroupWarps;
         const int row = (warp & 3) * 32 + lane;
         const uint32_t op = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kOpCol0;
         const long long mine = pair_id < tiles ? (tiles - 1 - pair_id) / npairs + 1 : 0;
@@ -727,8 +860,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
         int s = group, ws = group;
         uint32_t parity = 1u, wparity = 0;
         for (long long j = group; j < steps; j += kGroups) {
-            if (!warp_wait_bar(smem_u32(&bars->empty[s]), parity, ab, lane) ||
-                !warp_wait_bar(smem_u32(&bars->wfull[ws]), wparity, ab, lane))
+            if (!group_wait(1 + group, kGroupWarps * 32, in_group == 0 && lane == 0, smem_u32(&bars->empty[s]), parity,
+                            smem_u32(&bars->wfull[ws]), wparity, ab))
                 break;
             tc_fence_after();
             widen_half_row(st_w(ws), row, 0, op + s * kOpCols);
@@ -757,7 +890,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
 #pragma unroll
             for (int i = 0; i < 4; ++i) mine[32 * i + lane] = 32 * i + lane < mc ? __ldg(sa + m0 + 32 * i + lane) : 0.f;
             __syncwarp();
-            if (!warp_wait_bar(smem_u32(&bars->tfull), it & 1, ab, lane)) break;
+            if (!group_wait(8, kEpiWarps * 32, threadIdx.x == kEpiWarp0 * 32, smem_u32(&bars->tfull), it & 1, 0u, 0u, ab)) break;
             tc_fence_after();
             if constexpr (kOut == kF32) {
 #pragma unroll 1
@@ -824,20 +957,39 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// Ticket words (four per CTA of the tiles kernel) at the start of the workspace.
+// Ticket words (one per CTA of the tiles kernel) at the start of the workspace.
 constexpr size_t kControlBytes = 4096;
-constexpr int kMaxSms = static_cast<int>(kControlBytes / 16);
-// Rows of a that are widened at a time: bounds the workspace, and keeps them in L2.
+constexpr int kMaxCtas = static_cast<int>(kControlBytes / 4);
+// Rows of a that are widened at a time: bounds the workspace, and keeps them in L2. More rows are cut into equal chunks.
 constexpr long long kChunkRows = 8192;
+long long chunk_rows(long long M) {
+    const long long chunks = (M + kChunkRows - 1) / kChunkRows;
+    return chunks == 1 ? M : ((M + chunks - 1) / chunks + 255) / 256 * 256;
+}
 
 struct Plan {
-    int mp;   // rows of a per tile of the tiles kernel; 0: CTA pairs; -1: the rows kernel
+    int mp;       // rows of a per tile of the tiles kernel; 0: CTA pairs; -1: the rows kernel
+    bool split;   // tiles kernel: a cluster per tile, where the clusters are resident at once
+    bool share;   // tiles kernel: units shared between CTAs
+    bool widen;   // rows of a widened by a kernel before
 };
-Plan plan(long long M, long long N, int sms) {
-    if (M <= 2) return {-1};
-    const long long tiles256 = ((M + 255) / 256) * ((N + 255) / 256);
-    if (M > 128 && 2 * tiles256 > sms) return {0};
-    return {M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128};
+// Measured on 152 SMs (us a call):
+//   rows / tiles kernel: 4 x 43008 x 5376 38.7 / 44.9, 8 x 8192 x 8192 19.2 / 18.8, 8 x 2048 x 2048 3.1 / 6.5;
+//   tiles / pair kernel: 512 x 4096 x 4096 (128 tiles) 24.2 / 26.9, 300 x 2600 x 2080 (63) 15.2 / 17.3, 256 x 16384 x
+//     5376 (256) 53.8 / 33.3, 2048 x 2048 x 2048 (256) 29.9 / 20.0: pairs where 128-row tiles need a second wave;
+//   whole tiles / shared units: 16 x 20480 x 5376 (160 tiles) 38.3 / 25.9, 30720 columns (240) 38.6 / 35.3, 36864
+//     (288) 39.2 / 41.4, 43008 (336) 56.1 / 46.4; 64 rows 43.8 / 31.9, 44.0 / 42.8, 44.5 / 49.1, 63.1 / 55.0: shared
+//     where the last wave leaves a fifth of all SM time idle;
+//   whole tiles / a cluster per tile: 16 x 8192 x 5376 20.5 / 14.5 (2 CTAs), 3 x 4096 x 4096 17.5 / 9.0 (4), 16 x 4096
+//     x 1024 7.1 / 6.4 (4: 6 steps saved), 64 x 8192 x 2048 12.3 / 12.2 (2: 8 saved), 16 x 2048 x 512 5.6 / 6.3 (2: 2
+//     saved): from 6 saved steps on.
+Plan plan(long long M, long long N, long long K, int sms) {
+    if (M <= 4 || (M <= 6 && N * K <= 1ll << 27) || (M <= 8 && N * K <= 1ll << 26)) return {-1, false, false, false};
+    const long long cols = (N + tiles::BN - 1) / tiles::BN;
+    if (M > 128 && ((M + 127) / 128) * cols > sms) return {0, false, false, true};
+    const int mp = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    const long long tiles = ((M + mp - 1) / mp) * cols, waves = (tiles + sms - 1) / sms;
+    return {mp, 2 * tiles <= sms, tiles > sms && waves * sms * 4 > tiles * 5, mp > 64};
 }
 
 size_t partial_bytes(const DeviceProps& dp) {
@@ -853,32 +1005,39 @@ bool encode_wide(CUtensorMap* map, const __half* a, int rows, int K, int box_row
                      static_cast<uint64_t>(K) * 2, 64, static_cast<uint32_t>(box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Clusters of `size` CTAs of a kernel (one CTA per SM) that can be resident at once on the device, asked for once.
+int resident(const void* kern, const DeviceProps& dp, int size, int threads, size_t smem, std::atomic<int>* cache) {
+    std::atomic<int>& known = cache[dp.device & 63];
+    if (const int n = known.load(std::memory_order_relaxed)) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(size * (dp.sms / size)));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+        (void)cudaGetLastError();
+        n = dp.sms / size;
+    }
+    known.store(n, std::memory_order_relaxed);
+    return n;
+}
 template <int kOut>
 int resident_pairs(const DeviceProps& dp) {
-    static std::mutex mu;
-    static int cached[64] = {0};
-    const int dev = (dp.device >= 0 && dp.device < 64) ? dp.device : 0;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!cached[dev]) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * (dp.sms / 2));
-        cfg.blockDim = dim3(pair::kThreads);
-        cfg.dynamicSmemBytes = pair::kSmemBytes;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, pair::pair_kernel<kOut>, &cfg) != cudaSuccess || n <= 0) {
-            (void)cudaGetLastError();
-            n = dp.sms / 2;
-        }
-        cached[dev] = n;
-    }
-    return cached[dev];
+    static std::atomic<int> cache[64];
+    return resident(reinterpret_cast<const void*>(pair::pair_kernel<kOut>), dp, 2, pair::kThreads, pair::kSmemBytes, cache);
+}
+template <int kOut, int MP>
+int resident_clusters(const DeviceProps& dp, int size) {
+    static std::atomic<int> cache[tiles::kMaxSplit + 1][64];
+    return resident(reinterpret_cast<const void*>(tiles::tiles_kernel<kOut, MP>), dp, size, tiles::kThreads,
+                    tiles::smem_bytes<MP>(), cache[size]);
 }
 
 // Kernels that use tensor memory are launched without programmatic
@@ -910,52 +1069,79 @@ cudaError_t launch_pair(const Int8MatmulArgs& a, const __half* wide, const Devic
 }
 
 template <int kOut, int MP>
-cudaError_t launch_tiles(const Int8MatmulArgs& a, const __half* wide, float* partials, uint32_t* tickets,
+cudaError_t launch_tiles(const Int8MatmulArgs& a, const Plan& pl, const __half* wide, float* partials, uint32_t* tickets,
                          const DeviceProps& dp, cudaStream_t s) {
+    using C = tiles::Cfg<MP>;
     auto kern = tiles::tiles_kernel<kOut, MP>;
     constexpr size_t kSmem = tiles::smem_bytes<MP>();
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
     if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), dp.device, kSmem); e != cudaSuccess)
         return e;
     CUtensorMap tw, tx;
-    if (!encode_codes(&tw, a.b, a.N, a.K, tiles::BN) || !encode_wide(&tx, wide, a.M, a.K, MP))
+    if (!encode_codes(&tw, a.b, a.N, a.K, tiles::BN) ||
+        !(C::kInline ? encode_codes(&tx, a.a, a.M, a.K, MP) : encode_wide(&tx, wide, a.M, a.K, MP)))
         return cudaErrorInvalidValue;
-    const long long units = static_cast<long long>((a.M + MP - 1) / MP) * ((a.N + tiles::BN - 1) / tiles::BN) *
-                            ((a.K + kStepK - 1) / kStepK);
+    const long long tiles = static_cast<long long>((a.M + MP - 1) / MP) * ((a.N + tiles::BN - 1) / tiles::BN);
+    const long long steps = (a.K + kStepK - 1) / kStepK, units = tiles * steps;
+    if (units >= 1ll << 31) return cudaErrorInvalidValue;   // 35 TB of codes
+    int split = 1;
+    if (pl.split) {
+        // the largest cluster, up to 6 CTAs, of which all fit at once (50 tiles: clusters of 3 do not, 25.8 us
+        // instead of 17.6 with 2)
+        split = static_cast<int>(std::min<long long>({6, dp.sms / tiles, steps / 2}));
+        while (split > 1 && tiles > resident_clusters<kOut, MP>(dp, split)) --split;
+        if (split > 1 && steps - steps / split < 6) split = 1;
+    }
+    const long long grid = split > 1 ? tiles * split : std::min<long long>({tiles, dp.sms, kMaxCtas});
+    const long long items = pl.share ? units : tiles;
+    const tiles::Work work{split, pl.share ? 1 : 0, static_cast<int>(items / grid), static_cast<int>(items % grid)};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>({units, dp.sms, kMaxSms})));
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(tiles::kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, kern, tw, tx, a.sa, a.sb, a.y, a.M, a.N, a.K, partials, tickets);
+    cudaLaunchAttribute attr[1];
+    if (split > 1) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, tw, tx, a.sa, a.sb, a.y, a.M, a.N, a.K, work, partials, tickets);
 }
 
 template <int kOut>
 cudaError_t launch_typed(const Int8MatmulArgs& all, void* workspace, const DeviceProps& dp, cudaStream_t s) {
-    const Plan pl = plan(all.M, all.N, dp.sms);
-    if (pl.mp < 0) return all.M == 1 ? rows::launch<kOut, 1>(all, s) : rows::launch<kOut, 2>(all, s);
+    const Plan pl = plan(all.M, all.N, all.K, dp.sms);
+    if (pl.mp < 0) return rows::launch<kOut>(all, s);
     uint32_t* tickets = static_cast<uint32_t*>(workspace);
-    float* partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kControlBytes);
-    __half* wide = reinterpret_cast<__half*>(reinterpret_cast<uint8_t*>(partials) + (pl.mp ? partial_bytes(dp) : 0));
-    for (long long m0 = 0; m0 < all.M; m0 += kChunkRows) {
+    uint8_t* at = static_cast<uint8_t*>(workspace) + kControlBytes;
+    float* partials = reinterpret_cast<float*>(at);
+    __half* wide = reinterpret_cast<__half*>(at + (pl.share ? partial_bytes(dp) : 0));
+    const long long chunk = chunk_rows(all.M);
+    for (long long m0 = 0; m0 < all.M; m0 += chunk) {
         Int8MatmulArgs a = all;
-        a.M = static_cast<int>(std::min<long long>(kChunkRows, all.M - m0));
+        a.M = static_cast<int>(std::min(chunk, all.M - m0));
         a.a += m0 * all.K;
         a.sa += m0;
         a.y = static_cast<uint8_t*>(all.y) + m0 * all.N * (kOut == kF32 ? 4 : 2);
-        const long long items = static_cast<long long>(a.M) * a.K / 8;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>((items + 255) / 256, dp.sms * 16ll)));
-        cfg.blockDim = dim3(256);
-        cfg.stream = s;
-        cudaError_t e = cudaLaunchKernelEx(&cfg, widen_kernel, a.a, wide, items);
-        if (e != cudaSuccess) return e;
+        cudaError_t e = cudaSuccess;
+        if (pl.widen) {
+            const long long items = static_cast<long long>(a.M) * a.K / 8;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>((items + 255) / 256, dp.sms * 16ll)));
+            cfg.blockDim = dim3(256);
+            cfg.stream = s;
+            if ((e = cudaLaunchKernelEx(&cfg, widen_kernel, a.a, wide, items)) != cudaSuccess) return e;
+        }
         switch (pl.mp) {
             case 0: e = launch_pair<kOut>(a, wide, dp, s); break;
-            case 16: e = launch_tiles<kOut, 16>(a, wide, partials, tickets, dp, s); break;
-            case 32: e = launch_tiles<kOut, 32>(a, wide, partials, tickets, dp, s); break;
-            case 64: e = launch_tiles<kOut, 64>(a, wide, partials, tickets, dp, s); break;
-            default: e = launch_tiles<kOut, 128>(a, wide, partials, tickets, dp, s); break;
+            case 16: e = launch_tiles<kOut, 16>(a, pl, wide, partials, tickets, dp, s); break;
+            case 32: e = launch_tiles<kOut, 32>(a, pl, wide, partials, tickets, dp, s); break;
+            case 64: e = launch_tiles<kOut, 64>(a, pl, wide, partials, tickets, dp, s); break;
+            default: e = launch_tiles<kOut, 128>(a, pl, wide, partials, tickets, dp, s); break;
         }
         if (e != cudaSuccess) return e;
     }
@@ -965,10 +1151,10 @@ cudaError_t launch_typed(const Int8MatmulArgs& all, void* workspace, const Devic
 }  // namespace
 
 size_t int8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceProps& dp) {
-    const Plan pl = plan(M, N, dp.sms);
-    if (pl.mp < 0) return 0;
-    const size_t wide = static_cast<size_t>(std::min<long long>(M, kChunkRows)) * static_cast<size_t>(K) * 2;
-    return kControlBytes + (pl.mp ? partial_bytes(dp) : 0) + wide;
+    const Plan pl = plan(M, N, K, dp.sms);
+    const size_t wide = pl.widen ? static_cast<size_t>(chunk_rows(M)) * static_cast<size_t>(K) * 2 : 0;
+    const size_t parts = pl.share ? partial_bytes(dp) : 0;
+    return wide + parts ? kControlBytes + parts + wide : 0;
 }
 
 cudaError_t launch_int8_matmul(const Int8MatmulArgs& a, int out_type, void* workspace, const DeviceProps& dp,
