@@ -134,7 +134,7 @@ def _stream_ptr(stream=None) -> int:
         return int(stream.cuda_stream)
     if _raw_stream is None:
         return int(_torch().cuda.current_stream().cuda_stream)
-    return _raw_stream(_torch_module.cuda.current_device())
+    return _raw_stream(_current_device())
 
 
 def _check(fn: str, status: int) -> None:
@@ -630,16 +630,24 @@ def int8_quantize(x, out=None, stream=None):
     Activations: a row per token. A weight: [N, K], a row per output channel."""
     torch = _torch()
     _cuda_contig("x", x)
-    dt = _dtype_code(x.dtype)
+    dt = _dtype_codes.get(x.dtype)
+    if dt is None:
+        dt = _dtype_code(x.dtype)
     if x.dim() != 2:
         raise ValueError(f"x must be 2-D, got {x.dim()}-D")
-    R, K = x.shape
-    codes, scale = (None, None) if out is None else out
-    codes = _out("codes", codes, (R, K), torch.int8, x.device, stream)
-    scale = _out("scale", scale, (R,), torch.float32, x.device, stream)
+    R, K = shape = x.shape
+    if out is None and stream is None:
+        device = x.device
+        codes = torch.empty(shape, dtype=torch.int8, device=device)
+        scale = torch.empty((R,), dtype=torch.float32, device=device)
+    else:
+        codes, scale = (None, None) if out is None else out
+        codes = _out("codes", codes, shape, torch.int8, x.device, stream)
+        scale = _out("scale", scale, (R,), torch.float32, x.device, stream)
     st = load_library().w4a16_int8_quantize(x.data_ptr(), codes.data_ptr(), scale.data_ptr(), R, K, dt,
-                                            _stream_ptr(stream))
-    _check("w4a16_int8_quantize", st)
+                                                      _stream_ptr(stream))
+    if st:
+        _check("w4a16_int8_quantize", st)
     return codes, scale
 
 
@@ -663,10 +671,14 @@ def int8_dequant(codes, scale, out_dtype=None, out=None, stream=None):
     if out_dtype is None:
         out_dtype = _torch().bfloat16 if out is None else out.dtype
     dt = _dtype_code(out_dtype)
-    out = _out("out", out, (R, K), out_dtype, codes.device, stream)
+    if out is None and stream is None:
+        out = _torch_module.empty((R, K), dtype=out_dtype, device=codes.device)
+    else:
+        out = _out("out", out, (R, K), out_dtype, codes.device, stream)
     st = load_library().w4a16_int8_dequant(codes.data_ptr(), scale.data_ptr(), out.data_ptr(), R, K, dt,
-                                           _stream_ptr(stream))
-    _check("w4a16_int8_dequant", st)
+                                                     _stream_ptr(stream))
+    if st:
+        _check("w4a16_int8_dequant", st)
     return out
 
 
@@ -685,12 +697,28 @@ def int8_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, workspace=None
     lib = load_library()
     device = a.device
     out = _out("out", out, (M, N), out_dtype, device, stream)
-    ws_ptr, ws_bytes = _workspace(workspace, "int8_matmul", lib.w4a16_int8_matmul_workspace_bytes, (M, N, K), device,
-                                  stream)
+    if workspace is None and M <= 4:   # dot products: none
+        ws_ptr = ws_bytes = 0
+    else:
+        ws_ptr, ws_bytes = _workspace(workspace, "int8_matmul", lib.w4a16_int8_matmul_workspace_bytes, (M, N, K),
+                                      device, stream)
     st = lib.w4a16_int8_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr(), M,
                                N, K, dt, ws_ptr, ws_bytes, _stream_ptr(stream))
-    _check("w4a16_int8_matmul", st)
+    if st:
+        _check("w4a16_int8_matmul", st)
     return out
+
+
+def _norm_vector(name: str, t, dtype, H: int, current: int) -> int:
+    """Address of a vector over the channels, checked; 0 for none."""
+    if t is None:
+        return 0
+    _cuda_contig(name, t, current)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (H,):
+        raise ValueError(f"{name} shape {tuple(t.shape)} does not match {(H,)}")
+    return t.data_ptr()
 
 
 def block_norm(residual, weight=None, h=None, after=None, gate=None, scale: float = 1.0, eps: float = 1e-6,
@@ -709,52 +737,73 @@ def block_norm(residual, weight=None, h=None, after=None, gate=None, scale: floa
     r' alone; without `h`, r' is `residual` itself. `out` may give the outputs to
     write into, as a tuple in the order of the result (r' may be `residual`)."""
     torch = _torch()
-    if h is None and weight is None:
-        raise ValueError("h or weight must be given")
-    if h is None and (after is not None or gate is not None):
-        raise ValueError("after and gate need h")
-    if quantize and weight is None:
-        raise ValueError("quantize needs weight")
     _cuda_contig("residual", residual)
     current = residual.get_device()
     if residual.dim() != 2:
         raise ValueError(f"residual must be 2-D, got {residual.dim()}-D")
-    T, H = residual.shape
-    dtype = (weight if h is None else h).dtype
+    T, H = shape = residual.shape
+    if h is not None:
+        dtype = h.dtype
+        _cuda_contig("h", h, current)
+        if h.shape != shape:
+            raise ValueError(f"h shape {tuple(h.shape)} does not match {tuple(shape)}")
+        h_ptr = h.data_ptr()
+    else:
+        if weight is None:
+            raise ValueError("h or weight must be given")
+        if after is not None or gate is not None:
+            raise ValueError("after and gate need h")
+        dtype, h_ptr = weight.dtype, 0
+    if quantize and weight is None:
+        raise ValueError("quantize needs weight")
     dt, rdt = _dtype_code(dtype), _dtype_code(residual.dtype)
     if rdt != dt and rdt != F32:
         raise TypeError(f"residual must be {dtype} or float32, got {residual.dtype}")
-    kind = GATE_CHANNEL
+    weight_ptr = _norm_vector("weight", weight, dtype, H, current)
+    after_ptr = _norm_vector("after", after, dtype, H, current)
+    gate_ptr, kind = 0, GATE_CHANNEL
     if gate is not None:
-        kind = {(H,): GATE_CHANNEL, (T, H): GATE_ELEMENT, (T, 1): GATE_TOKEN}.get(tuple(gate.shape))
-        if kind is None:
-            raise ValueError(f"gate shape {tuple(gate.shape)} is none of {(H,)}, {(T, 1)}, {(T, H)}")
-    for name, t, shape in (("h", h, (T, H)), ("after", after, (H,)), ("gate", gate, None), ("weight", weight, (H,))):
-        if t is None:
-            continue
-        _cuda_contig(name, t, current)
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{name} shape {tuple(t.shape)} does not match {shape}")
-    device = residual.device
-    outs = [None] * 3 if out is None else list(out) if isinstance(out, (tuple, list)) else [out]
-    if out is not None and len(outs) != (1 if weight is None else 3 if quantize else 2):
-        raise ValueError(f"out holds {len(outs)} tensors")
-    new = residual if h is None else _out("residual out", outs[0], (T, H), residual.dtype, device, stream)
-    if h is None and outs[0] is not None and outs[0] is not residual:
-        raise ValueError("without h the residual is returned as it is")
+        if gate.shape == (H,):
+            gate_ptr = _norm_vector("gate", gate, dtype, H, current)
+        else:
+            kind = GATE_ELEMENT if gate.shape == shape else GATE_TOKEN
+            if kind == GATE_TOKEN and gate.shape != (T, 1):
+                raise ValueError(f"gate shape {tuple(gate.shape)} is none of {(H,)}, {(T, 1)}, {(T, H)}")
+            _cuda_contig("gate", gate, current)
+            if gate.dtype != dtype:
+                raise TypeError(f"gate must be {dtype}, got {gate.dtype}")
+            gate_ptr = gate.data_ptr()
     y = codes = code_scale = None
-    if quantize:
-        codes = _out("codes", outs[1], (T, H), torch.int8, device, stream)
-        code_scale = _out("scale", outs[2], (T,), torch.float32, device, stream)
-    elif weight is not None:
-        y = _out("y", outs[1], (T, H), dtype, device, stream)
-    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
-    st = load_library().w4a16_block_norm(residual.data_ptr(), rdt, ptr(h), ptr(after), ptr(gate), kind, scale,
-                                         0 if h is None else new.data_ptr(), ptr(weight), eps, ptr(y), ptr(codes),
-                                         ptr(code_scale), T, H, dt, _stream_ptr(stream))
-    _check("w4a16_block_norm", st)
+    if out is None and stream is None:
+        device = residual.device
+        new = residual if h is None else torch.empty(shape, dtype=residual.dtype, device=device)
+        if quantize:
+            codes = torch.empty(shape, dtype=torch.int8, device=device)
+            code_scale = torch.empty((T,), dtype=torch.float32, device=device)
+        elif weight is not None:
+            y = torch.empty(shape, dtype=dtype, device=device)
+    else:
+        outs = [None] * 3 if out is None else list(out) if isinstance(out, (tuple, list)) else [out]
+        if out is not None and len(outs) != (1 if weight is None else 3 if quantize else 2):
+            raise ValueError(f"out holds {len(outs)} tensors")
+        device = residual.device
+        if h is not None:
+            new = _out("residual out", outs[0], shape, residual.dtype, device, stream)
+        elif outs[0] is None or outs[0] is residual:
+            new = residual
+        else:
+            raise ValueError("without h the residual is returned as it is")
+        if quantize:
+            codes = _out("codes", outs[1], shape, torch.int8, device, stream)
+            code_scale = _out("scale", outs[2], (T,), torch.float32, device, stream)
+        elif weight is not None:
+            y = _out("y", outs[1], shape, dtype, device, stream)
+    st = load_library().w4a16_block_norm(
+        residual.data_ptr(), rdt, h_ptr, after_ptr, gate_ptr, kind, scale, 0 if h is None else new.data_ptr(),
+        weight_ptr, eps, 0 if y is None else y.data_ptr(), 0 if codes is None else codes.data_ptr(),
+        0 if codes is None else code_scale.data_ptr(), T, H, dt, _stream_ptr(stream))
+    if st:
+        _check("w4a16_block_norm", st)
     if weight is None:
         return new
     return (new, codes, code_scale) if quantize else (new, y)

@@ -474,7 +474,7 @@ w4a16_status w4a16_int8_quantize(const void* x, int8_t* codes, float* scale, int
     if (!aligned16(x) || !aligned16(codes) || !aligned16(scale)) return W4A16_ERR_ALIGN;
     DeviceProps dp;
     if ((st = device_gate(&dp)) != W4A16_OK) return st;
-    return from_cuda(w4a16::launch_int8_quantize(x, codes, scale, rows, cols, static_cast<int>(dt),
+    return from_cuda(w4a16::launch_int8_quantize(x, codes, scale, rows, cols, static_cast<int>(dt), dp,
                                                  reinterpret_cast<cudaStream_t>(stream)));
 }
 

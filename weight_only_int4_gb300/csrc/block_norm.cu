@@ -18,10 +18,11 @@ namespace {
 
 using namespace rowwise;
 
-template <int kAct, int kRes, int kPer>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const BlockNormArgs a) {
+template <int kAct, int kRes, int kPer, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNormArgs a) {
     __shared__ float scratch[3][32];
-    const long long row = blockIdx.x;
+    const long long row = blockIdx.x * static_cast<long long>(blockDim.y) + threadIdx.y;
+    if (row >= a.T) return;
     const int H = static_cast<int>(a.H), vecs = H >> 3;
     const float inv_h = 1.f / static_cast<float>(H);
     Vec8<kRes> rv[kPer];
@@ -122,13 +123,16 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const BlockNormArgs a)
 
 template <int kAct, int kRes>
 cudaError_t launch_typed(const BlockNormArgs& a, cudaStream_t s) {
-    const long long vecs = a.H / 8;
+    const Layout l = layout_of(a.H / 8, 4);   // by H alone: a row's sums do not depend on the number of rows
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.T));
+    cfg.gridDim = dim3(static_cast<unsigned>((a.T + l.y - 1) / l.y));
+    cfg.blockDim = dim3(static_cast<unsigned>(l.x), static_cast<unsigned>(l.y));
     cfg.stream = s;
-    const int per = vecs <= 1024 ? 1 : 2;
-    cfg.blockDim = dim3(static_cast<unsigned>(((vecs + per - 1) / per + 31) / 32 * 32));
-    return cudaLaunchKernelEx(&cfg, per == 1 ? block_norm_kernel<kAct, kRes, 1> : block_norm_kernel<kAct, kRes, 2>, a);
+    switch (l.per) {
+        case 1: return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 1, 1024>, a);
+        case 2: return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 2, 1024>, a);
+        default: return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 4, 512>, a);
+    }
 }
 
 }  // namespace

@@ -16,16 +16,17 @@ namespace {
 
 using namespace rowwise;
 
-// A thread block takes a row: each thread holds kPer vectors of 8 elements in
-// their own type between the maximum and the codes, so the row is read once.
-template <int kType, int kPer>
-__global__ void __launch_bounds__(1024) quant_row_kernel(const void* __restrict__ x, int8_t* __restrict__ codes,
-                                                         float* __restrict__ scales, int K) {
+// A thread block (or warp) takes a row: each thread holds kPer vectors of 8
+// elements in their own type between the maximum and the codes, so the row is read
+// once.
+template <int kType, int kPer, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads) quant_row_kernel(const void* __restrict__ x, int8_t* __restrict__ codes,
+                                                                float* __restrict__ scales, long long rows, int K) {
     __shared__ uint32_t scratch[32];
-    const long long row = blockIdx.x;
+    const long long row = blockIdx.x * static_cast<long long>(blockDim.y) + threadIdx.y;
+    if (row >= rows) return;
     const int vecs = K >> 3;
     Vec8<kType> v[kPer];
-    float f[8];
     uint32_t m = 0;
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
@@ -34,15 +35,13 @@ __global__ void __launch_bounds__(1024) quant_row_kernel(const void* __restrict_
         if (c < vecs) v[p].load_stream(x, row * K + 8ll * c);
     }
 #pragma unroll
-    for (int p = 0; p < kPer; ++p) {
-        v[p].widen(f);
-        m = magnitude(f, m);
-    }
-    const RowCodes code(block_max(m, scratch));
+    for (int p = 0; p < kPer; ++p) m = raw_magnitude(v[p], m);
+    const RowCodes code(block_max(raw_to_f32<kType>(m), scratch));
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
         const int c = p * blockDim.x + threadIdx.x;
         if (c >= vecs) break;
+        float f[8];
         v[p].widen(f);
         *reinterpret_cast<uint2*>(codes + row * K + 8ll * c) = code(f);
     }
@@ -56,18 +55,17 @@ __global__ void __launch_bounds__(1024) quant_long_kernel(const void* __restrict
     __shared__ uint32_t scratch[32];
     const long long row = blockIdx.x;
     const int vecs = K >> 3;
-    float f[8];
     uint32_t m = 0;
 #pragma unroll 4
     for (int c = threadIdx.x; c < vecs; c += blockDim.x) {
         Vec8<kType> v;
         v.load_stream(x, row * K + 8ll * c);
-        v.widen(f);
-        m = magnitude(f, m);
+        m = raw_magnitude(v, m);
     }
-    const RowCodes code(block_max(m, scratch));
+    const RowCodes code(block_max(raw_to_f32<kType>(m), scratch));
 #pragma unroll 4
     for (int c = threadIdx.x; c < vecs; c += blockDim.x) {
+        float f[8];
         Vec8<kType> v;
         v.load_stream(x, row * K + 8ll * c);
         v.widen(f);
@@ -76,61 +74,90 @@ __global__ void __launch_bounds__(1024) quant_long_kernel(const void* __restrict
     if (threadIdx.x == 0) scales[row] = code.scale;
 }
 
-// A thread takes 8 codes: c * s in FP32, rounded to the output type.
+// A thread takes 8 codes at a time, four such loads in flight: c * s in FP32,
+// rounded to the output type.
 template <int kType, typename Index>
 __global__ void __launch_bounds__(256) dequant_kernel(const int8_t* __restrict__ codes,
                                                       const float* __restrict__ scales, void* __restrict__ y,
                                                       Index items, Index vecs) {
+    constexpr int kUnroll = 4;
     const Index step = static_cast<Index>(static_cast<long long>(gridDim.x) * 256);
-    for (Index i = static_cast<Index>(blockIdx.x * 256ll + threadIdx.x); i < items; i += step) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(codes) + i);
-        const float s = __ldg(scales + i / vecs);
-        float f[8];
+    for (Index i0 = static_cast<Index>(blockIdx.x * 256ll + threadIdx.x); i0 < items; i0 += step * kUnroll) {
+        uint2 q[kUnroll];
+        float s[kUnroll];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = static_cast<float>(static_cast<int8_t>((j < 4 ? q.x : q.y) >> (8 * (j & 3)))) * s;
-        Vec8<kType> o;
-        o.round(f);
-        o.store(y, 8ll * i);
+        for (int u = 0; u < kUnroll; ++u) {
+            const Index i = i0 + step * u;
+            if (i < items) {
+                q[u] = __ldg(reinterpret_cast<const uint2*>(codes) + i);
+                s[u] = __ldg(scales + i / vecs);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const Index i = i0 + step * u;
+            if (i >= items) break;
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                f[j] = static_cast<float>(static_cast<int8_t>((j < 4 ? q[u].x : q[u].y) >> (8 * (j & 3)))) * s[u];
+            Vec8<kType> o;
+            o.round(f);
+            o.store(y, 8ll * i);
+        }
     }
 }
 
 // Ordinary launches, as in mx_quant.cu.
 template <typename... Params, typename... Args>
-cudaError_t launch(void (*kern)(Params...), long long blocks, int threads, cudaStream_t s, Args... args) {
+cudaError_t launch(void (*kern)(Params...), long long blocks, dim3 threads, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.blockDim = threads;
     cfg.stream = s;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
 }
 
 template <int kType>
-cudaError_t quantize(const void* x, int8_t* codes, float* scales, long long rows, long long K, cudaStream_t s) {
+cudaError_t quantize(const void* x, int8_t* codes, float* scales, long long rows, long long K, const DeviceProps& dp,
+                     cudaStream_t s) {
+    constexpr int kMost = kType == kF32 ? 4 : 8;
     const long long vecs = K / 8;
-    auto threads = [&](int per) { return static_cast<int>(((vecs + per - 1) / per + 31) / 32 * 32); };
-    if (vecs <= 1024) return launch(quant_row_kernel<kType, 1>, rows, threads(1), s, x, codes, scales, K);
-    if (vecs <= 2048) return launch(quant_row_kernel<kType, 2>, rows, threads(2), s, x, codes, scales, K);
-    if (vecs <= 4096) return launch(quant_row_kernel<kType, 4>, rows, threads(4), s, x, codes, scales, K);
-    return launch(quant_long_kernel<kType>, rows, 1024, s, x, codes, scales, K);
+    if (vecs > 512 * kMost) return launch(quant_long_kernel<kType>, rows, dim3(1024), s, x, codes, scales, K);
+    Layout l = layout_of(vecs, kMost);
+    if (rows <= 2ll * dp.sms) {   // the latency of a row is what counts: as many threads as there are
+        while (l.per > 1 && vecs <= 512ll * l.per) l.per /= 2;
+        l.x = static_cast<int>(((vecs + l.per - 1) / l.per + 31) / 32 * 32);
+        l.y = 1;
+    }
+    const dim3 threads(static_cast<unsigned>(l.x), static_cast<unsigned>(l.y));
+    const long long blocks = (rows + l.y - 1) / l.y;
+    if constexpr (kMost == 8)
+        if (l.per == 8) return launch(quant_row_kernel<kType, 8, 512>, blocks, threads, s, x, codes, scales, rows, K);
+    switch (l.per) {
+        case 1: return launch(quant_row_kernel<kType, 1, 1024>, blocks, threads, s, x, codes, scales, rows, K);
+        case 2: return launch(quant_row_kernel<kType, 2, 1024>, blocks, threads, s, x, codes, scales, rows, K);
+        default: return launch(quant_row_kernel<kType, 4, 1024>, blocks, threads, s, x, codes, scales, rows, K);
+    }
 }
 
 template <int kType>
 cudaError_t dequantize(const int8_t* codes, const float* scales, void* y, long long rows, long long K,
                        const DeviceProps& dp, cudaStream_t s) {
     const long long vecs = K / 8, items = rows * vecs;
-    const long long grid = std::min<long long>((items + 255) / 256, static_cast<long long>(dp.sms) * 32);
+    const long long grid = std::min<long long>((items + 255) / 256, static_cast<long long>(dp.sms) * 16);
     if (items < (1ll << 31) - (1ll << 26))
-        return launch(dequant_kernel<kType, unsigned>, grid, 256, s, codes, scales, y, items, vecs);
-    return launch(dequant_kernel<kType, unsigned long long>, grid, 256, s, codes, scales, y, items, vecs);
+        return launch(dequant_kernel<kType, unsigned>, grid, dim3(256), s, codes, scales, y, items, vecs);
+    return launch(dequant_kernel<kType, unsigned long long>, grid, dim3(256), s, codes, scales, y, items, vecs);
 }
 
 }  // namespace
 
 cudaError_t launch_int8_quantize(const void* x, int8_t* codes, float* scales, int64_t rows, int64_t cols, int type,
-                                 cudaStream_t s) {
-    if (type == kF16) return quantize<kF16>(x, codes, scales, rows, cols, s);
-    if (type == kBf16) return quantize<kBf16>(x, codes, scales, rows, cols, s);
-    return quantize<kF32>(x, codes, scales, rows, cols, s);
+                                 const DeviceProps& dp, cudaStream_t s) {
+    if (type == kF16) return quantize<kF16>(x, codes, scales, rows, cols, dp, s);
+    if (type == kBf16) return quantize<kBf16>(x, codes, scales, rows, cols, dp, s);
+    return quantize<kF32>(x, codes, scales, rows, cols, dp, s);
 }
 
 cudaError_t launch_int8_dequant(const int8_t* codes, const float* scales, void* y, int64_t rows, int64_t cols,

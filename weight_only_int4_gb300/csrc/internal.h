@@ -179,7 +179,7 @@ cudaError_t read_and_clear_mx_moe_error(uint32_t* out);
 
 // Rows of int8 codes with one FP32 scale each; type as w4a16_dtype.
 cudaError_t launch_int8_quantize(const void* x, int8_t* codes, float* scales, int64_t rows, int64_t cols, int type,
-                                 cudaStream_t s);
+                                 const DeviceProps& dp, cudaStream_t s);
 cudaError_t launch_int8_dequant(const int8_t* codes, const float* scales, void* y, int64_t rows, int64_t cols,
                                 int type, const DeviceProps& dp, cudaStream_t s);
 

@@ -95,9 +95,49 @@ __device__ __forceinline__ uint32_t magnitude(const float (&f)[8], uint32_t m) {
     return m;
 }
 
-// Sum / maximum over all threads of the block, the same in every thread, the
-// sum in a fixed order. `scratch`: 32 words that no thread uses until the next
-// barrier but one (callers alternate two arrays). Every thread calls it.
+// As two packed 16-bit magnitudes.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// Running maximum of a row in its own type, and that as FP32 bits.
+template <int kType>
+__device__ __forceinline__ uint32_t raw_magnitude(const Vec8<kType>& x, uint32_t m) {
+    if constexpr (kType == kF32) {
+        float f[8];
+        x.widen(f);
+        return magnitude(f, m);
+    } else {
+        const uint4 q = x.v[0];
+        return max_u16x2(m, max_u16x2(max_u16x2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu),
+                                      max_u16x2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu)));
+    }
+}
+template <int kType>
+__device__ __forceinline__ uint32_t raw_to_f32(uint32_t m) {
+    if constexpr (kType == kF32) return m;
+    const uint32_t v = max(m & 0xFFFFu, m >> 16);
+    if constexpr (kType == kBf16) return v << 16;
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(v))));
+}
+
+// How rows of `vecs` vectors are laid over threads: x threads hold a row, `per`
+// vectors each; rows that one warp holds come y to a block (no barriers).
+struct Layout {
+    int per, x, y;
+};
+// Up to `most` vectors per thread (a power of two), no more threads than they need.
+inline Layout layout_of(long long vecs, int most) {
+    int per = 1;
+    while (per < most && vecs > 32ll * per) per *= 2;
+    const long long x = ((vecs + per - 1) / per + 31) / 32 * 32;
+    return {per, static_cast<int>(x), x == 32 ? 4 : 1};
+}
+
+// Sum / maximum over the threads of a row (the block, or a warp of its own), the
+// same in every thread, the sum in a fixed order. `scratch`: 32 words that no other
+// reduction of the row uses. Every thread calls it.
 __device__ __forceinline__ float block_sum(float v, float* scratch) {
 #pragma unroll
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
