@@ -629,13 +629,13 @@ def int8_quantize(x, out=None, stream=None):
     (codes int8 [R, K], scale float32 [R]); `out` may give both to write into.
     Activations: a row per token. A weight: [N, K], a row per output channel."""
     torch = _torch()
-    _cuda_contig("x", x)
-    dt = _dtype_codes.get(x.dtype)
-    if dt is None:
-        dt = _dtype_code(x.dtype)
-    if x.dim() != 2:
-        raise ValueError(f"x must be 2-D, got {x.dim()}-D")
-    R, K = shape = x.shape
+    if not _here(x, _device_now()):
+        _cuda_contig("x", x)
+    dt = _dtype_code(x.dtype)
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must be 2-D, got {len(shape)}-D")
+    R, K = shape
     if out is None and stream is None:
         device = x.device
         codes = torch.empty(shape, dtype=torch.int8, device=device)
@@ -651,15 +651,29 @@ def int8_quantize(x, out=None, stream=None):
     return codes, scale
 
 
-def _int8_rows(name: str, codes, scale):
+def _device_now() -> int:
+    """The current device; no device's number where there is none to ask."""
+    try:
+        return _current_device()
+    except RuntimeError:
+        return -2
+
+
+def _here(t, current: int) -> bool:
+    """Whether a tensor is dense and on the current device."""
+    return t.get_device() == current and t.is_contiguous()
+
+
+def _int8_rows(name: str, codes, scale, current: int):
     """Checks int8 rows and their scales, returns rows and K."""
-    torch = _torch()
-    _cuda_contig(name, codes)
-    _cuda_contig(name + " scale", scale, codes.get_device())
-    if codes.dim() != 2 or codes.dtype != torch.int8:
+    if not (_here(codes, current) and _here(scale, current)):
+        _cuda_contig(name, codes)
+        _cuda_contig(name + " scale", scale)
+    shape = codes.shape
+    if codes.dtype != _torch_module.int8 or len(shape) != 2:
         raise TypeError(f"{name} must be a 2-D torch.int8 tensor of codes")
-    R, K = codes.shape
-    if scale.dtype != torch.float32 or scale.shape != (R,):
+    R, K = shape
+    if scale.dtype != _torch_module.float32 or scale.shape != (R,):
         raise ValueError(f"{name} scale must be torch.float32 ({R},), got {scale.dtype} {tuple(scale.shape)}")
     return R, K
 
@@ -667,12 +681,13 @@ def _int8_rows(name: str, codes, scale):
 def int8_dequant(codes, scale, out_dtype=None, out=None, stream=None):
     """Dense copy [R, K] of int8 rows: code * scale, in `out_dtype` (bfloat16
     unless given; float16 and float32 too)."""
-    R, K = _int8_rows("codes", codes, scale)
+    torch = _torch()
+    R, K = _int8_rows("codes", codes, scale, _device_now())
     if out_dtype is None:
-        out_dtype = _torch().bfloat16 if out is None else out.dtype
+        out_dtype = torch.bfloat16 if out is None else out.dtype
     dt = _dtype_code(out_dtype)
     if out is None and stream is None:
-        out = _torch_module.empty((R, K), dtype=out_dtype, device=codes.device)
+        out = torch.empty((R, K), dtype=out_dtype, device=codes.device)
     else:
         out = _out("out", out, (R, K), out_dtype, codes.device, stream)
     st = load_library().w4a16_int8_dequant(codes.data_ptr(), scale.data_ptr(), out.data_ptr(), R, K, dt,
@@ -687,16 +702,21 @@ def int8_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, workspace=None
     (activations through int8_quantize) and B [N, K] (a weight, one output channel
     per row). Returns y [M, N] in `out_dtype` (bfloat16 unless given; float16 and
     float32 too)."""
-    M, K = _int8_rows("a", a, a_scale)
-    N, Kb = _int8_rows("b", b, b_scale)
+    torch = _torch()
+    current = _device_now()
+    M, K = _int8_rows("a", a, a_scale, current)
+    N, Kb = _int8_rows("b", b, b_scale, current)
     if K != Kb:
         raise ValueError(f"a has K = {K}, b has K = {Kb}")
     if out_dtype is None:
-        out_dtype = _torch().bfloat16 if out is None else out.dtype
+        out_dtype = torch.bfloat16 if out is None else out.dtype
     dt = _dtype_code(out_dtype)
     lib = load_library()
     device = a.device
-    out = _out("out", out, (M, N), out_dtype, device, stream)
+    if out is None and stream is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=device)
+    else:
+        out = _out("out", out, (M, N), out_dtype, device, stream)
     if workspace is None and M <= 4:   # dot products: none
         ws_ptr = ws_bytes = 0
     else:
@@ -713,7 +733,8 @@ def _norm_vector(name: str, t, dtype, H: int, current: int) -> int:
     """Address of a vector over the channels, checked; 0 for none."""
     if t is None:
         return 0
-    _cuda_contig(name, t, current)
+    if not _here(t, current):
+        _cuda_contig(name, t)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != (H,):
@@ -737,14 +758,17 @@ def block_norm(residual, weight=None, h=None, after=None, gate=None, scale: floa
     r' alone; without `h`, r' is `residual` itself. `out` may give the outputs to
     write into, as a tuple in the order of the result (r' may be `residual`)."""
     torch = _torch()
-    _cuda_contig("residual", residual)
-    current = residual.get_device()
-    if residual.dim() != 2:
-        raise ValueError(f"residual must be 2-D, got {residual.dim()}-D")
-    T, H = shape = residual.shape
+    current = _device_now()
+    if not _here(residual, current):
+        _cuda_contig("residual", residual)
+    shape = residual.shape
+    if len(shape) != 2:
+        raise ValueError(f"residual must be 2-D, got {len(shape)}-D")
+    T, H = shape
     if h is not None:
         dtype = h.dtype
-        _cuda_contig("h", h, current)
+        if not _here(h, current):
+            _cuda_contig("h", h)
         if h.shape != shape:
             raise ValueError(f"h shape {tuple(h.shape)} does not match {tuple(shape)}")
         h_ptr = h.data_ptr()
@@ -769,7 +793,8 @@ def block_norm(residual, weight=None, h=None, after=None, gate=None, scale: floa
             kind = GATE_ELEMENT if gate.shape == shape else GATE_TOKEN
             if kind == GATE_TOKEN and gate.shape != (T, 1):
                 raise ValueError(f"gate shape {tuple(gate.shape)} is none of {(H,)}, {(T, 1)}, {(T, H)}")
-            _cuda_contig("gate", gate, current)
+            if not _here(gate, current):
+                _cuda_contig("gate", gate)
             if gate.dtype != dtype:
                 raise TypeError(f"gate must be {dtype}, got {gate.dtype}")
             gate_ptr = gate.data_ptr()

@@ -8,7 +8,8 @@
 // the first load to the last store, so h and r are read once and r' and y
 // written once. All arithmetic is FP32: u and the r' that is normalised are not
 // rounded in between; r', y and the scale are rounded once, when they are
-// stored. Two or three reductions separate the passes over the registers.
+// stored. Up to three reductions separate the passes over the registers.
+//
 // Bound by HBM bandwidth or, for few rows, by the launch and the reductions.
 #include "internal.h"
 #include "rowwise.cuh"
@@ -18,38 +19,46 @@ namespace {
 
 using namespace rowwise;
 
-template <int kAct, int kRes, int kPer, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNormArgs a) {
+// A row per block, or (kWarps) per warp, blockDim.y rows to a block.
+template <int kAct, int kRes, int kPer, int kMaxThreads, bool kWarps>
+__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
     __shared__ float scratch[3][32];
-    const long long row = blockIdx.x * static_cast<long long>(blockDim.y) + threadIdx.y;
-    if (row >= a.T) return;
-    const int H = static_cast<int>(a.H), vecs = H >> 3;
+    const long long row = kWarps ? blockIdx.x * static_cast<long long>(blockDim.y) + threadIdx.y : blockIdx.x;
+    if (kWarps && row >= a.T) return;
+    const int H = static_cast<int>(a.H);
+    const uint32_t vecs = static_cast<uint32_t>(H) >> 3;
     const float inv_h = 1.f / static_cast<float>(H);
+    constexpr uint32_t kActVec = 8 * kBytes<kAct>, kResVec = 8 * kBytes<kRes>;
+    auto bytes = [](const void* p) { return static_cast<const uint8_t*>(p); };
+    const uint8_t* h_row = bytes(a.h) + row * H * kBytes<kAct>;
+    const uint8_t* r_row = bytes(a.residual) + row * H * kBytes<kRes>;
+    uint8_t* out_row = static_cast<uint8_t*>(a.residual_out) + row * H * kBytes<kRes>;
     Vec8<kRes> rv[kPer];
     Vec8<kAct> hv[kPer];
-    float f[8];
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-        const int c = p * blockDim.x + threadIdx.x;
+        const uint32_t c = p * blockDim.x + threadIdx.x;
         rv[p].zero();
         hv[p].zero();
         if (c < vecs) {
-            rv[p].load_stream(a.residual, row * H + 8ll * c);
-            if (a.h) hv[p].load_stream(a.h, row * H + 8ll * c);
+            rv[p].load_stream(r_row + c * kResVec);
+            if (a.h) hv[p].load_stream(h_row + c * kActVec);
         }
     }
+    Pair f[4];
     float norm_h = 1.f;
     if (a.after) {
-        float sum = 0.f;
+        Pair sum = both(0.f);
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
             hv[p].widen(f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum = __fmaf_rn(f[i], f[i], sum);
+            for (int i = 0; i < 4; ++i) sum = fma2(f[i], f[i], sum);
         }
-        norm_h = rsqrtf(block_sum(sum, scratch[0]) * inv_h + a.eps);
+        const float2 t = parts(sum);
+        norm_h = rsqrtf(block_sum<kWarps>(t.x + t.y, scratch[0]) * inv_h + a.eps);
     }
-    float r[kPer][8], sum = 0.f;
+    Pair r[kPer][4], sum = both(0.f);
     float row_gate = a.scale;
     if (a.gate && a.gate_kind == kGateToken) {
         const uint16_t* p16 = static_cast<const uint16_t*>(a.gate) + row;
@@ -57,82 +66,87 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNorm
         else if constexpr (kAct == kBf16) row_gate *= __uint_as_float(static_cast<uint32_t>(__ldg(p16)) << 16);
         else row_gate *= __half2float(__ushort_as_half(__ldg(p16)));
     }
+    const Pair by_h = both(norm_h), by_gate = both(row_gate);
+    const bool vector_gate = a.gate && a.gate_kind != kGateToken;
+    const uint8_t* gate_row = bytes(a.gate) + (a.gate_kind == kGateElement ? row * H * kBytes<kAct> : 0);
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-        const int c = p * blockDim.x + threadIdx.x;
+        const uint32_t c = p * blockDim.x + threadIdx.x;
         rv[p].widen(r[p]);
-        if (c >= vecs || !a.h) {
+        if (c < vecs && a.h) {
+            Pair u[4];
+            hv[p].widen(u);
+            if (a.after) {
+                Vec8<kAct> w;
+                w.load_shared(bytes(a.after) + c * kActVec);
+                w.widen(f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum = __fmaf_rn(r[p][i], r[p][i], sum);
-            continue;
-        }
-        float u[8];
-        hv[p].widen(u);
-        if (a.after) {
-            Vec8<kAct> w;
-            w.load_shared(a.after, 8ll * c);
-            w.widen(f);
+                for (int i = 0; i < 4; ++i) u[i] = mul2(u[i], mul2(by_h, f[i]));
+            }
+            if (vector_gate) {
+                Vec8<kAct> g;
+                g.load_shared(gate_row + c * kActVec);
+                g.widen(f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] *= norm_h * f[i];
-        }
-        if (a.gate && a.gate_kind != kGateToken) {
-            Vec8<kAct> g;
-            if (a.gate_kind == kGateChannel) g.load_shared(a.gate, 8ll * c);
-            else g.load_stream(a.gate, row * H + 8ll * c);
-            g.widen(f);
+                for (int i = 0; i < 4; ++i) u[i] = mul2(u[i], f[i]);
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] *= f[i];
+            for (int i = 0; i < 4; ++i) r[p][i] = fma2(by_gate, u[i], r[p][i]);
+            rv[p].round(r[p]);
+            rv[p].store(out_row + c * kResVec);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            r[p][i] = __fmaf_rn(row_gate, u[i], r[p][i]);
-            sum = __fmaf_rn(r[p][i], r[p][i], sum);
-        }
-        rv[p].round(r[p]);
-        rv[p].store(a.residual_out, row * H + 8ll * c);
+        for (int i = 0; i < 4; ++i) sum = fma2(r[p][i], r[p][i], sum);
     }
     if (!a.weight) return;
-    const float norm_r = rsqrtf(block_sum(sum, scratch[1]) * inv_h + a.eps);
+    const float2 t = parts(sum);
+    const Pair by_r = both(rsqrtf(block_sum<kWarps>(t.x + t.y, scratch[1]) * inv_h + a.eps));
+    uint8_t* y_row = static_cast<uint8_t*>(a.y) + row * H * kBytes<kAct>;
     uint32_t m = 0;
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-        const int c = p * blockDim.x + threadIdx.x;
+        const uint32_t c = p * blockDim.x + threadIdx.x;
         if (c >= vecs) break;
         Vec8<kAct> w;
-        w.load_shared(a.weight, 8ll * c);
+        w.load_shared(bytes(a.weight) + c * kActVec);
         w.widen(f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[p][i] *= norm_r * f[i];
+        for (int i = 0; i < 4; ++i) r[p][i] = mul2(r[p][i], mul2(by_r, f[i]));
         if (a.codes) {
             m = magnitude(r[p], m);
         } else {
             w.round(r[p]);
-            w.store(a.y, row * H + 8ll * c);
+            w.store(y_row + c * kActVec);
         }
     }
     if (!a.codes) return;
-    const RowCodes code(block_max(m, reinterpret_cast<uint32_t*>(scratch[2])));
+    int8_t* codes_row = a.codes + row * H;
+    const RowCodes<kF32> code(block_max<kWarps>(m, reinterpret_cast<uint32_t*>(scratch[2])));
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-        const int c = p * blockDim.x + threadIdx.x;
+        const uint32_t c = p * blockDim.x + threadIdx.x;
         if (c >= vecs) break;
-        *reinterpret_cast<uint2*>(a.codes + row * H + 8ll * c) = code(r[p]);
+        *reinterpret_cast<uint2*>(codes_row + 8u * c) = code(r[p]);
     }
     if (threadIdx.x == 0) a.code_scales[row] = code.scale;
 }
 
 template <int kAct, int kRes>
 cudaError_t launch_typed(const BlockNormArgs& a, cudaStream_t s) {
-    const Layout l = layout_of(a.H / 8, 4);   // by H alone: a row's sums do not depend on the number of rows
+    // by H alone: a row's sums do not depend on the number of rows
+    const Layout l = layout_of(a.H / 8, kRes == kF32 && a.H <= 8192 ? 2 : 4);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((a.T + l.y - 1) / l.y));
     cfg.blockDim = dim3(static_cast<unsigned>(l.x), static_cast<unsigned>(l.y));
     cfg.stream = s;
-    switch (l.per) {
-        case 1: return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 1, 1024>, a);
-        case 2: return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 2, 1024>, a);
-        default: return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 4, 512>, a);
-    }
+    if (l.y > 1) switch (l.per) {
+            case 1: return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 1, 128, true>, a);
+            case 2: return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 2, 128, true>, a);
+            default: return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 4, 128, true>, a);
+        }
+    if constexpr (kRes == kF32)
+        if (l.per == 2) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 2, 512, false>, a);
+    return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 4, 512, false>, a);
 }
 
 }  // namespace

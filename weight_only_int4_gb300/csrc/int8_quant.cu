@@ -16,34 +16,36 @@ namespace {
 
 using namespace rowwise;
 
-// A thread block (or warp) takes a row: each thread holds kPer vectors of 8
-// elements in their own type between the maximum and the codes, so the row is read
-// once.
-template <int kType, int kPer, int kMaxThreads>
+// A thread block takes a row (kWarps: each of its warps one): each thread holds
+// kPer vectors of 8 elements in their own type between the maximum and the codes,
+// so the row is read once.
+template <int kType, int kPer, int kMaxThreads, bool kWarps = false>
 __global__ void __launch_bounds__(kMaxThreads) quant_row_kernel(const void* __restrict__ x, int8_t* __restrict__ codes,
                                                                 float* __restrict__ scales, long long rows, int K) {
     __shared__ uint32_t scratch[32];
-    const long long row = blockIdx.x * static_cast<long long>(blockDim.y) + threadIdx.y;
-    if (row >= rows) return;
+    const long long row = kWarps ? blockIdx.x * static_cast<long long>(blockDim.y) + threadIdx.y : blockIdx.x;
+    if (kWarps && row >= rows) return;
     const int vecs = K >> 3;
+    const uint8_t* from = static_cast<const uint8_t*>(x) + row * K * kBytes<kType>;
+    int8_t* to = codes + row * K;
     Vec8<kType> v[kPer];
     uint32_t m = 0;
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-        const int c = p * blockDim.x + threadIdx.x;
+        const uint32_t c = p * blockDim.x + threadIdx.x;
         v[p].zero();
-        if (c < vecs) v[p].load_stream(x, row * K + 8ll * c);
+        if (c < vecs) v[p].load_stream(from + c * (8u * kBytes<kType>));
     }
 #pragma unroll
     for (int p = 0; p < kPer; ++p) m = raw_magnitude(v[p], m);
-    const RowCodes code(block_max(raw_to_f32<kType>(m), scratch));
+    const RowCodes<kType> code(block_max<kWarps>(raw_to_f32<kType>(m), scratch));
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-        const int c = p * blockDim.x + threadIdx.x;
+        const uint32_t c = p * blockDim.x + threadIdx.x;
         if (c >= vecs) break;
-        float f[8];
+        Pair f[4];
         v[p].widen(f);
-        *reinterpret_cast<uint2*>(codes + row * K + 8ll * c) = code(f);
+        *reinterpret_cast<uint2*>(to + 8u * c) = code(f);
     }
     if (threadIdx.x == 0) scales[row] = code.scale;
 }
@@ -55,19 +57,20 @@ __global__ void __launch_bounds__(1024) quant_long_kernel(const void* __restrict
     __shared__ uint32_t scratch[32];
     const long long row = blockIdx.x;
     const int vecs = K >> 3;
+    const uint8_t* from = static_cast<const uint8_t*>(x) + row * K * kBytes<kType>;
     uint32_t m = 0;
 #pragma unroll 4
-    for (int c = threadIdx.x; c < vecs; c += blockDim.x) {
+    for (int c = threadIdx.x; c < vecs; c += 1024) {
         Vec8<kType> v;
-        v.load_stream(x, row * K + 8ll * c);
+        v.load_stream(from + 8ll * kBytes<kType> * c);
         m = raw_magnitude(v, m);
     }
-    const RowCodes code(block_max(raw_to_f32<kType>(m), scratch));
+    const RowCodes<kType> code(block_max<false>(raw_to_f32<kType>(m), scratch));
 #pragma unroll 4
-    for (int c = threadIdx.x; c < vecs; c += blockDim.x) {
-        float f[8];
+    for (int c = threadIdx.x; c < vecs; c += 1024) {
+        Pair f[4];
         Vec8<kType> v;
-        v.load_stream(x, row * K + 8ll * c);
+        v.load_stream(from + 8ll * kBytes<kType> * c);
         v.widen(f);
         *reinterpret_cast<uint2*>(codes + row * K + 8ll * c) = code(f);
     }
@@ -97,13 +100,16 @@ __global__ void __launch_bounds__(256) dequant_kernel(const int8_t* __restrict__
         for (int u = 0; u < kUnroll; ++u) {
             const Index i = i0 + step * u;
             if (i >= items) break;
-            float f[8];
+            Pair f[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                f[j] = static_cast<float>(static_cast<int8_t>((j < 4 ? q[u].x : q[u].y) >> (8 * (j & 3)))) * s[u];
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t w = (j < 2 ? q[u].x : q[u].y) >> (16 * (j & 1));
+                f[j] = mul2(pair(static_cast<float>(static_cast<int8_t>(w)),
+                                 static_cast<float>(static_cast<int8_t>(w >> 8))), both(s[u]));
+            }
             Vec8<kType> o;
             o.round(f);
-            o.store(y, 8ll * i);
+            o.store(static_cast<uint8_t*>(y) + 8ll * kBytes<kType> * i);
         }
     }
 }
@@ -121,23 +127,35 @@ cudaError_t launch(void (*kern)(Params...), long long blocks, dim3 threads, cuda
 template <int kType>
 cudaError_t quantize(const void* x, int8_t* codes, float* scales, long long rows, long long K, const DeviceProps& dp,
                      cudaStream_t s) {
-    constexpr int kMost = kType == kF32 ? 4 : 8;
+    constexpr int kMost = kType == kF32 ? 4 : 8;   // vectors of 32 registers in all
     const long long vecs = K / 8;
-    if (vecs > 512 * kMost) return launch(quant_long_kernel<kType>, rows, dim3(1024), s, x, codes, scales, K);
+    if (vecs > 1024 * kMost) return launch(quant_long_kernel<kType>, rows, dim3(1024), s, x, codes, scales, K);
     Layout l = layout_of(vecs, kMost);
     if (rows <= 2ll * dp.sms) {   // the latency of a row is what counts: as many threads as there are
-        while (l.per > 1 && vecs <= 512ll * l.per) l.per /= 2;
+        l.per = vecs <= 1024 ? 1 : vecs <= 2048 ? std::min(4, kMost) : l.per;
         l.x = static_cast<int>(((vecs + l.per - 1) / l.per + 31) / 32 * 32);
         l.y = 1;
     }
     const dim3 threads(static_cast<unsigned>(l.x), static_cast<unsigned>(l.y));
     const long long blocks = (rows + l.y - 1) / l.y;
+    if (l.x > 512) {   // long rows: twice the vectors
+        const dim3 half(static_cast<unsigned>((vecs + 2 * kMost - 1) / (2 * kMost) + 31) / 32 * 32);
+        return launch(quant_row_kernel<kType, 2 * kMost, 512>, blocks, half, s, x, codes, scales, rows, K);
+    }
+    if (l.y > 1)
+        switch (l.per) {
+            case 1: return launch(quant_row_kernel<kType, 1, 128, true>, blocks, threads, s, x, codes, scales, rows, K);
+            case 2: return launch(quant_row_kernel<kType, 2, 128, true>, blocks, threads, s, x, codes, scales, rows, K);
+            case 4: return launch(quant_row_kernel<kType, 4, 128, true>, blocks, threads, s, x, codes, scales, rows, K);
+            default:
+                return launch(quant_row_kernel<kType, kMost, 128, true>, blocks, threads, s, x, codes, scales, rows, K);
+        }
     if constexpr (kMost == 8)
         if (l.per == 8) return launch(quant_row_kernel<kType, 8, 512>, blocks, threads, s, x, codes, scales, rows, K);
     switch (l.per) {
         case 1: return launch(quant_row_kernel<kType, 1, 1024>, blocks, threads, s, x, codes, scales, rows, K);
-        case 2: return launch(quant_row_kernel<kType, 2, 1024>, blocks, threads, s, x, codes, scales, rows, K);
-        default: return launch(quant_row_kernel<kType, 4, 1024>, blocks, threads, s, x, codes, scales, rows, K);
+        case 2: return launch(quant_row_kernel<kType, 2, 512>, blocks, threads, s, x, codes, scales, rows, K);
+        default: return launch(quant_row_kernel<kType, 4, 512>, blocks, threads, s, x, codes, scales, rows, K);
     }
 }
 

@@ -16,21 +16,50 @@ enum : int { kF16 = 0, kBf16 = 1, kF32 = 2 };
 template <int kType>
 constexpr int kBytes = kType == kF32 ? 4 : 2;
 
+// Two FP32 values in a 64-bit register, two operations per instruction, each
+// rounded as alone: what bounds these kernels next to the memory is the
+// instructions they issue.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float x, float y) {
+    Pair d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
+__device__ __forceinline__ float2 parts(Pair p) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(p));
+    return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // Eight consecutive elements in their own type: 16 bytes, or 32 for FP32.
 template <int kType>
 struct Vec8 {
     static constexpr int kQuads = kType == kF32 ? 2 : 1;
     uint4 v[kQuads];
-    static __device__ const uint4* place(const void* x, long long elem) {
-        return reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + elem * kBytes<kType>);
-    }
+    // `at`: the thread's byte in the array, the vector's first
     __device__ void zero() {
 #pragma unroll
         for (auto& q : v) q = make_uint4(0, 0, 0, 0);
     }
     // read once: not kept in L1
-    __device__ void load_stream(const void* x, long long elem) {
-        const uint4* p = place(x, elem);
+    __device__ void load_stream(const void* at) {
+        const uint4* p = static_cast<const uint4*>(at);
 #pragma unroll
         for (int i = 0; i < kQuads; ++i)
             asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -38,61 +67,57 @@ struct Vec8 {
                          : "l"(p + i));
     }
     // read again by other rows: kept
-    __device__ void load_shared(const void* x, long long elem) {
-        const uint4* p = place(x, elem);
+    __device__ void load_shared(const void* at) {
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i) v[i] = __ldg(p + i);
+        for (int i = 0; i < kQuads; ++i) v[i] = __ldg(static_cast<const uint4*>(at) + i);
     }
-    __device__ void store(void* x, long long elem) const {
-        uint4* p = const_cast<uint4*>(place(x, elem));
+    __device__ void store(void* at) const {
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i) p[i] = v[i];
+        for (int i = 0; i < kQuads; ++i) static_cast<uint4*>(at)[i] = v[i];
     }
-    __device__ void widen(float (&f)[8]) const {
+    __device__ void widen(Pair (&f)[4]) const {
         const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
-        if constexpr (kType == kF32) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (kType == kBf16) {
-                    f[2 * i] = __uint_as_float(w[i] << 16);
-                    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-                } else {
-                    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                    f[2 * i] = t.x;
-                    f[2 * i + 1] = t.y;
-                }
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kType == kF32) f[i] = pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+            if constexpr (kType == kBf16)
+                f[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+            if constexpr (kType == kF16) {
+                const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                f[i] = pair(h.x, h.y);
             }
         }
     }
-    __device__ void round(const float (&f)[8]) {
+    __device__ void round(const Pair (&f)[4]) {
         uint32_t* w = reinterpret_cast<uint32_t*>(v);
-        if constexpr (kType == kF32) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(f[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (kType == kBf16) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-                } else {
-                    const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-                }
+        for (int i = 0; i < 4; ++i) {
+            const float2 t = parts(f[i]);
+            if constexpr (kType == kF32) {
+                w[2 * i] = __float_as_uint(t.x);
+                w[2 * i + 1] = __float_as_uint(t.y);
+            } else if constexpr (kType == kBf16) {
+                const __nv_bfloat162 h = __float22bfloat162_rn(t);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __half2 h = __float22half2_rn(t);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
             }
         }
     }
 };
 
-// Largest magnitude as FP32 bits: the order of the bits is the order of the
-// magnitudes, infinity and NaN above every finite value.
-__device__ __forceinline__ uint32_t magnitude(const float (&f)[8], uint32_t m) {
+// Larger of a running magnitude and those of eight values, as FP32 bits; a NaN
+// stays one, so infinity and NaN end up above every finite value.
+__device__ __forceinline__ uint32_t magnitude(const Pair (&f)[4], uint32_t m) {
+    float v = __uint_as_float(m);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-    return m;
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = parts(f[i]);
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(fabsf(t.x)));
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(fabsf(t.y)));
+    }
+    return __float_as_uint(v);
 }
 
 // As two packed 16-bit magnitudes.
@@ -105,7 +130,7 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 template <int kType>
 __device__ __forceinline__ uint32_t raw_magnitude(const Vec8<kType>& x, uint32_t m) {
     if constexpr (kType == kF32) {
-        float f[8];
+        Pair f[4];
         x.widen(f);
         return magnitude(f, m);
     } else {
@@ -135,25 +160,27 @@ inline Layout layout_of(long long vecs, int most) {
     return {per, static_cast<int>(x), x == 32 ? 4 : 1};
 }
 
-// Sum / maximum over the threads of a row (the block, or a warp of its own), the
+// Sum / maximum over the threads of a row (the block, or with kWarps a warp), the
 // same in every thread, the sum in a fixed order. `scratch`: 32 words that no other
 // reduction of the row uses. Every thread calls it.
+template <bool kWarps>
 __device__ __forceinline__ float block_sum(float v, float* scratch) {
 #pragma unroll
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if (kWarps) return v;
     const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = (threadIdx.x & 31) < warps ? scratch[threadIdx.x & 31] : 0.f;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    v = scratch[0];
+#pragma unroll 4
+    for (int w = 1; w < warps; ++w) v += scratch[w];
     return v;
 }
+template <bool kWarps>
 __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* scratch) {
     v = __reduce_max_sync(0xffffffffu, v);
+    if (kWarps) return v;
     const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
     __syncthreads();
     return __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < warps ? scratch[threadIdx.x & 31] : 0u);
@@ -163,27 +190,47 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* scratch) {
 //
 //     c = RN(127 v / amax), ties to even,   scale = RN(amax / 127),
 //
-// decided exactly. q = v * (127 / amax) is off by at most 2^-16 (two roundings
-// of relative size 2^-24 at |q| <= 127), so the nearest whole number is right
-// unless q lies within 2^-15 of a half; there 254 |v| is compared with
-// (2 k + 1) amax, k the whole number below, each product held as a rounded value
-// and its exact remainder. Rows far from 1 are moved there by a power of two,
-// so neither 127 / amax nor a product leaves the FP32 range.
+// decided exactly. f = 127 / amax is off by a relative 2^-23 at most and the product
+// v f enters a fused addition, so the nearest whole number is right unless
+// 127 v / amax lies within 2^-16 of a half.
+//
+// FP32 values: there 254 |v| is compared with (2 k + 1) amax, k the whole number
+// below, each product held as a rounded value and its exact remainder.
+//
+// 16-bit values: v and amax have at most 11 bits, X and A as whole numbers. With
+// q = 127 X / (A 2^j), what is not a half is at least 1 / (2 A 2^j) >= 2^-20 q away
+// from it, more than the error: only halves themselves matter. They are the
+// solutions of 254 X = (2 k + 1) A 2^j. Where 127 does not divide A, the odd part of A
+// divides X and 2 k + 1 = 127: v is half of amax, q = 63.5, and f rounded up takes
+// it to 64, the even one. Where 127 divides A, f is exact for A = 127 2^i (bfloat16
+// has no other such A) and the fused addition rounds halves to even itself; else the row is
+// compared as above.
+//
+// Rows far from 1 are moved there by a power of two, so neither f nor a product
+// leaves the FP32 range.
+template <int kType>
 struct RowCodes {
     float amax;     // after the power of two
-    float factor;   // 127 / amax; 0 for a row of zeros or with an infinity or NaN
+    float factor;   // 127 / amax, rounded up; 0 for a row of zeros or with an infinity or NaN
     float move;
     float scale;    // NaN for a row with an infinity or NaN
+    bool compare;
 
     __device__ explicit RowCodes(uint32_t amax_bits) {
         const float a = __uint_as_float(amax_bits);
         const bool plain = amax_bits != 0u && amax_bits < 0x7F800000u;
         move = a > 0x1p100f ? 0x1p-64f : a < 0x1p-64f ? 0x1p64f : 1.f;
         amax = a * move;
-        factor = plain ? __fdiv_rn(127.f, amax) : 0.f;
+        factor = __fdiv_rn(127.f, amax);
+        const float below = __fmaf_rn(factor, amax, -127.f);   // exact
+        if (below < 0.f) factor = __uint_as_float(__float_as_uint(factor) + 1u);
+        if (!plain) factor = 0.f;
         scale = plain ? __fdiv_rn(a, 127.f) : amax_bits ? __uint_as_float(0x7FC00000u) : 0.f;
+        compare = kType == kF32 ||
+                  (kType == kF16 && ((__float_as_uint(amax) & 0x7FFFFFu) | 0x800000u) % 127u == 0u && below != 0.f);
     }
     static constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to a whole number in the low bits
+    static constexpr float kNear = 0.5f - 0x1p-15f;
 
     // The code of v where q is next to a half: k is the lower of the two whole numbers around |q|.
     __device__ float decide(float v) const {
@@ -197,27 +244,44 @@ struct RowCodes {
     }
 
     // Eight codes, one per byte. A factor of 0 gives zeros even for an infinity or NaN.
-    __device__ uint2 operator()(const float (&x)[8]) const {
+    __device__ uint2 operator()(Pair (&v)[4]) const {
         if (factor == 0.f) return make_uint2(0u, 0u);
-        float v[8], f[8], worst = 0.f;
+        if (move != 1.f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[i] = x[i];
-            if (move != 1.f) v[i] *= move;
-            f[i] = __fmaf_rn(v[i], factor, kMagic);
-            worst = fmaxf(worst, fabsf(__fmaf_rn(v[i], factor, kMagic - f[i])));
+            for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(move));
         }
-        if (worst > 0.5f - 0x1p-15f) {
+        Pair f[4];
+        const Pair by = both(factor), magic = both(kMagic);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (fabsf(__fmaf_rn(v[i], factor, kMagic - f[i])) > 0.5f - 0x1p-15f) f[i] = kMagic + decide(v[i]);
+        for (int i = 0; i < 4; ++i) f[i] = fma2(v[i], by, magic);
+        if (compare) {
+            const Pair minus_by = both(-factor), minus_magic = both(-kMagic);
+            Pair d[4];   // minus what the code is off by
+            float worst = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                d[i] = fma2(v[i], minus_by, add2(f[i], minus_magic));
+                const float2 t = parts(d[i]);
+                worst = fmaxf(worst, fmaxf(fabsf(t.x), fabsf(t.y)));
+            }
+            if (worst > kNear) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 t = parts(d[i]), x = parts(v[i]);
+                    float2 c = parts(f[i]);
+                    if (fabsf(t.x) > kNear) c.x = kMagic + decide(x.x);
+                    if (fabsf(t.y) > kNear) c.y = kMagic + decide(x.y);
+                    f[i] = pair(c.x, c.y);
+                }
             }
         }
-        uint32_t w[8];
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(f[i]);
-        return make_uint2(prmt(prmt(w[0], w[1], 0x0040u), prmt(w[2], w[3], 0x0040u), 0x5410u),
-                          prmt(prmt(w[4], w[5], 0x0040u), prmt(w[6], w[7], 0x0040u), 0x5410u));
+        for (int i = 0; i < 4; ++i) {
+            const float2 t = parts(f[i]);
+            w[i] = prmt(__float_as_uint(t.x), __float_as_uint(t.y), 0x0040u);
+        }
+        return make_uint2(prmt(w[0], w[1], 0x5410u), prmt(w[2], w[3], 0x5410u));
     }
 };
 
