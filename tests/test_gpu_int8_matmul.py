@@ -119,6 +119,21 @@ def test_exact_sums(M):
     assert torch.equal(y.double(), a.double() @ b.double().T)
 
 
+@pytest.mark.parametrize("M,N", [(2, 264), (7, 264), (24, 264), (60, 20488), (128, 264), (200, 264), (300, 16392)])
+def test_largest_exact_sums(M, N):
+    """K = 1024 codes of full size: sums up to 2^24 are whole numbers still."""
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    sign = lambda *s: torch.randint(0, 2, s, device="cuda", generator=gen) * 2 - 1  # noqa: E731
+    one = lambda n: torch.ones(n, device="cuda")  # noqa: E731
+    a, b = (127 * sign(M, 1024)).to(torch.int8), (127 * sign(N, 1024)).to(torch.int8)
+    a[0], b[0] = 127, 127
+    a[1], b[1] = -128, -128
+    b[2, 1::2] = 126
+    y = w4.int8_matmul(a, one(M), b, one(N), out_dtype=torch.float32)
+    assert torch.equal(y.double(), a.double() @ b.double().T)
+    assert y[1, 1] == 2.0 ** 24
+
+
 @pytest.mark.parametrize("M", [1, 8, 40, 300])
 def test_special_scales(M):
     """NaN and infinite scales stay in their row and column; a scale of zero gives zeros."""

@@ -416,6 +416,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;
         fence_mbar_init();
+        fence_proxy_async_smem();   // this thread's copies complete on the barriers before any other synchronisation
         tma_prefetch_desc(&tw);
         tma_prefetch_desc(&tx);
         // the ring is filled before the other warps are ready
