@@ -21,7 +21,7 @@ using namespace rowwise;
 
 // A row per block, or (kWarps) per warp, blockDim.y rows to a block.
 template <int kAct, int kRes, int kPer, int kMaxThreads, bool kWarps>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, kPer == 4 && kRes != kF32 && !kWarps ? 2 : 0) block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
     __shared__ float scratch[3][32];
     const long long row = kWarps ? blockIdx.x * static_cast<long long>(blockDim.y) + threadIdx.y : blockIdx.x;
     if (kWarps && row >= a.T) return;
@@ -33,100 +33,114 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const __grid_co
     const uint8_t* h_row = bytes(a.h) + row * H * kBytes<kAct>;
     const uint8_t* r_row = bytes(a.residual) + row * H * kBytes<kRes>;
     uint8_t* out_row = static_cast<uint8_t*>(a.residual_out) + row * H * kBytes<kRes>;
+    // A thread past the row's end holds zeros, which change neither a sum nor the largest magnitude; it reads vectors that
+    // exist and stores nothing.
+    uint32_t at[kPer];
+    bool mine[kPer];
     Vec8<kRes> rv[kPer];
     Vec8<kAct> hv[kPer];
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
         const uint32_t c = p * blockDim.x + threadIdx.x;
+        mine[p] = c < vecs;
+        at[p] = min(c, vecs - 1u);
         rv[p].zero();
         hv[p].zero();
-        if (c < vecs) {
-            rv[p].load_stream(r_row + c * kResVec);
-            if (a.h) hv[p].load_stream(h_row + c * kActVec);
+        if (mine[p]) {
+            rv[p].load_stream(r_row + at[p] * kResVec);
+            if (a.h) hv[p].load_stream(h_row + at[p] * kActVec);
         }
     }
-    Pair f[4];
-    float norm_h = 1.f;
-    if (a.after) {
-        Pair sum = both(0.f);
+    Pair r[kPer][4];   // u, then r', then y
+    if (a.h) {
+        Pair by_gate = both(a.scale);
+        if (a.after) {
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int p = 0; p < kPer; ++p) sum = add_squares(hv[p], sum);
+            const Pair by_h = both(rsqrtf(block_sum<kWarps>(sum.x + sum.y, scratch[0]) * inv_h + a.eps));
+#pragma unroll
+            for (int p = 0; p < kPer; ++p) {
+                Vec8<kAct> w;
+                w.load_shared(bytes(a.after) + at[p] * kActVec);
+                products(hv[p], w, r[p]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[p][i] = mul2(r[p][i], by_h);
+            }
+        } else {
+#pragma unroll
+            for (int p = 0; p < kPer; ++p) hv[p].widen(r[p]);
+        }
+        if (a.gate) {
+            if (a.gate_kind == kGateToken) {
+                float g;
+                const uint16_t* p16 = static_cast<const uint16_t*>(a.gate) + row;
+                if constexpr (kAct == kF32) g = __ldg(static_cast<const float*>(a.gate) + row);
+                else if constexpr (kAct == kBf16) g = __uint_as_float(static_cast<uint32_t>(__ldg(p16)) << 16);
+                else g = __half2float(__ushort_as_half(__ldg(p16)));
+                by_gate = both(a.scale * g);
+            } else {
+                const uint8_t* gate_row = bytes(a.gate) + (a.gate_kind == kGateElement ? row * H * kBytes<kAct> : 0);
+#pragma unroll
+                for (int p = 0; p < kPer; ++p) {
+                    Vec8<kAct> g;
+                    Pair f[4];
+                    g.load_shared(gate_row + at[p] * kActVec);
+                    g.widen(f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[p][i] = mul2(r[p][i], f[i]);
+                }
+            }
+        }
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
-            hv[p].widen(f);
+            Pair f[4];
+            rv[p].widen(f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum = fma2(f[i], f[i], sum);
-        }
-        const float2 t = parts(sum);
-        norm_h = rsqrtf(block_sum<kWarps>(t.x + t.y, scratch[0]) * inv_h + a.eps);
-    }
-    Pair r[kPer][4], sum = both(0.f);
-    float row_gate = a.scale;
-    if (a.gate && a.gate_kind == kGateToken) {
-        const uint16_t* p16 = static_cast<const uint16_t*>(a.gate) + row;
-        if constexpr (kAct == kF32) row_gate *= __ldg(static_cast<const float*>(a.gate) + row);
-        else if constexpr (kAct == kBf16) row_gate *= __uint_as_float(static_cast<uint32_t>(__ldg(p16)) << 16);
-        else row_gate *= __half2float(__ushort_as_half(__ldg(p16)));
-    }
-    const Pair by_h = both(norm_h), by_gate = both(row_gate);
-    const bool vector_gate = a.gate && a.gate_kind != kGateToken;
-    const uint8_t* gate_row = bytes(a.gate) + (a.gate_kind == kGateElement ? row * H * kBytes<kAct> : 0);
-#pragma unroll
-    for (int p = 0; p < kPer; ++p) {
-        const uint32_t c = p * blockDim.x + threadIdx.x;
-        rv[p].widen(r[p]);
-        if (c < vecs && a.h) {
-            Pair u[4];
-            hv[p].widen(u);
-            if (a.after) {
-                Vec8<kAct> w;
-                w.load_shared(bytes(a.after) + c * kActVec);
-                w.widen(f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) u[i] = mul2(u[i], mul2(by_h, f[i]));
-            }
-            if (vector_gate) {
-                Vec8<kAct> g;
-                g.load_shared(gate_row + c * kActVec);
-                g.widen(f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) u[i] = mul2(u[i], f[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r[p][i] = fma2(by_gate, u[i], r[p][i]);
+            for (int i = 0; i < 4; ++i) r[p][i] = fma2(by_gate, r[p][i], f[i]);
             rv[p].round(r[p]);
-            rv[p].store(out_row + c * kResVec);
+            if (mine[p]) rv[p].store(out_row + at[p] * kResVec);
         }
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum = fma2(r[p][i], r[p][i], sum);
+        for (int p = 0; p < kPer; ++p) rv[p].widen(r[p]);
     }
     if (!a.weight) return;
+    Pair sum = both(0.f);
+#pragma unroll
+    for (int p = 0; p < kPer; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum = fma2(r[p][i], r[p][i], sum);
     const float2 t = parts(sum);
     const Pair by_r = both(rsqrtf(block_sum<kWarps>(t.x + t.y, scratch[1]) * inv_h + a.eps));
-    uint8_t* y_row = static_cast<uint8_t*>(a.y) + row * H * kBytes<kAct>;
-    uint32_t m = 0;
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-        const uint32_t c = p * blockDim.x + threadIdx.x;
-        if (c >= vecs) break;
         Vec8<kAct> w;
-        w.load_shared(bytes(a.weight) + c * kActVec);
+        Pair f[4];
+        w.load_shared(bytes(a.weight) + at[p] * kActVec);
         w.widen(f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) r[p][i] = mul2(r[p][i], mul2(by_r, f[i]));
-        if (a.codes) {
-            m = magnitude(r[p], m);
-        } else {
-            w.round(r[p]);
-            w.store(y_row + c * kActVec);
-        }
     }
-    if (!a.codes) return;
+    if (!a.codes) {
+        uint8_t* y_row = static_cast<uint8_t*>(a.y) + row * H * kBytes<kAct>;
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+            Vec8<kAct> w;
+            w.round(r[p]);
+            if (mine[p]) w.store(y_row + at[p] * kActVec);
+        }
+        return;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) m = magnitude(r[p], m);
     int8_t* codes_row = a.codes + row * H;
     const RowCodes<kF32> code(block_max<kWarps>(m, reinterpret_cast<uint32_t*>(scratch[2])));
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-        const uint32_t c = p * blockDim.x + threadIdx.x;
-        if (c >= vecs) break;
-        *reinterpret_cast<uint2*>(codes_row + 8u * c) = code(r[p]);
+        const uint2 c = code(r[p]);
+        if (mine[p]) *reinterpret_cast<uint2*>(codes_row + 8u * at[p]) = c;
     }
     if (threadIdx.x == 0) a.code_scales[row] = code.scale;
 }

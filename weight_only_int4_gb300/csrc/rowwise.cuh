@@ -107,6 +107,43 @@ struct Vec8 {
     }
 };
 
+// Sum of squares of eight values onto two sums, and the products of two vectors:
+// of 16-bit values without widening them first, each product exact.
+template <int kType>
+__device__ __forceinline__ float2 add_squares(const Vec8<kType>& x, float2 sum) {
+    if constexpr (kType == kF32) {
+        Pair f[4], s = pair(sum.x, sum.y);
+        x.widen(f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s = fma2(f[i], f[i], s);
+        return parts(s);
+    } else {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(x.v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sum.x = fma_mixed<kType == kBf16, 0, 0>(w[i], w[i], sum.x);
+            sum.y = fma_mixed<kType == kBf16, 1, 1>(w[i], w[i], sum.y);
+        }
+        return sum;
+    }
+}
+template <int kType>
+__device__ __forceinline__ void products(const Vec8<kType>& x, const Vec8<kType>& y, Pair (&f)[4]) {
+    if constexpr (kType == kF32) {
+        Pair g[4];
+        x.widen(f);
+        y.widen(g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], g[i]);
+    } else {
+        const uint32_t* a = reinterpret_cast<const uint32_t*>(x.v);
+        const uint32_t* b = reinterpret_cast<const uint32_t*>(y.v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = pair(fma_mixed<kType == kBf16, 0, 0>(a[i], b[i], 0.f), fma_mixed<kType == kBf16, 1, 1>(a[i], b[i], 0.f));
+    }
+}
+
 // Larger of a running magnitude and those of eight values, as FP32 bits; a NaN
 // stays one, so infinity and NaN end up above every finite value.
 __device__ __forceinline__ uint32_t magnitude(const Pair (&f)[4], uint32_t m) {
