@@ -1,8 +1,8 @@
 """The step between two blocks against 64-bit arithmetic.
 
 Tolerance. With e = 2^-24 per FP32 rounding: a sum of squares over a row is a
-chain of at most 16 fused additions per thread, 10 levels over threads, so it is
-off by at most 27 e, and its root by half of that; 1 / H, the mean, + eps add 3
+chain of at most 16 fused additions per thread, 11 more additions deep over
+threads, so it is off by at most 27 e, and its root by half of that; 1 / H, the mean, + eps add 3
 roundings (half of them after the root), rsqrtf 4 e (2 units in the last place).
 So a norm factor is off by at most 20 e, u by 23 e (three products), and r' by
 24 e |scale gate u| + 2 e |r'| before it is rounded to be stored. For y the

@@ -145,26 +145,23 @@ __device__ __forceinline__ void widen_half_row(uint32_t tile, int row, int half,
     tmem_st_32x32b_x32(taddr, o);
 }
 
-// 16 codes (chunk c of row r of a 128-byte-swizzled tile [rows x 128]) widened to the fp16 operand tile: two boxes of 64
-// columns, `box` bytes each, 128-byte swizzle. Lanes of either box begin with another of their two stores, so the eight
-// lanes of a row reach different banks.
-__device__ __forceinline__ void widen_chunk(uint32_t codes, uint32_t wide, uint32_t box, int r, int c) {
+// 16 codes of a 128-byte-swizzled tile [rows x 128] widened to the fp16 operand tile: two boxes of 64 columns, `box`
+// bytes each, 128-byte swizzle. Piece i of the tile's 8 per row: eight lanes take half a row each of two neighbours, so
+// that their stores reach different banks (their loads collide in pairs).
+__device__ __forceinline__ void widen_piece(uint32_t codes, uint32_t wide, uint32_t box, int i) {
+    const int c = i & 3, half = (i >> 3) & 1, r = ((i >> 4) << 1) | ((i >> 2) & 1);
     uint32_t w[4], o[8];
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(codes + r * 128 + ((c ^ (r & 7)) << 4)));
+                 : "r"(codes + r * 128 + (((4 * half + c) ^ (r & 7)) << 4)));
 #pragma unroll
     for (int j = 0; j < 4; ++j) widen4(w[j], o[2 * j], o[2 * j + 1]);
-    const uint32_t row = wide + (c >> 2) * box + r * 128;
-    const bool second = c >> 2;
+    const uint32_t row = wide + half * box + r * 128;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int h = second ? 1 - i : i;
-        const uint32_t at = row + (((2 * (c & 3) + h) ^ (r & 7)) << 4);
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(h ? o[4] : o[0]), "r"(h ? o[5] : o[1]),
-                     "r"(h ? o[6] : o[2]), "r"(h ? o[7] : o[3])
+    for (int h = 0; h < 2; ++h)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + (((2 * c + h) ^ (r & 7)) << 4)), "r"(o[4 * h]),
+                     "r"(o[4 * h + 1]), "r"(o[4 * h + 2]), "r"(o[4 * h + 3])
                      : "memory");
-    }
 }
 
 // MMAs (16 deep) of a K step.
@@ -210,7 +207,7 @@ __device__ __forceinline__ int dot16(uint4 a, uint4 b, int acc) {
 // ones leave few SMs idle; registers are left to the loads (one resident block
 // asked for: with the compiler's own choice 39.1 us instead of 34.6 at
 // 1 x 43008 x 5376, less in flight).
-// 1 x 43008 x 5376 34.5 us (6.7 TB/s), 4 rows 38.7; 1 x 2048 x 2048 1.9.
+// 1 x 43008 x 5376 34.5 us (6.7 TB/s), 4 rows 39.3; 1 x 2048 x 2048 1.9.
 constexpr int kWarps = 4;
 
 template <int kOut, int MT, int kRows, int kDeep>
@@ -423,6 +420,11 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
         for (int s = 0; s < min(S, u_end - u_begin); ++s) feed(s);
     }
     if (warp == 2) tmem_alloc(smem_u32(&bars->tmem_base), kTmemCols);
+    if (warp == 3) {   // the first tile's scales, on their way until the epilogue asks for them
+        const int m = t_begin % num_m * MP + 32 * lane, n = t_begin / num_m * BN + 32 * lane;
+        if (32 * lane < MP && m < M) asm volatile("prefetch.global.L1 [%0];" ::"l"(sa + m));
+        if (32 * lane < BN && n < N) asm volatile("prefetch.global.L1 [%0];" ::"l"(sb + n));
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -506,8 +508,8 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
             widen_half_row(st_w(s), row, 1, op + as * kOpCols + 32);
             if constexpr (C::kInline) {
 #pragma unroll
-                for (int c = in_group * 32 + lane; c < MP * 8; c += kGroupWarps * 32)
-                    widen_chunk(st_x(s), st_wide(as), C::kBox, c >> 3, c & 7);
+                for (int i = in_group * 32 + lane; i < MP * 8; i += kGroupWarps * 32)
+                    widen_piece(st_x(s), st_wide(as), C::kBox, i);
                 fence_proxy_async_smem();   // the MMAs read these stores
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars->empty[s]));   // every lane's loads have returned
@@ -663,9 +665,18 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
 //   warps 4..11  both: epilogue, two warps per lane quarter, 128 columns each
 //   warp 2       tensor memory
 //
+// What the odd CTA's widening warps publish lies in tensor memory alone: they wait
+// for their stores, fence (tcgen05.fence::before_thread_sync) and arrive on the even
+// CTA's barrier relaxed, which costs them nothing; the MMA thread waits relaxed and
+// fences after. Rows of a are published by the copies themselves.
+//
 // Tensor memory: one accumulator of 256 columns and four operand stages of 64.
 // The epilogue takes the accumulator into registers, scaled and rounded to 16
-// bits, and lets the next tile's MMAs start before it stores.
+// bits, and lets the next tile's MMAs start before it stores (FP32 results are
+// stored first: twice the registers).
+//
+// 2048 x 43008 x 5376 463 us, 2.04 PFLOP/s: at the rate of the fp16 MMAs (a
+// K step's eight take about 0.6 us, its 48 KB of loads 0.58 at 82 KB a us and SM).
 namespace pair {
 
 constexpr int BM = 256, BN = 256, CM = 128, CN = 128;
@@ -975,7 +986,8 @@ struct Plan {
     bool widen;   // rows of a widened by a kernel before
 };
 // Measured on 152 SMs (us a call):
-//   rows / tiles kernel: 4 x 43008 x 5376 38.7 / 44.9, 8 x 8192 x 8192 19.2 / 18.8, 8 x 2048 x 2048 3.1 / 6.5;
+//   rows / tiles kernel: 4 x 43008 x 5376 39.3 / 44.3, 6 x 8192 x 8192 18.0 / 19.0, 6 x 43008 x 5376 45.5 / 44.5, 8 x
+//     8192 x 4096 12.0 / 12.4, 8 x 8192 x 8192 19.9 / 19.0, 16 x 2048 x 2048 3.9 / 6.7, 16 x 4096 x 4096 11.0 / 9.7;
 //   tiles / pair kernel: 512 x 4096 x 4096 (128 tiles) 24.2 / 26.9, 300 x 2600 x 2080 (63) 15.2 / 17.3, 256 x 16384 x
 //     5376 (256) 53.8 / 33.3, 2048 x 2048 x 2048 (256) 29.9 / 20.0: pairs where 128-row tiles need a second wave;
 //   whole tiles / shared units: 16 x 20480 x 5376 (160 tiles) 38.3 / 25.9, 30720 columns (240) 38.6 / 35.3, 36864
@@ -985,7 +997,9 @@ struct Plan {
 //     x 1024 7.1 / 6.4 (4: 6 steps saved), 64 x 8192 x 2048 12.3 / 12.2 (2: 8 saved), 16 x 2048 x 512 5.6 / 6.3 (2: 2
 //     saved): from 6 saved steps on.
 Plan plan(long long M, long long N, long long K, int sms) {
-    if (M <= 4 || (M <= 6 && N * K <= 1ll << 27) || (M <= 8 && N * K <= 1ll << 26)) return {-1, false, false, false};
+    const long long weights = N * K;
+    if (M <= 4 || (M <= 6 && weights <= 1ll << 26) || (M <= 8 && weights <= 1ll << 25) || (M <= 16 && weights <= 1ll << 23))
+        return {-1, false, false, false};
     const long long cols = (N + tiles::BN - 1) / tiles::BN;
     if (M > 128 && ((M + 127) / 128) * cols > sms) return {0, false, false, true};
     const int mp = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;

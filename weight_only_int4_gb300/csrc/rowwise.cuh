@@ -198,7 +198,7 @@ inline Layout layout_of(long long vecs, int most) {
 }
 
 // Sum / maximum over the threads of a row (the block, or with kWarps a warp), the
-// same in every thread, the sum in a fixed order. `scratch`: 32 words that no other
+// same in every thread, the sum in a fixed order. `scratch`: 32 words, 16-byte aligned, that no other
 // reduction of the row uses. Every thread calls it.
 template <bool kWarps>
 __device__ __forceinline__ float block_sum(float v, float* scratch) {
@@ -207,11 +207,16 @@ __device__ __forceinline__ float block_sum(float v, float* scratch) {
     if (kWarps) return v;
     const int warps = blockDim.x >> 5;
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    if (threadIdx.x < 32 && threadIdx.x >= warps) scratch[threadIdx.x] = 0.f;
     __syncthreads();
-    v = scratch[0];
+    const float4* four = reinterpret_cast<const float4*>(scratch);
+    float4 s = four[0];
 #pragma unroll 4
-    for (int w = 1; w < warps; ++w) v += scratch[w];
-    return v;
+    for (int w = 4; w < warps; w += 4) {
+        const float4 t = four[w >> 2];
+        s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
+    }
+    return (s.x + s.y) + (s.z + s.w);
 }
 template <bool kWarps>
 __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* scratch) {
