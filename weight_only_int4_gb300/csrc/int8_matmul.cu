@@ -88,15 +88,18 @@ __device__ __forceinline__ bool uniform_wait_bar(uint32_t bar, uint32_t parity, 
     return __all_sync(0xffffffffu, ok);
 }
 
-// Several warps go on together once their first thread has seen up to two
-// phases complete: named barrier `id` spreads its verdict and orders the others'
-// accesses after its acquires. One thread polls, not one per warp: polls take
-// issue slots and shared-memory cycles from the warps at work (128-row tiles, 16
-// rows of a, steps of K measured at 0.47 us with 24 warps polling, 0.38 us so).
-__device__ __forceinline__ bool group_wait(int id, int threads, bool first, uint32_t bar0, uint32_t parity0,
-                                           uint32_t bar1, uint32_t parity1, const Abort& ab) {
+// Several warps go on together once their first thread has seen up to three
+// phases complete, in this order: named barrier `id` spreads its verdict and orders
+// the others' accesses after its acquires. One thread polls, not one per warp: polls
+// take issue slots and shared-memory cycles from the warps at work (128-row tiles, 16
+// rows of a, steps of K measured at 0.47 us with 24 warps polling, 0.39 us so).
+__device__ __forceinline__ bool group_wait(int id, int threads, bool first, const Abort& ab, uint32_t bar0,
+                                           uint32_t parity0, uint32_t bar1 = 0u, uint32_t parity1 = 0u,
+                                           uint32_t bar2 = 0u, uint32_t parity2 = 0u) {
     int ok = 1;
-    if (first) ok = wait_bar(bar0, parity0, ab) && (bar1 == 0u || wait_bar(bar1, parity1, ab));
+    if (first)
+        ok = wait_bar(bar0, parity0, ab) && (bar1 == 0u || wait_bar(bar1, parity1, ab)) &&
+             (bar2 == 0u || wait_bar(bar2, parity2, ab));
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %0, 0;\n\t"
         "barrier.cta.red.and.pred q, %1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
@@ -273,9 +276,10 @@ cudaError_t launch(const Int8MatmulArgs& a, cudaStream_t s) {
 // 128 rows of b against 16..128 rows of a
 // ---------------------------------------------------------------------------
 // Warp roles, one CTA per SM:
-//   warp 0       producer: per K step TMA brings the tile's codes [128 x 128]
-//                and MP rows of a, as codes (up to 64 rows) or widened before
-//                (128 rows: in two 64-column boxes), all with the 128-byte swizzle
+//   warps 0, 3   producers: per K step TMA brings the tile's codes [128 x 128]
+//                and MP rows of a, as codes (up to 64 rows, beside them) or
+//                widened before (128 rows: in two 64-column boxes, warp 3), all with
+//                the 128-byte swizzle
 //   warps 12..27 four groups, steps in turn, widen the codes of b into an operand
 //                stage of tensor memory (thread = row of b = lane) and those of a
 //                into an operand tile in shared memory
@@ -305,27 +309,30 @@ struct Cfg {
     // Up to 64 rows of a are widened here, by every CTA for itself: no kernel before this one, and half the bytes from
     // L2. With 128 rows shared memory would have to carry more than the step's loads leave it time for.
     static constexpr bool kInline = MP <= 64;
+    // Rows of a that are widened here share the stages of b's codes; those that came widened have stages of their own that go
+    // by the operand's and are refilled from L2.
+    static constexpr int kStages = MP == 16 ? 11 : MP == 32 ? 9 : 6;
+    static constexpr int kOpStages = 4, kXStages = kInline ? kStages : kOpStages;
     static constexpr uint32_t kWBytes = BN * kStepK;
     static constexpr uint32_t kXBytes = MP * kStepK * (kInline ? 1 : 2);   // rows of a as they are loaded
-    static constexpr uint32_t kStageBytes = kWBytes + kXBytes;
-    static constexpr int kStages = MP <= 32 ? 8 : MP == 64 ? 6 : 4;
+    static constexpr uint32_t kWideBytes = MP * kStepK * 2, kBox = kWideBytes / 2;
+    static constexpr uint32_t kXAt = kStages * kWBytes, kWideAt = kXAt + kXStages * kXBytes;
+    static constexpr uint32_t kRingBytes = kWideAt + (kInline ? kOpStages * kWideBytes : 0);
     static constexpr uint32_t kAccCols = MP < 32 ? 32 : MP;   // the epilogue reads up to 32 columns at a time
     static constexpr uint32_t kOpCol0 = 2 * kAccCols;
-    static constexpr int kOpStages = 4;
-    static constexpr uint32_t kWideBytes = MP * kStepK * 2, kBox = kWideBytes / 2;
-    static constexpr uint32_t kRingBytes = kStages * kStageBytes + (kInline ? kOpStages * kWideBytes : 0);
     static_assert(kOpCol0 + kOpStages * kOpCols <= kTmemCols, "tensor memory budget");
-    // A group takes loads from stages that other groups used in between. It waits for its operand stage first: then the
-    // MMAs of kOpStages steps before have retired, every step up to there had been widened, and the phase of the load
+    // A group takes codes from stages that other groups used in between. It waits for its operand stage first: then the
+    // MMAs of kOpStages steps before have retired, every step up to there had been widened, and the phase of the code
     // stage that it skipped is complete.
     static_assert(kStages >= kOpStages && kOpStages % kGroups == 0, "no group waits past an open phase");
-    static_assert(kStageBytes % 1024 == 0 && kWideBytes % 1024 == 0, "operand tiles stay 1024-byte aligned");
+    static_assert(kXBytes % 1024 == 0 && kWideBytes % 1024 == 0, "operand tiles stay 1024-byte aligned");
 };
 
 template <int MP>
 struct __align__(8) Barriers {
-    uint64_t full[Cfg<MP>::kStages];        // codes and rows of a landed
-    uint64_t empty[Cfg<MP>::kStages];       // widened; rows of a that came widened: the MMAs that read them retired
+    uint64_t full[Cfg<MP>::kStages];        // codes landed (kInline: of both)
+    uint64_t empty[Cfg<MP>::kStages];       // widened
+    uint64_t xfull[Cfg<MP>::kOpStages];     // rows of a that came widened landed; free with the operand stage
     uint64_t afull[Cfg<MP>::kOpStages];     // operand stage written
     uint64_t aempty[Cfg<MP>::kOpStages];    // MMAs that read it retired
     uint64_t tfull[2];
@@ -357,9 +364,9 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Barriers<MP>* bars = reinterpret_cast<Barriers<MP>*>(smem + C::kRingBytes);
     const uint32_t base = smem_u32(smem);
-    auto st_w = [&](int s) { return base + s * C::kStageBytes; };
-    auto st_x = [&](int s) { return base + s * C::kStageBytes + C::kWBytes; };
-    auto st_wide = [&](int s) { return base + S * C::kStageBytes + s * C::kWideBytes; };   // kInline
+    auto st_w = [&](int s) { return base + s * C::kWBytes; };
+    auto st_x = [&](int s) { return base + C::kXAt + s * C::kXBytes; };
+    auto st_wide = [&](int s) { return base + C::kWideAt + s * C::kWideBytes; };   // kInline
 
     // split > 1: this CTA's part, [row of a][128], once the ring is idle
     float* parts = reinterpret_cast<float*>(smem);
@@ -381,28 +388,40 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
         u_begin = (b * work.each + min(b, work.more)) * scale;
         u_end = u_begin + (work.each + (b < work.more ? 1 : 0)) * scale;
     }
-    const int t_begin = u_begin / kt_total, k_begin = u_begin - t_begin * kt_total;
+    const int t_begin = u_begin / kt_total, k_begin = u_begin - t_begin * kt_total, steps = u_end - u_begin;
     const Abort ab{&bars->abort, 0u, ~0u};
 
-    // the producer's place, and one step's copies
-    int fed = 0, at_k = k_begin, at_t = t_begin;
+    // A producer's place, kept from step to step: its divisions would be on the way of every refill.
+    int at_k = k_begin, at_t = t_begin, at_m = t_begin % num_m * MP, at_n = t_begin / num_m * BN;
+    auto advance = [&]() {
+        if (++at_k < kt_total) return;
+        at_k = 0;
+        ++at_t;
+        at_m = at_t % num_m * MP;
+        at_n = at_t / num_m * BN;
+    };
     auto feed = [&](int s) {
         const uint32_t fb = smem_u32(&bars->full[s]);
-        const int m0 = at_t % num_m * MP;
-        mbar_arrive_expect_tx(fb, C::kStageBytes);
-        tma_load_2d(st_w(s), &tw, at_k * kStepK, at_t / num_m * BN, fb);
-        tma_load_2d(st_x(s), &tx, at_k * kStepK, m0, fb);
-        if (!C::kInline) tma_load_2d(st_x(s) + C::kBox, &tx, at_k * kStepK + 64, m0, fb);
-        ++fed;
-        if (++at_k == kt_total) at_k = 0, ++at_t;
+        mbar_arrive_expect_tx(fb, C::kWBytes + (C::kInline ? C::kXBytes : 0u));
+        tma_load_2d(st_w(s), &tw, at_k * kStepK, at_n, fb);
+        if (C::kInline) tma_load_2d(st_x(s), &tx, at_k * kStepK, at_m, fb);
+        advance();
+    };
+    auto feed_wide = [&](int s) {
+        const uint32_t fb = smem_u32(&bars->xfull[s]);
+        mbar_arrive_expect_tx(fb, C::kXBytes);
+        tma_load_2d(st_x(s), &tx, at_k * kStepK, at_m, fb);
+        tma_load_2d(st_x(s) + C::kBox, &tx, at_k * kStepK + 64, at_m, fb);
+        advance();
     };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(smem_u32(&bars->full[s]), 1);
-            mbar_init(smem_u32(&bars->empty[s]), C::kInline ? kGroupWarps : 1);
+            mbar_init(smem_u32(&bars->empty[s]), kGroupWarps);
         }
         for (int s = 0; s < A; ++s) {
+            mbar_init(smem_u32(&bars->xfull[s]), 1);
             mbar_init(smem_u32(&bars->afull[s]), kGroupWarps);
             mbar_init(smem_u32(&bars->aempty[s]), 1);
         }
@@ -414,43 +433,38 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
         bars->abort = 0;
         fence_mbar_init();
         fence_proxy_async_smem();   // this thread's copies complete on the barriers before any other synchronisation
-        tma_prefetch_desc(&tw);
-        tma_prefetch_desc(&tx);
-        // the ring is filled before the other warps are ready
-        for (int s = 0; s < min(S, u_end - u_begin); ++s) feed(s);
+        // the rings are filled before the other warps are ready
+        for (int s = 0; s < min(S, steps); ++s) feed(s);
     }
     if (warp == 2) tmem_alloc(smem_u32(&bars->tmem_base), kTmemCols);
-    if (warp == 3) {   // the first tile's scales, on their way until the epilogue asks for them
-        const int m = t_begin % num_m * MP + 32 * lane, n = t_begin / num_m * BN + 32 * lane;
-        if (32 * lane < MP && m < M) asm volatile("prefetch.global.L1 [%0];" ::"l"(sa + m));
-        if (32 * lane < BN && n < N) asm volatile("prefetch.global.L1 [%0];" ::"l"(sb + n));
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ producer
+    if (warp == 0 || (!C::kInline && warp == 3)) {
+        // ------------------------------------------------------------ producers: codes (warp 0), widened rows (warp 3)
         if (lane == 0) {
-            uint32_t parity = 0;
-            int s = 0;
-            for (int i = S; i < u_end - u_begin; ++i) {
-                if (!wait_bar(smem_u32(&bars->empty[s]), parity, ab)) break;
-                feed(s);
-                if (++s == S) s = 0, parity ^= 1u;
+            const bool wide = warp == 3;
+            const int ring = wide ? A : S;
+            const uint32_t free = smem_u32(wide ? &bars->aempty[0] : &bars->empty[0]);
+            uint32_t parity = wide ? 1u : 0u;
+            int s = 0, i = wide ? 0 : S;   // codes: the ring has been filled
+            for (; i < steps; ++i) {
+                if (!wait_bar(free + 8 * s, parity, ab)) break;
+                if (wide) feed_wide(s);
+                else feed(s);
+                if (++s == ring) s = 0, parity ^= 1u;
             }
-            drain_ring(bars->full, S, fed);
-            if (!C::kInline) drain_ring(bars->empty, S, fed);
+            drain_ring(wide ? bars->xfull : bars->full, ring, min(i, steps));
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t kIdesc = umma_idesc_f16(BN, MP, false);
         const bool leader = elect_one();
         const uint64_t desc_x = sw128_kmajor_desc(C::kInline ? st_wide(0) : st_x(0));
-        const uint32_t bar_empty = smem_u32(&bars->empty[0]), bar_afull = smem_u32(&bars->afull[0]),
-                       bar_aempty = smem_u32(&bars->aempty[0]);
-        int s = 0, as = 0, seg = 0;
+        const uint32_t bar_afull = smem_u32(&bars->afull[0]), bar_aempty = smem_u32(&bars->aempty[0]);
+        int as = 0, seg = 0;
         uint32_t aparity = 0;
         bool ok = true;
         for (int u = u_begin, k0 = k_begin; u < u_end && ok; ++seg, k0 = 0) {
@@ -465,8 +479,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
                 // the group that wrote the stage had waited for the step's rows of a too
                 if (!uniform_wait_bar(bar_afull + 8 * as, aparity, ab, leader)) { ok = false; break; }
                 tc_fence_after();
-                const uint64_t x = desc_x + (C::kInline ? static_cast<uint64_t>(as) * (C::kWideBytes >> 4)
-                                                        : static_cast<uint64_t>(s) * (C::kStageBytes >> 4));
+                const uint64_t x = desc_x + static_cast<uint64_t>(as) * (C::kWideBytes >> 4);
                 const uint32_t a = tmem + C::kOpCol0 + as * kOpCols;
                 const int nk = step_mmas(K, kt);
                 if (leader) {
@@ -475,11 +488,9 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
                         if (kk < nk)
                             umma_f16_ta(d, a + 8 * kk, x + (kk >> 2) * (C::kBox >> 4) + 2 * (kk & 3), kIdesc,
                                         kt != k0 || kk);
-                    if (!C::kInline) umma_commit(bar_empty + 8 * s);
                     umma_commit(bar_aempty + 8 * as);
                 }
                 __syncwarp();
-                if (++s == S) s = 0;
                 if (++as == A) as = 0, aparity ^= 1u;
             }
             if (!ok) break;
@@ -496,12 +507,13 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
         const int group = (warp - kWidenWarp0) / kGroupWarps, in_group = (warp - kWidenWarp0) % kGroupWarps;
         const int row = (warp & 3) * 32 + lane;
         const uint32_t op = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kOpCol0;
-        const int steps = u_end - u_begin;
+        const uint32_t bar_free = smem_u32(&bars->aempty[0]), bar_full = smem_u32(&bars->full[0]),
+                       bar_x = smem_u32(&bars->xfull[0]);
         int s = group, as = group;
-        uint32_t parity = 0, aparity = 1u;
+        uint32_t parity = 0, aparity = 0;
         for (int j = group; j < steps; j += kGroups) {
-            if (!group_wait(1 + group, kGroupWarps * 32, in_group == 0 && lane == 0, smem_u32(&bars->aempty[as]), aparity,
-                            smem_u32(&bars->full[s]), parity, ab))
+            if (!group_wait(1 + group, kGroupWarps * 32, in_group == 0 && lane == 0, ab, bar_free + 8 * as, aparity ^ 1u,
+                            bar_full + 8 * s, parity, C::kInline ? 0u : bar_x + 8 * as, aparity))
                 break;
             tc_fence_after();
             widen_half_row(st_w(s), row, 0, op + as * kOpCols);
@@ -511,9 +523,9 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
                 for (int i = in_group * 32 + lane; i < MP * 8; i += kGroupWarps * 32)
                     widen_piece(st_x(s), st_wide(as), C::kBox, i);
                 fence_proxy_async_smem();   // the MMAs read these stores
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->empty[s]));   // every lane's loads have returned
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->empty[s]));   // every lane's loads have returned
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -534,8 +546,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
             const int m0 = t % num_m * MP, mc = min(MP, M - m0);
             const int n = t / num_m * BN + q * 32 + lane;
             const float tn = n < N ? __ldg(sb + n) : 0.f;
-            if (!group_wait(8, kEpiWarps * 32, threadIdx.x == kEpiWarp0 * 32, smem_u32(&bars->tfull[acc]), (seg >> 1) & 1, 0u,
-                            0u, ab))
+            if (!group_wait(8, kEpiWarps * 32, threadIdx.x == kEpiWarp0 * 32, ab, smem_u32(&bars->tfull[acc]), (seg >> 1) & 1))
                 break;
             tc_fence_after();
             const bool whole = k0 == 0 && k1 == kt_total;
@@ -872,8 +883,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
         int s = group, ws = group;
         uint32_t parity = 1u, wparity = 0;
         for (long long j = group; j < steps; j += kGroups) {
-            if (!group_wait(1 + group, kGroupWarps * 32, in_group == 0 && lane == 0, smem_u32(&bars->empty[s]), parity,
-                            smem_u32(&bars->wfull[ws]), wparity, ab))
+            if (!group_wait(1 + group, kGroupWarps * 32, in_group == 0 && lane == 0, ab, smem_u32(&bars->empty[s]), parity,
+                            smem_u32(&bars->wfull[ws]), wparity))
                 break;
             tc_fence_after();
             widen_half_row(st_w(ws), row, 0, op + s * kOpCols);
@@ -902,7 +913,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
 #pragma unroll
             for (int i = 0; i < 4; ++i) mine[32 * i + lane] = 32 * i + lane < mc ? __ldg(sa + m0 + 32 * i + lane) : 0.f;
             __syncwarp();
-            if (!group_wait(8, kEpiWarps * 32, threadIdx.x == kEpiWarp0 * 32, smem_u32(&bars->tfull), it & 1, 0u, 0u, ab)) break;
+            if (!group_wait(8, kEpiWarps * 32, threadIdx.x == kEpiWarp0 * 32, ab, smem_u32(&bars->tfull), it & 1)) break;
             tc_fence_after();
             if constexpr (kOut == kF32) {
 #pragma unroll 1
