@@ -997,20 +997,19 @@ struct Plan {
     bool widen;   // rows of a widened by a kernel before
 };
 // Measured on 152 SMs (us a call):
-//   rows / tiles kernel: 4 x 43008 x 5376 39.3 / 44.3, 6 x 8192 x 8192 18.0 / 19.0, 6 x 43008 x 5376 45.5 / 44.5, 8 x
-//     8192 x 4096 12.0 / 12.4, 8 x 8192 x 8192 19.9 / 19.0, 16 x 2048 x 2048 3.9 / 6.7, 16 x 4096 x 4096 11.0 / 9.7;
-//   tiles / pair kernel: 512 x 4096 x 4096 (128 tiles) 24.2 / 26.9, 300 x 2600 x 2080 (63) 15.2 / 17.3, 256 x 16384 x
-//     5376 (256) 53.8 / 33.3, 2048 x 2048 x 2048 (256) 29.9 / 20.0: pairs where 128-row tiles need a second wave;
-//   whole tiles / shared units: 16 x 20480 x 5376 (160 tiles) 38.3 / 25.9, 30720 columns (240) 38.6 / 35.3, 36864
-//     (288) 39.2 / 41.4, 43008 (336) 56.1 / 46.4; 64 rows 43.8 / 31.9, 44.0 / 42.8, 44.5 / 49.1, 63.1 / 55.0: shared
+//   rows / tiles kernel: 4 x 43008 x 5376 39.3 / 42.5, 8 x 8192 x 4096 12.0 / 12.2, 5 x 8192 x 8192 17.9 / 17.5, 8 x
+//     43008 x 5376 63.9 / 43.4, 16 x 4096 x 2048 7.4 / 7.6, 16 x 4096 x 4096 11.0 / 9.7;
+//   tiles / pair kernel: 512 x 4096 x 4096 (128 tiles) 21.0 / 26.1, 300 x 2600 x 2080 (63) 14.7 / 17.2, 600 x 4096 x
+//     4096 (160) 29.0 / 27.1, 256 x 16384 x 5376 (256) 43.9 / 33.1: pairs where 128-row tiles need a second wave;
+//   whole tiles / shared units: 16 x 20480 x 5376 (160 tiles) 33.9 / 24.9, 30720 columns (240) 35.0 / 33.8, 36864
+//     (288) 35.8 / 39.5, 43008 (336) 50.4 / 44.6; 64 rows 40.0 / 31.1, 41.0 / 41.1, 41.7 / 47.4, 58.1 / 52.5: shared
 //     where the last wave leaves a fifth of all SM time idle;
-//   whole tiles / a cluster per tile: 16 x 8192 x 5376 20.5 / 14.5 (2 CTAs), 3 x 4096 x 4096 17.5 / 9.0 (4), 16 x 4096
-//     x 1024 7.1 / 6.4 (4: 6 steps saved), 64 x 8192 x 2048 12.3 / 12.2 (2: 8 saved), 16 x 2048 x 512 5.6 / 6.3 (2: 2
+//   whole tiles / a cluster per tile: 16 x 8192 x 5376 17.9 / 13.5 (2 CTAs), 64 x 4096 x 4096 17.7 / 11.3 (4), 16 x 4096
+//     x 1024 7.2 / 6.4 (4: 6 steps saved), 128 x 8192 x 2048 15.2 / 15.7 (2: 8 saved), 16 x 2048 x 512 5.7 / 6.3 (2: 2
 //     saved): from 6 saved steps on.
 Plan plan(long long M, long long N, long long K, int sms) {
     const long long weights = N * K;
-    if (M <= 4 || (M <= 6 && weights <= 1ll << 26) || (M <= 8 && weights <= 1ll << 25) || (M <= 16 && weights <= 1ll << 23))
-        return {-1, false, false, false};
+    if (M <= 4 || (M <= 8 && weights <= 1ll << 25) || (M <= 16 && weights <= 1ll << 23)) return {-1, false, false, false};
     const long long cols = (N + tiles::BN - 1) / tiles::BN;
     if (M > 128 && ((M + 127) / 128) * cols > sms) return {0, false, false, true};
     const int mp = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
@@ -1112,8 +1111,8 @@ cudaError_t launch_tiles(const Int8MatmulArgs& a, const Plan& pl, const __half* 
     if (units >= 1ll << 31) return cudaErrorInvalidValue;   // 35 TB of codes
     int split = 1;
     if (pl.split) {
-        // the largest cluster, up to 6 CTAs, of which all fit at once (50 tiles: clusters of 3 do not, 25.8 us
-        // instead of 17.6 with 2)
+        // the largest cluster, up to 6 CTAs, of which all fit at once (50 tiles at 64 x 6400 x 5376: clusters of 3
+        // do not, 25.8 us instead of 17.6 with 2, on an earlier kernel)
         split = static_cast<int>(std::min<long long>({6, dp.sms / tiles, steps / 2}));
         while (split > 1 && tiles > resident_clusters<kOut, MP>(dp, split)) --split;
         if (split > 1 && steps - steps / split < 6) split = 1;
