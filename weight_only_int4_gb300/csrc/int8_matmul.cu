@@ -295,6 +295,11 @@ cudaError_t launch(const Int8MatmulArgs& a, cudaStream_t s) {
 //     tile. A tile that lies in two CTAs' ranges is finished by the later of them,
 //     which adds the two FP32 parts from global memory, the lower CTA's first.
 // All three are deterministic.
+//
+// 64 x 16384 x 5376 23.0 us, 16 x 43008 x 5376 44.6, 128 x 43008 x 5376 60.8, 512 x
+// 4096 x 4096 21.0. A step takes 0.39 us with 16 rows and 0.40 with 64 (HBM: 0.37
+// for 152 CTAs), 0.48 with 128 (48 KB a step into the SM); launch to first load, the
+// last epilogue and joins take 5 to 8 us.
 namespace tiles {
 
 constexpr int BN = 128;
