@@ -89,6 +89,14 @@ def test_plans(M, N, K, dtype):
     run(M, N, K, dtype)
 
 
+# A whole wave of pairs and the other columns on 128-row tiles: both write rows of the same y.
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [(300, 10248, 2064), (436, 10680, 4112), (900, 9224, 2064), (1030, 5128, 4112),
+                                   (513, 8200, 8208)])
+def test_waves_and_the_rest(M, N, K, dtype):
+    run(M, N, K, dtype)
+
+
 def test_chunks_of_many_rows():
     """More rows than are widened at a time, in both kernels that take widened rows."""
     run(8200, 1032, 144, torch.bfloat16)

@@ -510,7 +510,7 @@ w4a16_status w4a16_int8_matmul(const int8_t* a, const float* a_scale, const int8
     DeviceProps dp;
     if ((st = device_gate(&dp)) != W4A16_OK) return st;
     if ((workspace ? workspace_bytes : 0) < w4a16::int8_matmul_workspace_bytes(M, N, K, dp)) return W4A16_ERR_WORKSPACE;
-    const w4a16::Int8MatmulArgs args{a, a_scale, b, b_scale, y, (int)M, (int)N, (int)K};
+    const w4a16::Int8MatmulArgs args{a, a_scale, b, b_scale, y, (int)M, (int)N, (int)K, (int)N};
     return from_cuda(w4a16::launch_int8_matmul(args, static_cast<int>(dt), workspace, dp,
                                                reinterpret_cast<cudaStream_t>(stream)));
 }

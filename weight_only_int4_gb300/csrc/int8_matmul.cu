@@ -362,7 +362,7 @@ template <int kOut, int MP>
 __global__ void __launch_bounds__(kThreads, 1)
 tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
              const float* __restrict__ sa, const float* __restrict__ sb, void* __restrict__ y, int M, int N, int K,
-             const Work work, float* __restrict__ partials, uint32_t* __restrict__ tickets) {
+             int ld, const Work work, float* __restrict__ partials, uint32_t* __restrict__ tickets) {
     using C = Cfg<MP>;
     constexpr int S = C::kStages, A = C::kOpStages;
     extern __shared__ uint8_t smem_raw[];
@@ -574,7 +574,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
 #pragma unroll
                         for (int i = 0; i < kCols; ++i)
                             if (c + i < mc)
-                                store1<kOut>(y, static_cast<size_t>(m0 + c + i) * N + n,
+                                store1<kOut>(y, static_cast<size_t>(m0 + c + i) * ld + n,
                                              __uint_as_float(r[i]) * __ldg(sa + m0 + c + i) * tn);
                     }
                 } else {
@@ -604,7 +604,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
 #pragma unroll
             for (int c = 0; c < kMaxSplit; ++c)
                 if (c < split) sum += v[c];
-            if (n < N) store1<kOut>(y, static_cast<size_t>(m0 + m) * N + n, sum * __ldg(sa + m0 + m) * tn);
+            if (n < N) store1<kOut>(y, static_cast<size_t>(m0 + m) * ld + n, sum * __ldg(sa + m0 + m) * tn);
         }
         cluster_sync();   // no CTA leaves while another may read its part
     } else {
@@ -657,7 +657,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             const int m = c + j * kRowsAtOnce;
-            if (m < mc) store1<kOut>(y, static_cast<size_t>(m0 + m) * N + n, (p[j] + v[j]) * __ldg(sa + m0 + m) * tn);
+            if (m < mc) store1<kOut>(y, static_cast<size_t>(m0 + m) * ld + n, (p[j] + v[j]) * __ldg(sa + m0 + m) * tn);
         }
     }
 }
@@ -754,7 +754,8 @@ __device__ __forceinline__ void store_two_rows(uint16_t*& dst, long long pitch, 
 template <int kOut>
 __global__ void __launch_bounds__(kThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
-            const float* __restrict__ sa, const float* __restrict__ sb, void* __restrict__ y, int M, int N, int K) {
+            const float* __restrict__ sa, const float* __restrict__ sb, void* __restrict__ y, int M, int N, int K,
+            int ld) {
     extern __shared__ uint8_t smem_raw[];
     // the same layout in both CTAs: the MMA addresses the peer's rows of a at this CTA's offsets
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -930,7 +931,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (ch * 32 + i < mc)
-                                store1<kOut>(y, static_cast<size_t>(m0 + ch * 32 + i) * N + n,
+                                store1<kOut>(y, static_cast<size_t>(m0 + ch * 32 + i) * ld + n,
                                              __uint_as_float(r[i]) * mine[ch * 32 + i] * tn);
                     }
                 }
@@ -962,8 +963,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
                 if (lane == 0) mbar_arrive_cluster_relaxed(smem_u32(&bars->tempty), 0);
                 // no branch around the stores: the roundings above would be put off into it, and the raw sums, twice the
                 // registers, kept until then
-                uint16_t* dst = static_cast<uint16_t*>(y) + static_cast<size_t>(m0) * N + n;
-                const long long pitch = 2ll * N;
+                uint16_t* dst = static_cast<uint16_t*>(y) + static_cast<size_t>(m0) * ld + n;
+                const long long pitch = 2ll * ld;
                 const int left = n < N ? mc : 0;
 #pragma unroll
                 for (int i = 0; i < 64; ++i) store_two_rows(dst, pitch, o[i], left - 2 * i);
@@ -1095,7 +1096,7 @@ cudaError_t launch_pair(const Int8MatmulArgs& a, const __half* wide, const Devic
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tw, tx, a.sa, a.sb, a.y, a.M, a.N, a.K);
+    return cudaLaunchKernelEx(&cfg, kern, tw, tx, a.sa, a.sb, a.y, a.M, a.N, a.K, a.ld);
 }
 
 template <int kOut, int MP>
@@ -1139,7 +1140,43 @@ cudaError_t launch_tiles(const Int8MatmulArgs& a, const Plan& pl, const __half* 
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, kern, tw, tx, a.sa, a.sb, a.y, a.M, a.N, a.K, work, partials, tickets);
+    return cudaLaunchKernelEx(&cfg, kern, tw, tx, a.sa, a.sb, a.y, a.M, a.N, a.K, a.ld, work, partials, tickets);
+}
+
+// Columns of y that the pairs take; the rest goes to the tiles kernel, where whole
+// waves of pairs and that are faster than another wave of pairs. A K step of a wave
+// takes 0.6 us on pairs, 0.5 on 128-row tiles (split over clusters of up to 4), the second
+// kernel 6 us besides. Pairs alone / both (us): 436 x 10672 x 13200 (84 tiles on 76 pairs)
+// 124.5 / 89.6, 1024 x 5120 x 5376 (80) 58.3 / 45.8, 900 x 9216 x 2048 (144) 35.1 / 29.8, 600 x 8192 x 4096 (96) 47.2 /
+// 45.2; left to pairs: 1500 x 4096 x 4096 (96), 2048 x 43008 x 5376 (1344).
+long long pair_columns(long long M, long long N, long long K, int sms, int pairs) {
+    const long long num_m = (M + 255) / 256, num_n = (N + 255) / 256, steps = (K + kStepK - 1) / kStepK;
+    const long long waves = num_m * num_n / pairs;   // whole ones
+    const long long cut = waves * pairs / num_m;     // columns of tiles in them
+    if (waves < 1 || cut >= num_n) return N;
+    const long long rest = ((M + 127) / 128) * ((N - cut * 256 + tiles::BN - 1) / tiles::BN);
+    if (rest > sms) return N;
+    const long long split = std::min<long long>({4, sms / rest, std::max<long long>(1, steps / 2)});
+    // in hundredths of a microsecond
+    return 60 * steps > 50 * ((steps + split - 1) / split) + 600 ? cut * 256 : N;
+}
+
+template <int kOut>
+cudaError_t launch_pairs(const Int8MatmulArgs& all, const __half* wide, const DeviceProps& dp, cudaStream_t s) {
+    if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(pair::pair_kernel<kOut>), dp.device,
+                                            pair::kSmemBytes);
+        e != cudaSuccess)
+        return e;
+    const long long cut = pair_columns(all.M, all.N, all.K, dp.sms, resident_pairs<kOut>(dp));
+    Int8MatmulArgs a = all;
+    a.N = static_cast<int>(cut);
+    const cudaError_t e = launch_pair<kOut>(a, wide, dp, s);
+    if (e != cudaSuccess || cut == all.N) return e;
+    a.N = static_cast<int>(all.N - cut);
+    a.b += cut * all.K;
+    a.sb += cut;
+    a.y = static_cast<uint8_t*>(all.y) + cut * (kOut == kF32 ? 4 : 2);
+    return launch_tiles<kOut, 128>(a, {128, true, false, true}, wide, nullptr, nullptr, dp, s);
 }
 
 template <int kOut>
@@ -1167,7 +1204,7 @@ cudaError_t launch_typed(const Int8MatmulArgs& all, void* workspace, const Devic
             if ((e = cudaLaunchKernelEx(&cfg, widen_kernel, a.a, wide, items)) != cudaSuccess) return e;
         }
         switch (pl.mp) {
-            case 0: e = launch_pair<kOut>(a, wide, dp, s); break;
+            case 0: e = launch_pairs<kOut>(a, wide, dp, s); break;
             case 16: e = launch_tiles<kOut, 16>(a, pl, wide, partials, tickets, dp, s); break;
             case 32: e = launch_tiles<kOut, 32>(a, pl, wide, partials, tickets, dp, s); break;
             case 64: e = launch_tiles<kOut, 64>(a, pl, wide, partials, tickets, dp, s); break;

@@ -193,6 +193,7 @@ struct Int8MatmulArgs {
     const float* sb;
     void* y;
     int M, N, K;
+    int ld;   // elements from one row of y to the next
 };
 size_t int8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceProps& dp);
 cudaError_t launch_int8_matmul(const Int8MatmulArgs& a, int out_type, void* workspace, const DeviceProps& dp,
