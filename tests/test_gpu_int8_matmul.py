@@ -84,7 +84,7 @@ def test_sizes(M, N, K):
                                    (513, 5000, 2064), (16, 20488, 1040), (30, 43008, 272), (64, 24584, 400),
                                    (128, 20488, 656), (100, 21000, 16), (12, 6400, 5376), (40, 264, 4112),
                                    (8, 8192, 4096), (8, 8200, 8208), (6, 8192, 4096), (6, 16392, 8192), (5, 520, 1040),
-                                   (7, 40, 8208), (9, 2056, 1040), (13, 264, 8208), (16, 2048, 4096)])
+                                   (7, 40, 8208), (8, 12296, 144), (16, 6152, 272), (9, 2056, 1040), (13, 264, 8208), (16, 2048, 4096)])
 def test_plans(M, N, K, dtype):
     run(M, N, K, dtype)
 

@@ -1004,7 +1004,9 @@ struct Plan {
 };
 // Measured on 152 SMs (us a call):
 //   rows / tiles kernel: 4 x 43008 x 5376 39.3 / 42.5, 8 x 8192 x 4096 12.0 / 12.2, 5 x 8192 x 8192 17.9 / 17.5, 8 x
-//     43008 x 5376 63.9 / 43.4, 16 x 4096 x 2048 7.4 / 7.6, 16 x 4096 x 4096 11.0 / 9.7;
+//     43008 x 5376 63.9 / 43.4, 16 x 4096 x 2048 7.4 / 7.6, 16 x 4096 x 4096 11.0 / 9.7; by the sums per warp, of which
+//     each lane's part is added at the end: 8 x 8192 x 1024 5.5 / 7.3, 8 x 16384 x 512 8.0 / 6.3, 16 x 32024 x 144
+//     21.3 / 6.6;
 //   tiles / pair kernel: 512 x 4096 x 4096 (128 tiles) 21.0 / 26.1, 300 x 2600 x 2080 (63) 14.7 / 17.2, 600 x 4096 x
 //     4096 (160) 29.0 / 27.1, 256 x 16384 x 5376 (256) 43.9 / 33.1: pairs where 128-row tiles need a second wave;
 //   whole tiles / shared units: 16 x 20480 x 5376 (160 tiles) 33.9 / 24.9, 30720 columns (240) 35.0 / 33.8, 36864
@@ -1015,7 +1017,8 @@ struct Plan {
 //     saved): from 6 saved steps on.
 Plan plan(long long M, long long N, long long K, int sms) {
     const long long weights = N * K;
-    if (M <= 4 || (M <= 8 && weights <= 1ll << 25) || (M <= 16 && weights <= 1ll << 23)) return {-1, false, false, false};
+    if (M <= 4 || (M * N <= 3ll << 15 && weights <= (M <= 8 ? 1ll << 25 : M <= 16 ? 1ll << 23 : 0)))
+        return {-1, false, false, false};
     const long long cols = (N + tiles::BN - 1) / tiles::BN;
     if (M > 128 && ((M + 127) / 128) * cols > sms) return {0, false, false, true};
     const int mp = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
