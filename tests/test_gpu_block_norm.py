@@ -92,7 +92,8 @@ def check(o, dtype, res, scale=1.0, eps=1e-6):
 
 
 @pytest.mark.parametrize("dtype,res", PAIRS)
-@pytest.mark.parametrize("T,H", [(1, 16), (2, 256), (3, 272), (1, 5376), (77, 2608), (5, 8192), (4, 8208), (3, 16384)])
+@pytest.mark.parametrize("T,H", [(1, 16), (2, 256), (3, 272), (1, 5376), (77, 2608), (5, 8192), (4, 8208), (3, 12288),
+                                 (2, 12304), (3, 16384)])
 def test_shapes(T, H, dtype, res):
     check(inputs(T, H, dtype, res, "channel"), dtype, res, scale=0.22)
 

@@ -27,10 +27,11 @@ using namespace rowwise;
 
 // A row per block, or (kWarps) per warp, blockDim.y rows to a block. Vectors per
 // thread (us, 8192 x 5376): bf16 residual 4 (59.9; 2: 67.5, 1: 88.8), FP32 residual 2
-// (83.7; 4: 92.4, 1: 108.6). Four vectors of 16 bits are held to 64 registers: with the
-// 90 the compiler would take, 67.1.
+// (83.7; 4: 92.4, 1: 108.6; 4452 x 9040 to int8 87.4, 4: 105) but 4 in the longest rows of 16
+// bits (4096 x 16384 136; 2: 165). Four vectors are held to 64 registers: with the 90 the
+// compiler would take, 67.1.
 template <int kAct, int kRes, int kPer, int kMaxThreads, bool kWarps>
-__global__ void __launch_bounds__(kMaxThreads, kPer == 4 && kRes != kF32 && !kWarps ? 2 : 0)
+__global__ void __launch_bounds__(kMaxThreads, kPer == 4 && !kWarps ? 2 : 0)
 block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
     __shared__ __align__(16) float scratch[3][32];
     const long long row = kWarps ? blockIdx.x * static_cast<long long>(blockDim.y) + threadIdx.y : blockIdx.x;
@@ -158,19 +159,21 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
 template <int kAct, int kRes>
 cudaError_t launch_typed(const BlockNormArgs& a, cudaStream_t s) {
     // by H alone: a row's sums do not depend on the number of rows
-    const Layout l = layout_of(a.H / 8, kRes == kF32 && a.H <= 8192 ? 2 : 4);
+    const bool two = kRes == kF32 && (kAct == kF32 || a.H <= 12288);
+    const Layout l = layout_of(a.H / 8, two ? 2 : 4);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((a.T + l.y - 1) / l.y));
     cfg.blockDim = dim3(static_cast<unsigned>(l.x), static_cast<unsigned>(l.y));
     cfg.stream = s;
-    if (l.y > 1) switch (l.per) {
-            case 1: return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 1, 128, true>, a);
-            case 2: return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 2, 128, true>, a);
-            default: return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 4, 128, true>, a);
-        }
+    if (l.y > 1) {
+        if (l.per == 1) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 1, 128, true>, a);
+        if (l.per == 2) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 2, 128, true>, a);
+        if constexpr (kRes != kF32) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 4, 128, true>, a);
+    }
     if constexpr (kRes == kF32)
-        if (l.per == 2) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 2, 512, false>, a);
-    return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 4, 512, false>, a);
+        if (two) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 2, 1024, false>, a);
+    if constexpr (kAct != kF32) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 4, 512, false>, a);
+    return cudaErrorInvalidValue;   // not reached
 }
 
 }  // namespace
