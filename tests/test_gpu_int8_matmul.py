@@ -89,6 +89,14 @@ def test_plans(M, N, K, dtype):
     run(M, N, K, dtype)
 
 
+# On 152 SMs: tiles of 32, 64 and 128 rows, several of them along M, whole and in clusters of 2 to 8.
+@pytest.mark.parametrize("M,N,K", [(669, 24, 16352), (200, 2056, 2064), (3107, 40, 1008), (1097, 200, 1264), (65, 4104, 4112),
+                                   (301, 2600, 2080), (257, 4096, 1040), (7201, 104, 656), (9000, 128, 272),
+                                   (81, 5384, 2064), (513, 4104, 272), (12000, 104, 144), (40, 264, 8208), (129, 8, 32)])
+def test_rows_per_tile(M, N, K):
+    run(M, N, K, torch.bfloat16)
+
+
 # A whole wave of pairs and the other columns on 128-row tiles: both write rows of the same y.
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("M,N,K", [(300, 10248, 2064), (436, 10680, 4112), (900, 9224, 2064), (1030, 5128, 4112),

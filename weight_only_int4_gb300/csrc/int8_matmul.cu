@@ -307,7 +307,7 @@ constexpr int kThreads = 896;
 constexpr int kEpiWarps = 8, kWidenWarp0 = 12, kGroups = 4, kGroupWarps = 4;
 constexpr size_t kSlotFloats = 128 * 128;   // partial tile, [row of a][row of b]
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxSplit = 6;
+constexpr int kMaxSplit = 8;
 
 template <int MP>
 struct Cfg {
@@ -1002,6 +1002,11 @@ struct Plan {
     bool share;   // tiles kernel: units shared between CTAs
     bool widen;   // rows of a widened by a kernel before
 };
+// CTAs of a cluster per tile: the largest that `sms` SMs have room for, from 6 saved steps on.
+long long cluster_of(long long tiles, long long steps, long long sms) {
+    const long long split = std::min<long long>({tiles::kMaxSplit, sms / tiles, steps / 2});
+    return split > 1 && steps - steps / split >= 6 ? split : 1;
+}
 // Measured on 152 SMs (us a call):
 //   rows / tiles kernel: 4 x 43008 x 5376 39.3 / 42.5, 8 x 8192 x 4096 12.0 / 12.2, 5 x 8192 x 8192 17.9 / 17.5, 8 x
 //     43008 x 5376 63.9 / 43.4, 16 x 4096 x 2048 7.4 / 7.6, 16 x 4096 x 4096 11.0 / 9.7; by the sums per warp, of which
@@ -1015,13 +1020,30 @@ struct Plan {
 //   whole tiles / a cluster per tile: 16 x 8192 x 5376 17.9 / 13.5 (2 CTAs), 64 x 4096 x 4096 17.7 / 11.3 (4), 16 x 4096
 //     x 1024 7.2 / 6.4 (4: 6 steps saved), 128 x 8192 x 2048 15.2 / 15.7 (2: 8 saved), 16 x 2048 x 512 5.7 / 6.3 (2: 2
 //     saved): from 6 saved steps on.
+//   fewer rows per tile than there are, where the tiles still fit one wave: rows of a are widened in the kernel, and more SMs
+//     take part (128 / 64 / 32 rows; clusters of up to 6): 300 x 2600 x 2080 16.4 / 11.9 / 15.9, 668 x 24 x 16352 22.0 / 15.2 / 13.4, 7200 x 96 x
+//     5920 42.9 / 24.0 / 32.1, 200 x 2048 x 2048 11.7 / 11.3 / 10.0, 256 x 4096 x 4096 19.7 / 17.9 / 26.7, 80 x 5376 x 5376
+//     17.0 / 21.6 / 19.1, 128 x 8192 x 5376 22.0 / 22.0 / 34.0. By an estimate, within 2 us of these times: the steps of a CTA, what a tile takes besides, 2 us to add the parts of a cluster, the
+//     widening kernel's launch and bytes.
 Plan plan(long long M, long long N, long long K, int sms) {
     const long long weights = N * K;
     if (M <= 4 || (M * N <= 3ll << 15 && weights <= (M <= 8 ? 1ll << 25 : M <= 16 ? 1ll << 23 : 0)))
         return {-1, false, false, false};
-    const long long cols = (N + tiles::BN - 1) / tiles::BN;
+    const long long cols = (N + tiles::BN - 1) / tiles::BN, steps = (K + kStepK - 1) / kStepK;
     if (M > 128 && ((M + 127) / 128) * cols > sms) return {0, false, false, true};
-    const int mp = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    const int most = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    int mp = most;
+    long long least = 1ll << 62;
+    for (int rows = most; rows >= 32; rows /= 2) {
+        const long long tiles = ((M + rows - 1) / rows) * cols;
+        if (tiles > sms) break;
+        const long long split = cluster_of(tiles, steps, sms);
+        // in hundredths of a microsecond
+        const long long step = rows == 128 ? 48 : rows == 64 ? 40 : 39, fixed = rows == 128 ? 600 : rows == 64 ? 500 : 400;
+        const long long estimate = (steps + split - 1) / split * step + fixed + (split > 1 ? 200 : 0) +
+                                   (rows == 128 ? 400 + M * K * 3 / 70000 : 0);
+        if (estimate < least) least = estimate, mp = rows;
+    }
     const long long tiles = ((M + mp - 1) / mp) * cols, waves = (tiles + sms - 1) / sms;
     return {mp, 2 * tiles <= sms, tiles > sms && waves * sms * 4 > tiles * 5, mp > 64};
 }
@@ -1120,9 +1142,9 @@ cudaError_t launch_tiles(const Int8MatmulArgs& a, const Plan& pl, const __half* 
     if (units >= 1ll << 31) return cudaErrorInvalidValue;   // 35 TB of codes
     int split = 1;
     if (pl.split) {
-        // the largest cluster, up to 6 CTAs, of which all fit at once (50 tiles at 64 x 6400 x 5376: clusters of 3
-        // do not, 25.8 us instead of 17.6 with 2, on an earlier kernel)
-        split = static_cast<int>(std::min<long long>({6, dp.sms / tiles, steps / 2}));
+        split = static_cast<int>(cluster_of(tiles, steps, dp.sms));
+        // all of them resident at once (50 tiles at 64 x 6400 x 5376: clusters of 3 are not, 25.8 us instead of 17.6
+        // with 2, on an earlier kernel)
         while (split > 1 && tiles > resident_clusters<kOut, MP>(dp, split)) --split;
         if (split > 1 && steps - steps / split < 6) split = 1;
     }
@@ -1190,7 +1212,7 @@ cudaError_t launch_typed(const Int8MatmulArgs& all, void* workspace, const Devic
     uint8_t* at = static_cast<uint8_t*>(workspace) + kControlBytes;
     float* partials = reinterpret_cast<float*>(at);
     __half* wide = reinterpret_cast<__half*>(at + (pl.share ? partial_bytes(dp) : 0));
-    const long long chunk = chunk_rows(all.M);
+    const long long chunk = pl.widen ? chunk_rows(all.M) : all.M;
     for (long long m0 = 0; m0 < all.M; m0 += chunk) {
         Int8MatmulArgs a = all;
         a.M = static_cast<int>(std::min(chunk, all.M - m0));

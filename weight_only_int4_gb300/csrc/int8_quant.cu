@@ -140,7 +140,7 @@ cudaError_t quantize(const void* x, int8_t* codes, float* scales, long long rows
     }
     const dim3 threads(static_cast<unsigned>(l.x), static_cast<unsigned>(l.y));
     const long long blocks = (rows + l.y - 1) / l.y;
-    if (l.x > 512) {   // long rows: twice the vectors
+    if (l.per == kMost && l.x > 512) {   // long rows: twice the vectors
         const dim3 half(static_cast<unsigned>((vecs + 2 * kMost - 1) / (2 * kMost) + 31) / 32 * 32);
         return launch(quant_row_kernel<kType, 2 * kMost, 512>, blocks, half, s, x, codes, scales, rows, K);
     }
@@ -154,11 +154,8 @@ cudaError_t quantize(const void* x, int8_t* codes, float* scales, long long rows
         }
     if constexpr (kMost == 8)
         if (l.per == 8) return launch(quant_row_kernel<kType, 8, 512>, blocks, threads, s, x, codes, scales, rows, K);
-    switch (l.per) {
-        case 1: return launch(quant_row_kernel<kType, 1, 1024>, blocks, threads, s, x, codes, scales, rows, K);
-        case 2: return launch(quant_row_kernel<kType, 2, 512>, blocks, threads, s, x, codes, scales, rows, K);
-        default: return launch(quant_row_kernel<kType, 4, 512>, blocks, threads, s, x, codes, scales, rows, K);
-    }
+    if (l.per == 1) return launch(quant_row_kernel<kType, 1, 1024>, blocks, threads, s, x, codes, scales, rows, K);
+    return launch(quant_row_kernel<kType, 4, 512>, blocks, threads, s, x, codes, scales, rows, K);
 }
 
 template <int kType>
