@@ -8,14 +8,15 @@
 // 2^24. The weights b, which every call streams, are widened on the way from
 // shared memory to tensor memory, where the MMA takes its first operand from:
 // they cross HBM, L2 and shared memory as single bytes. The activations a are
-// widened to fp16 in the workspace by a kernel of their own before it.
+// widened in the kernel too (tiles of up to 64 rows) or to fp16 in the workspace by a
+// kernel of their own before it.
 //
 // Three kernels:
 //   rows    few rows of a: dot products of four bytes (dp4a), exact in 32 bits;
 //           streams b. The instruction's rate (about 18 lanes a cycle and SM, measured)
 //           bounds it from four rows on.
-//   tiles   128 rows of b against 16..128 rows of a per tile, tiles shared
-//           between CTAs by (tile, K step) units.
+//   tiles   128 rows of b against 16..128 rows of a per tile; whole tiles, a cluster
+//           per tile, or tiles shared between CTAs by (tile, K step) units.
 //   pair    256 x 256 tiles on CTA pairs (cta_group::2).
 //
 // Every mbarrier wait is bounded (about two seconds). On expiry the kernel
@@ -1012,19 +1013,20 @@ long long cluster_of(long long tiles, long long steps, long long sms) {
 //     43008 x 5376 63.9 / 43.4, 16 x 4096 x 2048 7.4 / 7.6, 16 x 4096 x 4096 11.0 / 9.7; by the sums per warp, of which
 //     each lane's part is added at the end: 8 x 8192 x 1024 5.5 / 7.3, 8 x 16384 x 512 8.0 / 6.3, 16 x 32024 x 144
 //     21.3 / 6.6;
-//   tiles / pair kernel: 512 x 4096 x 4096 (128 tiles) 21.0 / 26.1, 300 x 2600 x 2080 (63) 14.7 / 17.2, 600 x 4096 x
-//     4096 (160) 29.0 / 27.1, 256 x 16384 x 5376 (256) 43.9 / 33.1: pairs where 128-row tiles need a second wave;
+//   tiles / pair kernel: 512 x 4096 x 4096 (128 tiles) 21.0 / 26.1, 600 x 4096 x 4096 (160) 29.0 / 27.1, 256 x 16384 x 5376 (256)
+//     43.9 / 33.1: pairs where 128-row tiles need a second wave;
 //   whole tiles / shared units: 16 x 20480 x 5376 (160 tiles) 33.9 / 24.9, 30720 columns (240) 35.0 / 33.8, 36864
 //     (288) 35.8 / 39.5, 43008 (336) 50.4 / 44.6; 64 rows 40.0 / 31.1, 41.0 / 41.1, 41.7 / 47.4, 58.1 / 52.5: shared
 //     where the last wave leaves a fifth of all SM time idle;
 //   whole tiles / a cluster per tile: 16 x 8192 x 5376 17.9 / 13.5 (2 CTAs), 64 x 4096 x 4096 17.7 / 11.3 (4), 16 x 4096
 //     x 1024 7.2 / 6.4 (4: 6 steps saved), 128 x 8192 x 2048 15.2 / 15.7 (2: 8 saved), 16 x 2048 x 512 5.7 / 6.3 (2: 2
-//     saved): from 6 saved steps on.
-//   fewer rows per tile than there are, where the tiles still fit one wave: rows of a are widened in the kernel, and more SMs
-//     take part (128 / 64 / 32 rows; clusters of up to 6): 300 x 2600 x 2080 16.4 / 11.9 / 15.9, 668 x 24 x 16352 22.0 / 15.2 / 13.4, 7200 x 96 x
-//     5920 42.9 / 24.0 / 32.1, 200 x 2048 x 2048 11.7 / 11.3 / 10.0, 256 x 4096 x 4096 19.7 / 17.9 / 26.7, 80 x 5376 x 5376
-//     17.0 / 21.6 / 19.1, 128 x 8192 x 5376 22.0 / 22.0 / 34.0. By an estimate, within 2 us of these times: the steps of a CTA, what a tile takes besides, 2 us to add the parts of a cluster, the
-//     widening kernel's launch and bytes.
+//     saved): from 6 saved steps on;
+//   fewer rows per tile than there are (128 / 64 / 32), where the tiles still fit one wave: up to 64 rows are widened in
+//     the kernel, and more SMs take part: 300 x 2600 x 2080 16.4 / 11.9 / 15.9, 668 x 24 x 16352 22.0 / 15.2 / 13.4,
+//     7200 x 96 x 5920 42.9 / 24.0 / 32.1, 200 x 2048 x 2048 11.7 / 11.3 / 10.0, 256 x 4096 x 4096 19.7 / 17.9 / 26.7,
+//     80 x 5376 x 5376 17.0 / 21.6 / 19.1, 128 x 8192 x 5376 22.0 / 22.0 / 34.0. By an estimate, within 2 us of these
+//     times: the steps of a CTA, what a tile takes besides, 2 us to add the parts of a cluster, the widening kernel's
+//     launch and bytes.
 Plan plan(long long M, long long N, long long K, int sms) {
     const long long weights = N * K;
     if (M <= 4 || (M * N <= 3ll << 15 && weights <= (M <= 8 ? 1ll << 25 : M <= 16 ? 1ll << 23 : 0)))

@@ -19,7 +19,7 @@ using namespace rowwise;
 // A thread block takes a row (kWarps: each of its warps one): each thread holds
 // kPer vectors of 8 elements in their own type between the maximum and the codes,
 // so the row is read once. 43008 x 5376 bf16 99.0 us (7.0 TB/s; 203 with one vector
-// per thread, 130 with four), FP32 162.9 (7.1); 2048 x 5376 bf16 7.2 us, 1 x 5376 2.2.
+// per thread, 130 with four), FP32 162.9 (7.1); 2048 x 5376 bf16 7.2 us, 1 x 5376 1.5.
 template <int kType, int kPer, int kMaxThreads, bool kWarps = false>
 __global__ void __launch_bounds__(kMaxThreads) quant_row_kernel(const void* __restrict__ x, int8_t* __restrict__ codes,
                                                                 float* __restrict__ scales, long long rows, int K) {
