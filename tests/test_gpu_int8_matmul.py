@@ -105,6 +105,17 @@ def test_waves_and_the_rest(M, N, K, dtype):
     run(M, N, K, dtype)
 
 
+# CTA pairs with tiles of every height, part of a wave and several; columns and rows that end inside a tile.
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [(420, 5944, 8208), (200, 9736, 8208), (129, 10000, 12304), (1100, 20488, 4112),
+                                   (260, 6536, 8304), (2050, 2568, 8192), (8300, 2568, 5376), (300, 16392, 272), (380, 20488, 400),
+                                   (640, 8200, 144), (150, 30728, 528), (225, 20008, 1040), (700, 5000, 2064), (1000, 6152, 160)])
+def test_pair_tiles(M, N, K, dtype):
+    a, sa, b, sb, y = run(M, N, K, dtype)
+    for _ in range(3):
+        assert torch.equal(w4.int8_matmul(a, sa, b, sb, out_dtype=dtype), y)
+
+
 def test_chunks_of_many_rows():
     """More rows than are widened at a time, in both kernels that take widened rows."""
     run(8200, 1032, 144, torch.bfloat16)
@@ -181,7 +192,7 @@ def test_workspace_serves_every_shape():
     """One workspace in turn for shapes of every plan, its first bytes zero again after each."""
     lib = w4.load_library()
     shapes = [(16, 16384, 512), (300, 2600, 2080), (1, 2048, 4096), (64, 4096, 5376), (100, 8200, 96), (2, 520, 64),
-              (2100, 2048, 1040), (128, 16384, 512), (24, 43008, 272), (16, 16384, 512)]
+              (2100, 2048, 1040), (436, 10680, 4112), (128, 16384, 512), (24, 43008, 272), (16, 16384, 512)]
     need = max(lib.w4a16_int8_matmul_workspace_bytes(*s) for s in shapes)
     ws = torch.full((max(need, 4096),), 0xA5, dtype=torch.uint8, device="cuda")
     ws[:4096].zero_()
@@ -205,7 +216,8 @@ def test_small_workspace_is_refused():
 
 
 @pytest.mark.parametrize("shapes", [((64, 16384, 512), (16, 8192, 512)), ((300, 2600, 2080), (140, 2600, 512)),
-                                    ((1, 2048, 2048), (8, 2048, 512))])
+                                    ((1, 2048, 2048), (8, 2048, 512)),
+                                    ((436, 10680, 4112), (200, 9736, 8208))])
 def test_graphs_captured_cold(shapes):
     """Two graphs of calls without a workspace, captured before any eager call, replayed in every order."""
     calls = [operands(*s, 21 + i) for i, s in enumerate(shapes)]

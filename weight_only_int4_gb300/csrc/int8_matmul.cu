@@ -696,7 +696,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
 // K step's eight take about 0.6 us, its 48 KB of loads 0.58 at 82 KB a us and SM).
 namespace pair {
 
-constexpr int BM = 256, BN = 256, CM = 128, CN = 128;
+constexpr int BN = 256, CM = 128, CN = 128;   // CM: rows of a per CTA at most
 constexpr int kThreads = 640;
 constexpr int kEpiWarps = 8, kWidenWarp0 = 12, kGroups = 2, kGroupWarps = 4;
 constexpr int kStages = 4, kWStages = 5;     // of a and operands; of codes
@@ -756,7 +756,7 @@ template <int kOut>
 __global__ void __launch_bounds__(kThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
             const float* __restrict__ sa, const float* __restrict__ sb, void* __restrict__ y, int M, int N, int K,
-            int ld) {
+            int ld, int bm) {
     extern __shared__ uint8_t smem_raw[];
     // the same layout in both CTAs: the MMA addresses the peer's rows of a at this CTA's offsets
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -769,7 +769,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
     const int pair_id = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int num_m = (M + BM - 1) / BM, num_n = (N + BN - 1) / BN;
+    const int half = bm / 2, num_m = (M + bm - 1) / bm, num_n = (N + BN - 1) / BN;
     const long long tiles = static_cast<long long>(num_m) * num_n;
     const int kt_total = (K + kStepK - 1) / kStepK;
     const Abort ab{&bars->abort, smem_u32(&bars->abort), static_cast<uint32_t>(rank ^ 1)};
@@ -811,7 +811,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
             bool ok = true;
             for (long long t = pair_id; t < tiles && ok; t += npairs) {
                 const Place at = place_of(t, num_m, num_n);
-                const int m0 = at.m * BM + rank * CM, n0 = at.n * BN + rank * CN;
+                const int m0 = at.m * bm + rank * half, n0 = at.n * BN + rank * CN;
                 for (int kt = 0; kt < kt_total; ++kt) {
                     if (!wait_bar(bar_empty + 8 * s, parity, ab)) { ok = false; break; }
                     if (codes) {
@@ -819,7 +819,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
                         mbar_arrive_expect_tx(fb, kWBytes);
                         tma_load_2d(st_w(s), &tw, kt * kStepK, n0, fb);
                     } else {
-                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&bars->xfull[s]), 2 * kXBytes);
+                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&bars->xfull[s]), bm * kStepK * 2);
                         tma_load_2d_pair(st_x(s), &tx, kt * kStepK, m0, even + 8u * s);
                         tma_load_2d_pair(st_x(s) + kXBytes / 2, &tx, kt * kStepK + 64, m0, even + 8u * s);
                     }
@@ -838,7 +838,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs (even CTA)
         if (rank == 0) {
-            constexpr uint32_t kIdesc = umma_idesc_f16(BN, BM, false);
+            const uint32_t idesc = umma_idesc_f16(BN, bm, false);
             constexpr uint16_t kPair = 0x3;
             const bool leader = elect_one();
             const uint64_t desc_x = sw128_kmajor_desc(st_x(0));
@@ -864,7 +864,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
 #pragma unroll
                         for (int kk = 0; kk < kStepK / 16; ++kk)
                             if (kk < nk)
-                                umma_f16_ta_pair(tmem, a + 8 * kk, x + (kk >> 2) * (kXBytes >> 5) + 2 * (kk & 3), kIdesc,
+                                umma_f16_ta_pair(tmem, a + 8 * kk, x + (kk >> 2) * (kXBytes >> 5) + 2 * (kk & 3), idesc,
                                                  kt || kk);
                         umma_commit_pair_mc(bar_empty + 8 * s, kPair);
                     }
@@ -908,13 +908,13 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
     } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3, side = (warp - kEpiWarp0) >> 2;
-        const uint32_t d = tmem + (static_cast<uint32_t>(q * 32) << 16) + side * 128;
+        const uint32_t d = tmem + (static_cast<uint32_t>(q * 32) << 16) + side * half;
         float* mine = scales + (warp - kEpiWarp0) * 128;
         int it = 0;
         for (long long t = pair_id; t < tiles; t += npairs, ++it) {
             const Place at = place_of(t, num_m, num_n);
             const int n = at.n * BN + rank * CN + q * 32 + lane;
-            const int m0 = at.m * BM + side * 128, mc = min(128, M - m0);
+            const int m0 = at.m * bm + side * half, mc = min(half, M - m0);
             const float tn = n < N ? __ldg(sb + n) : 0.f;
             __syncwarp();
 #pragma unroll
@@ -924,7 +924,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
             tc_fence_after();
             if constexpr (kOut == kF32) {
 #pragma unroll 1
-                for (int ch = 0; ch < 4; ++ch) {
+                for (int ch = 0; ch * 32 < half; ++ch) {
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(d + ch * 32, r);
                     tmem_wait_ld();
@@ -940,7 +940,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster_relaxed(smem_u32(&bars->tempty), 0);
             } else {
-                uint32_t o[64];
+                uint32_t o[64];   // of lower tiles the last are not stored
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch) {
                     uint32_t r[16];
@@ -997,6 +997,35 @@ long long chunk_rows(long long M) {
     return chunks == 1 ? M : ((M + chunks - 1) / chunks + 255) / 256 * 256;
 }
 
+// Rows of a per tile of the pairs, and the columns of y that the pairs take: all of them, or those of whole waves, the rest
+// going to 128-row tiles (split over clusters of up to 4) in a second kernel. By an estimate in hundredths of a microsecond:
+// a K step of a pair takes 0.38 us with up to 128 rows, 0.44, 0.46, 0.51 and 0.58 with 160, 192, 224 and 256 (two tiles
+// along M; 0.47 to 0.58 with one, bound by HBM); one on 128-row tiles 0.5, the second kernel 6 us besides. With tiles of
+// 256 rows / so (us): 600 x 4096 x 4096 27.2 / 22.0, 300 x 16384 x 1024 23.4 / 17.3, 420 x 5944 x 16944 81.9 / 64.7,
+// 4096 x 4096 x 4096 90.1 / 81.6. All columns on pairs of 256 rows / whole waves and the rest: 436 x 10672 x 13200 (84 tiles
+// on 76 pairs) 124.5 / 89.6, 1024 x 5120 x 5376 (80) 58.3 / 45.8.
+struct PairPlan {
+    int bm;
+    long long columns, cost;
+};
+PairPlan pair_plan(long long M, long long N, long long K, int sms, long long pairs) {
+    const long long num_n = (N + pair::BN - 1) / pair::BN, steps = (K + kStepK - 1) / kStepK;
+    PairPlan best{0, 0, 1ll << 62};
+    for (long long parts = (M + 255) / 256; parts <= (M + 127) / 128; ++parts) {
+        const long long bm = ((M + parts - 1) / parts + 31) / 32 * 32, num_m = (M + bm - 1) / bm, tiles = num_m * num_n;
+        const long long step = 38 + std::max(0ll, bm - 128) * 5 / 32, all = (tiles + pairs - 1) / pairs * steps * step;
+        if (all < best.cost) best = {static_cast<int>(bm), N, all};
+        const long long waves = tiles / pairs, cut = waves * pairs / num_m;   // whole waves, columns of tiles in them
+        if (waves < 1 || cut >= num_n) continue;
+        const long long rest = ((M + 127) / 128) * ((N - cut * pair::BN + tiles::BN - 1) / tiles::BN);
+        if (rest > sms) continue;
+        const long long split = std::min<long long>({4, sms / rest, std::max<long long>(1, steps / 2)});
+        const long long both = waves * steps * step + 50 * ((steps + split - 1) / split) + 600;
+        if (both < best.cost) best = {static_cast<int>(bm), cut * pair::BN, both};
+    }
+    return best;
+}
+
 struct Plan {
     int mp;       // rows of a per tile of the tiles kernel; 0: CTA pairs; -1: the rows kernel
     bool split;   // tiles kernel: a cluster per tile, where the clusters are resident at once
@@ -1032,19 +1061,24 @@ Plan plan(long long M, long long N, long long K, int sms) {
     if (M <= 4 || (M * N <= 3ll << 15 && weights <= (M <= 8 ? 1ll << 25 : M <= 16 ? 1ll << 23 : 0)))
         return {-1, false, false, false};
     const long long cols = (N + tiles::BN - 1) / tiles::BN, steps = (K + kStepK - 1) / kStepK;
-    if (M > 128 && ((M + 127) / 128) * cols > sms) return {0, false, false, true};
     const int most = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     int mp = most;
-    long long least = 1ll << 62;
-    for (int rows = most; rows >= 32; rows /= 2) {
-        const long long tiles = ((M + rows - 1) / rows) * cols;
-        if (tiles > sms) break;
-        const long long split = cluster_of(tiles, steps, sms);
+    if (M > 128 || cols <= sms) {
         // in hundredths of a microsecond
-        const long long step = rows == 128 ? 48 : rows == 64 ? 40 : 39, fixed = rows == 128 ? 600 : rows == 64 ? 500 : 400;
-        const long long estimate = (steps + split - 1) / split * step + fixed + (split > 1 ? 200 : 0) +
-                                   (rows == 128 ? 400 + M * K * 3 / 70000 : 0);
-        if (estimate < least) least = estimate, mp = rows;
+        const long long widen = 400 + M * K * 3 / 70000;
+        long long least = 1ll << 62;
+        if (M > 64) least = pair_plan(M, N, K, sms, sms / 2).cost + 400 + widen, mp = 0;
+        for (int rows = most; rows >= 16; rows /= 2) {
+            const long long tiles = ((M + rows - 1) / rows) * cols;
+            if (tiles > sms || rows < std::min(32, most)) break;
+            const long long split = cluster_of(tiles, steps, sms);
+            if (rows == 128 && split == 1) continue;
+            const long long step = rows == 128 ? 48 : rows == 64 ? 40 : 39, fixed = rows == 128 ? 600 : rows == 64 ? 500 : 400;
+            const long long estimate =
+                (steps + split - 1) / split * step + fixed + (split > 1 ? 200 : 0) + (rows == 128 ? widen : 0);
+            if (estimate < least) least = estimate, mp = rows;
+        }
+        if (!mp) return {0, false, false, true};
     }
     const long long tiles = ((M + mp - 1) / mp) * cols, waves = (tiles + sms - 1) / sms;
     return {mp, 2 * tiles <= sms, tiles > sms && waves * sms * 4 > tiles * 5, mp > 64};
@@ -1101,15 +1135,15 @@ int resident_clusters(const DeviceProps& dp, int size) {
 // Kernels that use tensor memory are launched without programmatic
 // serialization, as those of mx_matmul.cu.
 template <int kOut>
-cudaError_t launch_pair(const Int8MatmulArgs& a, const __half* wide, const DeviceProps& dp, cudaStream_t s) {
+cudaError_t launch_pair(const Int8MatmulArgs& a, int bm, const __half* wide, const DeviceProps& dp, cudaStream_t s) {
     auto kern = pair::pair_kernel<kOut>;
     if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), dp.device, pair::kSmemBytes);
         e != cudaSuccess)
         return e;
     CUtensorMap tw, tx;
-    if (!encode_codes(&tw, a.b, a.N, a.K, pair::CN) || !encode_wide(&tx, wide, a.M, a.K, pair::CM))
+    if (!encode_codes(&tw, a.b, a.N, a.K, pair::CN) || !encode_wide(&tx, wide, a.M, a.K, bm / 2))
         return cudaErrorInvalidValue;
-    const long long tiles = static_cast<long long>((a.M + pair::BM - 1) / pair::BM) * ((a.N + pair::BN - 1) / pair::BN);
+    const long long tiles = static_cast<long long>((a.M + bm - 1) / bm) * ((a.N + pair::BN - 1) / pair::BN);
     const long long pairs = std::max<long long>(1, std::min<long long>(tiles, resident_pairs<kOut>(dp)));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
@@ -1123,7 +1157,7 @@ cudaError_t launch_pair(const Int8MatmulArgs& a, const __half* wide, const Devic
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tw, tx, a.sa, a.sb, a.y, a.M, a.N, a.K, a.ld);
+    return cudaLaunchKernelEx(&cfg, kern, tw, tx, a.sa, a.sb, a.y, a.M, a.N, a.K, a.ld, bm);
 }
 
 template <int kOut, int MP>
@@ -1170,34 +1204,17 @@ cudaError_t launch_tiles(const Int8MatmulArgs& a, const Plan& pl, const __half* 
     return cudaLaunchKernelEx(&cfg, kern, tw, tx, a.sa, a.sb, a.y, a.M, a.N, a.K, a.ld, work, partials, tickets);
 }
 
-// Columns of y that the pairs take; the rest goes to the tiles kernel, where whole
-// waves of pairs and that are faster than another wave of pairs. A K step of a wave
-// takes 0.6 us on pairs, 0.5 on 128-row tiles (split over clusters of up to 4), the second
-// kernel 6 us besides. Pairs alone / both (us): 436 x 10672 x 13200 (84 tiles on 76 pairs)
-// 124.5 / 89.6, 1024 x 5120 x 5376 (80) 58.3 / 45.8, 900 x 9216 x 2048 (144) 35.1 / 29.8, 600 x 8192 x 4096 (96) 47.2 /
-// 45.2; left to pairs: 1500 x 4096 x 4096 (96), 2048 x 43008 x 5376 (1344).
-long long pair_columns(long long M, long long N, long long K, int sms, int pairs) {
-    const long long num_m = (M + 255) / 256, num_n = (N + 255) / 256, steps = (K + kStepK - 1) / kStepK;
-    const long long waves = num_m * num_n / pairs;   // whole ones
-    const long long cut = waves * pairs / num_m;     // columns of tiles in them
-    if (waves < 1 || cut >= num_n) return N;
-    const long long rest = ((M + 127) / 128) * ((N - cut * 256 + tiles::BN - 1) / tiles::BN);
-    if (rest > sms) return N;
-    const long long split = std::min<long long>({4, sms / rest, std::max<long long>(1, steps / 2)});
-    // in hundredths of a microsecond
-    return 60 * steps > 50 * ((steps + split - 1) / split) + 600 ? cut * 256 : N;
-}
-
 template <int kOut>
 cudaError_t launch_pairs(const Int8MatmulArgs& all, const __half* wide, const DeviceProps& dp, cudaStream_t s) {
     if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(pair::pair_kernel<kOut>), dp.device,
                                             pair::kSmemBytes);
         e != cudaSuccess)
         return e;
-    const long long cut = pair_columns(all.M, all.N, all.K, dp.sms, resident_pairs<kOut>(dp));
+    const PairPlan pl = pair_plan(all.M, all.N, all.K, dp.sms, resident_pairs<kOut>(dp));
+    const long long cut = pl.columns;
     Int8MatmulArgs a = all;
     a.N = static_cast<int>(cut);
-    const cudaError_t e = launch_pair<kOut>(a, wide, dp, s);
+    const cudaError_t e = launch_pair<kOut>(a, pl.bm, wide, dp, s);
     if (e != cudaSuccess || cut == all.N) return e;
     a.N = static_cast<int>(all.N - cut);
     a.b += cut * all.K;
