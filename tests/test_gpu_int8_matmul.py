@@ -109,7 +109,8 @@ def test_waves_and_the_rest(M, N, K, dtype):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("M,N,K", [(420, 5944, 8208), (200, 9736, 8208), (129, 10000, 12304), (1100, 20488, 4112),
                                    (260, 6536, 8304), (2050, 2568, 8192), (8300, 2568, 5376), (300, 16392, 272), (380, 20488, 400),
-                                   (640, 8200, 144), (150, 30728, 528), (225, 20008, 1040), (700, 5000, 2064), (1000, 6152, 160)])
+                                   (640, 8200, 144), (150, 30728, 528), (225, 20008, 1040), (700, 5000, 2064), (1000, 6152, 160),
+                                   (70, 17000, 1040), (100, 16392, 400), (128, 19456, 144), (4190, 424, 1040)])
 def test_pair_tiles(M, N, K, dtype):
     a, sa, b, sb, y = run(M, N, K, dtype)
     for _ in range(3):

@@ -17,7 +17,7 @@
 //           bounds it from four rows on.
 //   tiles   128 rows of b against 16..128 rows of a per tile; whole tiles, a cluster
 //           per tile, or tiles shared between CTAs by (tile, K step) units.
-//   pair    256 x 256 tiles on CTA pairs (cta_group::2).
+//   pair    256 rows of b against up to 256 rows of a on CTA pairs (cta_group::2).
 //
 // Every mbarrier wait is bounded (about two seconds). On expiry the kernel
 // records the timeout in a device word, raises the abort flag, every role
@@ -297,9 +297,8 @@ cudaError_t launch(const Int8MatmulArgs& a, cudaStream_t s) {
 //     which adds the two FP32 parts from global memory, the lower CTA's first.
 // All three are deterministic.
 //
-// 64 x 16384 x 5376 23.0 us, 16 x 43008 x 5376 44.6, 128 x 43008 x 5376 60.8, 512 x
-// 4096 x 4096 21.0. A step takes 0.39 us with 16 rows and 0.40 with 64 (HBM: 0.37
-// for 152 CTAs), 0.48 with 128 (48 KB a step into the SM); launch to first load, the
+// 64 x 16384 x 5376 23.0 us, 16 x 43008 x 5376 44.6, 128 x 43008 x 5376 60.8. A step
+// takes 0.39 us with 16 rows and 0.40 with 64 (HBM: 0.37 for 152 CTAs), 0.48 with 128 (48 KB a step into the SM); launch to first load, the
 // last epilogue and joins take 5 to 8 us.
 namespace tiles {
 
@@ -666,12 +665,12 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
 }  // namespace tiles
 
 // ---------------------------------------------------------------------------
-// CTA pairs, 256 x 256 tiles
+// CTA pairs: 256 rows of b against bm (a multiple of 32, up to 256) rows of a
 // ---------------------------------------------------------------------------
 // CTA r of the pair holds rows [128 r, 128 r + 128) of the tile's block of b (its
-// tensor-memory lanes) and the same rows of its block of a (its half of the MMA's
-// second operand). Per K step an SM receives 16 KB of codes and 32 KB of fp16
-// rows of a for 16.8 MFLOP.
+// tensor-memory lanes) and bm / 2 rows of its block of a (its half of the MMA's
+// second operand). Per K step an SM receives 16 KB of codes and, with bm = 256, 32 KB
+// of fp16 rows of a for 16.8 MFLOP.
 //
 //   warp 3       both: TMA of the CTA's codes (a ring of its own)
 //   warp 0       both: TMA of the CTA's rows of a, complete on the even CTA's barrier
@@ -679,7 +678,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
 //                an operand stage of the CTA's tensor memory and arrive on the
 //                even CTA's barrier
 //   warp 1       even: issues the pair's MMAs; its commits free the stages in both
-//   warps 4..11  both: epilogue, two warps per lane quarter, 128 columns each
+//   warps 4..11  both: epilogue, two warps per lane quarter, bm / 2 columns each
 //   warp 2       tensor memory
 //
 // What the odd CTA's widening warps publish lies in tensor memory alone: they wait
@@ -687,12 +686,14 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
 // CTA's barrier relaxed, which costs them nothing; the MMA thread waits relaxed and
 // fences after. Rows of a are published by the copies themselves.
 //
-// Tensor memory: one accumulator of 256 columns and four operand stages of 64.
+// Tensor memory: one accumulator of up to 256 columns and four operand stages of 64.
 // The epilogue takes the accumulator into registers, scaled and rounded to 16
 // bits, and lets the next tile's MMAs start before it stores (FP32 results are
-// stored first: twice the registers).
+// stored first: twice the registers). Two accumulators for bm <= 128 were no faster
+// (2048 x 16384 x 512 42 us instead of 34 with bm = 256), nor was sharing K steps
+// between pairs: the FP32 parts of a tile are 256 KB (512 x 5376 x 5376 44 us instead of 33).
 //
-// 2048 x 43008 x 5376 463 us, 2.04 PFLOP/s: at the rate of the fp16 MMAs (a
+// 2048 x 43008 x 5376 457 us, 2.07 PFLOP/s: at the rate of the fp16 MMAs (a
 // K step's eight take about 0.6 us, its 48 KB of loads 0.58 at 82 KB a us and SM).
 namespace pair {
 
@@ -1042,8 +1043,9 @@ long long cluster_of(long long tiles, long long steps, long long sms) {
 //     43008 x 5376 63.9 / 43.4, 16 x 4096 x 2048 7.4 / 7.6, 16 x 4096 x 4096 11.0 / 9.7; by the sums per warp, of which
 //     each lane's part is added at the end: 8 x 8192 x 1024 5.5 / 7.3, 8 x 16384 x 512 8.0 / 6.3, 16 x 32024 x 144
 //     21.3 / 6.6;
-//   tiles / pair kernel: 512 x 4096 x 4096 (128 tiles) 21.0 / 26.1, 600 x 4096 x 4096 (160) 29.0 / 27.1, 256 x 16384 x 5376 (256)
-//     43.9 / 33.1: pairs where 128-row tiles need a second wave;
+//   128-row tiles / pairs: whole, one wave, 4190 x 424 x 8720 57.3 / 49.2, 231 x 7352 x 4272 23.5 / 21.1, 512 x 4096 x
+//     4096 20.9 / 20.5, 128 x 19456 x 12288 58.5 / 53.1; a cluster per tile, 256 x 4096 x 14336 35.1 / 50.0; two
+//     waves 256 x 16384 x 5376 43.9 / 33.1: pairs but where a cluster works on a tile;
 //   whole tiles / shared units: 16 x 20480 x 5376 (160 tiles) 33.9 / 24.9, 30720 columns (240) 35.0 / 33.8, 36864
 //     (288) 35.8 / 39.5, 43008 (336) 50.4 / 44.6; 64 rows 40.0 / 31.1, 41.0 / 41.1, 41.7 / 47.4, 58.1 / 52.5: shared
 //     where the last wave leaves a fifth of all SM time idle;
@@ -1065,7 +1067,7 @@ Plan plan(long long M, long long N, long long K, int sms) {
     int mp = most;
     if (M > 128 || cols <= sms) {
         // in hundredths of a microsecond
-        const long long widen = 400 + M * K * 3 / 70000;
+        const long long widen = 400 + M * K * 3 / 70000;   // the launch, and the kernel's bytes
         long long least = 1ll << 62;
         if (M > 64) least = pair_plan(M, N, K, sms, sms / 2).cost + 400 + widen, mp = 0;
         for (int rows = most; rows >= 16; rows /= 2) {
@@ -1073,7 +1075,8 @@ Plan plan(long long M, long long N, long long K, int sms) {
             if (tiles > sms || rows < std::min(32, most)) break;
             const long long split = cluster_of(tiles, steps, sms);
             if (rows == 128 && split == 1) continue;
-            const long long step = rows == 128 ? 48 : rows == 64 ? 40 : 39, fixed = rows == 128 ? 600 : rows == 64 ? 500 : 400;
+            const long long step = rows == 128 ? 48 : rows == 64 ? 40 : 39;
+            const long long fixed = rows == 128 ? 600 : rows == 64 ? 500 : 400;
             const long long estimate =
                 (steps + split - 1) / split * step + fixed + (split > 1 ? 200 : 0) + (rows == 128 ? widen : 0);
             if (estimate < least) least = estimate, mp = rows;
