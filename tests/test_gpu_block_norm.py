@@ -93,7 +93,7 @@ def check(o, dtype, res, scale=1.0, eps=1e-6):
 
 @pytest.mark.parametrize("dtype,res", PAIRS)
 @pytest.mark.parametrize("T,H", [(1, 16), (2, 256), (3, 272), (1, 5376), (77, 2608), (5, 8192), (4, 8208), (3, 12288),
-                                 (2, 12304), (3, 16384)])
+                                 (2, 12304), (3, 16384), (5, 1040), (2, 6128), (3, 6144), (2, 9216), (3, 9232), (2, 11008)])
 def test_shapes(T, H, dtype, res):
     check(inputs(T, H, dtype, res, "channel"), dtype, res, scale=0.22)
 

@@ -11,12 +11,12 @@
 // stored. Up to three reductions separate the passes over the registers.
 //
 // What bounds it: HBM for many rows (8192 x 5376, bf16, norms on both sides and a
-// gate: 59.9 us, 5.9 TB/s; 8192 x 5376 with an FP32 residual 83.7 us, 6.3). In between,
+// gate: 55.9 us, 6.3 TB/s; 8192 x 5376 with an FP32 residual 83.2 us, 6.4). In between,
 // latencies and issue slots: blocks start together, wait for their loads together and then
-// compute together (2048 x 5376 to int8 18.7 us where the bytes take 11.5, some 25
-// instructions an element). One row: 3.5 us, launch and three reductions. Bulk copies of
+// compute together (2048 x 5376 to int8 17.2 us where the bytes take 11.5, some 25
+// instructions an element). One row: 3.3 us, launch and three reductions. Bulk copies of
 // the next rows into a ring of shared memory by persistent blocks were slower, 80 us
-// instead of 59: they take registers, and so rows in flight.
+// instead of 59 then: they take registers, and so rows in flight.
 #include "internal.h"
 #include "rowwise.cuh"
 
@@ -25,13 +25,15 @@ namespace {
 
 using namespace rowwise;
 
-// A row per block, or (kWarps) per warp, blockDim.y rows to a block. Vectors per
-// thread (us, 8192 x 5376): bf16 residual 4 (59.9; 2: 67.5, 1: 88.8), FP32 residual 2
-// (83.7; 4: 92.4, 1: 108.6; 4452 x 9040 to int8 87.4, 4: 105) but 4 in the longest rows of 16
-// bits (4096 x 16384 136; 2: 165). Four vectors are held to 64 registers: with the 90 the
-// compiler would take, 67.1.
-template <int kAct, int kRes, int kPer, int kMaxThreads, bool kWarps>
-__global__ void __launch_bounds__(kMaxThreads, kPer == 4 && !kWarps ? 2 : 0)
+// A row per block, or (kWarps) per warp, blockDim.y rows to a block. Vectors per thread, and threads x blocks per SM that
+// the registers are held to (us, bf16, 44 M elements):
+//   bf16 residual, norms on both sides and a gate: 3 vectors, 384 x 3 (56 registers): 56.3 at H = 5120, 57.8 at 8192, 60.5 at
+//     9040; 3 vectors, 512 x 2 (58): 57.2, 66.2, 66.0; 4 vectors, 512 x 2 (64): 59.8, 60.6, 65.7; with 2 vectors 67.5 at
+//     5376, with 1 88.8. Rows of more than 9216: 3 vectors, 512 x 2, 59.9 at 12288, 4 65.8;
+//   FP32 residual, the same / to int8: 2 vectors 82.0 / 79.0 at 4096, 92.6 / 91.9 at 6912, 117 / 121 at 11008; 3 vectors 87.1 /
+//     78.5, 89.0 / 79.6, 95.4 / 86.9.
+template <int kAct, int kRes, int kPer, int kMaxThreads, int kBlocks, bool kWarps>
+__global__ void __launch_bounds__(kMaxThreads, kBlocks)
 block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
     __shared__ __align__(16) float scratch[3][32];
     const long long row = kWarps ? blockIdx.x * static_cast<long long>(blockDim.y) + threadIdx.y : blockIdx.x;
@@ -159,20 +161,31 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
 template <int kAct, int kRes>
 cudaError_t launch_typed(const BlockNormArgs& a, cudaStream_t s) {
     // by H alone: a row's sums do not depend on the number of rows
-    const bool two = kRes == kF32 && (kAct == kF32 || a.H <= 12288);
-    const Layout l = layout_of(a.H / 8, two ? 2 : 4);
+    const long long vecs = a.H / 8;
+    const Layout l = layout_of(vecs, kRes == kF32 ? 2 : 4);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((a.T + l.y - 1) / l.y));
     cfg.blockDim = dim3(static_cast<unsigned>(l.x), static_cast<unsigned>(l.y));
     cfg.stream = s;
     if (l.y > 1) {
-        if (l.per == 1) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 1, 128, true>, a);
-        if (l.per == 2) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 2, 128, true>, a);
-        if constexpr (kRes != kF32) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 4, 128, true>, a);
+        if (l.per == 1) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 1, 128, 0, true>, a);
+        if (l.per == 2) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 2, 128, 0, true>, a);
+        if constexpr (kRes != kF32) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 4, 128, 0, true>, a);
     }
-    if constexpr (kRes == kF32)
-        if (two) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 2, 1024, false>, a);
-    if constexpr (kAct != kF32) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 4, 512, false>, a);
+    [[maybe_unused]] auto threads = [&](int per) { return static_cast<unsigned>((vecs + per - 1) / per + 31) / 32 * 32; };
+    if constexpr (kRes == kF32) {
+        if (kAct == kF32 || a.H < 6144)
+            return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 2, 1024, 0, false>, a);
+    }
+    if constexpr (kAct != kF32) {
+        if (a.H > 12288) {
+            cfg.blockDim.x = threads(4);
+            return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 4, 512, 2, false>, a);
+        }
+        cfg.blockDim.x = threads(3);
+        if (cfg.blockDim.x > 384) return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 3, 512, 2, false>, a);
+        return cudaLaunchKernelEx(&cfg, block_norm_kernel<kAct, kRes, 3, 384, 3, false>, a);
+    }
     return cudaErrorInvalidValue;   // not reached
 }
 
