@@ -111,7 +111,9 @@ __device__ __forceinline__ bool group_wait(int id, int threads, bool first, cons
 }
 
 // Bounded wait for the last phase of each ring barrier that `steps` steps have
-// used: nothing may be in flight to a CTA that has left.
+// used: nothing, neither a copy nor the arrival of a commit, may be in flight to a
+// CTA that has left. A later commit's arrival on another barrier does not say that
+// this one's has landed, so every barrier that commits arrive on is drained.
 __device__ __forceinline__ void drain_ring(const uint64_t* bars, int stages, long long steps) {
     const unsigned long long t0 = clock64();
     for (long long i = steps > stages ? steps - stages : 0; i < steps; ++i)
@@ -469,7 +471,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
         const bool leader = elect_one();
         const uint64_t desc_x = sw128_kmajor_desc(C::kInline ? st_wide(0) : st_x(0));
         const uint32_t bar_afull = smem_u32(&bars->afull[0]), bar_aempty = smem_u32(&bars->aempty[0]);
-        int as = 0, seg = 0;
+        int as = 0, seg = 0, committed = 0;
         uint32_t aparity = 0;
         bool ok = true;
         for (int u = u_begin, k0 = k_begin; u < u_end && ok; ++seg, k0 = 0) {
@@ -495,6 +497,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
                                         kt != k0 || kk);
                     umma_commit(bar_aempty + 8 * as);
                 }
+                ++committed;
                 __syncwarp();
                 if (++as == A) as = 0, aparity ^= 1u;
             }
@@ -506,6 +509,8 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
         if (leader) {
             umma_commit(smem_u32(&bars->drain));
             drain_ring(&bars->drain, 1, 1);
+            drain_ring(bars->aempty, A, committed);
+            drain_ring(bars->tfull, 2, seg);   // the epilogue may have given up
         }
     } else if (warp >= kWidenWarp0) {
         // ------------------------------------------------------------ codes to operands
@@ -921,7 +926,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
 #pragma unroll
             for (int i = 0; i < 4; ++i) mine[32 * i + lane] = 32 * i + lane < mc ? __ldg(sa + m0 + 32 * i + lane) : 0.f;
             __syncwarp();
-            if (!group_wait(8, kEpiWarps * 32, threadIdx.x == kEpiWarp0 * 32, ab, smem_u32(&bars->tfull), it & 1)) break;
+            if (!group_wait(8, kEpiWarps * 32, threadIdx.x == kEpiWarp0 * 32, ab, smem_u32(&bars->tfull), it & 1)) {
+                // one commit at most is on its way to this CTA
+                if (threadIdx.x == kEpiWarp0 * 32) drain_ring(&bars->tfull, 1, it + 1);
+                break;
+            }
             tc_fence_after();
             if constexpr (kOut == kF32) {
 #pragma unroll 1
