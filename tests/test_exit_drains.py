@@ -46,7 +46,9 @@ def committed_and_drained(body):
     return committed, drained
 
 
-@pytest.mark.parametrize("source,names", [("int8_matmul.cu", {"tiles_kernel", "pair_kernel"})])
+@pytest.mark.parametrize("source,names", [("int8_matmul.cu", {"tiles_kernel", "pair_kernel"}),
+                                          ("mx_matmul.cu", {"rows_kernel", "pair_kernel"}),
+                                          ("gemm.cu", {"gemm_kernel"}), ("gemm_skinny.cu", {"gemm_skinny_kernel"})])
 def test_stages(source, names):
     seen = set()
     for name, body in kernels(source):
@@ -57,3 +59,8 @@ def test_stages(source, names):
         assert {"drain", "tfull"} < committed
         assert committed <= drained, (name, committed - drained)
     assert seen == names
+
+
+def test_every_source_that_commits():
+    named = {n for n in os.listdir(CSRC) if n.endswith(".cu") and "umma_commit" in open(os.path.join(CSRC, n)).read()}
+    assert named == {"int8_matmul.cu", "mx_matmul.cu", "gemm.cu", "gemm_skinny.cu"}

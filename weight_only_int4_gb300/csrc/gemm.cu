@@ -284,9 +284,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
         const int half = lane >> 4, sub = lane & 15;
         int stage = 0;
         uint32_t phase = 0;
-        uint32_t issued_parity[kLoadStages];
-        bool issued[kLoadStages];
-        for (int s = 0; s < kLoadStages; ++s) issued[s] = false, issued_parity[s] = 0;
+        long long steps = 0;
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += npairs) {
             const int m_blk = t % num_m, n_blk = t / num_m;
@@ -317,20 +315,15 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
                     tma_load_2d(ld_a(stage), &tmap_x, kt * BK, row0, fb);
                     tma_load_2d(smem_u32(ld_w(stage)), &tmap_w, col0, kt * (BK / 8), fb);
                 }
-                issued[stage] = true;
-                issued_parity[stage] = phase;
+                ++steps;
                 if (++stage == kLoadStages) { stage = 0; phase ^= 1u; }
             }
         }
-        // copies still in flight must land before this CTA's shared memory is released
+        // copies and commits still in flight must land before this CTA's shared memory is released
         if (lane == 0) {
-            for (int s = 0; s < kLoadStages; ++s) {
-                if (!issued[s]) continue;
-                const uint32_t fb = smem_u32(&bars->lfull[s]);
-                const unsigned long long t0 = clock64();
-                while (!mbar_try_wait(fb, issued_parity[s]) && clock64() - t0 < kWaitLimitCycles) {
-                }
-            }
+            drain_ring(bars->lfull, kLoadStages, steps);
+            drain_ring(bars->lempty, kLoadStages, steps);
+            drain_ring(bars->bempty, kBStages, steps);
         }
     } else if (rank == 1 && warp >= 1 && warp <= kRelayWarps) {
         // ------------------------------------------------------------ relays (odd CTA)
@@ -391,18 +384,20 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ 
             }
             // every MMA issued by this thread retires before tensor memory is freed
             umma_commit_pair(smem_u32(&bars->drain));
-            const unsigned long long t0 = clock64();
-            while (!mbar_try_wait(smem_u32(&bars->drain), 0) && clock64() - t0 < kWaitLimitCycles) {
-            }
+            drain_ring(&bars->drain, 1, 1);
         }
     } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + 4) {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;                 // tensor-memory lane quarter of this warp
-        int acc = 0;
+        int acc = 0, it = 0;
         uint32_t acc_phase = 0;
-        for (int t = pair; t < tiles; t += npairs) {
+        for (int t = pair; t < tiles; t += npairs, ++it) {
             const int m_blk = t % num_m, n_blk = t / num_m;
-            if (!warp_wait_bar(smem_u32(&bars->tfull[acc]), acc_phase, ab, lane)) break;
+            if (!warp_wait_bar(smem_u32(&bars->tfull[acc]), acc_phase, ab, lane)) {
+                // up to two commits may be on their way to this CTA
+                if (q == 0 && lane == 0) drain_ring(bars->tfull, 2, it + 2);
+                break;
+            }
             tc_fence_after();
             const int m = m_blk * BM + static_cast<int>(rank) * CM + q * 32 + lane;
             uint16_t* yrow = y + static_cast<size_t>(m) * N;

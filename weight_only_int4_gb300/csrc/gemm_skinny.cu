@@ -376,8 +376,9 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             constexpr uint32_t kIdesc = umma_idesc_f16(BN, MP, kBf16);
             int ls = 0, as = 0;
             uint32_t aph = 0;
-            int acc = 0;
+            int acc = 0, segments = 0;
             uint32_t acc_phase = 0;
+            long long steps = 0;   // committed
             bool ok = true;
             Segments seg{u_begin, u_end, kt_total, streamk != 0, tiles};
             int t, k0, k1;
@@ -401,18 +402,21 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
                     }
                     umma_commit(smem_u32(&bars->lempty[ls]));
                     umma_commit(smem_u32(&bars->aempty[as]));
+                    ++steps;
                     if (++ls == L) ls = 0;
                     if (++as == kOpStages) { as = 0; aph ^= 1u; }
                 }
                 if (!ok) break;
                 umma_commit(smem_u32(&bars->tfull[acc]));
+                ++segments;
                 if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
             }
-            // every MMA issued by this thread retires before tensor memory is freed
+            // every MMA issued by this thread retires before tensor memory is freed, and every commit has arrived
             umma_commit(smem_u32(&bars->drain));
-            const unsigned long long t0 = clock64();
-            while (!mbar_try_wait(smem_u32(&bars->drain), 0) && clock64() - t0 < kWaitLimitCycles) {
-            }
+            drain_ring(&bars->drain, 1, 1);
+            drain_ring(bars->lempty, L, steps);
+            drain_ring(bars->aempty, kOpStages, steps);
+            drain_ring(bars->tfull, 2, segments);
         }
     } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + 4) {
         // ------------------------------------------------------------ epilogue

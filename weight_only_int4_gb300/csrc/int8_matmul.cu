@@ -110,18 +110,6 @@ __device__ __forceinline__ bool group_wait(int id, int threads, bool first, cons
     return ok != 0;
 }
 
-// Bounded wait for the last phase of each ring barrier that `steps` steps have
-// used: nothing, neither a copy nor the arrival of a commit, may be in flight to a
-// CTA that has left. A later commit's arrival on another barrier does not say that
-// this one's has landed, so every barrier that commits arrive on is drained.
-__device__ __forceinline__ void drain_ring(const uint64_t* bars, int stages, long long steps) {
-    const unsigned long long t0 = clock64();
-    for (long long i = steps > stages ? steps - stages : 0; i < steps; ++i)
-        while (!mbar_try_wait(smem_u32(bars + i % stages), static_cast<uint32_t>(i / stages) & 1u) &&
-               clock64() - t0 < kWaitLimitCycles) {
-        }
-}
-
 template <int kOut>
 __device__ __forceinline__ void store1(void* y, size_t at, float v) {
     if constexpr (kOut == kF32) static_cast<float*>(y)[at] = v;

@@ -98,18 +98,6 @@ __device__ __forceinline__ bool warp_wait_bar(uint32_t bar, uint32_t parity, con
     return ok != 0;
 }
 
-// Bounded wait for the last phase of each ring barrier that `steps` steps have
-// used, before the ring's shared memory is given back: no copy, and no arrival
-// of a tensor-core commit, may be in flight to a CTA that has left (the next
-// kernel's CTA, started early, keeps its own barriers there).
-__device__ __forceinline__ void drain_ring(const uint64_t* bars, int stages, long long steps) {
-    const unsigned long long t0 = clock64();
-    for (long long i = steps > stages ? steps - stages : 0; i < steps; ++i)
-        while (!mbar_try_wait(smem_u32(bars + i % stages), static_cast<uint32_t>(i / stages) & 1u) &&
-               clock64() - t0 < kWaitLimitCycles) {
-        }
-}
-
 template <int kOut>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     if constexpr (kOut == kBf16) {
@@ -344,7 +332,11 @@ pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
         int it = 0;
         for (long long t = pair_id; t < tiles; t += npairs, ++it) {
             const int m_blk = static_cast<int>(t % num_m), n_blk = static_cast<int>(t / num_m);
-            if (!warp_wait_bar(smem_u32(&bars->tfull[it & 1]), (it >> 1) & 1, ab, lane)) break;
+            if (!warp_wait_bar(smem_u32(&bars->tfull[it & 1]), (it >> 1) & 1, ab, lane)) {
+                // up to two commits may be on their way to this CTA
+                if (q == 0 && lane == 0) drain_ring(bars->tfull, 2, it + 2);
+                break;
+            }
             tc_fence_after();
             const uint32_t d = tmem + lanes + ((it & 1) ? kAcc1 : 0u);
             const int m = m_blk * BM + static_cast<int>(rank) * CM + q * 32 + lane;
@@ -590,6 +582,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUte
         if (leader) {
             umma_commit(smem_u32(&bars->drain));
             drain_ring(&bars->drain, 1, 1);
+            drain_ring(bars->tfull, 2, seg);   // the epilogue may have given up
         }
     } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------------ epilogue

@@ -68,6 +68,21 @@ __device__ __forceinline__ bool mbar_try_wait_suspend(uint32_t bar, uint32_t par
     return ok != 0;
 }
 
+// Bounded wait (about two seconds at 2 GHz) for the last phase of each ring barrier that
+// `steps` steps have used, before the ring's shared memory is given back: nothing,
+// neither a copy nor the arrival of a commit, may be in flight to a CTA that has left (the
+// next kernel's CTA keeps its own barriers there). A later commit's arrival on
+// another barrier does not say that this one's has landed, so every barrier that commits
+// arrive on is drained.
+__device__ __forceinline__ void drain_ring(const uint64_t* bars, int stages, long long steps) {
+    constexpr unsigned long long kLimitCycles = 4000000000ull;
+    const unsigned long long t0 = clock64();
+    for (long long i = steps > stages ? steps - stages : 0; i < steps; ++i)
+        while (!mbar_try_wait(smem_u32(bars + i % stages), static_cast<uint32_t>(i / stages) & 1u) &&
+               clock64() - t0 < kLimitCycles) {
+        }
+}
+
 // One lane of a converged warp (the same on every call).
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;
