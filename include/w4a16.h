@@ -598,8 +598,9 @@ typedef enum {
  * One of h and weight at least; after and gate only with h. Outputs other than
  * residual_out must not overlap the inputs or one another.
  * scale finite, eps positive and finite (UNSUPPORTED otherwise). H % 16 == 0, H <= 16384.
- * Magnitudes whose square leaves the FP32 range are normalised to zero, as the
- * formula in FP32 gives it. A row with an infinity or a NaN yields NaN in that
+ * u and y are formed in the order written; scale, gate and u are multiplied in any
+ * order. Rows whose sum of squares leaves the FP32 range are normalised to zero, as
+ * the formula in FP32 gives it. A row with an infinity or a NaN yields NaN in that
  * row (codes 0, scale NaN) and leaves other rows alone. Deterministic; a row does
  * not depend on the others. An ordinary launch (no programmatic serialization).
  * Errors: NULL (residual, or a pointer that another one asks for), DTYPE, SHAPE

@@ -8,7 +8,9 @@
 // the first load to the last store, so h and r are read once and r' and y
 // written once. All arithmetic is FP32: u and the r' that is normalised are not
 // rounded in between; r', y and the scale are rounded once, when they are
-// stored. Up to three reductions separate the passes over the registers.
+// stored. Both norms are formed in the order written: h * after or rsqrt * weight
+// first would leave the FP32 range where the formula does not (zero rows under
+// large weights would give NaN). Up to three reductions separate the passes over the registers.
 //
 // What bounds it: HBM for many rows (8192 x 5376, bf16, norms on both sides and a
 // gate: 55.9 us, 6.3 TB/s; 8192 x 5376 with an FP32 residual 83.2 us, 6.4). In between,
@@ -76,9 +78,11 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
             for (int p = 0; p < kPer; ++p) {
                 Vec8<kAct> w;
                 w.load_shared(bytes(a.after) + at[p] * kActVec);
-                products(hv[p], w, r[p]);
+                Pair f[4];
+                hv[p].widen(r[p]);
+                w.widen(f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) r[p][i] = mul2(r[p][i], by_h);
+                for (int i = 0; i < 4; ++i) r[p][i] = mul2(mul2(r[p][i], by_h), f[i]);
             }
         } else {
 #pragma unroll
@@ -133,7 +137,7 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
         w.load_shared(bytes(a.weight) + at[p] * kActVec);
         w.widen(f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[p][i] = mul2(r[p][i], mul2(by_r, f[i]));
+        for (int i = 0; i < 4; ++i) r[p][i] = mul2(mul2(r[p][i], by_r), f[i]);
     }
     if (!a.codes) {
         uint8_t* y_row = static_cast<uint8_t*>(a.y) + row * H * kBytes<kAct>;

@@ -107,8 +107,8 @@ struct Vec8 {
     }
 };
 
-// Sum of squares of eight values onto two sums, and the products of two vectors:
-// of 16-bit values without widening them first, each product exact.
+// Sum of squares of eight values onto two sums: of 16-bit values without widening
+// them first, each square exact.
 template <int kType>
 __device__ __forceinline__ float2 add_squares(const Vec8<kType>& x, float2 sum) {
     if constexpr (kType == kF32) {
@@ -125,22 +125,6 @@ __device__ __forceinline__ float2 add_squares(const Vec8<kType>& x, float2 sum) 
             sum.y = fma_mixed<kType == kBf16, 1, 1>(w[i], w[i], sum.y);
         }
         return sum;
-    }
-}
-template <int kType>
-__device__ __forceinline__ void products(const Vec8<kType>& x, const Vec8<kType>& y, Pair (&f)[4]) {
-    if constexpr (kType == kF32) {
-        Pair g[4];
-        x.widen(f);
-        y.widen(g);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], g[i]);
-    } else {
-        const uint32_t* a = reinterpret_cast<const uint32_t*>(x.v);
-        const uint32_t* b = reinterpret_cast<const uint32_t*>(y.v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            f[i] = pair(fma_mixed<kType == kBf16, 0, 0>(a[i], b[i], 0.f), fma_mixed<kType == kBf16, 1, 1>(a[i], b[i], 0.f));
     }
 }
 
