@@ -540,9 +540,12 @@ w4a16_status w4a16_int8_dequant(const int8_t* codes, const float* scale, void* y
  *
  * A [M, K]: activations quantised by w4a16_int8_quantize, a scale per token.
  * B [N, K]: a weight quantised once, a scale per output channel. Any int8 value
- * may occur, -128 too. Sums are exact while they are below 2^24 in magnitude
- * (K <= 1024 always; K of any size for operands that are not nearly all of one
- * sign and of full size), beyond that held in FP32 or wider. Both scales are
+ * may occur, -128 too. A sum is exact where none of its partial sums exceeds 2^24 in
+ * magnitude: wherever sum |a b| does not, so for K <= 1024 always, and beyond that
+ * for a mean |a b| of up to 2^24 / K (780 at K = 21504). Past it, few rows (up to 4,
+ * up to 16 of a small layer and output) are still summed in 32-bit integers and
+ * rounded once, more are summed in FP32 with an error of up to
+ * (K / 16 + 256) 2^-23 sum |a b|: there y of a row may depend on M. Both scales are
  * applied in FP32, a_scale first, and the result is rounded once to `dt` (F16,
  * BF16 or F32). A NaN scale makes every y of its row or column NaN.
  *

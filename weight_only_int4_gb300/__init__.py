@@ -701,7 +701,8 @@ def int8_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, workspace=None
     """y = (A @ B.T) * a_scale[:, None] * b_scale of two int8 operands: A [M, K]
     (activations through int8_quantize) and B [N, K] (a weight, one output channel
     per row). Returns y [M, N] in `out_dtype` (bfloat16 unless given; float16 and
-    float32 too)."""
+    float32 too). Sums are exact while every partial sum stays within 2^24; past
+    that more than a few rows are summed in FP32, and y of a row may depend on M."""
     torch = _torch()
     current = _device_now()
     M, K = _int8_rows("a", a, a_scale, current)

@@ -4,8 +4,8 @@
 //
 // sm_103a has no 8-bit integer tensor instruction of any rate, so the codes go
 // through the fp16 one: a code is a whole number of at most 8 bits, exact in
-// fp16, a product exact in FP32, and the FP32 sum exact while it stays below
-// 2^24. The weights b, which every call streams, are widened on the way from
+// fp16, a product exact in FP32, and the FP32 sum exact while every partial sum
+// stays within 2^24. The weights b, which every call streams, are widened on the way from
 // shared memory to tensor memory, where the MMA takes its first operand from:
 // they cross HBM, L2 and shared memory as single bytes. The activations a are
 // widened in the kernel too (tiles of up to 64 rows) or to fp16 in the workspace by a
