@@ -651,6 +651,22 @@ w4a16_status w4a16_selftest_wait_timeout(w4a16_stream stream);
  */
 w4a16_status w4a16_selftest_mxfp4_matmul_plan(int64_t M, int64_t N, int64_t K, int sms, int* plan);
 
+/*
+ * w4a16_selftest_int8_matmul_plan -- how w4a16_int8_matmul would run a shape (its
+ * first rows, where they are cut into chunks) on a device of `sms` SMs, all
+ * clusters resident, for tests that have to reach each way of running it. Host
+ * only. (No counterpart on the pages this library follows.)
+ * plan[0]  rows of A per tile of 128 rows of B (16, 32, 64 or 128), 0: CTA pairs,
+ *          -1: dot products
+ * plan[1]  CTAs of a cluster that split a tile's K (1: not split); with pairs, a
+ *          tile of the columns that they leave
+ * plan[2]  1 if tiles are shared between CTAs through the workspace
+ * plan[3]  rows of A per tile of the pairs, 0 without pairs
+ * plan[4]  columns of y that the pairs take, 0 without pairs
+ * Errors: NULL, SHAPE.
+ */
+w4a16_status w4a16_selftest_int8_matmul_plan(int64_t M, int64_t N, int64_t K, int sms, int* plan);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* w4a16_status_string(w4a16_status status);
 

@@ -497,6 +497,17 @@ size_t w4a16_int8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     return w4a16::int8_matmul_workspace_bytes(M, N, K, dp);
 }
 
+w4a16_status w4a16_selftest_int8_matmul_plan(int64_t M, int64_t N, int64_t K, int sms, int* plan) {
+    if (!plan) return W4A16_ERR_NULL;
+    const w4a16_status st = check_int8_product(M, N, K);
+    if (st != W4A16_OK) return st;
+    if (sms < 1) return W4A16_ERR_SHAPE;
+    int p[5];
+    w4a16::int8_matmul_plan(M, N, K, sms, p);
+    for (int i = 0; i < 5; ++i) plan[i] = p[i];
+    return W4A16_OK;
+}
+
 w4a16_status w4a16_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale, void* y,
                                int64_t M, int64_t N, int64_t K, w4a16_dtype dt, void* workspace,
                                size_t workspace_bytes, w4a16_stream stream) {

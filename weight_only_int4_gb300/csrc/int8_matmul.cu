@@ -1014,7 +1014,7 @@ PairPlan pair_plan(long long M, long long N, long long K, int sms, long long pai
         const long long step = 38 + std::max(0ll, bm - 128) * 5 / 32, all = (tiles + pairs - 1) / pairs * steps * step;
         if (all < best.cost) best = {static_cast<int>(bm), N, all};
         const long long waves = tiles / pairs, cut = waves * pairs / num_m;   // whole waves, columns of tiles in them
-        if (waves < 1 || cut >= num_n) continue;
+        if (cut < 1 || cut >= num_n) continue;
         const long long rest = ((M + 127) / 128) * ((N - cut * pair::BN + tiles::BN - 1) / tiles::BN);
         if (rest > sms) continue;
         const long long split = std::min<long long>({4, sms / rest, std::max<long long>(1, steps / 2)});
@@ -1066,7 +1066,7 @@ Plan plan(long long M, long long N, long long K, int sms) {
         // in hundredths of a microsecond
         const long long widen = 400 + M * K * 3 / 70000;   // the launch, and the kernel's bytes
         long long least = 1ll << 62;
-        if (M > 64) least = pair_plan(M, N, K, sms, sms / 2).cost + 400 + widen, mp = 0;
+        if (M > 64) least = pair_plan(M, N, K, sms, std::max(1, sms / 2)).cost + 400 + widen, mp = 0;
         for (int rows = most; rows >= 16; rows /= 2) {
             const long long tiles = ((M + rows - 1) / rows) * cols;
             if (tiles > sms || rows < std::min(32, most)) break;
@@ -1266,6 +1266,21 @@ size_t int8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, const Device
     const size_t wide = pl.widen ? static_cast<size_t>(chunk_rows(M)) * static_cast<size_t>(K) * 2 : 0;
     const size_t parts = pl.share ? partial_bytes(dp) : 0;
     return wide + parts ? kControlBytes + parts + wide : 0;
+}
+
+void int8_matmul_plan(int64_t M, int64_t N, int64_t K, int sms, int (&out)[5]) {
+    const Plan pl = plan(M, N, K, sms);
+    const long long rows = pl.widen ? std::min<long long>(M, chunk_rows(M)) : M;
+    long long mp = pl.mp, columns = N;
+    out[0] = pl.mp, out[1] = 1, out[2] = pl.share, out[3] = 0, out[4] = 0;
+    if (pl.mp == 0) {
+        const PairPlan pp = pair_plan(rows, N, K, sms, std::max(1, sms / 2));
+        out[3] = pp.bm, out[4] = static_cast<int>(pp.columns);
+        mp = 128, columns = N - pp.columns;   // the rest
+    }
+    if (columns && (pl.split || pl.mp == 0))
+        out[1] = static_cast<int>(cluster_of((rows + mp - 1) / mp * ((columns + tiles::BN - 1) / tiles::BN),
+                                             (K + kStepK - 1) / kStepK, sms));
 }
 
 cudaError_t launch_int8_matmul(const Int8MatmulArgs& a, int out_type, void* workspace, const DeviceProps& dp,

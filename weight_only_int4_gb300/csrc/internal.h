@@ -196,6 +196,8 @@ struct Int8MatmulArgs {
     int ld;   // elements from one row of y to the next
 };
 size_t int8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, const DeviceProps& dp);
+// How a shape would be run, see w4a16_selftest_int8_matmul_plan.
+void int8_matmul_plan(int64_t M, int64_t N, int64_t K, int sms, int (&out)[5]);
 cudaError_t launch_int8_matmul(const Int8MatmulArgs& a, int out_type, void* workspace, const DeviceProps& dp,
                                cudaStream_t s);
 
