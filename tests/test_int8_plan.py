@@ -129,3 +129,11 @@ def test_refusals(lib):
     assert lib.w4a16_selftest_int8_matmul_plan(1, 8, 16, SMS, None) == w4.ERR_NULL
     for bad in ((0, 8, 16, SMS), (1, 12, 16, SMS), (1, 8, 24, SMS), (1, 8, 131072, SMS), (1, 8, 16, 0)):
         assert lib.w4a16_selftest_int8_matmul_plan(*bad, out) == w4.ERR_SHAPE
+
+
+@pytest.mark.parametrize("sms", [20, 148, 152, 160])
+def test_up_to_four_rows_need_no_workspace(lib, sms):
+    """The binding does not ask for their workspace."""
+    for _, N, K in draws(sms, 2000, (1, 18, 17)):
+        for M in (1, 2, 3, 4):
+            assert plan(lib, M, N, min(K, 131056), sms) == (-1, 1, 0, 0, 0)
