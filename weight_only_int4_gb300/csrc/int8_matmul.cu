@@ -459,8 +459,8 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
         const bool leader = elect_one();
         const uint64_t desc_x = sw128_kmajor_desc(C::kInline ? st_wide(0) : st_x(0));
         const uint32_t bar_afull = smem_u32(&bars->afull[0]), bar_aempty = smem_u32(&bars->aempty[0]);
-        int as = 0, seg = 0, committed = 0;
-        uint32_t aparity = 0;
+        int seg = 0;
+        uint32_t committed = 0;   // steps
         bool ok = true;
         for (int u = u_begin, k0 = k_begin; u < u_end && ok; ++seg, k0 = 0) {
             const int k1 = min(kt_total, k0 + (u_end - u));
@@ -472,7 +472,8 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
             const uint32_t d = tmem + acc * C::kAccCols;
             for (int kt = k0; kt < k1; ++kt) {
                 // the group that wrote the stage had waited for the step's rows of a too
-                if (!uniform_wait_bar(bar_afull + 8 * as, aparity, ab, leader)) { ok = false; break; }
+                const uint32_t as = committed % A;
+                if (!uniform_wait_bar(bar_afull + 8 * as, committed / A & 1u, ab, leader)) { ok = false; break; }
                 tc_fence_after();
                 const uint64_t x = desc_x + static_cast<uint64_t>(as) * (C::kWideBytes >> 4);
                 const uint32_t a = tmem + C::kOpCol0 + as * kOpCols;
@@ -487,7 +488,6 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
                 }
                 ++committed;
                 __syncwarp();
-                if (++as == A) as = 0, aparity ^= 1u;
             }
             if (!ok) break;
             if (leader) umma_commit(smem_u32(&bars->tfull[acc]));
@@ -498,7 +498,6 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
             umma_commit(smem_u32(&bars->drain));
             drain_ring(&bars->drain, 1, 1);
             drain_ring(bars->aempty, A, committed);
-            drain_ring(bars->tfull, 2, seg);   // the epilogue may have given up
         }
     } else if (warp >= kWidenWarp0) {
         // ------------------------------------------------------------ codes to operands
@@ -544,8 +543,11 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
             const int m0 = t % num_m * MP, mc = min(MP, M - m0);
             const int n = t / num_m * BN + q * 32 + lane;
             const float tn = n < N ? __ldg(sb + n) : 0.f;
-            if (!group_wait(8, kEpiWarps * 32, threadIdx.x == kEpiWarp0 * 32, ab, smem_u32(&bars->tfull[acc]), (seg >> 1) & 1))
+            if (!group_wait(8, kEpiWarps * 32, threadIdx.x == kEpiWarp0 * 32, ab, smem_u32(&bars->tfull[acc]), (seg >> 1) & 1)) {
+                // up to two commits may be on their way
+                if (threadIdx.x == kEpiWarp0 * 32) drain_ring(bars->tfull, 2, seg + 2);
                 break;
+            }
             tc_fence_after();
             const bool whole = k0 == 0 && k1 == kt_total;
             // slot 1: the tile begins here; slot 0: an earlier CTA began it
