@@ -13,10 +13,10 @@
 // large weights would give NaN). Up to three reductions separate the passes over the registers.
 //
 // What bounds it: HBM for many rows (8192 x 5376, bf16, norms on both sides and a
-// gate: 55.9 us, 6.3 TB/s; 8192 x 5376 with an FP32 residual 83.2 us, 6.4). In between,
+// gate: 56.1 us, 6.3 TB/s; 8192 x 5376 with an FP32 residual 83.5 us, 6.3). In between,
 // latencies and issue slots: blocks start together, wait for their loads together and then
-// compute together (2048 x 5376 to int8 17.2 us where the bytes take 11.5, some 25
-// instructions an element). One row: 3.3 us, launch and three reductions. Bulk copies of
+// compute together (2048 x 5376 to int8 17.4 us where the bytes take 11.5, some 26
+// instructions an element). One row: 3.4 us, launch and three reductions. Bulk copies of
 // the next rows into a ring of shared memory by persistent blocks were slower, 80 us
 // instead of 59 then: they take registers, and so rows in flight.
 #include "internal.h"
@@ -33,7 +33,11 @@ using namespace rowwise;
 //     9040; 3 vectors, 512 x 2 (58): 57.2, 66.2, 66.0; 4 vectors, 512 x 2 (64): 59.8, 60.6, 65.7; with 2 vectors 67.5 at
 //     5376, with 1 88.8. Rows of more than 9216: 3 vectors, 512 x 2, 59.9 at 12288, 4 65.8;
 //   FP32 residual, the same / to int8: 2 vectors 82.0 / 79.0 at 4096, 92.6 / 91.9 at 6912, 117 / 121 at 11008; 3 vectors 87.1 /
-//     78.5, 89.0 / 79.6, 95.4 / 86.9.
+//     78.5, 89.0 / 79.6, 95.4 / 86.9. Rows of more than 12288: 4 vectors, 512 x 2 (64, 212 bytes of spills) 125 / 107 at 12304,
+//     112 / 100 at 16384; without spills 4 vectors, 512 x 1 (114) 129 / 130, 120 / 117; 3 vectors, 704 x 1 (74) 127 / 126, 115 /
+//     116; 2 vectors, 1024 (60) 129 / 130, 117 / 119. One row of 16384 alone 7.0 us; 6.1, 6.1, 6.4 in the others.
+//   FP32 activations: 2 vectors, up to 1024 threads; 8192 x 8192 199 us, 498 x 13568 to int8 27.5.
+// Kernels held to 56 registers spill 8 bytes (bf16 residual) or 28 (FP32), 4 vectors with a 16-bit residual 20.
 template <int kAct, int kRes, int kPer, int kMaxThreads, int kBlocks, bool kWarps>
 __global__ void __launch_bounds__(kMaxThreads, kBlocks)
 block_norm_kernel(const __grid_constant__ BlockNormArgs a) {

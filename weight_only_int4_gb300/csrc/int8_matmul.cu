@@ -2,8 +2,9 @@
 //
 //     y[m, n] = (sum_k a[m, k] b[n, k]) * sa[m] * sb[n].
 //
-// sm_103a has no 8-bit integer tensor instruction of any rate, so the codes go
-// through the fp16 one: a code is a whole number of at most 8 bits, exact in
+// sm_103a's tcgen05.mma has no integer kind, and its warp-level int8 product
+// (mma.sync) runs at 158 Top/s, a quarter of the warp-level fp16 one's 604
+// (measured), so the codes go through the fp16 tcgen05.mma: a code is a whole number of at most 8 bits, exact in
 // fp16, a product exact in FP32, and the FP32 sum exact while every partial sum
 // stays within 2^24. The weights b, which every call streams, are widened on the way from
 // shared memory to tensor memory, where the MMA takes its first operand from:
@@ -201,7 +202,8 @@ __device__ __forceinline__ int dot16(uint4 a, uint4 b, int acc) {
 // ones leave few SMs idle; registers are left to the loads (one resident block
 // asked for: with the compiler's own choice 39.1 us instead of 34.6 at
 // 1 x 43008 x 5376, less in flight).
-// 1 x 43008 x 5376 34.5 us (6.7 TB/s), 4 rows 39.3; 1 x 2048 x 2048 1.9.
+// 1 x 43008 x 5376 34.5 us (6.7 TB/s), 4 rows 39.3; 1 x 2048 x 2048 1.9; 1 x 4096 x 131056 80.2 (6.7 TB/s). With few
+// rows of b a warp still walks all of K: 8 x 264 x 8208 9.9 us, 4 x 264 x 131056 99 (the bytes take 5).
 constexpr int kWarps = 4;
 
 template <int kOut, int MT, int kRows, int kDeep>
@@ -287,9 +289,15 @@ cudaError_t launch(const Int8MatmulArgs& a, cudaStream_t s) {
 //     which adds the two FP32 parts from global memory, the lower CTA's first.
 // All three are deterministic.
 //
-// 64 x 16384 x 5376 23.0 us, 16 x 43008 x 5376 44.6, 128 x 43008 x 5376 60.8. A step
-// takes 0.39 us with 16 rows and 0.40 with 64 (HBM: 0.37 for 152 CTAs), 0.48 with 128 (48 KB a step into the SM); launch to first load, the
-// last epilogue and joins take 5 to 8 us.
+// 64 x 16384 x 5376 23.4 us, 16 x 43008 x 5376 44.5, 64 rows 52.4, 128 60.9; K of any length:
+// 64 x 4096 x 65536 60.4. From K = 2688 to 21504, a step and what does not go with K take
+//   one tile to a CTA (N = 16384)    0.37 to 0.41 us and 5 to 7 us with 16 rows, 0.39 to 0.41 and 6 to 7 with 64;
+//   units shared (N = 43008)         0.36 to 0.38 and 9 to 12 with 16 rows, 0.37 to 0.39 and 11 to 15 with 32, 0.40 to
+//                                    0.43 and 12 to 16 with 64, 0.41 to 0.44 and 18 to 23 with 128, the kernel that
+//                                    widens them included.
+// HBM alone: 0.37 us a step for 152 CTAs, 0.31 for the 128 that N = 16384 gives a tile. Sharing costs some 5 us over whole
+// tiles, parts in global memory and their joins, and more with more rows. 72 registers a thread, 4 to 12 bytes of spills
+// with 32 rows and more.
 namespace tiles {
 
 constexpr int BN = 128;
@@ -688,8 +696,12 @@ tiles_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUt
 // (2048 x 16384 x 512 42 us instead of 34 with bm = 256), nor was sharing K steps
 // between pairs: the FP32 parts of a tile are 256 KB (512 x 5376 x 5376 44 us instead of 33).
 //
-// 2048 x 43008 x 5376 457 us, 2.07 PFLOP/s: at the rate of the fp16 MMAs (a
-// K step's eight take about 0.6 us, its 48 KB of loads 0.58 at 82 KB a us and SM).
+// 2048 x 43008 x 5376 458 us in a burst, 2.07 PFLOP/s: at the rate of the fp16 MMAs (a
+// K step's eight take about 0.6 us, its 48 KB of loads 0.58 at 82 KB a us and SM). In a
+// loop the power limit decides, and with it the codes: 463 to 483 us with uniform ones, 449
+// to 464 as activations and weights have them. FP32 results, twice the bytes, stored before
+// the next tile's MMAs start: 517 us; 4096 x 4096 x 4096 96 (bf16 82), 2048 x 16384 x 1024 75
+// (51). 2048 x 4096 x 65536 632. 96 registers a thread; 24 bytes of spills with 16-bit results.
 namespace pair {
 
 constexpr int BN = 256, CM = 128, CN = 128;   // CM: rows of a per CTA at most
@@ -998,12 +1010,14 @@ long long chunk_rows(long long M) {
 }
 
 // Rows of a per tile of the pairs, and the columns of y that the pairs take: all of them, or those of whole waves, the rest
-// going to 128-row tiles (split over clusters of up to 4) in a second kernel. By an estimate in hundredths of a microsecond:
+// going to 128-row tiles in a second kernel, in clusters of up to 8. By an estimate in hundredths of a microsecond:
 // a K step of a pair takes 0.38 us with up to 128 rows, 0.44, 0.46, 0.51 and 0.58 with 160, 192, 224 and 256 (two tiles
-// along M; 0.47 to 0.58 with one, bound by HBM); one on 128-row tiles 0.5, the second kernel 6 us besides. With tiles of
+// along M; 0.47 to 0.58 with one, bound by HBM); one on 128-row tiles 0.5, the second kernel 6 us besides. Clusters count as 4
+// at most: with all 8 counted the rest is chosen where it loses (201 x 10936 x 11536 52.8 us, then 61.9; 343 x 13488 x 10320
+// 81.4 / 88.5; 2351 x 1808 x 13088 97.9 / 94.1), with 4 launched it takes longer (353 x 13032 x 21312 155 / 164). With tiles of
 // 256 rows / so (us): 600 x 4096 x 4096 27.2 / 22.0, 300 x 16384 x 1024 23.4 / 17.3, 420 x 5944 x 16944 81.9 / 64.7,
 // 4096 x 4096 x 4096 90.1 / 81.6. All columns on pairs of 256 rows / whole waves and the rest: 436 x 10672 x 13200 (84 tiles
-// on 76 pairs) 124.5 / 89.6, 1024 x 5120 x 5376 (80) 58.3 / 45.8.
+// on 76 pairs) 124.5 / 85.2, 1024 x 5120 x 5376 (80) 58.3 / 45.8.
 struct PairPlan {
     int bm;
     long long columns, cost;

@@ -52,7 +52,8 @@ __global__ void __launch_bounds__(kMaxThreads) quant_row_kernel(const void* __re
 }
 
 // Rows longer than a block holds (65536 elements of 16 bits, 32768 of 32): read
-// twice, the second time mostly from L2.
+// twice, the second time mostly from L2. 2048 x 65552 bf16 103 us (3.9 TB/s; 77 at 65536,
+// held in registers), 2048 x 131056 212, FP32 385 (3.5).
 template <int kType>
 __global__ void __launch_bounds__(1024) quant_long_kernel(const void* __restrict__ x, int8_t* __restrict__ codes,
                                                           float* __restrict__ scales, int K) {
@@ -80,7 +81,8 @@ __global__ void __launch_bounds__(1024) quant_long_kernel(const void* __restrict
 }
 
 // A thread takes 8 codes at a time, four such loads in flight: c * s in FP32,
-// rounded to the output type. 43008 x 5376 to bf16 111 us (6.2 TB/s).
+// rounded to the output type. 43008 x 5376 to bf16 or fp16 112 us (6.2 TB/s), to FP32 265
+// (4.4).
 template <int kType, typename Index>
 __global__ void __launch_bounds__(256) dequant_kernel(const int8_t* __restrict__ codes,
                                                       const float* __restrict__ scales, void* __restrict__ y,
